@@ -31,6 +31,15 @@ EXPORTS = ("b2b_gemm_create", "b2b_gemm_run", "b2b_chain_create", "b2b_chain_cre
            "b2b_mfma_probe", "b2b_fp8_convert_probe")
 # measurement instruments (b2b_bench.h)
 BENCH_EXPORTS = ("b2b_bench_mfma", "b2b_bench_copy", "b2b_bench_stream")
+# attention operators (b2b_attn.h)
+ATTN_EXPORTS = ("b2b_attn_create", "b2b_attn_workspace", "b2b_attn_run", "b2b_prefix_attn_workspace",
+                "b2b_prefix_attn_run", "b2b_attn_destroy")
+ATTN_CAUSAL = 1
+
+
+class Rows(ctypes.Structure):
+    """b2b_rows_t: rows of heads in device memory, strides in elements."""
+    _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
 
 
 class B2BError(RuntimeError):
@@ -77,7 +86,14 @@ def lib():
         L.b2b_bench_mfma.argtypes = [i32, i32, i64, vp, ctypes.POINTER(ctypes.c_double), vp]
         L.b2b_bench_copy.argtypes = [vp, vp, i64, i32, vp]
         L.b2b_bench_stream.argtypes = [vp, i64, vp, i64, i32, vp]
-        for n in EXPORTS + BENCH_EXPORTS:
+        sz, szp = ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t)
+        L.b2b_attn_create.argtypes = [ctypes.POINTER(vp), i32, i32, i32, i32, ctypes.c_float, u32]
+        L.b2b_attn_workspace.argtypes = [vp, i32, i64, i64, szp]
+        L.b2b_attn_run.argtypes = [vp, i32, i64, i64, Rows, Rows, Rows, Rows, vp, vp, vp, vp, sz, vp]
+        L.b2b_prefix_attn_workspace.argtypes = [vp, i32, i64, i64, szp]
+        L.b2b_prefix_attn_run.argtypes = [vp, i32, i64, i64, Rows, Rows, Rows, Rows, i64, Rows, i64, vp, Rows, vp, sz, vp]
+        L.b2b_attn_destroy.argtypes = [vp]
+        for n in EXPORTS + BENCH_EXPORTS + ATTN_EXPORTS:
             if n not in ("b2b_status_string",):
                 getattr(L, n).restype = i32
         _lib = L
@@ -435,3 +451,11 @@ def to_host(t):
     if t.dtype in (torch.float64, torch.float32):
         return t.numpy()
     return t.view(torch.int16).numpy().view(np.uint16)
+
+
+def __getattr__(name):
+    """The attention plans (chip_fusion_amd.attention), imported when first named."""
+    if name in ("Attention", "PrefixAttention"):
+        from . import attention
+        return getattr(attention, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -1,0 +1,198 @@
+"""Attention plans (b2b_attn.h): argument checks and marshalling for the
+library's attention kernels.
+
+Tensors are taken as they lie: [rows, heads, dim] with any row and head
+strides that are multiples of 8 elements, dim contiguous -- slices of a fused
+projection, or [heads, rows, dim] storage seen transposed.  Everything runs
+on the device that holds the tensors, on `stream` or on that device's current
+stream; outputs and workspaces that a call allocates come from torch's
+allocator on that stream, so overlapping calls and captured graphs each have
+their own.
+"""
+import contextlib
+import ctypes
+
+import torch
+
+from . import ATTN_CAUSAL, DTYPES, Rows, TORCH_DTYPES, _check, lib
+
+
+def _rows(t, name, dtype, shape):
+    """ValueError unless t is a device tensor [rows, heads, dim] that the
+    kernels can address; its b2b_rows_t."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name}: a torch tensor is expected, got {type(t).__name__}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: dtype {dtype} expected, got {t.dtype}")
+    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        want = ", ".join("any" if n is None else str(n) for n in shape)
+        raise ValueError(f"{name}: shape [{want}] expected, got {list(t.shape)}")
+    if t.numel() == 0:
+        return Rows(None, 0, 0)
+    if t.stride(-1) != 1 and t.shape[-1] != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    rows, heads, dim = t.shape[-3:]
+    ld = t.stride(-3) if rows > 1 else dim      # a stride that is never stepped by
+    hs = t.stride(-2) if heads > 1 else 0
+    if ld % 8 or hs % 8 or t.data_ptr() % 16:
+        raise ValueError(f"{name}: rows and heads must start on 16-byte boundaries")
+    if ld < dim:
+        raise ValueError(f"{name}: rows overlap (row stride {ld}, {dim} columns)")
+    return Rows(t.data_ptr(), ld, hs)
+
+
+def _starts(cu, name, seqs=None):
+    if not isinstance(cu, torch.Tensor) or cu.dtype != torch.int32 or cu.dim() != 1 or not cu.is_contiguous():
+        raise ValueError(f"{name}: a contiguous 1-D int32 tensor is expected")
+    if cu.numel() < 1 or (seqs is not None and cu.numel() != seqs + 1):
+        raise ValueError(f"{name}: {'at least one value' if seqs is None else f'{seqs + 1} values'} expected, "
+                         f"got {cu.numel()}")
+    return cu.numel() - 1
+
+
+def _on_one_device(**tensors):
+    """The CUDA device that holds all the tensors."""
+    first = None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if t.device.type != "cuda":
+            raise ValueError(f"{name}: a device (cuda) tensor is expected, got one on {t.device}")
+        if first is not None and t.device != first:
+            raise ValueError(f"{name}: on {t.device}, the others on {first}")
+        first = t.device
+    return first
+
+
+@contextlib.contextmanager
+def _running_on(device, stream):
+    """Makes the tensors' device current and `stream` (or its current stream)
+    the one that allocations belong to; yields the stream's handle."""
+    with torch.cuda.device(device):
+        s = torch.cuda.current_stream(device) if stream is None else stream
+        if s.device != device:
+            raise ValueError(f"stream: on {s.device}, the tensors on {device}")
+        with torch.cuda.stream(s):
+            yield ctypes.c_void_p(s.cuda_stream)
+
+
+def _bytes(call, handle, *sizes):
+    n = ctypes.c_size_t()
+    _check(getattr(lib(), call)(handle, *sizes, ctypes.byref(n)), call)
+    return n.value
+
+
+def _workspace(n, device):
+    """n bytes for one run (the allocator keeps them until the stream is past it)."""
+    return (None, None) if n == 0 else (lambda w: (w, ctypes.c_void_p(w.data_ptr())))(
+        torch.empty(n, dtype=torch.uint8, device=device))
+
+
+def _ptr(t):
+    return None if t is None else ctypes.c_void_p(t.data_ptr())
+
+
+class _Heads:
+    """A plan of the attention of a model's heads (b2b_attn_create)."""
+
+    def __init__(self, dtype, heads, kv_heads, head_dim, scale, flags):
+        code = DTYPES[dtype] if isinstance(dtype, str) else int(dtype)
+        if scale is not None and not scale > 0:
+            raise ValueError("scale: a positive number is expected")
+        self.heads, self.kv_heads, self.dim = heads, kv_heads, head_dim
+        h = ctypes.c_void_p()
+        _check(lib().b2b_attn_create(ctypes.byref(h), code, heads, kv_heads, head_dim, scale or 0.0, flags),
+               "b2b_attn_create")
+        self._h = h
+        self.dtype = TORCH_DTYPES[code]
+
+    def close(self):
+        if getattr(self, "_h", None):
+            lib().b2b_attn_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class Attention(_Heads):
+    """Attention over packed sequences (b2b_attn_run): softmax(scale Q.K^T).V
+    for each sequence and head, causal (aligned to the last key) or full.
+
+    scale: of the scores, dim ** -0.5 by default."""
+
+    def __init__(self, dtype, heads, kv_heads, head_dim, causal=True, scale=None):
+        super().__init__(dtype, heads, kv_heads, head_dim, scale, ATTN_CAUSAL if causal else 0)
+
+    def run(self, Q, K, V, cu_q, cu_k=None, O=None, lse=False, stream=None):
+        """Q [rows, heads, dim], K and V [keys, kv_heads, dim]; sequence s has
+        rows cu_q[s] .. cu_q[s+1]-1 of Q and cu_k[s] .. cu_k[s+1]-1 of K and V
+        (device int32; cu_k defaults to cu_q).  Returns O, or (O, LSE) with
+        `lse` (True, or a float32 tensor [rows, heads] to write).  Rows that
+        belong to no sequence are not written."""
+        cu_k = cu_q if cu_k is None else cu_k
+        seqs = _starts(cu_q, "cu_q")
+        _starts(cu_k, "cu_k", seqs)
+        q = _rows(Q, "Q", self.dtype, (None, self.heads, self.dim))
+        k = _rows(K, "K", self.dtype, (None, self.kv_heads, self.dim))
+        v = _rows(V, "V", self.dtype, (K.shape[0], self.kv_heads, self.dim))
+        want = lse is not False and lse is not None
+        LSE = lse if isinstance(lse, torch.Tensor) else None
+        if O is not None:
+            _rows(O, "O", self.dtype, tuple(Q.shape))
+        if LSE is not None and (LSE.dtype != torch.float32 or LSE.shape != Q.shape[:2] or not LSE.is_contiguous()):
+            raise ValueError("lse: a contiguous float32 tensor [rows, heads] is expected")
+        device = _on_one_device(Q=Q, K=K, V=V, cu_q=cu_q, cu_k=cu_k, O=O, lse=LSE)
+        with _running_on(device, stream) as s:
+            if O is None:
+                O = torch.empty(Q.shape, dtype=Q.dtype, device=device)
+            if want and LSE is None:
+                LSE = torch.empty(Q.shape[:2], dtype=torch.float32, device=device)
+            n = _bytes("b2b_attn_workspace", self._h, seqs, Q.shape[0], K.shape[0])
+            ws, wp = _workspace(n, device)
+            st = lib().b2b_attn_run(self._h, seqs, Q.shape[0], K.shape[0], q, k, v,
+                                    _rows(O, "O", self.dtype, tuple(Q.shape)), _ptr(cu_q), _ptr(cu_k), _ptr(LSE), wp,
+                                    n, s)
+            _check(st, "b2b_attn_run")
+        return (O, LSE) if want else O
+
+
+class PrefixAttention(_Heads):
+    """Attention of one new token a request, all requests behind one shared
+    prefix (b2b_prefix_attn_run): the prefix is read once for the batch."""
+
+    def __init__(self, dtype, heads, kv_heads, head_dim, scale=None):
+        super().__init__(dtype, heads, kv_heads, head_dim, scale, 0)
+
+    def run(self, Q, Kp, Vp, K, V, lens, O=None, stream=None):
+        """Q [batch, heads, dim]; Kp, Vp [prefix, kv_heads, dim], the shared
+        keys and values; K, V [batch, own, kv_heads, dim], of which request b
+        has the first lens[b] (device int32).  Returns O [batch, heads, dim]."""
+        q = _rows(Q, "Q", self.dtype, (None, self.heads, self.dim))
+        batch = Q.shape[0]
+        kp = _rows(Kp, "Kp", self.dtype, (None, self.kv_heads, self.dim))
+        vp = _rows(Vp, "Vp", self.dtype, (Kp.shape[0], self.kv_heads, self.dim))
+        k = _rows(K, "K", self.dtype, (batch, None, self.kv_heads, self.dim))
+        v = _rows(V, "V", self.dtype, tuple(K.shape))
+        for t, name in ((K, "K"), (V, "V")):
+            if batch > 1 and t.stride(0) % 8:
+                raise ValueError(f"{name}: requests must start on 16-byte boundaries")
+        if not isinstance(lens, torch.Tensor) or lens.dtype != torch.int32 or tuple(lens.shape) != (batch,) \
+                or not lens.is_contiguous():
+            raise ValueError(f"lens: a contiguous int32 tensor [{batch}] is expected")
+        if O is not None:
+            _rows(O, "O", self.dtype, tuple(Q.shape))
+        device = _on_one_device(Q=Q, Kp=Kp, Vp=Vp, K=K, V=V, lens=lens, O=O)
+        with _running_on(device, stream) as s:
+            if O is None:
+                O = torch.empty(Q.shape, dtype=Q.dtype, device=device)
+            n = _bytes("b2b_prefix_attn_workspace", self._h, batch, Kp.shape[0], K.shape[1])
+            ws, wp = _workspace(n, device)
+            step = lambda t: t.stride(0) if batch > 1 else 0
+            st = lib().b2b_prefix_attn_run(self._h, batch, Kp.shape[0], K.shape[1], q, kp, vp, k, step(K), v, step(V),
+                                           _ptr(lens), _rows(O, "O", self.dtype, tuple(Q.shape)), wp, n, s)
+            _check(st, "b2b_prefix_attn_run")
+        return O

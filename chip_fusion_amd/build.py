@@ -32,9 +32,11 @@ def _code_only(text):
     return " ".join(text.split())
 
 
-# sources with no cascade kernel in them: planning, validation and launch
-# code, and the measurement instruments (matrix-core loop, copy and stream)
-NON_CASCADE_SOURCES = ("api.hip", "plan.cpp", "plan.hpp", "microbench.hip")
+# sources with no GEMM-cascade kernel in them: planning, validation and launch
+# code, the measurement instruments (matrix-core loop, copy and stream), and
+# the attention operators
+NON_CASCADE_SOURCES = ("api.hip", "plan.cpp", "plan.hpp", "microbench.hip",
+                       "attn.hpp", "attn_launch.hpp", "attn_api.hip", "inst_attn_f16.hip", "inst_attn_bf16.hip")
 
 
 def source_digest():

@@ -1,0 +1,569 @@
+// Attention as a cascade of two products: O = softmax(scale Q.K^T + mask).V,
+// the scores and the probabilities kept on chip.
+//
+// The same rearrangement problem as in the GEMM cascades: the result of the
+// first product is the second one's operand.  The first product is computed
+// transposed, S^T = K.Q^T on v_mfma_f32_32x32x16 (operand: lane l holds row
+// l%32 and the 8 k values 8*(l/32)+u; result: lane l holds column l%32 and
+// rows 8*(r/4) + 4*(l/32) + r%4, r < 16), so a lane holds scores of one query
+// row.  Its maximum and its sum over the keys are then sums over the lane's
+// own registers and one exchange between the two 32-lane halves, and the
+// probabilities, rounded and packed, are the second product's operand as they
+// lie: O^T = V^T.P^T takes its keys in the order
+//     16s + 8*(u/4) + 4*(l/32) + u%4        (K-step s, slot u)
+// which V's transposing LDS reads follow.  Nothing moves between lanes, and
+// O^T's accumulators again hold one query row a lane, so the softmax's
+// rescaling is one factor a lane.
+//
+// Queries of the heads that share a key head lie side by side in a tile:
+// row rr of a sequence is token rr / G, head kvh * G + rr % G.  Short
+// sequences then fill tiles G times better and every key tile that is read
+// serves all heads of its group.
+//
+// One pass over the keys with a running maximum m and sum l (log2 scale: the
+// scale factor carries log2 e, and v_exp_f32 is a power of two).  m moves only
+// when a row's new maximum exceeds it by more than 8: probabilities then stay
+// below 2^8, which 16-bit types and fp32 sums hold as exactly as values
+// below 1, and most tiles rescale nothing.  m starts at the lowest finite
+// value, so that a row which sees no key needs no branch: its probabilities
+// are exp2(-inf) = 0, its sum stays 0 and its output is written as 0.
+#pragma once
+#include "kernels_gen.hpp"
+
+namespace b2bk {
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLowest = -3.402823466e38f;
+constexpr float kMaxLag = 8.f;     // how far (log2) a running maximum may lag behind
+
+// One operand: rows of heads, strides in elements, head_dim contiguous.
+struct AttnRows {
+    const void* p;
+    int64_t ld, hs;     // from row to row, from head to head
+};
+
+struct AttnArgs {
+    AttnRows Q, K, V;
+    void* O;
+    int64_t ldo, hso;
+    const int32_t* cu_q;    // seqs + 1 starts (rows of Q and O); null: sequence s is row s alone
+    const int32_t* cu_k;    // seqs + 1 starts (rows of K and V); null: see kv_stride
+    const int32_t* lens;    // with kv_stride: keys of each sequence
+    int64_t k_stride, v_stride;   // from sequence to sequence, where cu_k is null
+    int64_t rows, keys;     // rows of Q; rows of K (cu_k) or the most keys of a sequence (lens)
+    float* lse;             // [rows, heads], natural logarithm, or null
+    float* part;            // partial results [slots, rows, heads, D], and their
+    float* part_lse;        // [slots, rows, heads] log2-sum-exp2
+    int32_t seqs, heads, kv_heads, group, dim, causal;
+    int32_t splits, slot0;  // parts of the keys; the first one's slot
+    int32_t tiles;          // row tiles (the grid's bound)
+    float sc;               // scale * log2 e
+};
+
+// ---------------------------------------------------------------------------
+// Where a workgroup works
+// ---------------------------------------------------------------------------
+struct SeqTile {
+    int seq, local, tiles;   // sequence, tile within it, tiles it has
+    int64_t q0;              // first row of Q
+    int nq;                  // rows (tokens)
+};
+
+// Sequence starts come from device memory: clamped to the rows there are, so
+// that no values of theirs lead outside the tensors.
+__device__ inline void seq_range(const int32_t* cu, int s, int64_t total, int64_t* start, int* n) {
+    int64_t a = cu[s], b = cu[s + 1];
+    a = a < 0 ? 0 : (a > total ? total : a);
+    b = b < a ? a : (b > total ? total : b);
+    *start = a;
+    *n = (int)(b - a);
+}
+
+// The sequence and place of row tile `tile`, tiles of bm rows of n * group:
+// every wave scans the starts 64 at a time.
+__device__ inline bool find_tile(const int32_t* cu, int seqs, int64_t rows, int group, int bm, int tile, SeqTile* out) {
+    const int lane = threadIdx.x & 63;
+    int before = 0;
+    for (int s0 = 0; s0 < seqs; s0 += 64) {
+        const int s = s0 + lane;
+        int64_t start = 0;
+        int n = 0;
+        if (s < seqs) seq_range(cu, s, rows, &start, &n);
+        const int mine = (int)(((int64_t)n * group + bm - 1) / bm);
+        int sum = mine;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int o = __shfl_up(sum, d);
+            if (lane >= d) sum += o;
+        }
+        const unsigned long long hit = __ballot(before + sum > tile);
+        if (hit) {
+            const int at = __ffsll(hit) - 1;
+            out->seq = __builtin_amdgcn_readfirstlane(s0 + at);
+            out->tiles = __builtin_amdgcn_readfirstlane(__shfl(mine, at));
+            out->local = __builtin_amdgcn_readfirstlane(tile - before - __shfl(sum, at)) + out->tiles;
+            out->nq = __builtin_amdgcn_readfirstlane(__shfl(n, at));
+            const unsigned lo = __builtin_amdgcn_readfirstlane(__shfl((int)(unsigned)start, at));
+            out->q0 = (int64_t)lo;     // rows fit 31 bits
+            return true;
+        }
+        before += __builtin_amdgcn_readfirstlane(__shfl(sum, 63));
+    }
+    return false;
+}
+
+// ---------------------------------------------------------------------------
+// Pieces shared by the kernels
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ float other_half(float x) {
+    unsigned a = __builtin_bit_cast(unsigned, x), b = a;
+    swap32(a, b);      // a: low half's value in the high lanes; b: high half's in the low ones
+    const unsigned l = threadIdx.x & 32;
+    return __builtin_bit_cast(float, l ? a : b);
+}
+
+// Query rows as the first product's operand: lane l holds row l%32, columns
+// 16s + 8*(l/32) + u; columns past D read as zero.
+template <int KS>
+__device__ __forceinline__ void attn_load_q(u4_t (&q)[KS], const AttnArgs& a, int64_t q0, int kvh, int rr, int rows,
+                                            int lane) {
+    const int h = lane >> 5;
+    const int pos = rr / a.group, g = rr - pos * a.group;
+    const char* p = (const char*)a.Q.p + ((q0 + pos) * a.Q.ld + (int64_t)(kvh * a.group + g) * a.Q.hs) * 2;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+        const int c = 16 * s + 8 * h;
+        q[s] = u4_t{0, 0, 0, 0};
+        if (rr < rows && c < a.dim) q[s] = *(const u4_t*)(p + 2 * c);
+    }
+}
+
+// LDS form of a tile of key or value rows: blocks of 32 columns, `R` rows x 64
+// bytes each.  Keys' 16-byte chunks are XORed with bits 2-3 of the row, so the
+// 16 rows that one pass of a 16-byte fragment read covers fall on all banks
+// once; values stay in order, and a transposing read's 4 rows are 256
+// consecutive bytes.
+// Copies row group rg (16 rows) of every block; one instruction moves
+// 16 rows x 64 bytes.  Rows past the resource and columns past D read as zero.
+template <int DB, int R, bool SWZ>
+__device__ __forceinline__ void attn_copy(const unsigned char* dst, __amdgpu_buffer_rsrc_t rs, int ld2, int dim, int rg,
+                                          int lane) {
+    const int row = 16 * rg + (lane >> 2);
+    const int chunk = SWZ ? ((lane & 3) ^ ((row >> 2) & 3)) : (lane & 3);
+    const int off = row * ld2 + chunk * 16;
+#pragma unroll
+    for (int b = 0; b < DB; ++b)
+        lds_dma16<false>(rs, dst + b * R * 64 + rg * 1024, 32 * b + 8 * chunk < dim ? off + 64 * b : -16);
+}
+
+// resource of key rows [row, row + n) of one head
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t attn_rsrc(const void* p, int64_t row, int64_t ld, int64_t at, int n,
+                                                            int dim) {
+    return make_rsrc((const char*)p + (row * ld + at) * 2, n > 0 ? (uint32_t)(((n - 1) * ld + dim) * 2) : 0u);
+}
+
+template <int DT>
+__device__ __forceinline__ u4_t attn_pack(const f16x_t& s, int k) {
+    return u4_t{Ty<DT>::pack(s[8 * k], s[8 * k + 1]), Ty<DT>::pack(s[8 * k + 2], s[8 * k + 3]),
+                Ty<DT>::pack(s[8 * k + 4], s[8 * k + 5]), Ty<DT>::pack(s[8 * k + 6], s[8 * k + 7])};
+}
+
+// A value fragment: 32 columns of block `t`, K-step `ks` (16 rows), in the
+// relabelled key order; vb: the lane's base.
+template <int R>
+__device__ __forceinline__ u4_t attn_vfrag(const unsigned char* v, int vb, int t, int ks) {
+    u4_t out;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        auto* p = (__attribute__((address_space(3))) unsigned char*)(lds_ptr_t)v + vb + t * R * 64 + 1024 * ks + 512 * e;
+        const u2_t w = __builtin_bit_cast(
+            u2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) tr4_t*)p));
+        out[2 * e] = w[0];
+        out[2 * e + 1] = w[1];
+    }
+    return out;
+}
+__device__ __forceinline__ int attn_vbase(int lane) {
+    const int g = lane >> 4, i = lane & 15;
+    return (4 * (g >> 1) + (i >> 2)) * 64 + 32 * (g & 1) + 8 * (i & 3);
+}
+// A key fragment's address for even (0) and odd (1) K-steps.
+__device__ __forceinline__ int attn_kbase(int lane, int odd) {
+    const int row = lane & 31, c = 2 * odd + (lane >> 5);
+    return row * 64 + ((c ^ ((row >> 2) & 3)) << 4);
+}
+
+// The softmax state of one query row a lane.
+struct RowState {
+    float m, l;
+    __device__ __forceinline__ void init() { m = kLowest; l = 0.f; }
+};
+
+// Scores of 32 rows x 32 NK keys -> probabilities, in place; returns with the
+// running maximum moved (and O, l rescaled) where it had to.
+template <int NK, int NO>
+__device__ __forceinline__ void attn_softmax(f16x_t (&s)[NK], RowState& st, f16x_t (&o)[NO], float sc) {
+    float mx = s[0][0];
+#pragma unroll
+    for (int k = 0; k < NK; ++k)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) mx = __builtin_fmaxf(mx, s[k][r]);
+    mx = __builtin_fmaxf(mx, other_half(mx)) * sc;
+    if (__any(mx - st.m > kMaxLag)) {
+        const float m1 = __builtin_fmaxf(st.m, mx);
+        const float alpha = __builtin_amdgcn_exp2f(st.m - m1);
+        st.m = m1;
+        st.l *= alpha;
+#pragma unroll
+        for (int t = 0; t < NO; ++t)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) o[t][r] *= alpha;
+    }
+    float sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < NK; ++k)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            s[k][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[k][r], sc, -st.m));
+            sum += s[k][r];
+        }
+    st.l += sum;
+}
+
+// Masks scores of keys at or past `lim` (counted from the tile's first key,
+// less 4 for the upper half of the lanes).
+template <int NK>
+__device__ __forceinline__ void attn_mask(f16x_t (&s)[NK], int lim) {
+#pragma unroll
+    for (int k = 0; k < NK; ++k)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+            if (32 * k + 8 * (r >> 2) + (r & 3) >= lim) s[k][r] = -__builtin_inff();
+}
+
+// Writes one query row: the output (rounded to the type, 8 consecutive columns
+// a store after a swap of lane halves), or the partial result in fp32.
+template <int DT, int DB, bool PART>
+__device__ __forceinline__ void attn_store(const AttnArgs& a, const f16x_t (&o)[DB], const RowState& st, int64_t q0,
+                                           int kvh, int rr, int rows, int slot, int lane) {
+    const int h = lane >> 5;
+    const float l = st.l + other_half(st.l);
+    // l: a NaN (from a NaN among the row's scores) goes through to the output
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int pos = rr / a.group, head = kvh * a.group + (rr - pos * a.group);
+    const int64_t row = q0 + pos;
+    const bool live = rr < rows;
+    const float lse2 = l == 0.f ? -__builtin_inff() : st.m + __builtin_amdgcn_logf(l);
+    if constexpr (PART) {
+        const int64_t at = ((int64_t)slot * a.rows + row) * a.heads + head;
+        if (live) {
+            if (h == 0) a.part_lse[at] = lse2;
+#pragma unroll
+            for (int t = 0; t < DB; ++t)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int c = 32 * t + 8 * q + 4 * h;
+                    if (c < a.dim)
+                        *(f4_t*)(a.part + at * a.dim + c) = f4_t{o[t][4 * q] * inv, o[t][4 * q + 1] * inv,
+                                                                 o[t][4 * q + 2] * inv, o[t][4 * q + 3] * inv};
+                }
+        }
+    } else {
+        if (live && h == 0 && a.lse) a.lse[row * a.heads + head] = lse2 * kLn2;
+        char* p = (char*)a.O + (row * a.ldo + (int64_t)head * a.hso) * 2;
+#pragma unroll
+        for (int t = 0; t < DB; ++t)
+#pragma unroll
+            for (int q = 0; q < 4; q += 2) {
+                unsigned x0 = Ty<DT>::pack(o[t][4 * q] * inv, o[t][4 * q + 1] * inv);
+                unsigned x1 = Ty<DT>::pack(o[t][4 * q + 2] * inv, o[t][4 * q + 3] * inv);
+                unsigned y0 = Ty<DT>::pack(o[t][4 * q + 4] * inv, o[t][4 * q + 5] * inv);
+                unsigned y1 = Ty<DT>::pack(o[t][4 * q + 6] * inv, o[t][4 * q + 7] * inv);
+                swap32(x0, y0);
+                swap32(x1, y1);
+                const int c = 32 * t + 8 * (q + h);
+                if (live && c < a.dim) *(u4_t*)(p + 2 * c) = u4_t{x0, x1, y0, y1};
+            }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Many rows: a workgroup's waves take 32 MT rows each and share the key tiles
+// ---------------------------------------------------------------------------
+template <int DT_, int DB_, int MT_, bool PART_>
+struct AttnCfg {
+    static constexpr int DT = DT_, DB = DB_, MT = MT_, WAVES = 4, THREADS = 64 * WAVES;
+    static constexpr bool PART = PART_;
+    static constexpr int BM = 32 * MT * WAVES, BN = 64;
+    static constexpr int KS = 2 * DB;                       // K-steps of the first product
+    static constexpr int TILE = BN * DB * 64, LDS_BYTES = 4 * TILE;
+    static_assert(LDS_BYTES <= 160 * 1024, "LDS");
+};
+
+template <class C>
+__device__ __forceinline__ void attn_tile_body(const AttnArgs& a) {
+    __shared__ __attribute__((aligned(1024))) unsigned char lds[C::LDS_BYTES];
+    using M = Ty32<C::DT>;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int kvh = blockIdx.x % a.kv_heads, rest = blockIdx.x / a.kv_heads;
+    const int split = rest % a.splits;
+    SeqTile w;
+    if (a.cu_q) {
+        if (!find_tile(a.cu_q, a.seqs, a.rows, a.group, C::BM, rest / a.splits, &w)) return;
+    } else {
+        // all rows are one sequence's
+        w.seq = 0;
+        w.q0 = 0;
+        w.nq = (int)a.rows;
+        w.tiles = a.tiles;
+        w.local = rest / a.splits;
+    }
+    int64_t k0 = 0;
+    int nk = (int)a.keys;
+    if (a.cu_k) seq_range(a.cu_k, w.seq, a.keys, &k0, &nk);
+    nk = __builtin_amdgcn_readfirstlane(nk);
+    // the last tile of a causal sequence sees the most keys: it starts first
+    const int row0 = (a.causal ? w.tiles - 1 - w.local : w.local) * C::BM;
+    const int rows = w.nq * a.group, shift = nk - w.nq;
+    auto sees = [&](int rr) -> int {     // keys that row rr sees
+        if (rr >= rows) return 0;
+        if (!a.causal) return nk;
+        const int n = rr / a.group + 1 + shift;
+        return n < 0 ? 0 : n;
+    };
+    const int last = (row0 + C::BM < rows ? row0 + C::BM : rows) - 1;
+    const int end = sees(last);                               // keys the workgroup needs
+    const int nt = (end + C::BN - 1) / C::BN;
+    const int t0 = (int)((int64_t)nt * split / a.splits), t1 = (int)((int64_t)nt * (split + 1) / a.splits);
+    const int wrow = row0 + 32 * C::MT * wave;                // this wave's first row
+    int lim[C::MT];
+    u4_t q[C::MT][C::KS];
+    f16x_t o[C::MT][C::DB];
+    RowState st[C::MT];
+#pragma unroll
+    for (int i = 0; i < C::MT; ++i) {
+        const int rr = wrow + 32 * i + (lane & 31);
+        lim[i] = sees(rr) - 4 * (lane >> 5);
+        attn_load_q<C::KS>(q[i], a, w.q0, kvh, rr, rows, lane);
+        st[i].init();
+#pragma unroll
+        for (int t = 0; t < C::DB; ++t) o[i][t] = f16x_t{};
+    }
+    // tiles below `clear` need no mask (they are full and every row of the wave sees them)
+    const int clear = wrow + 32 * C::MT <= rows ? sees(wrow) / C::BN : 0;
+    // tiles from `done` on show this wave nothing
+    const int wlast = (wrow + 32 * C::MT < rows ? wrow + 32 * C::MT : rows) - 1;
+    const int done = wrow < rows ? (sees(wlast) + C::BN - 1) / C::BN : 0;
+    const int64_t khead = (int64_t)kvh * a.K.hs, vhead = (int64_t)kvh * a.V.hs;
+    auto copy = [&](int t) {
+        const int n = nk - t * C::BN < C::BN ? nk - t * C::BN : C::BN;
+        const unsigned char* dst = lds + (t & 1) * 2 * C::TILE;
+        attn_copy<C::DB, C::BN, true>(dst, attn_rsrc(a.K.p, k0 + (int64_t)t * C::BN, a.K.ld, khead, n, a.dim),
+                                      (int)a.K.ld * 2, a.dim, wave, lane);
+        attn_copy<C::DB, C::BN, false>(dst + C::TILE,
+                                       attn_rsrc(a.V.p, k0 + (int64_t)t * C::BN, a.V.ld, vhead, n, a.dim),
+                                       (int)a.V.ld * 2, a.dim, wave, lane);
+    };
+    const int kb0 = attn_kbase(lane, 0), kb1 = attn_kbase(lane, 1), vb = attn_vbase(lane);
+    if (t0 < t1) copy(t0);
+    for (int t = t0; t < t1; ++t) {
+        barrier_vm<0>();          // tile t is in LDS, and everyone is done with tile t - 1
+        if (t + 1 < t1) copy(t + 1);
+        if (t >= done) continue;
+        const unsigned char* kt = lds + (t & 1) * 2 * C::TILE;
+        const unsigned char* vt = kt + C::TILE;
+        f16x_t s[C::MT][2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+#pragma unroll
+            for (int i = 0; i < C::MT; ++i) s[i][k] = f16x_t{};
+#pragma unroll
+            for (int j = 0; j < C::KS; ++j) {
+                const u4_t f = *(const u4_t*)(kt + ((j & 1) ? kb1 : kb0) + (j >> 1) * C::BN * 64 + k * 2048);
+#pragma unroll
+                for (int i = 0; i < C::MT; ++i) s[i][k] = M::mma(f, q[i][j], s[i][k]);
+            }
+        }
+        u4_t p[C::MT][4];
+#pragma unroll
+        for (int i = 0; i < C::MT; ++i) {
+            if (t >= clear) attn_mask<2>(s[i], lim[i] - t * C::BN);
+            attn_softmax<2, C::DB>(s[i], st[i], o[i], a.sc);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) p[i][k] = attn_pack<C::DT>(s[i][k >> 1], k & 1);
+        }
+#pragma unroll
+        for (int b = 0; b < C::DB; ++b)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const u4_t f = attn_vfrag<C::BN>(vt, vb, b, k);
+#pragma unroll
+                for (int i = 0; i < C::MT; ++i) o[i][b] = M::mma(f, p[i][k], o[i][b]);
+            }
+    }
+#pragma unroll
+    for (int i = 0; i < C::MT; ++i)
+        attn_store<C::DT, C::DB, C::PART>(a, o[i], st[i], w.q0, kvh, wrow + 32 * i + (lane & 31), rows, a.slot0 + split,
+                                          lane);
+}
+
+template <class C>
+__global__ __launch_bounds__(C::THREADS) void attn_tile_kernel(AttnArgs a) {
+    attn_tile_body<C>(a);
+}
+
+// ---------------------------------------------------------------------------
+// Few rows (up to 32 a workgroup): the waves take different keys
+// ---------------------------------------------------------------------------
+// What bounds it is the bytes of K and V: each wave streams tiles of 32 keys
+// of its own through two slots of its own LDS (no barrier until the end), and
+// the four waves' results are joined there.
+template <int DT_, int DB_>
+struct AttnRowsCfg {
+    static constexpr int DT = DT_, DB = DB_, WAVES = 4, THREADS = 64 * WAVES, BN = 32, KS = 2 * DB;
+    static constexpr int TILE = BN * DB * 64, WAVE_BYTES = 4 * TILE, LDS_BYTES = WAVES * WAVE_BYTES;
+    static constexpr int LOADS = 4 * DB;      // copies of a tile: 2 row groups x DB blocks, K and V
+    static_assert(LDS_BYTES <= 160 * 1024, "LDS");
+    static_assert(WAVES == 4, "the join is written for four waves");
+};
+
+template <class C>
+__device__ __forceinline__ void attn_rows_body(const AttnArgs& a) {
+    __shared__ __attribute__((aligned(1024))) unsigned char lds[C::LDS_BYTES];
+    __shared__ float join[2][C::WAVES][32];
+    using M = Ty32<C::DT>;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int kvh = blockIdx.x % a.kv_heads;
+    int rest = blockIdx.x / a.kv_heads;
+    const int split = rest % a.splits;
+    rest /= a.splits;
+    const int tile = rest % a.tiles, seq = rest / a.tiles;    // tiles: row tiles of a sequence
+    const int rows = a.group, rr = 32 * tile + (lane & 31);
+    int nk = a.lens[seq];
+    nk = nk < 0 ? 0 : (nk > (int)a.keys ? (int)a.keys : nk);
+    nk = __builtin_amdgcn_readfirstlane(nk);
+    const int nt = (nk + C::BN - 1) / C::BN;
+    const int t0 = (int)((int64_t)nt * split / a.splits), t1 = (int)((int64_t)nt * (split + 1) / a.splits);
+    u4_t q[C::KS];
+    f16x_t o[C::DB];
+    RowState st;
+    attn_load_q<C::KS>(q, a, seq, kvh, rr, rows, lane);
+    st.init();
+#pragma unroll
+    for (int t = 0; t < C::DB; ++t) o[t] = f16x_t{};
+    unsigned char* mine = lds + wave * C::WAVE_BYTES;
+    const int64_t khead = (int64_t)kvh * a.K.hs + seq * a.k_stride, vhead = (int64_t)kvh * a.V.hs + seq * a.v_stride;
+    auto copy = [&](int t, int slot) {      // past the end: the same number of copies, of nothing
+        const int n = t < t1 ? (nk - t * C::BN < C::BN ? nk - t * C::BN : C::BN) : 0;
+        const int64_t at = t < t1 ? (int64_t)t * C::BN : 0;
+        const unsigned char* dst = mine + slot * 2 * C::TILE;
+        const auto kr = attn_rsrc(a.K.p, at, a.K.ld, khead, n, a.dim), vr = attn_rsrc(a.V.p, at, a.V.ld, vhead, n, a.dim);
+#pragma unroll
+        for (int rg = 0; rg < 2; ++rg) {
+            attn_copy<C::DB, C::BN, true>(dst, kr, (int)a.K.ld * 2, a.dim, rg, lane);
+            attn_copy<C::DB, C::BN, false>(dst + C::TILE, vr, (int)a.V.ld * 2, a.dim, rg, lane);
+        }
+    };
+    const int kb0 = attn_kbase(lane, 0), kb1 = attn_kbase(lane, 1), vb = attn_vbase(lane);
+    int slot = 0;
+    if (t0 + wave < t1) copy(t0 + wave, 0);
+    for (int t = t0 + wave; t < t1; t += C::WAVES, slot ^= 1) {
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");    // the other slot has been read
+        copy(t + C::WAVES, slot ^ 1);
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(C::LOADS) : "memory");
+        const unsigned char* kt = mine + slot * 2 * C::TILE;
+        const unsigned char* vt = kt + C::TILE;
+        f16x_t s[1] = {f16x_t{}};
+#pragma unroll
+        for (int j = 0; j < C::KS; ++j)
+            s[0] = M::mma(*(const u4_t*)(kt + ((j & 1) ? kb1 : kb0) + (j >> 1) * C::BN * 64), q[j], s[0]);
+        if ((t + 1) * C::BN > nk) attn_mask<1>(s, nk - t * C::BN - 4 * (lane >> 5));
+        attn_softmax<1, C::DB>(s, st, o, a.sc);
+        u4_t p[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) p[k] = attn_pack<C::DT>(s[0], k);
+#pragma unroll
+        for (int b = 0; b < C::DB; ++b)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) o[b] = M::mma(attn_vfrag<C::BN>(vt, vb, b, k), p[k], o[b]);
+    }
+    // join: every wave's maximum and sum, then its rows, scaled to the common maximum
+    const float l = st.l + other_half(st.l);
+    if (lane < 32) {
+        join[0][wave][lane] = st.m;
+        join[1][wave][lane] = l;
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");     // copies of nothing still write zeros
+    __syncthreads();
+    float m = kLowest, sum = 0.f;
+#pragma unroll
+    for (int v = 0; v < C::WAVES; ++v) m = __builtin_fmaxf(m, join[0][v][lane & 31]);
+#pragma unroll
+    for (int v = 0; v < C::WAVES; ++v)
+        sum += join[1][v][lane & 31] * __builtin_amdgcn_exp2f(join[0][v][lane & 31] - m);
+    const float f = __builtin_amdgcn_exp2f(st.m - m) * (sum == 0.f ? 0.f : 1.f / sum);
+    float* mo = (float*)mine;      // [column quad][row]: 4 floats of a row, 16 bytes a lane
+#pragma unroll
+    for (int b = 0; b < C::DB; ++b)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+            *(f4_t*)(mo + ((8 * b + 2 * g + (lane >> 5)) * 32 + (lane & 31)) * 4) =
+                f4_t{o[b][4 * g] * f, o[b][4 * g + 1] * f, o[b][4 * g + 2] * f, o[b][4 * g + 3] * f};
+    __syncthreads();
+    const int64_t at0 = ((int64_t)(a.slot0 + split) * a.rows + seq) * a.heads + kvh * a.group;
+    if (wave == 0 && lane < 32 && rr < rows)
+        a.part_lse[at0 + rr] = sum == 0.f ? -__builtin_inff() : m + __builtin_amdgcn_logf(sum);
+    for (int i = threadIdx.x; i < 32 * 8 * C::DB; i += C::THREADS) {
+        const int row = i / (8 * C::DB), c = i % (8 * C::DB), r = 32 * tile + row;
+        if (r >= rows || 4 * c >= a.dim) continue;
+        f4_t v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int x = 0; x < C::WAVES; ++x) {
+            const f4_t y = *(const f4_t*)((const float*)(lds + x * C::WAVE_BYTES) + (c * 32 + row) * 4);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] += y[e];
+        }
+        *(f4_t*)(a.part + (at0 + r) * a.dim + 4 * c) = v;
+    }
+}
+
+template <class C>
+__global__ __launch_bounds__(C::THREADS) void attn_rows_kernel(AttnArgs a) {
+    attn_rows_body<C>(a);
+}
+
+// ---------------------------------------------------------------------------
+// Joining partial results: one wave a (row, head)
+// ---------------------------------------------------------------------------
+// O = sum_s w_s O_s / sum_s w_s with w_s = 2^(lse_s - max); parts that saw no
+// key have lse = -inf and weight 0.
+template <int DT>
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int slots) {
+    const int lane = threadIdx.x & 63;
+    const int64_t n = a.rows * a.heads, at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (at >= n) return;
+    const int64_t row = at / a.heads;
+    const int head = (int)(at - row * a.heads);
+    float m = -__builtin_inff();
+    for (int s = lane; s < slots; s += 64) m = __builtin_fmaxf(m, a.part_lse[s * n + at]);
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) m = __builtin_fmaxf(m, __shfl_xor(m, d));
+    const float m0 = m == -__builtin_inff() ? 0.f : m;
+    float sum = 0.f, x = 0.f, y = 0.f;
+    const bool live = 2 * lane < a.dim;
+    for (int s = 0; s < slots; ++s) {
+        const float w = __builtin_amdgcn_exp2f(a.part_lse[s * n + at] - m0);
+        sum += w;
+        if (live) {
+            const float2 v = *(const float2*)(a.part + (s * n + at) * a.dim + 2 * lane);
+            x += w * v.x;
+            y += w * v.y;
+        }
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    if (live)
+        *(unsigned*)((char*)a.O + (row * a.ldo + (int64_t)head * a.hso + 2 * lane) * 2) = Ty<DT>::pack(x * inv, y * inv);
+    if (lane == 0 && a.lse) a.lse[at] = sum == 0.f ? -__builtin_inff() : (m0 + __builtin_amdgcn_logf(sum)) * kLn2;
+}
+
+}  // namespace b2bk

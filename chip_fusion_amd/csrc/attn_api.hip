@@ -1,0 +1,229 @@
+// C ABI of the attention operators (b2b_attn.h): checks, how a call is split
+// over workgroups, launches.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <new>
+
+#include "attn_launch.hpp"
+#include "b2b_attn.h"
+
+struct b2b_attn_plan {
+    int dtype, heads, kv_heads, dim;
+    float scale;
+    bool causal;
+};
+
+namespace {
+
+constexpr int64_t kMaxStride = (int64_t)1 << 23;    // 64 rows' offsets stay below 2^30 bytes
+
+// Rows of heads that the kernels can address: n rows, 16-byte pieces.
+bool rows_ok(const b2b_rows_t& r, int64_t n, int dim) {
+    if (!r.data || (uintptr_t)r.data % 16) return false;
+    if (r.row_stride % 8 || r.head_stride % 8 || r.head_stride < 0) return false;
+    return n <= 1 || (r.row_stride >= dim && r.row_stride <= kMaxStride);
+}
+b2bk::AttnRows dev(const b2b_rows_t& r, int dim) {
+    // a single row's stride is never stepped by; the kernels still size resources with it
+    return {r.data, r.row_stride >= dim && r.row_stride <= kMaxStride ? r.row_stride : dim, r.head_stride};
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// How a call with this many query rows a key head (in all, and a sequence on
+// average) and keys is laid over workgroups.
+struct Split {
+    int mt;            // 32-row sub-tiles a wave
+    int64_t tiles;     // row tiles at most
+    int splits;        // parts of the keys
+};
+Split plan_tiles(const b2b_attn_plan* p, int64_t seqs, int64_t rows, int64_t keys, bool packed) {
+    const int64_t group = p->heads / p->kv_heads;
+    Split s;
+    s.mt = rows * group / seqs > 128 ? 2 : 1;
+    const int bm = b2b::attn_bm(s.mt);
+    s.tiles = packed ? rows * group / bm + seqs : ceil_div(rows * group, bm);
+    const int64_t wgs = s.tiles * p->kv_heads;
+    // too few workgroups to fill the chip: the keys in parts of 256 or more
+    s.splits = (int)std::max<int64_t>(1, std::min<int64_t>({256 / wgs, keys / seqs / 256, 64}));
+    return s;
+}
+// the many-requests kernel's parts of a request's own keys
+int plan_own(const b2b_attn_plan* p, int64_t batch, int64_t own) {
+    const int64_t wgs = batch * p->kv_heads * ceil_div(p->heads / p->kv_heads, 32);
+    return (int)std::max<int64_t>(1, std::min<int64_t>({256 / wgs, own / 256, 64}));
+}
+
+size_t part_bytes(const b2b_attn_plan* p, int64_t slots, int64_t rows) {
+    return (size_t)slots * rows * p->heads * (p->dim + 1) * 4;
+}
+
+bool sizes_ok(const b2b_attn_plan* p, int64_t seqs, int64_t rows, int64_t keys) {
+    return seqs >= 0 && rows >= 0 && keys >= 0 && rows * (int64_t)p->heads <= INT32_MAX && rows <= INT32_MAX &&
+           keys <= INT32_MAX / 2 && seqs <= INT32_MAX / 2;
+}
+
+const b2b::AttnLaunch& launchers(const b2b_attn_plan* p) {
+    return p->dtype == B2B_DTYPE_F16 ? b2b::attn_f16() : b2b::attn_bf16();
+}
+
+b2bk::AttnArgs base_args(const b2b_attn_plan* p) {
+    b2bk::AttnArgs a = {};
+    a.heads = p->heads;
+    a.kv_heads = p->kv_heads;
+    a.group = p->heads / p->kv_heads;
+    a.dim = p->dim;
+    a.sc = p->scale * b2bk::kLog2e;
+    a.splits = 1;
+    return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+b2b_status_t b2b_attn_create(b2b_attn_t* plan, b2b_dtype_t dtype, int32_t heads, int32_t kv_heads, int32_t head_dim,
+                             float scale, uint32_t flags) {
+    if (!plan) return B2B_ERROR_INVALID_VALUE;
+    *plan = nullptr;
+    if (heads < 1 || kv_heads < 1 || heads % kv_heads || heads > 65536 || head_dim < 1 ||
+        (flags & ~(uint32_t)B2B_ATTN_CAUSAL))
+        return B2B_ERROR_INVALID_VALUE;
+    if (!(scale >= 0.f) || !std::isfinite(scale)) return B2B_ERROR_INVALID_VALUE;
+    if ((dtype != B2B_DTYPE_F16 && dtype != B2B_DTYPE_BF16) || head_dim % 8 || head_dim > 128)
+        return B2B_ERROR_NOT_SUPPORTED;
+    b2b_attn_plan* p = new (std::nothrow) b2b_attn_plan();
+    if (!p) return B2B_ERROR_OUT_OF_MEMORY;
+    p->dtype = dtype;
+    p->heads = heads;
+    p->kv_heads = kv_heads;
+    p->dim = head_dim;
+    p->scale = scale > 0.f ? scale : (float)(1.0 / std::sqrt((double)head_dim));
+    p->causal = (flags & B2B_ATTN_CAUSAL) != 0;
+    *plan = p;
+    return B2B_SUCCESS;
+}
+
+b2b_status_t b2b_attn_destroy(b2b_attn_t plan) {
+    delete plan;
+    return B2B_SUCCESS;
+}
+
+b2b_status_t b2b_attn_workspace(b2b_attn_t p, int32_t seqs, int64_t rows, int64_t keys, size_t* bytes) {
+    if (!p || !bytes || !sizes_ok(p, seqs, rows, keys)) return B2B_ERROR_INVALID_VALUE;
+    *bytes = 0;
+    if (!seqs || !rows) return B2B_SUCCESS;
+    const Split s = plan_tiles(p, seqs, rows, keys, true);
+    if (s.splits > 1) *bytes = part_bytes(p, s.splits, rows);
+    return B2B_SUCCESS;
+}
+
+b2b_status_t b2b_attn_run(b2b_attn_t p, int32_t seqs, int64_t rows, int64_t keys, b2b_rows_t Q, b2b_rows_t K,
+                          b2b_rows_t V, b2b_rows_t O, const int32_t* cu_q, const int32_t* cu_k, float* lse,
+                          void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    if (!p || !sizes_ok(p, seqs, rows, keys)) return B2B_ERROR_INVALID_VALUE;
+    if (!seqs || !rows) return B2B_SUCCESS;
+    const int dim = p->dim;
+    if (!rows_ok(Q, rows, dim) || !rows_ok(O, rows, dim) || !cu_q || !cu_k) return B2B_ERROR_INVALID_VALUE;
+    if (keys && (!rows_ok(K, keys, dim) || !rows_ok(V, keys, dim))) return B2B_ERROR_INVALID_VALUE;
+    if (O.data == Q.data || O.data == K.data || O.data == V.data || (uintptr_t)lse % 4) return B2B_ERROR_INVALID_VALUE;
+    const Split s = plan_tiles(p, seqs, rows, keys, true);
+    size_t need = s.splits > 1 ? part_bytes(p, s.splits, rows) : 0;
+    if (need && (!workspace || (uintptr_t)workspace % 16 || workspace_bytes < need)) return B2B_ERROR_INVALID_VALUE;
+    b2bk::AttnArgs a = base_args(p);
+    a.Q = dev(Q, dim);
+    a.K = dev(K, dim);
+    a.V = dev(V, dim);
+    a.O = const_cast<void*>(O.data);
+    a.ldo = O.row_stride;
+    a.hso = O.head_stride;
+    a.cu_q = cu_q;
+    a.cu_k = cu_k;
+    a.rows = rows;
+    a.keys = keys;
+    a.lse = lse;
+    a.seqs = seqs;
+    a.causal = p->causal;
+    a.splits = s.splits;
+    a.tiles = (int32_t)s.tiles;
+    a.part = (float*)workspace;
+    a.part_lse = a.part + (size_t)s.splits * rows * p->heads * dim;
+    const int64_t grid = s.tiles * p->kv_heads * s.splits;
+    if (grid > INT32_MAX) return B2B_ERROR_INVALID_VALUE;
+    const b2b::AttnLaunch& L = launchers(p);
+    if (L.tile(a, s.mt, s.splits > 1, (unsigned)grid, stream) != hipSuccess) return B2B_ERROR_HIP;
+    if (s.splits > 1 && L.join(a, s.splits, stream) != hipSuccess) return B2B_ERROR_HIP;
+    return B2B_SUCCESS;
+}
+
+b2b_status_t b2b_prefix_attn_workspace(b2b_attn_t p, int32_t batch, int64_t prefix, int64_t own, size_t* bytes) {
+    if (!p || !bytes || !sizes_ok(p, batch, batch, prefix) || own < 0 || own > INT32_MAX / 2)
+        return B2B_ERROR_INVALID_VALUE;
+    *bytes = 0;
+    if (!batch) return B2B_SUCCESS;
+    const int64_t slots = (prefix ? plan_tiles(p, 1, batch, prefix, false).splits : 0) + (own ? plan_own(p, batch, own) : 0);
+    *bytes = part_bytes(p, slots, batch);
+    return B2B_SUCCESS;
+}
+
+b2b_status_t b2b_prefix_attn_run(b2b_attn_t p, int32_t batch, int64_t prefix, int64_t own, b2b_rows_t Q,
+                                 b2b_rows_t Kp, b2b_rows_t Vp, b2b_rows_t K, int64_t k_stride, b2b_rows_t V,
+                                 int64_t v_stride, const int32_t* lens, b2b_rows_t O, void* workspace,
+                                 size_t workspace_bytes, hipStream_t stream) {
+    size_t need = 0;
+    if (!p || p->causal) return B2B_ERROR_INVALID_VALUE;
+    const b2b_status_t st = b2b_prefix_attn_workspace(p, batch, prefix, own, &need);
+    if (st != B2B_SUCCESS) return st;
+    if (!batch) return B2B_SUCCESS;
+    const int dim = p->dim;
+    if (!rows_ok(Q, batch, dim) || !rows_ok(O, batch, dim) || O.data == Q.data) return B2B_ERROR_INVALID_VALUE;
+    if (prefix && (!rows_ok(Kp, prefix, dim) || !rows_ok(Vp, prefix, dim) || O.data == Kp.data || O.data == Vp.data))
+        return B2B_ERROR_INVALID_VALUE;
+    if (own && (!rows_ok(K, own, dim) || !rows_ok(V, own, dim) || !lens || k_stride < 0 || v_stride < 0 ||
+                k_stride % 8 || v_stride % 8 || O.data == K.data || O.data == V.data))
+        return B2B_ERROR_INVALID_VALUE;
+    if (need && (!workspace || (uintptr_t)workspace % 16 || workspace_bytes < need)) return B2B_ERROR_INVALID_VALUE;
+    const b2b::AttnLaunch& L = launchers(p);
+    b2bk::AttnArgs a = base_args(p);
+    a.Q = dev(Q, dim);
+    a.O = const_cast<void*>(O.data);
+    a.ldo = O.row_stride;
+    a.hso = O.head_stride;
+    a.rows = batch;
+    const Split s = prefix ? plan_tiles(p, 1, batch, prefix, false) : Split{1, 0, 0};
+    const int own_parts = own ? plan_own(p, batch, own) : 0, slots = s.splits + own_parts;
+    a.part = (float*)workspace;
+    a.part_lse = a.part + (size_t)slots * batch * p->heads * dim;
+    const int64_t grid_p = s.tiles * p->kv_heads * s.splits;
+    const int64_t row_tiles = ceil_div(p->heads / p->kv_heads, 32);
+    const int64_t grid_o = (int64_t)batch * row_tiles * p->kv_heads * own_parts;
+    if (grid_p > INT32_MAX || grid_o > INT32_MAX) return B2B_ERROR_INVALID_VALUE;
+    if (prefix) {
+        a.K = dev(Kp, dim);
+        a.V = dev(Vp, dim);
+        a.keys = prefix;
+        a.seqs = 1;
+        a.splits = s.splits;
+        a.tiles = (int32_t)s.tiles;
+        if (L.tile(a, s.mt, true, (unsigned)grid_p, stream) != hipSuccess) return B2B_ERROR_HIP;
+    }
+    if (own) {
+        a.K = dev(K, dim);
+        a.V = dev(V, dim);
+        a.lens = lens;
+        a.k_stride = k_stride;
+        a.v_stride = v_stride;
+        a.keys = own;
+        a.seqs = batch;
+        a.splits = own_parts;
+        a.slot0 = s.splits;
+        a.tiles = (int32_t)row_tiles;
+        if (L.rows(a, (unsigned)grid_o, stream) != hipSuccess) return B2B_ERROR_HIP;
+    }
+    return L.join(a, slots, stream) == hipSuccess ? B2B_SUCCESS : B2B_ERROR_HIP;
+}
+
+}  // extern "C"

@@ -1,0 +1,66 @@
+// Launchers of the attention kernels, one translation unit per type.
+#pragma once
+#include <hip/hip_runtime.h>
+
+#include "attn.hpp"
+
+namespace b2b {
+
+// row tile of the many-rows kernel with mt sub-tiles of 32 rows a wave
+constexpr int attn_bm(int mt) { return 128 * mt; }
+
+struct AttnLaunch {
+    // grid workgroups of the many-rows kernel (dim: columns, mt: 1 or 2; part: partial results)
+    hipError_t (*tile)(const b2bk::AttnArgs&, int mt, bool part, unsigned grid, hipStream_t);
+    hipError_t (*rows)(const b2bk::AttnArgs&, unsigned grid, hipStream_t);
+    hipError_t (*join)(const b2bk::AttnArgs&, int slots, hipStream_t);
+};
+
+const AttnLaunch& attn_f16();
+const AttnLaunch& attn_bf16();
+
+template <int DT>
+struct AttnLaunchers {
+    template <int DB>
+    static hipError_t tile_db(const b2bk::AttnArgs& a, int mt, bool part, unsigned grid, hipStream_t s) {
+        auto go = [&](auto c) {
+            using C = decltype(c);
+            hipLaunchKernelGGL(b2bk::attn_tile_kernel<C>, dim3(grid), dim3(C::THREADS), 0, s, a);
+        };
+        if (mt == 2) {
+            if (part) go(b2bk::AttnCfg<DT, DB, 2, true>{});
+            else go(b2bk::AttnCfg<DT, DB, 2, false>{});
+        } else {
+            if (part) go(b2bk::AttnCfg<DT, DB, 1, true>{});
+            else go(b2bk::AttnCfg<DT, DB, 1, false>{});
+        }
+        return hipGetLastError();
+    }
+    static hipError_t tile(const b2bk::AttnArgs& a, int mt, bool part, unsigned grid, hipStream_t s) {
+        if (a.dim <= 64) return tile_db<2>(a, mt, part, grid, s);
+        if (a.dim <= 96) return tile_db<3>(a, mt, part, grid, s);
+        return tile_db<4>(a, mt, part, grid, s);
+    }
+    template <int DB>
+    static hipError_t rows_db(const b2bk::AttnArgs& a, unsigned grid, hipStream_t s) {
+        using C = b2bk::AttnRowsCfg<DT, DB>;
+        hipLaunchKernelGGL(b2bk::attn_rows_kernel<C>, dim3(grid), dim3(C::THREADS), 0, s, a);
+        return hipGetLastError();
+    }
+    static hipError_t rows(const b2bk::AttnArgs& a, unsigned grid, hipStream_t s) {
+        if (a.dim <= 64) return rows_db<2>(a, grid, s);
+        if (a.dim <= 96) return rows_db<3>(a, grid, s);
+        return rows_db<4>(a, grid, s);
+    }
+    static hipError_t join(const b2bk::AttnArgs& a, int slots, hipStream_t s) {
+        const int64_t n = a.rows * a.heads;
+        hipLaunchKernelGGL(b2bk::attn_join_kernel<DT>, dim3((unsigned)((n + 3) / 4)), dim3(256), 0, s, a, slots);
+        return hipGetLastError();
+    }
+    static const AttnLaunch& table() {
+        static const AttnLaunch t = {&tile, &rows, &join};
+        return t;
+    }
+};
+
+}  // namespace b2b

@@ -1,0 +1,265 @@
+"""Attention over packed sequences and behind a shared prefix against the
+definition in 64 bits, at the sizes, masks and layouts where it can go wrong."""
+import itertools
+import math
+
+import pytest
+import torch
+
+import attn_ref as R
+import chip_fusion_amd as cf
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f16": torch.float16, "bf16": torch.bfloat16}
+
+
+def _flush(msg):
+    print(f"\n[case] {msg}", flush=True)
+
+
+def _randn(seed, shape, dtype, std=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(shape, generator=g, device="cuda") * std).to(dtype)
+
+
+def _cu(lens):
+    return torch.tensor(R.starts(lens), dtype=torch.int32, device="cuda")
+
+
+def _case(dtype, heads, kv, dim, lq, lk, seed=1, std=1.5):
+    T = DT[dtype]
+    q = _randn(seed, (sum(lq), heads, dim), T, std)
+    k = _randn(seed + 1, (sum(lk), kv, dim), T)
+    v = _randn(seed + 2, (sum(lk), kv, dim), T)
+    return q, k, v
+
+
+CASES = [
+    # dtype, heads, kv heads, dim, query lengths, key lengths, causal
+    ("f16", 1, 1, 64, [1], [1], True),
+    ("bf16", 2, 1, 8, [3, 1], [3, 1], True),
+    ("f16", 4, 4, 40, [63, 64, 65], [63, 64, 65], True),
+    ("bf16", 4, 2, 64, [127, 0, 1, 129, 2], [127, 0, 1, 129, 2], True),
+    ("f16", 6, 2, 72, [31, 33], [95, 97], True),              # pieces behind earlier keys
+    ("bf16", 8, 1, 80, [5, 70], [64, 71], False),
+    ("f16", 3, 1, 96, [100], [300], True),
+    ("bf16", 5, 5, 128, [257], [257], True),
+    ("f16", 8, 2, 128, [300, 20], [300, 20], False),
+    ("bf16", 8, 2, 128, [40, 9], [12, 0], True),              # more rows than keys: the first see none
+    ("f16", 2, 2, 64, [50, 3], [0, 7], False),                # a sequence without keys
+    ("f16", 24, 2, 112, [17], [1500], True),                  # few rows, many keys: split
+    ("bf16", 2, 2, 128, [260], [2100], False),
+    ("f16", 4, 1, 64, [600], [600], True),
+]
+
+
+@pytest.mark.parametrize("case", range(len(CASES)))
+def test_attention(case):
+    dtype, H, Hkv, D, lq, lk, causal = CASES[case]
+    _flush(f"attention {CASES[case]}")
+    q, k, v = _case(dtype, H, Hkv, D, lq, lk)
+    O = torch.full_like(q, math.nan)
+    plan = cf.Attention(dtype, H, Hkv, D, causal=causal)
+    got, lse = plan.run(q, k, v, _cu(lq), _cu(lk), O=O, lse=True)
+    assert got is O
+    torch.cuda.synchronize()
+    want, want_lse, b, bl = R.attention(q, k, v, R.starts(lq), R.starts(lk), causal, D ** -0.5)
+    R.check(got, want, b, "O")
+    R.check(lse, want_lse, bl, "LSE")
+    again = plan.run(q, k, v, _cu(lq), _cu(lk))
+    assert torch.equal(again, got)          # the same values on every run
+
+
+@pytest.mark.parametrize("seqs", [1, 65, 200])
+def test_many_sequences(seqs):
+    """More sequences than a wave scans at once, empty ones among them."""
+    lens = [(7 * i) % 23 for i in range(seqs)]
+    _flush(f"attention {seqs} sequences")
+    q, k, v = _case("bf16", 4, 2, 64, lens, lens, seed=11)
+    got = cf.Attention("bf16", 4, 2, 64).run(q, k, v, _cu(lens))
+    torch.cuda.synchronize()
+    want, _, b, _ = R.attention(q, k, v, R.starts(lens), R.starts(lens), True, 0.125)
+    R.check(got, want, b)
+
+
+@pytest.mark.parametrize("scale", [None, 0.02, 3.0])
+def test_scale_and_large_scores(scale):
+    """Scores from nearly equal to one key taking all of the weight."""
+    _flush(f"attention scale {scale}")
+    q, k, v = _case("bf16", 2, 2, 64, [150], [150], seed=21, std=8.0)
+    got, lse = cf.Attention("bf16", 2, 2, 64, scale=scale).run(q, k, v, _cu([150]), lse=True)
+    torch.cuda.synchronize()
+    want, wl, b, bl = R.attention(q, k, v, [0, 150], [0, 150], True, 0.125 if scale is None else scale)
+    R.check(got, want, b)
+    R.check(lse, wl, bl)
+
+
+def test_rising_scores_move_the_maximum():
+    """Keys in rising order of their scores: the running maximum moves in every
+    tile, by less and by more than the lag that is allowed."""
+    for step in (0.2, 3.0):
+        _flush(f"attention rising by {step}")
+        n = 400
+        q = torch.ones((n, 1, 64), dtype=torch.float16, device="cuda")
+        k = (torch.arange(n, device="cuda").float()[:, None, None] * (step / 64)).expand(n, 1, 64).half().contiguous()
+        v = _randn(5, (n, 1, 64), torch.float16)
+        got, lse = cf.Attention("f16", 1, 1, 64, causal=False, scale=1.0).run(q, k, v, _cu([n]), lse=True)
+        torch.cuda.synchronize()
+        want, wl, b, bl = R.attention(q, k, v, [0, n], [0, n], False, 1.0)
+        R.check(got, want, b)
+        R.check(lse, wl, bl)
+
+
+def test_layouts():
+    """Slices of a fused projection, head-major storage, padded rows."""
+    H, Hkv, D, n = 6, 2, 64, 140
+    cu = _cu([100, 40])
+    fused = _randn(31, (n, (H + 2 * Hkv) * D + 24), torch.float16)
+    q, k, v = (fused[:, a * D:b * D].view(n, b - a, D) for a, b in ((0, H), (H, H + Hkv), (H + Hkv, H + 2 * Hkv)))
+    plan = cf.Attention("f16", H, Hkv, D)
+    want = plan.run(q.contiguous(), k.contiguous(), v.contiguous(), cu)
+    _flush("attention layouts: fused projection")
+    assert torch.equal(plan.run(q, k, v, cu), want)
+    _flush("attention layouts: head-major")
+    hm = lambda x: x.transpose(0, 1).contiguous().transpose(0, 1)
+    O = torch.full((H, n, D), math.nan, dtype=torch.float16, device="cuda").transpose(0, 1)
+    assert plan.run(hm(q), hm(k), hm(v), cu, O=O) is O
+    assert torch.equal(O, want)
+    ref, _, b, _ = R.attention(q, k, v, [0, 100, 140], [0, 100, 140], True, 0.125)
+    R.check(want, ref, b)
+
+
+def test_rows_outside_the_sequences_stay():
+    """Rows behind the last sequence are neither read as keys nor written,
+    whatever they hold; starts past the tensors are clamped."""
+    q, k, v = _case("bf16", 4, 2, 64, [90], [90], seed=41)
+    for x in (q, k, v):
+        x[60:] = math.nan
+    O = torch.full_like(q, 7.0)
+    _flush("attention rows outside")
+    plan = cf.Attention("bf16", 4, 2, 64, causal=False)
+    plan.run(q, k, v, _cu([20, 40]), O=O)
+    torch.cuda.synchronize()
+    want, _, b, _ = R.attention(q[:60], k[:60], v[:60], [0, 20, 60], [0, 20, 60], False, 0.125)
+    R.check(O[:60], want, b)
+    assert bool((O[60:] == 7.0).all())
+    got = plan.run(q[:60], k[:60], v[:60], torch.tensor([0, 20, 1 << 30], dtype=torch.int32, device="cuda"))
+    assert torch.equal(got, O[:60])
+
+
+def test_nan_and_infinities_where_they_are_seen():
+    """A NaN among a row's keys makes that row NaN and no other; a query's NaN
+    its own row; an infinite score ends in NaN as the definition does."""
+    q, k, v = _case("f16", 2, 2, 64, [100], [100], seed=51)
+    q[70, 0, 3] = math.nan
+    k[40, 1] = math.nan
+    _flush("attention NaN")
+    got = cf.Attention("f16", 2, 2, 64).run(q, k, v, _cu([100]))
+    torch.cuda.synchronize()
+    nan = torch.isnan(got).any(-1)
+    assert nan[70, 0] and int(nan[:, 0].sum()) == 1
+    assert not nan[:40, 1].any() and bool(nan[40:, 1].all())
+
+
+def test_empty_calls():
+    plan = cf.Attention("f16", 2, 2, 64)
+    e = torch.empty((0, 2, 64), dtype=torch.float16, device="cuda")
+    assert plan.run(e, e, e, _cu([])).shape == (0, 2, 64)
+    q = _randn(1, (5, 2, 64), torch.float16)
+    out, lse = plan.run(q, e, e, _cu([5]), _cu([0]), lse=True)       # rows without any key
+    torch.cuda.synchronize()
+    assert bool((out == 0).all()) and bool((lse == -math.inf).all())
+
+
+def test_graph_replays_and_streams():
+    """Captured twice (each graph with its own workspace) and replayed with new
+    values and new lengths in turn; then two streams at once."""
+    H, Hkv, D = 4, 1, 128
+    plan = cf.Attention("bf16", H, Hkv, D)
+    lq, lk = [17, 3], [1200, 900]             # split over keys: uses a workspace
+    q, k, v = _case("bf16", H, Hkv, D, lq, lk, seed=61)
+    cu_q, cu_k = _cu(lq), _cu(lk)
+    _flush("attention graph")
+    plan.run(q, k, v, cu_q, cu_k)
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(plan.run(q, k, v, cu_q, cu_k))
+        graphs.append(g)
+    for rep, (a, b) in enumerate([(lq, lk), ([10, 10], [800, 1300]), ([0, 20], [1, 2099])]):
+        q2, k2, v2 = _case("bf16", H, Hkv, D, a, b, seed=70 + rep)
+        q.copy_(q2), k.copy_(k2), v.copy_(v2), cu_q.copy_(_cu(a)), cu_k.copy_(_cu(b))
+        torch.cuda.synchronize()
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        want = plan.run(q2, k2, v2, _cu(a), _cu(b))
+        for o in outs:
+            assert torch.equal(o, want), rep
+    _flush("attention two streams")
+    sets = [_case("bf16", H, Hkv, D, lq, lk, seed=80 + i) for i in range(2)]
+    want = [plan.run(*x, _cu(lq), _cu(lk)) for x in sets]
+    cq, ck = _cu(lq), _cu(lk)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [plan.run(*x, cq, ck, stream=s) for _ in range(3) for x, s in zip(sets, streams)]
+    torch.cuda.synchronize()
+    for i, o in enumerate(got):
+        assert torch.equal(o, want[i % 2])
+
+
+PREFIX = [
+    # dtype, heads, kv heads, dim, batch, prefix, own keys
+    ("f16", 1, 1, 64, 1, 1, 1),
+    ("bf16", 4, 2, 128, 3, 100, 20),
+    ("f16", 32, 8, 96, 9, 700, 300),
+    ("bf16", 40, 1, 80, 5, 33, 1),           # more heads a key head than a row tile holds
+    ("f16", 8, 8, 64, 130, 2000, 65),
+    ("bf16", 6, 3, 128, 2, 0, 50),           # no prefix
+    ("f16", 6, 3, 120, 4, 65, 0),            # nothing but the prefix
+    ("bf16", 16, 4, 128, 7, 5000, 1030),
+]
+
+
+@pytest.mark.parametrize("case", range(len(PREFIX)))
+def test_prefix_attention(case):
+    dtype, H, Hkv, D, B, P, S = PREFIX[case]
+    _flush(f"prefix {PREFIX[case]}")
+    T = DT[dtype]
+    q, kp, vp = _randn(1, (B, H, D), T, 1.5), _randn(2, (P, Hkv, D), T), _randn(3, (P, Hkv, D), T)
+    k, v = _randn(4, (B, S, Hkv, D), T), _randn(5, (B, S, Hkv, D), T)
+    lens = [(i * 37) % (S + 1) for i in range(B)]
+    lens[-1] = S
+    for b, n in enumerate(lens):              # past a request's keys: anything
+        k[b, n:], v[b, n:] = math.nan, math.inf
+    O = torch.full_like(q, math.nan)
+    got = cf.PrefixAttention(dtype, H, Hkv, D).run(q, kp, vp, k, v,
+                                                   torch.tensor(lens, dtype=torch.int32, device="cuda"), O=O)
+    torch.cuda.synchronize()
+    K = torch.cat([torch.cat([kp, k[b, :n]]) for b, n in enumerate(lens)])
+    V = torch.cat([torch.cat([vp, v[b, :n]]) for b, n in enumerate(lens)])
+    want, _, b, _ = R.attention(q, K, V, list(range(B + 1)), R.starts([P + n for n in lens]), False, D ** -0.5)
+    # joining parts: a few more roundings in 32 bits
+    R.check(got, want, b + 2.0 ** -20 * want.abs(), "O")
+
+
+def test_prompt_then_tokens():
+    """As they are used together: a prompt's last row by Attention is what
+    PrefixAttention gives for that token behind the rest of the prompt."""
+    H, Hkv, D, P, S = 8, 2, 128, 500, 37
+    T = torch.bfloat16
+    k, v = _randn(7, (P + S, Hkv, D), T), _randn(8, (P + S, Hkv, D), T)
+    q = _randn(9, (P + S, H, D), T)
+    _flush("prompt then tokens")
+    whole = cf.Attention("bf16", H, Hkv, D).run(q, k, v, _cu([P + S]))
+    B = S                                      # request b holds the first b + 1 keys behind the prefix
+    own_k, own_v = k[None, P:].expand(B, S, Hkv, D), v[None, P:].expand(B, S, Hkv, D)
+    lens = torch.arange(1, S + 1, dtype=torch.int32, device="cuda")
+    tok = cf.PrefixAttention("bf16", H, Hkv, D).run(q[P:], k[:P], v[:P], own_k, own_v, lens)
+    torch.cuda.synchronize()
+    want, _, b, _ = R.attention(q, k, v, [0, P + S], [0, P + S], True, D ** -0.5)
+    R.check(whole, want, b)
+    R.check(tok, want[P:], b[P:] + 2.0 ** -20)

@@ -33,7 +33,8 @@ EXPORTS = ("b2b_gemm_create", "b2b_gemm_run", "b2b_chain_create", "b2b_chain_cre
 BENCH_EXPORTS = ("b2b_bench_mfma", "b2b_bench_copy", "b2b_bench_stream")
 # attention operators (b2b_attn.h)
 ATTN_EXPORTS = ("b2b_attn_create", "b2b_attn_workspace", "b2b_attn_run", "b2b_prefix_attn_workspace",
-                "b2b_prefix_attn_run", "b2b_attn_destroy")
+                "b2b_prefix_attn_run", "b2b_attn_destroy", "b2b_linear_attn_create", "b2b_linear_attn_workspace",
+                "b2b_linear_attn_run", "b2b_linear_attn_step", "b2b_linear_attn_destroy")
 ATTN_CAUSAL = 1
 
 
@@ -93,6 +94,11 @@ def lib():
         L.b2b_prefix_attn_workspace.argtypes = [vp, i32, i64, i64, szp]
         L.b2b_prefix_attn_run.argtypes = [vp, i32, i64, i64, Rows, Rows, Rows, Rows, i64, Rows, i64, vp, Rows, vp, sz, vp]
         L.b2b_attn_destroy.argtypes = [vp]
+        L.b2b_linear_attn_create.argtypes = [ctypes.POINTER(vp), i32, i32, i32, i32, ctypes.c_float]
+        L.b2b_linear_attn_workspace.argtypes = [vp, i32, i64, szp]
+        L.b2b_linear_attn_run.argtypes = [vp, i32, i64, Rows, Rows, Rows, Rows, vp, vp, vp, vp, vp, sz, vp]
+        L.b2b_linear_attn_step.argtypes = [vp, i32, Rows, Rows, Rows, Rows, vp, vp, vp, vp]
+        L.b2b_linear_attn_destroy.argtypes = [vp]
         for n in EXPORTS + BENCH_EXPORTS + ATTN_EXPORTS:
             if n not in ("b2b_status_string",):
                 getattr(L, n).restype = i32
@@ -455,7 +461,7 @@ def to_host(t):
 
 def __getattr__(name):
     """The attention plans (chip_fusion_amd.attention), imported when first named."""
-    if name in ("Attention", "PrefixAttention"):
+    if name in ("Attention", "PrefixAttention", "LinearAttention"):
         from . import attention
         return getattr(attention, name)
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

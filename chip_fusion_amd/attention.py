@@ -196,3 +196,94 @@ class PrefixAttention(_Heads):
                                            _ptr(lens), _rows(O, "O", self.dtype, tuple(Q.shape)), wp, n, s)
             _check(st, "b2b_prefix_attn_run")
         return O
+
+
+class LinearAttention:
+    """Linear attention with a decay for each head (b2b_linear_attn_create):
+    S_t = exp(log_decay) S_{t-1} + k_t v_t^T, o_t = scale q_t^T S_t, with
+    float32 states [heads, dim, dim] (row: key element, column: value element).
+
+    scale: dim ** -0.5 by default."""
+
+    def __init__(self, dtype, heads, kv_heads, head_dim, scale=None):
+        code = DTYPES[dtype] if isinstance(dtype, str) else int(dtype)
+        if scale is not None and not scale > 0:
+            raise ValueError("scale: a positive number is expected")
+        self.heads, self.kv_heads, self.dim = heads, kv_heads, head_dim
+        h = ctypes.c_void_p()
+        _check(lib().b2b_linear_attn_create(ctypes.byref(h), code, heads, kv_heads, head_dim, scale or 0.0),
+               "b2b_linear_attn_create")
+        self._h = h
+        self.dtype = TORCH_DTYPES[code]
+
+    def _operands(self, Q, K, V, log_decay, O):
+        q = _rows(Q, "Q", self.dtype, (None, self.heads, self.dim))
+        k = _rows(K, "K", self.dtype, (Q.shape[0], self.kv_heads, self.dim))
+        v = _rows(V, "V", self.dtype, (Q.shape[0], self.kv_heads, self.dim))
+        if O is not None:
+            _rows(O, "O", self.dtype, tuple(Q.shape))
+        if not isinstance(log_decay, torch.Tensor) or log_decay.dtype != torch.float32 \
+                or tuple(log_decay.shape) != (self.heads,) or not log_decay.is_contiguous():
+            raise ValueError(f"log_decay: a contiguous float32 tensor [{self.heads}] is expected")
+        return q, k, v
+
+    def _state(self, t, name, n):
+        if t is None:
+            return
+        want = (n, self.heads, self.dim, self.dim)
+        if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or tuple(t.shape) != want \
+                or not t.is_contiguous() or t.data_ptr() % 16:
+            raise ValueError(f"{name}: a contiguous, 16-byte aligned float32 tensor {list(want)} is expected")
+
+    def run(self, Q, K, V, log_decay, cu, state=None, O=None, state_out=None, stream=None):
+        """Prompts: Q [rows, heads, dim], K and V [rows, kv_heads, dim], rows
+        cu[s] .. cu[s+1]-1 being sequence s (device int32); state: the states
+        before them [seqs, heads, dim, dim] (zero by default).  Returns O and
+        the states after them (state_out, which may be `state`)."""
+        q, k, v = self._operands(Q, K, V, log_decay, O)
+        seqs = _starts(cu, "cu")
+        self._state(state, "state", seqs)
+        self._state(state_out, "state_out", seqs)
+        device = _on_one_device(Q=Q, K=K, V=V, log_decay=log_decay, cu=cu, state=state, O=O, state_out=state_out)
+        with _running_on(device, stream) as s:
+            if O is None:
+                O = torch.empty(Q.shape, dtype=Q.dtype, device=device)
+            if state_out is None:
+                state_out = torch.empty((seqs, self.heads, self.dim, self.dim), dtype=torch.float32, device=device)
+            n = _bytes("b2b_linear_attn_workspace", self._h, seqs, Q.shape[0])
+            ws, wp = _workspace(n, device)
+            st = lib().b2b_linear_attn_run(self._h, seqs, Q.shape[0], q, k, v, _rows(O, "O", self.dtype, tuple(Q.shape)),
+                                           _ptr(log_decay), _ptr(cu), _ptr(state), _ptr(state_out), wp, n, s)
+            _check(st, "b2b_linear_attn_run")
+        return O, state_out
+
+    def step(self, Q, K, V, log_decay, state, O=None, state_out=None, stream=None):
+        """One token of each request: row b of Q, K and V on state b
+        [batch, heads, dim, dim].  Returns O and the states after it
+        (state_out, which may be `state`)."""
+        q, k, v = self._operands(Q, K, V, log_decay, O)
+        if state is None:
+            raise ValueError("state: a tensor is expected")
+        self._state(state, "state", Q.shape[0])
+        self._state(state_out, "state_out", Q.shape[0])
+        device = _on_one_device(Q=Q, K=K, V=V, log_decay=log_decay, state=state, O=O, state_out=state_out)
+        with _running_on(device, stream) as s:
+            if O is None:
+                O = torch.empty(Q.shape, dtype=Q.dtype, device=device)
+            if state_out is None:
+                state_out = torch.empty_like(state)
+            st = lib().b2b_linear_attn_step(self._h, Q.shape[0], q, k, v, _rows(O, "O", self.dtype, tuple(Q.shape)),
+                                            _ptr(log_decay), _ptr(state), _ptr(state_out), s)
+            _check(st, "b2b_linear_attn_step")
+        return O, state_out
+
+    def close(self):
+        if getattr(self, "_h", None):
+            lib().b2b_linear_attn_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass

@@ -36,7 +36,9 @@ def _code_only(text):
 # code, the measurement instruments (matrix-core loop, copy and stream), and
 # the attention operators
 NON_CASCADE_SOURCES = ("api.hip", "plan.cpp", "plan.hpp", "microbench.hip",
-                       "attn.hpp", "attn_launch.hpp", "attn_api.hip", "inst_attn_f16.hip", "inst_attn_bf16.hip")
+                       "attn.hpp", "attn_launch.hpp", "attn_api.hip", "inst_attn_f16.hip", "inst_attn_bf16.hip",
+                       "linear_attn.hpp", "linear_attn_launch.hpp", "inst_linear_attn_f16.hip",
+                       "inst_linear_attn_bf16.hip")
 
 
 def source_digest():

@@ -9,11 +9,17 @@
 
 #include "attn_launch.hpp"
 #include "b2b_attn.h"
+#include "linear_attn_launch.hpp"
 
 struct b2b_attn_plan {
     int dtype, heads, kv_heads, dim;
     float scale;
     bool causal;
+};
+
+struct b2b_linear_attn_plan {
+    int dtype, heads, kv_heads, dim;
+    float scale;
 };
 
 namespace {
@@ -224,6 +230,132 @@ b2b_status_t b2b_prefix_attn_run(b2b_attn_t p, int32_t batch, int64_t prefix, in
         if (L.rows(a, (unsigned)grid_o, stream) != hipSuccess) return B2B_ERROR_HIP;
     }
     return L.join(a, slots, stream) == hipSuccess ? B2B_SUCCESS : B2B_ERROR_HIP;
+}
+
+b2b_status_t b2b_linear_attn_create(b2b_linear_attn_t* plan, b2b_dtype_t dtype, int32_t heads, int32_t kv_heads,
+                                    int32_t head_dim, float scale) {
+    if (!plan) return B2B_ERROR_INVALID_VALUE;
+    *plan = nullptr;
+    if (heads < 1 || kv_heads < 1 || heads % kv_heads || heads > 65536 || head_dim < 1) return B2B_ERROR_INVALID_VALUE;
+    if (!(scale >= 0.f) || !std::isfinite(scale)) return B2B_ERROR_INVALID_VALUE;
+    if ((dtype != B2B_DTYPE_F16 && dtype != B2B_DTYPE_BF16) || (head_dim != 64 && head_dim != 128))
+        return B2B_ERROR_NOT_SUPPORTED;
+    b2b_linear_attn_plan* p = new (std::nothrow) b2b_linear_attn_plan();
+    if (!p) return B2B_ERROR_OUT_OF_MEMORY;
+    p->dtype = dtype;
+    p->heads = heads;
+    p->kv_heads = kv_heads;
+    p->dim = head_dim;
+    p->scale = scale > 0.f ? scale : (float)(1.0 / std::sqrt((double)head_dim));
+    *plan = p;
+    return B2B_SUCCESS;
+}
+
+b2b_status_t b2b_linear_attn_destroy(b2b_linear_attn_t plan) {
+    delete plan;
+    return B2B_SUCCESS;
+}
+
+}  // extern "C"
+
+namespace {
+
+// Tokens of a segment: sequences that leave most of the chip idle when a
+// workgroup takes a whole one's head are cut.
+int64_t lin_segment(const b2b_linear_attn_plan* p, int64_t seqs, int64_t rows) {
+    const int64_t want = 512 / p->heads;      // segments in all for two workgroups a compute unit
+    if (seqs >= want) return INT32_MAX;
+    return std::max<int64_t>(512, ceil_div(ceil_div(rows, want), 64) * 64);
+}
+bool lin_split(const b2b_linear_attn_plan* p, int64_t seqs, int64_t rows, int64_t* seg) {
+    *seg = lin_segment(p, seqs, rows);
+    return rows > *seg;
+}
+bool lin_sizes_ok(const b2b_linear_attn_plan* p, int64_t seqs, int64_t rows) {
+    return seqs >= 0 && rows >= 0 && rows <= INT32_MAX / 2 && seqs <= INT32_MAX / 2 &&
+           (rows + seqs) * (int64_t)p->heads <= INT32_MAX / 16;
+}
+size_t lin_bytes(const b2b_linear_attn_plan* p, int64_t seqs, int64_t rows) {
+    int64_t seg;
+    if (!seqs || !lin_split(p, seqs, rows, &seg)) return 0;
+    return (size_t)(rows / seg + seqs) * p->heads * p->dim * p->dim * 4;
+}
+b2bk::LinArgs lin_args(const b2b_linear_attn_plan* p, const b2b_rows_t& Q, const b2b_rows_t& K, const b2b_rows_t& V,
+                       const b2b_rows_t& O) {
+    b2bk::LinArgs a = {};
+    a.Q = dev(Q, p->dim);
+    a.K = dev(K, p->dim);
+    a.V = dev(V, p->dim);
+    a.O = const_cast<void*>(O.data);
+    a.ldo = O.row_stride;
+    a.hso = O.head_stride;
+    a.heads = p->heads;
+    a.kv_heads = p->kv_heads;
+    a.group = p->heads / p->kv_heads;
+    a.scale = p->scale;
+    return a;
+}
+bool lin_operands_ok(const b2b_linear_attn_plan* p, int64_t rows, const b2b_rows_t& Q, const b2b_rows_t& K,
+                     const b2b_rows_t& V, const b2b_rows_t& O) {
+    return rows_ok(Q, rows, p->dim) && rows_ok(K, rows, p->dim) && rows_ok(V, rows, p->dim) && rows_ok(O, rows, p->dim) &&
+           O.data != Q.data && O.data != K.data && O.data != V.data;
+}
+
+}  // namespace
+
+extern "C" {
+
+b2b_status_t b2b_linear_attn_workspace(b2b_linear_attn_t p, int32_t seqs, int64_t rows, size_t* bytes) {
+    if (!p || !bytes || !lin_sizes_ok(p, seqs, rows)) return B2B_ERROR_INVALID_VALUE;
+    *bytes = lin_bytes(p, seqs, rows);
+    return B2B_SUCCESS;
+}
+
+b2b_status_t b2b_linear_attn_run(b2b_linear_attn_t p, int32_t seqs, int64_t rows, b2b_rows_t Q, b2b_rows_t K,
+                                 b2b_rows_t V, b2b_rows_t O, const float* log_decay, const int32_t* cu,
+                                 const float* state_in, float* state_out, void* workspace, size_t workspace_bytes,
+                                 hipStream_t stream) {
+    if (!p || !lin_sizes_ok(p, seqs, rows)) return B2B_ERROR_INVALID_VALUE;
+    if (!seqs) return B2B_SUCCESS;
+    if (!log_decay || !cu || (uintptr_t)state_in % 16 || (uintptr_t)state_out % 16) return B2B_ERROR_INVALID_VALUE;
+    if (rows && !lin_operands_ok(p, rows, Q, K, V, O)) return B2B_ERROR_INVALID_VALUE;
+    const size_t need = lin_bytes(p, seqs, rows);
+    if (need && (!workspace || (uintptr_t)workspace % 16 || workspace_bytes < need)) return B2B_ERROR_INVALID_VALUE;
+    int64_t seg;
+    const bool split = lin_split(p, seqs, rows, &seg);
+    b2bk::LinArgs a = lin_args(p, Q, K, V, O);
+    a.cu = cu;
+    a.log_decay = log_decay;
+    a.s0 = state_in;
+    a.s1 = state_out;
+    a.part = (float*)workspace;
+    a.rows = rows;
+    a.seqs = seqs;
+    a.seg = (int32_t)seg;
+    const b2b::LinLaunch& L = p->dtype == B2B_DTYPE_F16 ? b2b::lin_f16() : b2b::lin_bf16();
+    const int64_t segs = split ? rows / seg + seqs : seqs;
+    if (split) {
+        if (L.run(a, p->dim, true, segs, stream) != hipSuccess) return B2B_ERROR_HIP;
+        if (L.scan(a, p->dim, stream) != hipSuccess) return B2B_ERROR_HIP;
+    }
+    return L.run(a, p->dim, false, segs, stream) == hipSuccess ? B2B_SUCCESS : B2B_ERROR_HIP;
+}
+
+b2b_status_t b2b_linear_attn_step(b2b_linear_attn_t p, int32_t batch, b2b_rows_t Q, b2b_rows_t K, b2b_rows_t V,
+                                  b2b_rows_t O, const float* log_decay, const float* state_in, float* state_out,
+                                  hipStream_t stream) {
+    if (!p || !lin_sizes_ok(p, batch, batch)) return B2B_ERROR_INVALID_VALUE;
+    if (!batch) return B2B_SUCCESS;
+    if (!log_decay || !state_in || !state_out || (uintptr_t)state_in % 16 || (uintptr_t)state_out % 16)
+        return B2B_ERROR_INVALID_VALUE;
+    if (!lin_operands_ok(p, batch, Q, K, V, O)) return B2B_ERROR_INVALID_VALUE;
+    b2bk::LinArgs a = lin_args(p, Q, K, V, O);
+    a.log_decay = log_decay;
+    a.s0 = state_in;
+    a.s1 = state_out;
+    a.rows = batch;
+    const b2b::LinLaunch& L = p->dtype == B2B_DTYPE_F16 ? b2b::lin_f16() : b2b::lin_bf16();
+    return L.step(a, p->dim, stream) == hipSuccess ? B2B_SUCCESS : B2B_ERROR_HIP;
 }
 
 }  // extern "C"

@@ -104,6 +104,49 @@ b2b_status_t b2b_prefix_attn_run(b2b_attn_t plan, int32_t batch, int64_t prefix,
 /* Releases a plan. NULL is a no-op. */
 b2b_status_t b2b_attn_destroy(b2b_attn_t plan);
 
+typedef struct b2b_linear_attn_plan* b2b_linear_attn_t;   /* opaque, owned by the library */
+
+/*
+ * Plans linear attention with a decay for each head: no softmax, and a state
+ * instead of a cache,
+ *     S_t = lambda_h S_{t-1} + k_t v_t^T        (head_dim x head_dim, row: key element)
+ *     o_t = scale q_t^T S_t,    lambda_h = exp(log_decay[h])
+ *   dtype       B2B_DTYPE_F16 or B2B_DTYPE_BF16: Q, K, V and O; states are
+ *               float32 and updated in float32 precision; the scores q.k and
+ *               the copy of the state that meets q are rounded to dtype
+ *   head_dim    64 or 128
+ *   scale       finite and positive (0: head_dim ^ -1/2)
+ */
+b2b_status_t b2b_linear_attn_create(b2b_linear_attn_t* plan, b2b_dtype_t dtype, int32_t heads, int32_t kv_heads,
+                                    int32_t head_dim, float scale);
+
+/*
+ * Packed prompts: rows cu[s] .. cu[s+1]-1 are sequence s, 64 tokens at a time.
+ *   log_decay   device float32 [heads], 0 or below
+ *   state_in    device float32 [seqs, heads, head_dim, head_dim], the states
+ *               before the sequences, or NULL (zero); 16-byte aligned
+ *   state_out   the states after them, or NULL; may be state_in.  A sequence
+ *               without tokens keeps its state
+ *   workspace   as for b2b_attn_run (b2b_linear_attn_workspace)
+ * Rows of O that belong to no sequence are not written.
+ */
+b2b_status_t b2b_linear_attn_workspace(b2b_linear_attn_t plan, int32_t seqs, int64_t rows, size_t* bytes);
+b2b_status_t b2b_linear_attn_run(b2b_linear_attn_t plan, int32_t seqs, int64_t rows, b2b_rows_t Q, b2b_rows_t K,
+                                 b2b_rows_t V, b2b_rows_t O, const float* log_decay, const int32_t* cu,
+                                 const float* state_in, float* state_out, void* workspace, size_t workspace_bytes,
+                                 hipStream_t stream);
+
+/*
+ * One token of each of `batch` requests (row b of Q, K, V and O): one step of
+ * the recurrence on state b.  state_out may be state_in (updated in place).
+ */
+b2b_status_t b2b_linear_attn_step(b2b_linear_attn_t plan, int32_t batch, b2b_rows_t Q, b2b_rows_t K, b2b_rows_t V,
+                                  b2b_rows_t O, const float* log_decay, const float* state_in, float* state_out,
+                                  hipStream_t stream);
+
+/* Releases a plan. NULL is a no-op. */
+b2b_status_t b2b_linear_attn_destroy(b2b_linear_attn_t plan);
+
 #ifdef __cplusplus
 }
 #endif

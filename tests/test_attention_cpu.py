@@ -137,3 +137,71 @@ def test_binding_checks_prefix():
         a.update(kw)
         with pytest.raises(ValueError, match=match):
             plan.run(**a)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(), OK), (dict(dtype=1, dim=128), OK), (dict(heads=0), INVALID), (dict(kv=3), INVALID), (dict(dim=-1), INVALID),
+    (dict(scale=-2.0), INVALID), (dict(scale=float("nan")), INVALID), (dict(dim=96), UNSUPPORTED), (dict(dtype=2), UNSUPPORTED),
+])
+def test_linear_create(kw, status):
+    a = dict(dtype=0, heads=4, kv=2, dim=64, scale=1.0)
+    a.update(kw)
+    h = ctypes.c_void_p(5)
+    st = cf.lib().b2b_linear_attn_create(ctypes.byref(h), a["dtype"], a["heads"], a["kv"], a["dim"], a["scale"])
+    assert st == status and bool(h.value) == (status == OK)
+    if status == OK:
+        assert cf.lib().b2b_linear_attn_destroy(h) == OK
+    assert cf.lib().b2b_linear_attn_destroy(None) == OK
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(seqs=-1), INVALID), (dict(rows=-1), INVALID), (dict(rows=1 << 30), INVALID), (dict(seqs=0), OK),
+    (dict(Q=_rows(None)), INVALID), (dict(K=_rows(ld=100)), INVALID), (dict(V=_rows(P + 4)), INVALID), (dict(O=_rows()), INVALID),
+    (dict(g=None), INVALID), (dict(cu=None), INVALID), (dict(s0=P + 4), INVALID), (dict(s1=P + 8), INVALID),
+    (dict(ws=None), INVALID), (dict(ws_bytes=64), INVALID), (dict(ws=P + 8), INVALID), (dict(plan=None), INVALID),
+])
+def test_linear_run_refuses(kw, status):
+    plan = cf.LinearAttention("f16", 4, 2, 64)
+    a = dict(plan=plan._h, seqs=1, rows=5000, Q=_rows(), K=_rows(P * 2), V=_rows(P * 3), O=_rows(P * 4), g=P, cu=P, s0=P,
+             s1=P, ws=P)
+    n = ctypes.c_size_t()
+    assert cf.lib().b2b_linear_attn_workspace(plan._h, 1, 5000, ctypes.byref(n)) == OK and n.value > 0
+    a["ws_bytes"] = n.value
+    a.update(kw)
+    st = cf.lib().b2b_linear_attn_run(a["plan"], a["seqs"], a["rows"], a["Q"], a["K"], a["V"], a["O"], a["g"], a["cu"],
+                                      a["s0"], a["s1"], a["ws"], a["ws_bytes"], None)
+    assert st == status
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(batch=-1), INVALID), (dict(batch=0), OK), (dict(Q=_rows(None)), INVALID), (dict(O=_rows()), INVALID),
+    (dict(s0=None), INVALID), (dict(s1=None), INVALID), (dict(s0=P + 8), INVALID), (dict(g=None), INVALID),
+])
+def test_linear_step_refuses(kw, status):
+    plan = cf.LinearAttention("f16", 4, 2, 64)
+    a = dict(batch=3, Q=_rows(), K=_rows(P * 2), V=_rows(P * 3), O=_rows(P * 4), g=P, s0=P, s1=P)
+    a.update(kw)
+    st = cf.lib().b2b_linear_attn_step(plan._h, a["batch"], a["Q"], a["K"], a["V"], a["O"], a["g"], a["s0"], a["s1"], None)
+    assert st == status
+
+
+def test_binding_checks_linear():
+    plan = cf.LinearAttention("f16", 4, 2, 64)
+    q, k, cu, g = _t(10, 4, 64), _t(10, 2, 64), _cu(0, 10), _t(4, dtype=torch.float32)
+    s = _t(1, 4, 64, 64, dtype=torch.float32)
+    for kw, match in [
+        (dict(Q=q.float()), "Q: dtype"), (dict(K=k[:9]), "K: shape"), (dict(V=_t(10, 4, 64)), "V: shape"),
+        (dict(log_decay=g[:3]), "log_decay"), (dict(log_decay=g.double()), "log_decay"), (dict(cu=cu.long()), "cu"),
+        (dict(state=s.half()), "state"), (dict(state=_t(2, 4, 64, 64, dtype=torch.float32)), "state"),
+        (dict(state_out=s.transpose(2, 3)), "state_out"), (dict(O=q[:3]), "O: shape"), (dict(), "device"),
+    ]:
+        a = dict(Q=q, K=k, V=k, log_decay=g, cu=cu)
+        a.update(kw)
+        with pytest.raises(ValueError, match=match):
+            plan.run(**a)
+    for kw, match in [(dict(state=None), "state"), (dict(state=s), "state"),
+                      (dict(state=_t(10, 4, 64, 64, dtype=torch.float32)), "device")]:
+        with pytest.raises(ValueError, match=match):
+            plan.step(q, k, k, g, **kw)
+    with pytest.raises(cf.B2BError, match="not supported"):
+        cf.LinearAttention("f16", 4, 2, 96)

@@ -9,7 +9,6 @@ stream; outputs and workspaces that a call allocates come from torch's
 allocator on that stream, so overlapping calls and captured graphs each have
 their own.
 """
-import contextlib
 import ctypes
 
 import torch
@@ -18,8 +17,18 @@ from . import ATTN_CAUSAL, DTYPES, Rows, TORCH_DTYPES, _check, lib
 
 
 def _rows(t, name, dtype, shape):
-    """ValueError unless t is a device tensor [rows, heads, dim] that the
-    kernels can address; its b2b_rows_t."""
+    """ValueError unless t is a tensor of that dtype and shape (None: any
+    size) whose last three dimensions are rows of heads that the kernels can
+    address; its b2b_rows_t."""
+    try:                                        # what nearly every call passes, in one look
+        rows, heads, dim = t.shape
+        ld, hs, one = t.stride()
+        p = t.data_ptr()
+        if (t.dtype is dtype and rows and heads == shape[1] and dim == shape[2] and (shape[0] is None or rows == shape[0])
+                and one == 1 and ld >= dim and not (ld & 7 or hs & 7 or p & 15)):
+            return Rows(p, ld, hs)
+    except (AttributeError, TypeError, ValueError):
+        pass
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name}: a torch tensor is expected, got {type(t).__name__}")
     if t.dtype != dtype:
@@ -50,46 +59,49 @@ def _starts(cu, name, seqs=None):
     return cu.numel() - 1
 
 
-def _on_one_device(**tensors):
-    """The CUDA device that holds all the tensors."""
-    first = None
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if t.device.type != "cuda":
-            raise ValueError(f"{name}: a device (cuda) tensor is expected, got one on {t.device}")
-        if first is not None and t.device != first:
-            raise ValueError(f"{name}: on {t.device}, the others on {first}")
-        first = t.device
-    return first
+def _device_of(names, *tensors):
+    """The CUDA device that holds all the tensors (None among them: not given)."""
+    index = tensors[0].get_device()
+    if index < 0 or any(t is not None and t.get_device() != index for t in tensors):
+        first = None
+        for name, t in zip(names.split(), tensors):
+            if t is None:
+                continue
+            if t.device.type != "cuda":
+                raise ValueError(f"{name}: a device (cuda) tensor is expected, got one on {t.device}")
+            if first is not None and t.device != first:
+                raise ValueError(f"{name}: on {t.device}, the others on {first}")
+            first = t.device
+    return index
 
 
-@contextlib.contextmanager
-def _running_on(device, stream):
-    """Makes the tensors' device current and `stream` (or its current stream)
-    the one that allocations belong to; yields the stream's handle."""
-    with torch.cuda.device(device):
-        s = torch.cuda.current_stream(device) if stream is None else stream
-        if s.device != device:
-            raise ValueError(f"stream: on {s.device}, the tensors on {device}")
+def _on(index, stream, call):
+    """call(handle) with the tensors' device current and `stream` (or that
+    device's current stream) the one that allocations belong to; handle: its
+    hipStream_t."""
+    if stream is None and torch.cuda.current_device() == index:
+        return call(torch._C._cuda_getCurrentRawStream(index))
+    with torch.cuda.device(index):
+        s = torch.cuda.current_stream() if stream is None else stream
+        if s.device.index != index:
+            raise ValueError(f"stream: on {s.device}, the tensors on cuda:{index}")
         with torch.cuda.stream(s):
-            yield ctypes.c_void_p(s.cuda_stream)
+            return call(s.cuda_stream)
 
 
-def _bytes(call, handle, *sizes):
+def _workspace(call, handle, like, *sizes):
+    """A workspace for one run (torch's allocator keeps it until the stream is
+    past it): the tensor, its address and its bytes."""
     n = ctypes.c_size_t()
-    _check(getattr(lib(), call)(handle, *sizes, ctypes.byref(n)), call)
-    return n.value
-
-
-def _workspace(n, device):
-    """n bytes for one run (the allocator keeps them until the stream is past it)."""
-    return (None, None) if n == 0 else (lambda w: (w, ctypes.c_void_p(w.data_ptr())))(
-        torch.empty(n, dtype=torch.uint8, device=device))
+    _check(call(handle, *sizes, ctypes.byref(n)), call.__name__)
+    if n.value == 0:
+        return None, None, 0
+    t = like.new_empty(n.value, dtype=torch.uint8)
+    return t, t.data_ptr(), n.value
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 class _Heads:
@@ -135,29 +147,35 @@ class Attention(_Heads):
         belong to no sequence are not written."""
         cu_k = cu_q if cu_k is None else cu_k
         seqs = _starts(cu_q, "cu_q")
-        _starts(cu_k, "cu_k", seqs)
+        if cu_k is not cu_q:
+            _starts(cu_k, "cu_k", seqs)
         q = _rows(Q, "Q", self.dtype, (None, self.heads, self.dim))
         k = _rows(K, "K", self.dtype, (None, self.kv_heads, self.dim))
-        v = _rows(V, "V", self.dtype, (K.shape[0], self.kv_heads, self.dim))
+        rows, keys = Q.shape[0], K.shape[0]
+        v = _rows(V, "V", self.dtype, (keys, self.kv_heads, self.dim))
         want = lse is not False and lse is not None
         LSE = lse if isinstance(lse, torch.Tensor) else None
         if O is not None:
-            _rows(O, "O", self.dtype, tuple(Q.shape))
+            o = _rows(O, "O", self.dtype, (rows, self.heads, self.dim))
         if LSE is not None and (LSE.dtype != torch.float32 or LSE.shape != Q.shape[:2] or not LSE.is_contiguous()):
             raise ValueError("lse: a contiguous float32 tensor [rows, heads] is expected")
-        device = _on_one_device(Q=Q, K=K, V=V, cu_q=cu_q, cu_k=cu_k, O=O, lse=LSE)
-        with _running_on(device, stream) as s:
-            if O is None:
-                O = torch.empty(Q.shape, dtype=Q.dtype, device=device)
-            if want and LSE is None:
-                LSE = torch.empty(Q.shape[:2], dtype=torch.float32, device=device)
-            n = _bytes("b2b_attn_workspace", self._h, seqs, Q.shape[0], K.shape[0])
-            ws, wp = _workspace(n, device)
-            st = lib().b2b_attn_run(self._h, seqs, Q.shape[0], K.shape[0], q, k, v,
-                                    _rows(O, "O", self.dtype, tuple(Q.shape)), _ptr(cu_q), _ptr(cu_k), _ptr(LSE), wp,
-                                    n, s)
+        index = _device_of("Q K V cu_q cu_k O lse", Q, K, V, cu_q, cu_k, O, LSE)
+
+        def call(stream):
+            out, ls = O, LSE
+            if out is None:
+                out = Q.new_empty(Q.shape)
+            if want and ls is None:
+                ls = Q.new_empty((rows, self.heads), dtype=torch.float32)
+            L = lib()
+            keep, wp, n = _workspace(L.b2b_attn_workspace, self._h, Q, seqs, rows, keys)
+            st = L.b2b_attn_run(self._h, seqs, rows, keys, q, k, v,
+                                o if O is not None else Rows(out.data_ptr(), self.heads * self.dim, self.dim),
+                                cu_q.data_ptr(), cu_k.data_ptr(), _ptr(ls), wp, n, stream)
             _check(st, "b2b_attn_run")
-        return (O, LSE) if want else O
+            return (out, ls) if want else out
+
+        return _on(index, stream, call)
 
 
 class PrefixAttention(_Heads):
@@ -174,28 +192,32 @@ class PrefixAttention(_Heads):
         q = _rows(Q, "Q", self.dtype, (None, self.heads, self.dim))
         batch = Q.shape[0]
         kp = _rows(Kp, "Kp", self.dtype, (None, self.kv_heads, self.dim))
-        vp = _rows(Vp, "Vp", self.dtype, (Kp.shape[0], self.kv_heads, self.dim))
+        prefix = Kp.shape[0]
+        vp = _rows(Vp, "Vp", self.dtype, (prefix, self.kv_heads, self.dim))
         k = _rows(K, "K", self.dtype, (batch, None, self.kv_heads, self.dim))
-        v = _rows(V, "V", self.dtype, tuple(K.shape))
-        for t, name in ((K, "K"), (V, "V")):
-            if batch > 1 and t.stride(0) % 8:
-                raise ValueError(f"{name}: requests must start on 16-byte boundaries")
+        own = K.shape[1]
+        v = _rows(V, "V", self.dtype, (batch, own, self.kv_heads, self.dim))
+        ks, vs = (K.stride(0), V.stride(0)) if batch > 1 and own else (0, 0)
+        if ks % 8 or vs % 8:
+            raise ValueError(f"{'K' if ks % 8 else 'V'}: requests must start on 16-byte boundaries")
         if not isinstance(lens, torch.Tensor) or lens.dtype != torch.int32 or tuple(lens.shape) != (batch,) \
                 or not lens.is_contiguous():
             raise ValueError(f"lens: a contiguous int32 tensor [{batch}] is expected")
         if O is not None:
-            _rows(O, "O", self.dtype, tuple(Q.shape))
-        device = _on_one_device(Q=Q, Kp=Kp, Vp=Vp, K=K, V=V, lens=lens, O=O)
-        with _running_on(device, stream) as s:
-            if O is None:
-                O = torch.empty(Q.shape, dtype=Q.dtype, device=device)
-            n = _bytes("b2b_prefix_attn_workspace", self._h, batch, Kp.shape[0], K.shape[1])
-            ws, wp = _workspace(n, device)
-            step = lambda t: t.stride(0) if batch > 1 else 0
-            st = lib().b2b_prefix_attn_run(self._h, batch, Kp.shape[0], K.shape[1], q, kp, vp, k, step(K), v, step(V),
-                                           _ptr(lens), _rows(O, "O", self.dtype, tuple(Q.shape)), wp, n, s)
+            o = _rows(O, "O", self.dtype, (batch, self.heads, self.dim))
+        index = _device_of("Q Kp Vp K V lens O", Q, Kp, Vp, K, V, lens, O)
+
+        def call(stream):
+            out = Q.new_empty(Q.shape) if O is None else O
+            L = lib()
+            keep, wp, n = _workspace(L.b2b_prefix_attn_workspace, self._h, Q, batch, prefix, own)
+            st = L.b2b_prefix_attn_run(self._h, batch, prefix, own, q, kp, vp, k, ks, v, vs, lens.data_ptr(),
+                                       o if O is not None else Rows(out.data_ptr(), self.heads * self.dim, self.dim),
+                                       wp, n, stream)
             _check(st, "b2b_prefix_attn_run")
-        return O
+            return out
+
+        return _on(index, stream, call)
 
 
 class LinearAttention:
@@ -244,18 +266,22 @@ class LinearAttention:
         seqs = _starts(cu, "cu")
         self._state(state, "state", seqs)
         self._state(state_out, "state_out", seqs)
-        device = _on_one_device(Q=Q, K=K, V=V, log_decay=log_decay, cu=cu, state=state, O=O, state_out=state_out)
-        with _running_on(device, stream) as s:
-            if O is None:
-                O = torch.empty(Q.shape, dtype=Q.dtype, device=device)
-            if state_out is None:
-                state_out = torch.empty((seqs, self.heads, self.dim, self.dim), dtype=torch.float32, device=device)
-            n = _bytes("b2b_linear_attn_workspace", self._h, seqs, Q.shape[0])
-            ws, wp = _workspace(n, device)
-            st = lib().b2b_linear_attn_run(self._h, seqs, Q.shape[0], q, k, v, _rows(O, "O", self.dtype, tuple(Q.shape)),
-                                           _ptr(log_decay), _ptr(cu), _ptr(state), _ptr(state_out), wp, n, s)
+        rows = Q.shape[0]
+        index = _device_of("Q K V log_decay cu state O state_out", Q, K, V, log_decay, cu, state, O, state_out)
+
+        def call(stream):
+            out = Q.new_empty(Q.shape) if O is None else O
+            after = state_out
+            if after is None:
+                after = Q.new_empty((seqs, self.heads, self.dim, self.dim), dtype=torch.float32)
+            L = lib()
+            keep, wp, n = _workspace(L.b2b_linear_attn_workspace, self._h, Q, seqs, rows)
+            st = L.b2b_linear_attn_run(self._h, seqs, rows, q, k, v, self._out(out, O is None), log_decay.data_ptr(),
+                                       cu.data_ptr(), _ptr(state), after.data_ptr(), wp, n, stream)
             _check(st, "b2b_linear_attn_run")
-        return O, state_out
+            return out, after
+
+        return _on(index, stream, call)
 
     def step(self, Q, K, V, log_decay, state, O=None, state_out=None, stream=None):
         """One token of each request: row b of Q, K and V on state b
@@ -266,16 +292,23 @@ class LinearAttention:
             raise ValueError("state: a tensor is expected")
         self._state(state, "state", Q.shape[0])
         self._state(state_out, "state_out", Q.shape[0])
-        device = _on_one_device(Q=Q, K=K, V=V, log_decay=log_decay, state=state, O=O, state_out=state_out)
-        with _running_on(device, stream) as s:
-            if O is None:
-                O = torch.empty(Q.shape, dtype=Q.dtype, device=device)
-            if state_out is None:
-                state_out = torch.empty_like(state)
-            st = lib().b2b_linear_attn_step(self._h, Q.shape[0], q, k, v, _rows(O, "O", self.dtype, tuple(Q.shape)),
-                                            _ptr(log_decay), _ptr(state), _ptr(state_out), s)
+        rows = Q.shape[0]
+        index = _device_of("Q K V log_decay state O state_out", Q, K, V, log_decay, state, O, state_out)
+
+        def call(stream):
+            out = Q.new_empty(Q.shape) if O is None else O
+            after = torch.empty_like(state) if state_out is None else state_out
+            st = lib().b2b_linear_attn_step(self._h, rows, q, k, v, self._out(out, O is None), log_decay.data_ptr(),
+                                            state.data_ptr(), after.data_ptr(), stream)
             _check(st, "b2b_linear_attn_step")
-        return O, state_out
+            return out, after
+
+        return _on(index, stream, call)
+
+    def _out(self, t, made):
+        if made:
+            return Rows(t.data_ptr(), self.heads * self.dim, self.dim)
+        return _rows(t, "O", self.dtype, tuple(t.shape))
 
     def close(self):
         if getattr(self, "_h", None):

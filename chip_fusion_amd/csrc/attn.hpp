@@ -199,10 +199,10 @@ struct RowState {
     __device__ __forceinline__ void init() { m = kLowest; l = 0.f; }
 };
 
-// Scores of 32 rows x 32 NK keys -> probabilities, in place; returns with the
-// running maximum moved (and O, l rescaled) where it had to.
+// Moves the running maximum (and rescales O and l) where a row's scores ask
+// for it: s, 32 rows x 32 NK keys.
 template <int NK, int NO>
-__device__ __forceinline__ void attn_softmax(f16x_t (&s)[NK], RowState& st, f16x_t (&o)[NO], float sc) {
+__device__ __forceinline__ void attn_move_max(const f16x_t (&s)[NK], RowState& st, f16x_t (&o)[NO], float sc) {
     float mx = s[0][0];
 #pragma unroll
     for (int k = 0; k < NK; ++k)
@@ -219,6 +219,11 @@ __device__ __forceinline__ void attn_softmax(f16x_t (&s)[NK], RowState& st, f16x
 #pragma unroll
             for (int r = 0; r < 16; ++r) o[t][r] *= alpha;
     }
+}
+
+// Scores -> probabilities, in place, and their sum.
+template <int NK>
+__device__ __forceinline__ void attn_probs(f16x_t (&s)[NK], RowState& st, float sc) {
     float sum = 0.f;
 #pragma unroll
     for (int k = 0; k < NK; ++k)
@@ -288,13 +293,13 @@ __device__ __forceinline__ void attn_store(const AttnArgs& a, const f16x_t (&o)[
 }
 
 // ---------------------------------------------------------------------------
-// Many rows: a workgroup's waves take 32 MT rows each and share the key tiles
+// Many rows: a workgroup's waves take 32 rows each and share the key tiles
 // ---------------------------------------------------------------------------
-template <int DT_, int DB_, int MT_, bool PART_>
+template <int DT_, int DB_, bool PART_>
 struct AttnCfg {
-    static constexpr int DT = DT_, DB = DB_, MT = MT_, WAVES = 4, THREADS = 64 * WAVES;
+    static constexpr int DT = DT_, DB = DB_, WAVES = 4, THREADS = 64 * WAVES;
     static constexpr bool PART = PART_;
-    static constexpr int BM = 32 * MT * WAVES, BN = 64;
+    static constexpr int BM = 32 * WAVES, BN = 64;
     static constexpr int KS = 2 * DB;                       // K-steps of the first product
     static constexpr int TILE = BN * DB * 64, LDS_BYTES = 4 * TILE;
     static_assert(LDS_BYTES <= 160 * 1024, "LDS");
@@ -335,80 +340,86 @@ __device__ __forceinline__ void attn_tile_body(const AttnArgs& a) {
     const int end = sees(last);                               // keys the workgroup needs
     const int nt = (end + C::BN - 1) / C::BN;
     const int t0 = (int)((int64_t)nt * split / a.splits), t1 = (int)((int64_t)nt * (split + 1) / a.splits);
-    const int wrow = row0 + 32 * C::MT * wave;                // this wave's first row
-    int lim[C::MT];
-    u4_t q[C::MT][C::KS];
-    f16x_t o[C::MT][C::DB];
-    RowState st[C::MT];
+    const int wrow = row0 + 32 * wave;                        // this wave's first row
+    const int rr = wrow + (lane & 31);
+    const int lim = sees(rr) - 4 * (lane >> 5);
+    u4_t q[C::KS];
+    f16x_t o[C::DB];
+    RowState st;
+    attn_load_q<C::KS>(q, a, w.q0, kvh, rr, rows, lane);
+    st.init();
 #pragma unroll
-    for (int i = 0; i < C::MT; ++i) {
-        const int rr = wrow + 32 * i + (lane & 31);
-        lim[i] = sees(rr) - 4 * (lane >> 5);
-        attn_load_q<C::KS>(q[i], a, w.q0, kvh, rr, rows, lane);
-        st[i].init();
-#pragma unroll
-        for (int t = 0; t < C::DB; ++t) o[i][t] = f16x_t{};
-    }
+    for (int t = 0; t < C::DB; ++t) o[t] = f16x_t{};
     // tiles below `clear` need no mask (they are full and every row of the wave sees them)
-    const int clear = wrow + 32 * C::MT <= rows ? sees(wrow) / C::BN : 0;
+    const int clear = wrow + 32 <= rows ? sees(wrow) / C::BN : 0;
     // tiles from `done` on show this wave nothing
-    const int wlast = (wrow + 32 * C::MT < rows ? wrow + 32 * C::MT : rows) - 1;
+    const int wlast = (wrow + 32 < rows ? wrow + 32 : rows) - 1;
     const int done = wrow < rows ? (sees(wlast) + C::BN - 1) / C::BN : 0;
     const int64_t khead = (int64_t)kvh * a.K.hs, vhead = (int64_t)kvh * a.V.hs;
-    auto copy = [&](int t) {
+    // Slots 0 and 1 hold keys, 2 and 3 values, of even and odd tiles.
+    auto copy_k = [&](int t) {
         const int n = nk - t * C::BN < C::BN ? nk - t * C::BN : C::BN;
-        const unsigned char* dst = lds + (t & 1) * 2 * C::TILE;
-        attn_copy<C::DB, C::BN, true>(dst, attn_rsrc(a.K.p, k0 + (int64_t)t * C::BN, a.K.ld, khead, n, a.dim),
+        attn_copy<C::DB, C::BN, true>(lds + (t & 1) * C::TILE,
+                                      attn_rsrc(a.K.p, k0 + (int64_t)t * C::BN, a.K.ld, khead, n, a.dim),
                                       (int)a.K.ld * 2, a.dim, wave, lane);
-        attn_copy<C::DB, C::BN, false>(dst + C::TILE,
+    };
+    auto copy_v = [&](int t) {
+        const int n = nk - t * C::BN < C::BN ? nk - t * C::BN : C::BN;
+        attn_copy<C::DB, C::BN, false>(lds + (2 + (t & 1)) * C::TILE,
                                        attn_rsrc(a.V.p, k0 + (int64_t)t * C::BN, a.V.ld, vhead, n, a.dim),
                                        (int)a.V.ld * 2, a.dim, wave, lane);
     };
     const int kb0 = attn_kbase(lane, 0), kb1 = attn_kbase(lane, 1), vb = attn_vbase(lane);
-    if (t0 < t1) copy(t0);
-    for (int t = t0; t < t1; ++t) {
-        barrier_vm<0>();          // tile t is in LDS, and everyone is done with tile t - 1
-        if (t + 1 < t1) copy(t + 1);
-        if (t >= done) continue;
-        const unsigned char* kt = lds + (t & 1) * 2 * C::TILE;
-        const unsigned char* vt = kt + C::TILE;
-        f16x_t s[C::MT][2];
+    auto scores = [&](int t, f16x_t (&s)[2]) __attribute__((always_inline)) {
+        const unsigned char* kt = lds + (t & 1) * C::TILE;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
+            s[k] = f16x_t{};
 #pragma unroll
-            for (int i = 0; i < C::MT; ++i) s[i][k] = f16x_t{};
-#pragma unroll
-            for (int j = 0; j < C::KS; ++j) {
-                const u4_t f = *(const u4_t*)(kt + ((j & 1) ? kb1 : kb0) + (j >> 1) * C::BN * 64 + k * 2048);
-#pragma unroll
-                for (int i = 0; i < C::MT; ++i) s[i][k] = M::mma(f, q[i][j], s[i][k]);
-            }
+            for (int j = 0; j < C::KS; ++j)
+                s[k] = M::mma(*(const u4_t*)(kt + ((j & 1) ? kb1 : kb0) + (j >> 1) * C::BN * 64 + k * 2048), q[j], s[k]);
         }
-        u4_t p[C::MT][4];
+    };
+    // One tile: its scores s become probabilities while the matrix cores
+    // compute the next tile's, then meet the values.
+    auto step = [&](int t, f16x_t (&s)[2], f16x_t (&next)[2]) __attribute__((always_inline)) {
+        barrier_vm<0>();          // keys t + 1 and values t are in LDS, and everyone is done with tile t - 1's
+        if (t + 2 < t1) copy_k(t + 2);
+        if (t + 1 < t1) copy_v(t + 1);
+        if (t >= done) return;
+        if (t >= clear) attn_mask<2>(s, lim - t * C::BN);
+        attn_move_max<2, C::DB>(s, st, o, a.sc);
+        scores(t + 1, next);      // past the end: of whatever the slot holds, and dropped
+        u4_t p[4];
+        attn_probs<2>(s, st, a.sc);
 #pragma unroll
-        for (int i = 0; i < C::MT; ++i) {
-            if (t >= clear) attn_mask<2>(s[i], lim[i] - t * C::BN);
-            attn_softmax<2, C::DB>(s[i], st[i], o[i], a.sc);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) p[i][k] = attn_pack<C::DT>(s[i][k >> 1], k & 1);
-        }
+        for (int k = 0; k < 4; ++k) p[k] = attn_pack<C::DT>(s[k >> 1], k & 1);
+        const unsigned char* vt = lds + (2 + (t & 1)) * C::TILE;
 #pragma unroll
         for (int b = 0; b < C::DB; ++b)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const u4_t f = attn_vfrag<C::BN>(vt, vb, b, k);
-#pragma unroll
-                for (int i = 0; i < C::MT; ++i) o[i][b] = M::mma(f, p[i][k], o[i][b]);
-            }
+            for (int k = 0; k < 4; ++k)
+                o[b] = M::mma(attn_vfrag<C::BN>(vt, vb, b, k), p[k], o[b]);
+    };
+    f16x_t sa[2], sb[2];
+    if (t0 < t1) {
+        copy_k(t0);
+        if (t0 + 1 < t1) copy_k(t0 + 1);
+        copy_v(t0);
+        barrier_vm<0>();
+        scores(t0, sa);
+        for (int t = t0;;) {
+            step(t, sa, sb);
+            if (++t >= t1) break;
+            step(t, sb, sa);
+            if (++t >= t1) break;
+        }
     }
-#pragma unroll
-    for (int i = 0; i < C::MT; ++i)
-        attn_store<C::DT, C::DB, C::PART>(a, o[i], st[i], w.q0, kvh, wrow + 32 * i + (lane & 31), rows, a.slot0 + split,
-                                          lane);
+    attn_store<C::DT, C::DB, C::PART>(a, o, st, w.q0, kvh, rr, rows, a.slot0 + split, lane);
 }
 
 template <class C>
-__global__ __launch_bounds__(C::THREADS) void attn_tile_kernel(AttnArgs a) {
+__global__ __launch_bounds__(C::THREADS, 2) void attn_tile_kernel(AttnArgs a) {
     attn_tile_body<C>(a);
 }
 
@@ -478,7 +489,8 @@ __device__ __forceinline__ void attn_rows_body(const AttnArgs& a) {
         for (int j = 0; j < C::KS; ++j)
             s[0] = M::mma(*(const u4_t*)(kt + ((j & 1) ? kb1 : kb0) + (j >> 1) * C::BN * 64), q[j], s[0]);
         if ((t + 1) * C::BN > nk) attn_mask<1>(s, nk - t * C::BN - 4 * (lane >> 5));
-        attn_softmax<1, C::DB>(s, st, o, a.sc);
+        attn_move_max<1, C::DB>(s, st, o, a.sc);
+        attn_probs<1>(s, st, a.sc);
         u4_t p[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) p[k] = attn_pack<C::DT>(s[0], k);

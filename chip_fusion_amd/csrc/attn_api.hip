@@ -42,16 +42,13 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // How a call with this many query rows a key head (in all, and a sequence on
 // average) and keys is laid over workgroups.
 struct Split {
-    int mt;            // 32-row sub-tiles a wave
     int64_t tiles;     // row tiles at most
     int splits;        // parts of the keys
 };
 Split plan_tiles(const b2b_attn_plan* p, int64_t seqs, int64_t rows, int64_t keys, bool packed) {
     const int64_t group = p->heads / p->kv_heads;
     Split s;
-    s.mt = rows * group / seqs > 128 ? 2 : 1;
-    const int bm = b2b::attn_bm(s.mt);
-    s.tiles = packed ? rows * group / bm + seqs : ceil_div(rows * group, bm);
+    s.tiles = packed ? rows * group / b2b::kAttnRows + seqs : ceil_div(rows * group, b2b::kAttnRows);
     const int64_t wgs = s.tiles * p->kv_heads;
     // too few workgroups to fill the chip: the keys in parts of 256 or more
     s.splits = (int)std::max<int64_t>(1, std::min<int64_t>({256 / wgs, keys / seqs / 256, 64}));
@@ -160,7 +157,7 @@ b2b_status_t b2b_attn_run(b2b_attn_t p, int32_t seqs, int64_t rows, int64_t keys
     const int64_t grid = s.tiles * p->kv_heads * s.splits;
     if (grid > INT32_MAX) return B2B_ERROR_INVALID_VALUE;
     const b2b::AttnLaunch& L = launchers(p);
-    if (L.tile(a, s.mt, s.splits > 1, (unsigned)grid, stream) != hipSuccess) return B2B_ERROR_HIP;
+    if (L.tile(a, s.splits > 1, (unsigned)grid, stream) != hipSuccess) return B2B_ERROR_HIP;
     if (s.splits > 1 && L.join(a, s.splits, stream) != hipSuccess) return B2B_ERROR_HIP;
     return B2B_SUCCESS;
 }
@@ -199,7 +196,7 @@ b2b_status_t b2b_prefix_attn_run(b2b_attn_t p, int32_t batch, int64_t prefix, in
     a.ldo = O.row_stride;
     a.hso = O.head_stride;
     a.rows = batch;
-    const Split s = prefix ? plan_tiles(p, 1, batch, prefix, false) : Split{1, 0, 0};
+    const Split s = prefix ? plan_tiles(p, 1, batch, prefix, false) : Split{0, 0};
     const int own_parts = own ? plan_own(p, batch, own) : 0, slots = s.splits + own_parts;
     a.part = (float*)workspace;
     a.part_lse = a.part + (size_t)slots * batch * p->heads * dim;
@@ -214,7 +211,7 @@ b2b_status_t b2b_prefix_attn_run(b2b_attn_t p, int32_t batch, int64_t prefix, in
         a.seqs = 1;
         a.splits = s.splits;
         a.tiles = (int32_t)s.tiles;
-        if (L.tile(a, s.mt, true, (unsigned)grid_p, stream) != hipSuccess) return B2B_ERROR_HIP;
+        if (L.tile(a, true, (unsigned)grid_p, stream) != hipSuccess) return B2B_ERROR_HIP;
     }
     if (own) {
         a.K = dev(K, dim);

@@ -6,12 +6,11 @@
 
 namespace b2b {
 
-// row tile of the many-rows kernel with mt sub-tiles of 32 rows a wave
-constexpr int attn_bm(int mt) { return 128 * mt; }
+constexpr int kAttnRows = b2bk::AttnCfg<b2bk::DT_F16, 2, false>::BM;   // row tile of the many-rows kernel
 
 struct AttnLaunch {
-    // grid workgroups of the many-rows kernel (dim: columns, mt: 1 or 2; part: partial results)
-    hipError_t (*tile)(const b2bk::AttnArgs&, int mt, bool part, unsigned grid, hipStream_t);
+    // grid workgroups of the many-rows kernel (part: partial results)
+    hipError_t (*tile)(const b2bk::AttnArgs&, bool part, unsigned grid, hipStream_t);
     hipError_t (*rows)(const b2bk::AttnArgs&, unsigned grid, hipStream_t);
     hipError_t (*join)(const b2bk::AttnArgs&, int slots, hipStream_t);
 };
@@ -22,24 +21,19 @@ const AttnLaunch& attn_bf16();
 template <int DT>
 struct AttnLaunchers {
     template <int DB>
-    static hipError_t tile_db(const b2bk::AttnArgs& a, int mt, bool part, unsigned grid, hipStream_t s) {
+    static hipError_t tile_db(const b2bk::AttnArgs& a, bool part, unsigned grid, hipStream_t s) {
         auto go = [&](auto c) {
             using C = decltype(c);
             hipLaunchKernelGGL(b2bk::attn_tile_kernel<C>, dim3(grid), dim3(C::THREADS), 0, s, a);
         };
-        if (mt == 2) {
-            if (part) go(b2bk::AttnCfg<DT, DB, 2, true>{});
-            else go(b2bk::AttnCfg<DT, DB, 2, false>{});
-        } else {
-            if (part) go(b2bk::AttnCfg<DT, DB, 1, true>{});
-            else go(b2bk::AttnCfg<DT, DB, 1, false>{});
-        }
+        if (part) go(b2bk::AttnCfg<DT, DB, true>{});
+        else go(b2bk::AttnCfg<DT, DB, false>{});
         return hipGetLastError();
     }
-    static hipError_t tile(const b2bk::AttnArgs& a, int mt, bool part, unsigned grid, hipStream_t s) {
-        if (a.dim <= 64) return tile_db<2>(a, mt, part, grid, s);
-        if (a.dim <= 96) return tile_db<3>(a, mt, part, grid, s);
-        return tile_db<4>(a, mt, part, grid, s);
+    static hipError_t tile(const b2bk::AttnArgs& a, bool part, unsigned grid, hipStream_t s) {
+        if (a.dim <= 64) return tile_db<2>(a, part, grid, s);
+        if (a.dim <= 96) return tile_db<3>(a, part, grid, s);
+        return tile_db<4>(a, part, grid, s);
     }
     template <int DB>
     static hipError_t rows_db(const b2bk::AttnArgs& a, unsigned grid, hipStream_t s) {

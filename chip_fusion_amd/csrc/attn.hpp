@@ -199,15 +199,21 @@ struct RowState {
     __device__ __forceinline__ void init() { m = kLowest; l = 0.f; }
 };
 
-// Moves the running maximum (and rescales O and l) where a row's scores ask
-// for it: s, 32 rows x 32 NK keys.
-template <int NK, int NO>
-__device__ __forceinline__ void attn_move_max(const f16x_t (&s)[NK], RowState& st, f16x_t (&o)[NO], float sc) {
+// The largest of a lane's scores (its half of the keys).
+template <int NK>
+__device__ __forceinline__ float attn_max(const f16x_t (&s)[NK]) {
     float mx = s[0][0];
 #pragma unroll
     for (int k = 0; k < NK; ++k)
 #pragma unroll
         for (int r = 0; r < 16; ++r) mx = __builtin_fmaxf(mx, s[k][r]);
+    return mx;
+}
+
+// Moves the running maximum (and rescales O and l) where the rows' largest
+// scores ask for it.
+template <int NO>
+__device__ __forceinline__ void attn_move_max(float mx, RowState& st, f16x_t (&o)[NO], float sc) {
     mx = __builtin_fmaxf(mx, other_half(mx)) * sc;
     if (__any(mx - st.m > kMaxLag)) {
         const float m1 = __builtin_fmaxf(st.m, mx);
@@ -372,23 +378,22 @@ __device__ __forceinline__ void attn_tile_body(const AttnArgs& a) {
     const int kb0 = attn_kbase(lane, 0), kb1 = attn_kbase(lane, 1), vb = attn_vbase(lane);
     auto scores = [&](int t, f16x_t (&s)[2]) __attribute__((always_inline)) {
         const unsigned char* kt = lds + (t & 1) * C::TILE;
+        s[0] = s[1] = f16x_t{};
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            s[k] = f16x_t{};
+        for (int j = 0; j < C::KS; ++j)
 #pragma unroll
-            for (int j = 0; j < C::KS; ++j)
+            for (int k = 0; k < 2; ++k)
                 s[k] = M::mma(*(const u4_t*)(kt + ((j & 1) ? kb1 : kb0) + (j >> 1) * C::BN * 64 + k * 2048), q[j], s[k]);
-        }
     };
     // One tile: its scores s become probabilities while the matrix cores
     // compute the next tile's, then meet the values.
-    auto step = [&](int t, f16x_t (&s)[2], f16x_t (&next)[2]) __attribute__((always_inline)) {
+    float mx = 0.f;
+    auto step = [&](int t, f16x_t (&s)[2], f16x_t (&next)[2], auto MASK) __attribute__((always_inline)) {
         barrier_vm<0>();          // keys t + 1 and values t are in LDS, and everyone is done with tile t - 1's
         if (t + 2 < t1) copy_k(t + 2);
         if (t + 1 < t1) copy_v(t + 1);
         if (t >= done) return;
-        if (t >= clear) attn_mask<2>(s, lim - t * C::BN);
-        attn_move_max<2, C::DB>(s, st, o, a.sc);
+        attn_move_max<C::DB>(mx, st, o, a.sc);
         scores(t + 1, next);      // past the end: of whatever the slot holds, and dropped
         u4_t p[4];
         attn_probs<2>(s, st, a.sc);
@@ -396,10 +401,12 @@ __device__ __forceinline__ void attn_tile_body(const AttnArgs& a) {
         for (int k = 0; k < 4; ++k) p[k] = attn_pack<C::DT>(s[k >> 1], k & 1);
         const unsigned char* vt = lds + (2 + (t & 1)) * C::TILE;
 #pragma unroll
-        for (int b = 0; b < C::DB; ++b)
+        for (int k = 0; k < 4; ++k)
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+            for (int b = 0; b < C::DB; ++b)
                 o[b] = M::mma(attn_vfrag<C::BN>(vt, vb, b, k), p[k], o[b]);
+        if constexpr (MASK.value) attn_mask<2>(next, lim - (t + 1) * C::BN);
+        mx = attn_max<2>(next);
     };
     f16x_t sa[2], sb[2];
     if (t0 < t1) {
@@ -408,10 +415,17 @@ __device__ __forceinline__ void attn_tile_body(const AttnArgs& a) {
         copy_v(t0);
         barrier_vm<0>();
         scores(t0, sa);
-        for (int t = t0;;) {
-            step(t, sa, sb);
+        if (t0 >= clear) attn_mask<2>(sa, lim - t0 * C::BN);
+        mx = attn_max<2>(sa);
+        int t = t0;
+        for (; t + 2 < clear && t + 2 < t1; t += 2) {     // tiles t + 1 and t + 2 need no mask
+            step(t, sa, sb, std::false_type{});
+            step(t + 1, sb, sa, std::false_type{});
+        }
+        for (;;) {
+            step(t, sa, sb, std::true_type{});
             if (++t >= t1) break;
-            step(t, sb, sa);
+            step(t, sb, sa, std::true_type{});
             if (++t >= t1) break;
         }
     }
@@ -489,7 +503,7 @@ __device__ __forceinline__ void attn_rows_body(const AttnArgs& a) {
         for (int j = 0; j < C::KS; ++j)
             s[0] = M::mma(*(const u4_t*)(kt + ((j & 1) ? kb1 : kb0) + (j >> 1) * C::BN * 64), q[j], s[0]);
         if ((t + 1) * C::BN > nk) attn_mask<1>(s, nk - t * C::BN - 4 * (lane >> 5));
-        attn_move_max<1, C::DB>(s, st, o, a.sc);
+        attn_move_max<C::DB>(attn_max<1>(s), st, o, a.sc);
         attn_probs<1>(s, st, a.sc);
         u4_t p[2];
 #pragma unroll

@@ -50,8 +50,8 @@ Split plan_tiles(const b2b_attn_plan* p, int64_t seqs, int64_t rows, int64_t key
     Split s;
     s.tiles = packed ? rows * group / b2b::kAttnRows + seqs : ceil_div(rows * group, b2b::kAttnRows);
     const int64_t wgs = s.tiles * p->kv_heads;
-    // too few workgroups to fill the chip: the keys in parts of 256 or more
-    s.splits = (int)std::max<int64_t>(1, std::min<int64_t>({256 / wgs, keys / seqs / 256, 64}));
+    // too few workgroups for two a compute unit: the keys in parts of 256 or more
+    s.splits = (int)std::max<int64_t>(1, std::min<int64_t>({512 / wgs, keys / seqs / 256, 64}));
     return s;
 }
 // the many-requests kernel's parts of a request's own keys

@@ -11,15 +11,15 @@
 // order of the attention kernels):
 //   * scores are computed transposed, S^T = K.Q^T, so decayed and rounded
 //     they are the operand of V^T.P^T as they lie;
-//   * the state's accumulators (lane: value column, registers: key columns)
-//     are, rounded, the operand of S^T.Q^T as they lie, so the state never
-//     leaves its wave's registers;
+//   * the state's accumulators (lane: value column, registers: key columns,
+//     their order set by the order in which the keys' columns are read) are,
+//     rounded, the operand of S^T.Q^T as they lie, so the state never leaves
+//     its wave's registers;
 //   * both end in O^T with one query row a lane, so the factor
 //     scale lambda^(i+1) is one multiplication a register.
 // Every wave owns 32 value columns: its part of the state (D x 32 floats, 64
 // registers at D = 128) and of the output.  Scores are recomputed by each
 // wave (24 of its ~90 matrix instructions a chunk) rather than exchanged.
-// K and Q are read in the relabelled order of the state's columns.
 //
 // The state is float32 and so are its terms: lambda^(n-1-j) v_j is split into
 // parts of the 16-bit type that together hold its 24 bits (bf16: three; fp16:
@@ -87,37 +87,32 @@ __device__ inline bool find_segment(const LinArgs& a, int tile, SeqTile* out) {
 
 // STATE: only the segments' own states (from zero), for the pass before the
 // outputs of sequences that are split.
+// LDS: two slots of keys, then values (STATE: two slots), then queries, then
+// decays: of the chunk's tokens up to its end, and of the scores.
 template <int DT_, int D_, bool STATE_>
 struct LinCfg {
     static constexpr int DT = DT_, D = D_, DB = D / 32, WAVES = DB, THREADS = 64 * WAVES, C = 64;
     static constexpr bool STATE = STATE_;
-    static constexpr int KS = 2 * DB, TILE = C * DB * 64, SLOT = (STATE ? 2 : 3) * TILE, LDS_BYTES = 2 * SLOT;
+    static constexpr int KS = 2 * DB, TILE = C * DB * 64, FALL = 4 * TILE, DECAYS = FALL + 256;
+    static constexpr int LDS_BYTES = DECAYS + (STATE ? 0 : 8192);
     static constexpr int PARTS = DT == DT_BF16 ? 3 : 2;
 };
 
-// A fragment of rows (lane l: row l%32 of the 32 at `p`) in the relabelled
-// order of its columns: two 8-byte pieces.  kb[2*odd + e]: the lane's bases.
-__device__ __forceinline__ void lin_rbase(int lane, int (&kb)[4]) {
-    const int row = lane & 31, h = lane >> 5;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) kb[c] = row * 64 + ((c ^ ((row >> 2) & 3)) << 4) + 8 * h;
-}
-template <int R>
-__device__ __forceinline__ u4_t lin_rfrag(const unsigned char* p, const int (&kb)[4], int s) {
-    const u2_t x = *(const u2_t*)(p + kb[2 * (s & 1)] + (s >> 1) * R * 64);
-    const u2_t y = *(const u2_t*)(p + kb[2 * (s & 1) + 1] + (s >> 1) * R * 64);
-    return u4_t{x[0], x[1], y[0], y[1]};
-}
 // A transposed fragment of the swizzled key tile: 32 columns of block t,
-// K-step ks of its rows; tb[e]: the lane's bases.
+// K-step ks of its rows; tb[e]: the lane's bases.  Of each 16 columns the
+// second and third four trade places: the product's result then has, in lane
+// half h and register r, column 16*(r/8) + 8h + r%8 of the block (lin_column),
+// which makes eight registers of the state an operand in the natural order.
 __device__ __forceinline__ void lin_tbase(int lane, int (&tb)[2]) {
     const int g = lane >> 4, i = lane & 15;
+    const int q = ((i & 1) << 1) | ((i >> 1) & 1);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-        const int chunk = (2 * (g & 1) + ((i & 3) >> 1)) ^ (2 * e + (g >> 1));
-        tb[e] = 512 * e + (4 * (g >> 1) + (i >> 2)) * 64 + chunk * 16 + (i & 1) * 8;
+        const int chunk = (2 * (g & 1) + (q >> 1)) ^ (2 * e + (g >> 1));
+        tb[e] = 512 * e + (4 * (g >> 1) + (i >> 2)) * 64 + chunk * 16 + (q & 1) * 8;
     }
 }
+__device__ __forceinline__ int lin_column(int r, int h) { return 16 * (r >> 3) + 8 * h + (r & 7); }
 template <int R>
 __device__ __forceinline__ u4_t lin_tfrag(const unsigned char* p, const int (&tb)[2], int t, int ks) {
     u4_t out;
@@ -210,110 +205,130 @@ __device__ __forceinline__ void lin_body(const LinArgs& a) {
 #pragma unroll
     for (int t = 0; t < C::DB; ++t)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) S[t][r] = from ? from[(32 * t + 8 * (r >> 2) + 4 * h + (r & 3)) * C::D] : 0.f;
+        for (int r = 0; r < 16; ++r) S[t][r] = from ? from[(32 * t + lin_column(r, h)) * C::D] : 0.f;
 
     const int chunks = (n + C::C - 1) / C::C;
     const int64_t qat = (int64_t)head * a.Q.hs, kat = (int64_t)kvh * a.K.hs, vat = (int64_t)kvh * a.V.hs;
-    auto copy = [&](int c) {
-        const int64_t row = row0 + (int64_t)c * C::C;
-        const int left = n - c * C::C < C::C ? n - c * C::C : C::C;
-        const unsigned char* dst = lds + (c & 1) * C::SLOT;
-        const auto kr = attn_rsrc(a.K.p, row, a.K.ld, kat, left, C::D), vr = attn_rsrc(a.V.p, row, a.V.ld, vat, left, C::D);
-        const auto qr = attn_rsrc(a.Q.p, row, a.Q.ld, qat, left, C::D);
+    auto copy = [&](const AttnRows& x, int64_t at, int c, int slot, auto SWZ) __attribute__((always_inline)) {
+        const auto rs = attn_rsrc(x.p, row0 + (int64_t)c * C::C, x.ld, at, n - c * C::C < C::C ? n - c * C::C : C::C, C::D);
 #pragma unroll
-        for (int rg = wave; rg < 4; rg += C::WAVES) {
-            attn_copy<C::DB, C::C, true>(dst, kr, (int)a.K.ld * 2, C::D, rg, lane);
-            attn_copy<C::DB, C::C, false>(dst + C::TILE, vr, (int)a.V.ld * 2, C::D, rg, lane);
-            if constexpr (!C::STATE) attn_copy<C::DB, C::C, true>(dst + 2 * C::TILE, qr, (int)a.Q.ld * 2, C::D, rg, lane);
-        }
+        for (int rg = wave; rg < 4; rg += C::WAVES)
+            attn_copy<C::DB, C::C, SWZ.value>(lds + slot * C::TILE, rs, (int)x.ld * 2, C::D, rg, lane);
     };
-    int kb[4], tb[2];
-    lin_rbase(lane, kb);
+    auto copy_k = [&](int c) { copy(a.K, kat, c, c & 1, std::true_type{}); };
+    auto copy_v = [&](int c) { copy(a.V, vat, c, C::STATE ? 2 + (c & 1) : 2, std::false_type{}); };
+    auto copy_q = [&](int c) { copy(a.Q, qat, c, 3, std::true_type{}); };
+    const int kb[2] = {attn_kbase(lane, 0), attn_kbase(lane, 1)};
+    int tb[2];
     lin_tbase(lane, tb);
+    auto rows32 = [&](int off, int s) __attribute__((always_inline)) {     // a fragment of 32 rows, K-step s
+        return *(const u4_t*)(lds + off + kb[s & 1] + (s >> 1) * C::C * 64);
+    };
     const int vb = attn_vbase(lane);
     // decays of the scores: of a pair of tokens in the same half of the chunk
     // (0 where the key comes later) and of a query in the second half with a
     // key in the first
-    float same[16], across[16];
+    // -- in LDS, 16 of each a lane: in registers they would cost two waves a SIMD
+    float into[2];
+    if constexpr (!C::STATE) {
+        for (int g = wave; g < 8; g += C::WAVES) {
+            f4_t d;
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-        const int j = 8 * (r >> 2) + 4 * h + (r & 3);
-        same[r] = j > m ? 0.f : a.scale * lin_pow(g2, m - j);
-        across[r] = a.scale * lin_pow(g2, 32 + m - j);
+            for (int r = 0; r < 4; ++r) {
+                const int j = 8 * (g & 3) + 4 * h + r;
+                d[r] = g >= 4 ? a.scale * lin_pow(g2, 32 + m - j) : (j > m ? 0.f : a.scale * lin_pow(g2, m - j));
+            }
+            *(f4_t*)(lds + C::DECAYS + g * 1024 + lane * 16) = d;
+        }
+        into[0] = a.scale * lin_pow(g2, m + 1);
+        into[1] = a.scale * lin_pow(g2, m + 33);
     }
-    const float into[2] = {a.scale * lin_pow(g2, m + 1), a.scale * lin_pow(g2, m + 33)};
+    float* fall = (float*)(lds + C::FALL);       // lambda^(n-1-j) of token j of the chunk
+    if (wave == 0) fall[lane] = lin_pow(g2, 63 - lane);
 
-    if (chunks > 0) copy(0);
+    if (chunks > 0) {
+        copy_k(0);
+        copy_v(0);
+        if constexpr (!C::STATE) copy_q(0);
+    }
     for (int c = 0; c < chunks; ++c) {
         barrier_vm<0>();       // chunk c is in LDS, and everyone is done with chunk c - 1
-        if (c + 1 < chunks) copy(c + 1);
-        const unsigned char* kt = lds + (c & 1) * C::SLOT;
-        const unsigned char* vt = kt + C::TILE;
-        const unsigned char* qt = vt + C::TILE;
+        if (c + 1 < chunks) copy_k(c + 1);
+        const unsigned char* kt = lds + (c & 1) * C::TILE;
         const int left = n - c * C::C < C::C ? n - c * C::C : C::C;
         u4_t v[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = attn_vfrag<C::C>(vt, vb, wave, k);
-        if constexpr (!C::STATE) {
-            u4_t q[2][C::KS];
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int s = 0; s < C::KS; ++s) q[i][s] = lin_rfrag<C::C>(qt + i * 2048, kb, s);
-            // from the state
-            f16x_t o[2] = {f16x_t{}, f16x_t{}};
+        for (int k = 0; k < 4; ++k) v[k] = attn_vfrag<C::C>(lds + (C::STATE ? 2 + (c & 1) : 2) * C::TILE, vb, wave, k);
+        if constexpr (C::STATE) {
+            if (c + 1 < chunks) copy_v(c + 1);
+        } else {
+            // the state as an operand
+            u4_t sp[C::KS];
             int e = 0;
             if constexpr (C::DT == DT_F16) e = lin_exponent(S);
-            const float down = __builtin_ldexpf(1.f, -e), up = __builtin_ldexpf(1.f, e);
-#pragma unroll
-            for (int s = 0; s < C::KS; ++s) {
-                f16x_t x = S[s >> 1];
-                if constexpr (C::DT == DT_F16)
-                    if (e != 0)
-#pragma unroll
-                        for (int r = 0; r < 16; ++r) x[r] *= down;
-                const u4_t f = attn_pack<C::DT>(x, s & 1);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) o[i] = M::mma(f, q[i][s], o[i]);
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float f = into[i] * up;
-#pragma unroll
-                for (int r = 0; r < 16; ++r) o[i][r] *= f;
-            }
-            // from the chunk's own tokens
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                f16x_t p[2] = {f16x_t{}, f16x_t{}};
+            if (e != 0) {
+                const float down = __builtin_ldexpf(1.f, -e);
 #pragma unroll
                 for (int s = 0; s < C::KS; ++s) {
-                    const u4_t f = lin_rfrag<C::C>(kt + k * 2048, kb, s);
+                    f16x_t x = S[s >> 1];
 #pragma unroll
-                    for (int i = k; i < 2; ++i) p[i] = M::mma(f, q[i][s], p[i]);
+                    for (int r = 0; r < 16; ++r) x[r] *= down;
+                    sp[s] = attn_pack<C::DT>(x, s & 1);
                 }
+            } else {
 #pragma unroll
-                for (int i = k; i < 2; ++i) {
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) p[i][r] = i == k ? (same[r] == 0.f ? 0.f : p[i][r] * same[r]) : p[i][r] * across[r];
-#pragma unroll
-                    for (int s = 0; s < 2; ++s) o[i] = M::mma(v[2 * k + s], attn_pack<C::DT>(p[i], s), o[i]);
-                }
+                for (int s = 0; s < C::KS; ++s) sp[s] = attn_pack<C::DT>(S[s >> 1], s & 1);
             }
+            const float up = __builtin_ldexpf(1.f, e);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
+                u4_t q[C::KS];
+#pragma unroll
+                for (int s = 0; s < C::KS; ++s) q[s] = rows32(3 * C::TILE + i * 2048, s);
+                if (i == 1) {
+                    // the last chunk's tokens count up to its own end
+                    if (left < C::C && wave == 0) fall[lane] = lin_pow(g2, left - 1 - lane);
+                    barrier_lds();       // everyone has read this chunk's values and queries
+                    if (c + 1 < chunks) {
+                        copy_v(c + 1);
+                        copy_q(c + 1);
+                    }
+                }
+                // from the state
+                f16x_t o = f16x_t{};
+#pragma unroll
+                for (int s = 0; s < C::KS; ++s) o = M::mma(sp[s], q[s], o);
+                const float f = into[i] * up;
+#pragma unroll
+                for (int r = 0; r < 16; ++r) o[r] *= f;
+                // from the chunk's own tokens
+#pragma unroll
+                for (int k = 0; k <= i; ++k) {
+                    f16x_t p = f16x_t{};
+#pragma unroll
+                    for (int s = 0; s < C::KS; ++s) p = M::mma(rows32((c & 1) * C::TILE + k * 2048, s), q[s], p);
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const f4_t d = *(const f4_t*)(lds + C::DECAYS + ((i == k ? 0 : 4) + g) * 1024 + lane * 16);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) p[4 * g + r] *= d[r];
+                    }
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) o = M::mma(v[2 * k + s], attn_pack<C::DT>(p, s), o);
+                }
                 const int row = 32 * i + m;
                 char* op = (char*)a.O + ((row0 + (int64_t)c * C::C + row) * a.ldo + (int64_t)head * a.hso + 32 * wave) * 2;
 #pragma unroll
                 for (int q4 = 0; q4 < 4; q4 += 2) {
-                    unsigned x0 = Ty<C::DT>::pack(o[i][4 * q4], o[i][4 * q4 + 1]);
-                    unsigned x1 = Ty<C::DT>::pack(o[i][4 * q4 + 2], o[i][4 * q4 + 3]);
-                    unsigned y0 = Ty<C::DT>::pack(o[i][4 * q4 + 4], o[i][4 * q4 + 5]);
-                    unsigned y1 = Ty<C::DT>::pack(o[i][4 * q4 + 6], o[i][4 * q4 + 7]);
+                    unsigned x0 = Ty<C::DT>::pack(o[4 * q4], o[4 * q4 + 1]);
+                    unsigned x1 = Ty<C::DT>::pack(o[4 * q4 + 2], o[4 * q4 + 3]);
+                    unsigned y0 = Ty<C::DT>::pack(o[4 * q4 + 4], o[4 * q4 + 5]);
+                    unsigned y1 = Ty<C::DT>::pack(o[4 * q4 + 6], o[4 * q4 + 7]);
                     swap32(x0, y0);
                     swap32(x1, y1);
                     if (row < left) *(u4_t*)(op + 16 * (q4 + h)) = u4_t{x0, x1, y0, y1};
                 }
+                __builtin_amdgcn_sched_barrier(0);   // the two halves' registers in turn
             }
         }
         // the state after the chunk
@@ -321,13 +336,16 @@ __device__ __forceinline__ void lin_body(const LinArgs& a) {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
 #pragma unroll
-            for (int d = 0; d < 4; ++d) {
-                const int j = 16 * k + 8 * (d >> 1) + 4 * h + 2 * (d & 1);
-                unsigned out[C::PARTS];
-                lin_split<C::DT>(lin_unpack<C::DT>(v[k][d], 0) * lin_pow(g2, left - 1 - j),
-                                 lin_unpack<C::DT>(v[k][d], 1) * lin_pow(g2, left - 2 - j), out);
+            for (int x = 0; x < 2; ++x) {
+                const f4_t w = *(const f4_t*)(fall + 16 * k + 8 * x + 4 * h);
 #pragma unroll
-                for (int p = 0; p < C::PARTS; ++p) vp[p][k][d] = out[p];
+                for (int y = 0; y < 2; ++y) {
+                    const unsigned two = v[k][2 * x + y];
+                    unsigned out[C::PARTS];
+                    lin_split<C::DT>(lin_unpack<C::DT>(two, 0) * w[2 * y], lin_unpack<C::DT>(two, 1) * w[2 * y + 1], out);
+#pragma unroll
+                    for (int p = 0; p < C::PARTS; ++p) vp[p][k][2 * x + y] = out[p];
+                }
             }
         const float keep = lin_pow(g2, left);
 #pragma unroll
@@ -360,11 +378,11 @@ __device__ __forceinline__ void lin_body(const LinArgs& a) {
 #pragma unroll
         for (int t = 0; t < C::DB; ++t)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) to[(32 * t + 8 * (r >> 2) + 4 * h + (r & 3)) * C::D] = S[t][r];
+            for (int r = 0; r < 16; ++r) to[(32 * t + lin_column(r, h)) * C::D] = S[t][r];
 }
 
 template <class C>
-__global__ __launch_bounds__(C::THREADS) void lin_kernel(LinArgs a) {
+__global__ __launch_bounds__(C::THREADS, 2) void lin_kernel(LinArgs a) {
     lin_body<C>(a);
 }
 
@@ -398,12 +416,20 @@ __global__ __launch_bounds__(256) void lin_scan_kernel(LinArgs a) {
     float* p = a.part + first * step + at;
     f4_t S = {0.f, 0.f, 0.f, 0.f};
     if (a.s0) S = *(const f4_t*)(a.s0 + seq * step + at);
-    for (int i = 0; i < tiles; ++i, p += step) {
-        f4_t u = {0.f, 0.f, 0.f, 0.f};
-        if (i + 1 < tiles) u = *(const f4_t*)p;
-        *(f4_t*)p = S;
+    // eight segments' loads in flight
+    for (int i0 = 0; i0 < tiles; i0 += 8) {
+        f4_t u[8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) S[e] = __builtin_fmaf(S[e], keep, u[e]);
+        for (int i = 0; i < 8; ++i)
+            if (i0 + i + 1 < tiles) u[i] = *(const f4_t*)(p + i * step);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (i0 + i < tiles) *(f4_t*)(p + i * step) = S;
+            if (i0 + i + 1 < tiles)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) S[e] = __builtin_fmaf(S[e], keep, u[i][e]);
+        }
+        p += 8 * step;
     }
 }
 

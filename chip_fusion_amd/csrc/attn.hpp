@@ -312,11 +312,10 @@ struct AttnCfg {
 };
 
 template <class C>
-__device__ __forceinline__ void attn_tile_body(const AttnArgs& a) {
-    __shared__ __attribute__((aligned(1024))) unsigned char lds[C::LDS_BYTES];
+__device__ __forceinline__ void attn_tile_body(const AttnArgs& a, unsigned char* lds, int block) {
     using M = Ty32<C::DT>;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int kvh = blockIdx.x % a.kv_heads, rest = blockIdx.x / a.kv_heads;
+    const int kvh = block % a.kv_heads, rest = block / a.kv_heads;
     const int split = rest % a.splits;
     SeqTile w;
     if (a.cu_q) {
@@ -434,32 +433,32 @@ __device__ __forceinline__ void attn_tile_body(const AttnArgs& a) {
 
 template <class C>
 __global__ __launch_bounds__(C::THREADS, 2) void attn_tile_kernel(AttnArgs a) {
-    attn_tile_body<C>(a);
+    __shared__ __attribute__((aligned(1024))) unsigned char lds[C::LDS_BYTES];
+    attn_tile_body<C>(a, lds, blockIdx.x);
 }
 
 // ---------------------------------------------------------------------------
 // Few rows (up to 32 a workgroup): the waves take different keys
 // ---------------------------------------------------------------------------
-// What bounds it is the bytes of K and V: each wave streams tiles of 32 keys
-// of its own through two slots of its own LDS (no barrier until the end), and
-// the four waves' results are joined there.
+// What bounds it is the bytes of K and V.  Each wave streams tiles of 32 keys
+// of its own through its own LDS, without a barrier until the end: the next
+// keys are on their way once the scores are computed, the next values once
+// the products are.  The four waves' results are joined in LDS.
 template <int DT_, int DB_>
 struct AttnRowsCfg {
     static constexpr int DT = DT_, DB = DB_, WAVES = 4, THREADS = 64 * WAVES, BN = 32, KS = 2 * DB;
-    static constexpr int TILE = BN * DB * 64, WAVE_BYTES = 4 * TILE, LDS_BYTES = WAVES * WAVE_BYTES;
-    static constexpr int LOADS = 4 * DB;      // copies of a tile: 2 row groups x DB blocks, K and V
-    static_assert(LDS_BYTES <= 160 * 1024, "LDS");
-    static_assert(WAVES == 4, "the join is written for four waves");
+    static constexpr int TILE = BN * DB * 64, WAVE_BYTES = 2 * TILE, JOIN = WAVES * WAVE_BYTES;
+    static constexpr int LDS_BYTES = JOIN + 2 * WAVES * 32 * 4;
+    static constexpr int LOADS = 2 * DB;      // copies of a tile of keys, or of values
+    static_assert(WAVES == 4 && BN * DB * 128 <= WAVE_BYTES, "the join: four waves, 32 rows of floats each");
 };
 
 template <class C>
-__device__ __forceinline__ void attn_rows_body(const AttnArgs& a) {
-    __shared__ __attribute__((aligned(1024))) unsigned char lds[C::LDS_BYTES];
-    __shared__ float join[2][C::WAVES][32];
+__device__ __forceinline__ void attn_rows_body(const AttnArgs& a, unsigned char* lds, int block) {
     using M = Ty32<C::DT>;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int kvh = blockIdx.x % a.kv_heads;
-    int rest = blockIdx.x / a.kv_heads;
+    const int kvh = block % a.kv_heads;
+    int rest = block / a.kv_heads;
     const int split = rest % a.splits;
     rest /= a.splits;
     const int tile = rest % a.tiles, seq = rest / a.tiles;    // tiles: row tiles of a sequence
@@ -478,55 +477,57 @@ __device__ __forceinline__ void attn_rows_body(const AttnArgs& a) {
     for (int t = 0; t < C::DB; ++t) o[t] = f16x_t{};
     unsigned char* mine = lds + wave * C::WAVE_BYTES;
     const int64_t khead = (int64_t)kvh * a.K.hs + seq * a.k_stride, vhead = (int64_t)kvh * a.V.hs + seq * a.v_stride;
-    auto copy = [&](int t, int slot) {      // past the end: the same number of copies, of nothing
+    auto copy = [&](const AttnRows& x, int64_t at, int t, int slot, auto SWZ) __attribute__((always_inline)) {
+        // past the end: the same number of copies, of nothing
         const int n = t < t1 ? (nk - t * C::BN < C::BN ? nk - t * C::BN : C::BN) : 0;
-        const int64_t at = t < t1 ? (int64_t)t * C::BN : 0;
-        const unsigned char* dst = mine + slot * 2 * C::TILE;
-        const auto kr = attn_rsrc(a.K.p, at, a.K.ld, khead, n, a.dim), vr = attn_rsrc(a.V.p, at, a.V.ld, vhead, n, a.dim);
+        const auto rs = attn_rsrc(x.p, t < t1 ? (int64_t)t * C::BN : 0, x.ld, at, n, a.dim);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");    // what the slot held has been read
 #pragma unroll
-        for (int rg = 0; rg < 2; ++rg) {
-            attn_copy<C::DB, C::BN, true>(dst, kr, (int)a.K.ld * 2, a.dim, rg, lane);
-            attn_copy<C::DB, C::BN, false>(dst + C::TILE, vr, (int)a.V.ld * 2, a.dim, rg, lane);
-        }
+        for (int rg = 0; rg < 2; ++rg)
+            attn_copy<C::DB, C::BN, SWZ.value>(mine + slot * C::TILE, rs, (int)x.ld * 2, a.dim, rg, lane);
     };
+    auto copy_k = [&](int t) { copy(a.K, khead, t, 0, std::true_type{}); };
+    auto copy_v = [&](int t) { copy(a.V, vhead, t, 1, std::false_type{}); };
     const int kb0 = attn_kbase(lane, 0), kb1 = attn_kbase(lane, 1), vb = attn_vbase(lane);
-    int slot = 0;
-    if (t0 + wave < t1) copy(t0 + wave, 0);
-    for (int t = t0 + wave; t < t1; t += C::WAVES, slot ^= 1) {
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");    // the other slot has been read
-        copy(t + C::WAVES, slot ^ 1);
-        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(C::LOADS) : "memory");
-        const unsigned char* kt = mine + slot * 2 * C::TILE;
-        const unsigned char* vt = kt + C::TILE;
+    if (t0 + wave < t1) {
+        copy_k(t0 + wave);
+        copy_v(t0 + wave);
+    }
+    for (int t = t0 + wave; t < t1; t += C::WAVES) {
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(C::LOADS) : "memory");      // the keys are there
         f16x_t s[1] = {f16x_t{}};
 #pragma unroll
         for (int j = 0; j < C::KS; ++j)
-            s[0] = M::mma(*(const u4_t*)(kt + ((j & 1) ? kb1 : kb0) + (j >> 1) * C::BN * 64), q[j], s[0]);
+            s[0] = M::mma(*(const u4_t*)(mine + ((j & 1) ? kb1 : kb0) + (j >> 1) * C::BN * 64), q[j], s[0]);
+        copy_k(t + C::WAVES);
         if ((t + 1) * C::BN > nk) attn_mask<1>(s, nk - t * C::BN - 4 * (lane >> 5));
         attn_move_max<C::DB>(attn_max<1>(s), st, o, a.sc);
         attn_probs<1>(s, st, a.sc);
         u4_t p[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) p[k] = attn_pack<C::DT>(s[0], k);
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(C::LOADS) : "memory");      // the values are
 #pragma unroll
         for (int b = 0; b < C::DB; ++b)
 #pragma unroll
-            for (int k = 0; k < 2; ++k) o[b] = M::mma(attn_vfrag<C::BN>(vt, vb, b, k), p[k], o[b]);
+            for (int k = 0; k < 2; ++k) o[b] = M::mma(attn_vfrag<C::BN>(mine + C::TILE, vb, b, k), p[k], o[b]);
+        copy_v(t + C::WAVES);
     }
     // join: every wave's maximum and sum, then its rows, scaled to the common maximum
+    float* ms = (float*)(lds + C::JOIN);           // [maximum, sum][wave][row]
     const float l = st.l + other_half(st.l);
     if (lane < 32) {
-        join[0][wave][lane] = st.m;
-        join[1][wave][lane] = l;
+        ms[wave * 32 + lane] = st.m;
+        ms[(C::WAVES + wave) * 32 + lane] = l;
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");     // copies of nothing still write zeros
     __syncthreads();
     float m = kLowest, sum = 0.f;
 #pragma unroll
-    for (int v = 0; v < C::WAVES; ++v) m = __builtin_fmaxf(m, join[0][v][lane & 31]);
+    for (int v = 0; v < C::WAVES; ++v) m = __builtin_fmaxf(m, ms[v * 32 + (lane & 31)]);
 #pragma unroll
     for (int v = 0; v < C::WAVES; ++v)
-        sum += join[1][v][lane & 31] * __builtin_amdgcn_exp2f(join[0][v][lane & 31] - m);
+        sum += ms[(C::WAVES + v) * 32 + (lane & 31)] * __builtin_amdgcn_exp2f(ms[v * 32 + (lane & 31)] - m);
     const float f = __builtin_amdgcn_exp2f(st.m - m) * (sum == 0.f ? 0.f : 1.f / sum);
     float* mo = (float*)mine;      // [column quad][row]: 4 floats of a row, 16 bytes a lane
 #pragma unroll
@@ -539,9 +540,10 @@ __device__ __forceinline__ void attn_rows_body(const AttnArgs& a) {
     const int64_t at0 = ((int64_t)(a.slot0 + split) * a.rows + seq) * a.heads + kvh * a.group;
     if (wave == 0 && lane < 32 && rr < rows)
         a.part_lse[at0 + rr] = sum == 0.f ? -__builtin_inff() : m + __builtin_amdgcn_logf(sum);
-    for (int i = threadIdx.x; i < 32 * 8 * C::DB; i += C::THREADS) {
-        const int row = i / (8 * C::DB), c = i % (8 * C::DB), r = 32 * tile + row;
-        if (r >= rows || 4 * c >= a.dim) continue;
+    const int live = rows - 32 * tile < 32 ? rows - 32 * tile : 32;
+    for (int i = threadIdx.x; i < live * 8 * C::DB; i += C::THREADS) {
+        const int row = i / (8 * C::DB), c = i % (8 * C::DB);
+        if (4 * c >= a.dim) continue;
         f4_t v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int x = 0; x < C::WAVES; ++x) {
@@ -549,46 +551,69 @@ __device__ __forceinline__ void attn_rows_body(const AttnArgs& a) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] += y[e];
         }
-        *(f4_t*)(a.part + (at0 + r) * a.dim + 4 * c) = v;
+        *(f4_t*)(a.part + (at0 + 32 * tile + row) * a.dim + 4 * c) = v;
     }
 }
 
-template <class C>
-__global__ __launch_bounds__(C::THREADS) void attn_rows_kernel(AttnArgs a) {
-    attn_rows_body<C>(a);
+// One launch for both kinds of keys of a batch behind a shared prefix: its
+// first workgroups take the prefix (bound by the matrix cores), the others
+// the requests' own keys (bound by memory); they fit a compute unit together.
+template <int DT, int DB>
+__global__ __launch_bounds__(256, 2) void attn_prefix_kernel(AttnArgs p, AttnArgs own, int prefix_blocks) {
+    using C = AttnCfg<DT, DB, true>;
+    using R = AttnRowsCfg<DT, DB>;
+    __shared__ __attribute__((aligned(1024))) unsigned char lds[C::LDS_BYTES > R::LDS_BYTES ? C::LDS_BYTES : R::LDS_BYTES];
+    if ((int)blockIdx.x < prefix_blocks) attn_tile_body<C>(p, lds, blockIdx.x);
+    else attn_rows_body<R>(own, lds, blockIdx.x - prefix_blocks);
 }
 
 // ---------------------------------------------------------------------------
-// Joining partial results: one wave a (row, head)
+// Joining partial results: a quarter of a wave a (row, head), 8 columns a lane
 // ---------------------------------------------------------------------------
 // O = sum_s w_s O_s / sum_s w_s with w_s = 2^(lse_s - max); parts that saw no
-// key have lse = -inf and weight 0.
+// key have lse = -inf and weight 0.  Four parts' loads are in flight at once.
 template <int DT>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int slots) {
-    const int lane = threadIdx.x & 63;
-    const int64_t n = a.rows * a.heads, at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int lane = threadIdx.x & 15;
+    const int64_t n = a.rows * a.heads, at = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
     if (at >= n) return;
     const int64_t row = at / a.heads;
     const int head = (int)(at - row * a.heads);
     float m = -__builtin_inff();
-    for (int s = lane; s < slots; s += 64) m = __builtin_fmaxf(m, a.part_lse[s * n + at]);
+    for (int s = lane; s < slots; s += 16) m = __builtin_fmaxf(m, a.part_lse[s * n + at]);
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) m = __builtin_fmaxf(m, __shfl_xor(m, d));
+    for (int d = 1; d < 16; d <<= 1) m = __builtin_fmaxf(m, __shfl_xor(m, d));
     const float m0 = m == -__builtin_inff() ? 0.f : m;
-    float sum = 0.f, x = 0.f, y = 0.f;
-    const bool live = 2 * lane < a.dim;
-    for (int s = 0; s < slots; ++s) {
-        const float w = __builtin_amdgcn_exp2f(a.part_lse[s * n + at] - m0);
-        sum += w;
-        if (live) {
-            const float2 v = *(const float2*)(a.part + (s * n + at) * a.dim + 2 * lane);
-            x += w * v.x;
-            y += w * v.y;
+    float sum = 0.f, x[8] = {};
+    const bool live = 8 * lane < a.dim;
+    const float* p = a.part + at * a.dim + 8 * lane;
+    for (int s0 = 0; s0 < slots; s0 += 4) {
+        float w[4];
+        f4_t v[4][2];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int s = s0 + i < slots ? s0 + i : slots - 1;
+            w[i] = s0 + i < slots ? a.part_lse[s * n + at] : -__builtin_inff();
+            v[i][0] = v[i][1] = f4_t{0.f, 0.f, 0.f, 0.f};
+            if (live) {
+                v[i][0] = *(const f4_t*)(p + s * n * a.dim);
+                v[i][1] = *(const f4_t*)(p + s * n * a.dim + 4);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float f = __builtin_amdgcn_exp2f(w[i] - m0);
+            sum += f;
+            // a weight of 0 leaves its part out, whatever that holds
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = f == 0.f ? x[e] : __builtin_fmaf(f, v[i][e >> 2][e & 3], x[e]);
         }
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     if (live)
-        *(unsigned*)((char*)a.O + (row * a.ldo + (int64_t)head * a.hso + 2 * lane) * 2) = Ty<DT>::pack(x * inv, y * inv);
+        *(u4_t*)((char*)a.O + (row * a.ldo + (int64_t)head * a.hso + 8 * lane) * 2) =
+            u4_t{Ty<DT>::pack(x[0] * inv, x[1] * inv), Ty<DT>::pack(x[2] * inv, x[3] * inv),
+                 Ty<DT>::pack(x[4] * inv, x[5] * inv), Ty<DT>::pack(x[6] * inv, x[7] * inv)};
     if (lane == 0 && a.lse) a.lse[at] = sum == 0.f ? -__builtin_inff() : (m0 + __builtin_amdgcn_logf(sum)) * kLn2;
 }
 

@@ -45,13 +45,14 @@ struct Split {
     int64_t tiles;     // row tiles at most
     int splits;        // parts of the keys
 };
-Split plan_tiles(const b2b_attn_plan* p, int64_t seqs, int64_t rows, int64_t keys, bool packed) {
+// fill: workgroups wanted
+Split plan_tiles(const b2b_attn_plan* p, int64_t seqs, int64_t rows, int64_t keys, bool packed, int64_t fill) {
     const int64_t group = p->heads / p->kv_heads;
     Split s;
     s.tiles = packed ? rows * group / b2b::kAttnRows + seqs : ceil_div(rows * group, b2b::kAttnRows);
     const int64_t wgs = s.tiles * p->kv_heads;
-    // too few workgroups for two a compute unit: the keys in parts of 256 or more
-    s.splits = (int)std::max<int64_t>(1, std::min<int64_t>({512 / wgs, keys / seqs / 256, 64}));
+    // too few workgroups: the keys in parts of 256 or more
+    s.splits = (int)std::max<int64_t>(1, std::min<int64_t>({fill / wgs, keys / seqs / 256, 64}));
     return s;
 }
 // the many-requests kernel's parts of a request's own keys
@@ -119,7 +120,7 @@ b2b_status_t b2b_attn_workspace(b2b_attn_t p, int32_t seqs, int64_t rows, int64_
     if (!p || !bytes || !sizes_ok(p, seqs, rows, keys)) return B2B_ERROR_INVALID_VALUE;
     *bytes = 0;
     if (!seqs || !rows) return B2B_SUCCESS;
-    const Split s = plan_tiles(p, seqs, rows, keys, true);
+    const Split s = plan_tiles(p, seqs, rows, keys, true, 512);
     if (s.splits > 1) *bytes = part_bytes(p, s.splits, rows);
     return B2B_SUCCESS;
 }
@@ -133,7 +134,7 @@ b2b_status_t b2b_attn_run(b2b_attn_t p, int32_t seqs, int64_t rows, int64_t keys
     if (!rows_ok(Q, rows, dim) || !rows_ok(O, rows, dim) || !cu_q || !cu_k) return B2B_ERROR_INVALID_VALUE;
     if (keys && (!rows_ok(K, keys, dim) || !rows_ok(V, keys, dim))) return B2B_ERROR_INVALID_VALUE;
     if (O.data == Q.data || O.data == K.data || O.data == V.data || (uintptr_t)lse % 4) return B2B_ERROR_INVALID_VALUE;
-    const Split s = plan_tiles(p, seqs, rows, keys, true);
+    const Split s = plan_tiles(p, seqs, rows, keys, true, 512);
     size_t need = s.splits > 1 ? part_bytes(p, s.splits, rows) : 0;
     if (need && (!workspace || (uintptr_t)workspace % 16 || workspace_bytes < need)) return B2B_ERROR_INVALID_VALUE;
     b2bk::AttnArgs a = base_args(p);
@@ -167,7 +168,7 @@ b2b_status_t b2b_prefix_attn_workspace(b2b_attn_t p, int32_t batch, int64_t pref
         return B2B_ERROR_INVALID_VALUE;
     *bytes = 0;
     if (!batch) return B2B_SUCCESS;
-    const int64_t slots = (prefix ? plan_tiles(p, 1, batch, prefix, false).splits : 0) + (own ? plan_own(p, batch, own) : 0);
+    const int64_t slots = (prefix ? plan_tiles(p, 1, batch, prefix, false, 256).splits : 0) + (own ? plan_own(p, batch, own) : 0);
     *bytes = part_bytes(p, slots, batch);
     return B2B_SUCCESS;
 }
@@ -196,36 +197,36 @@ b2b_status_t b2b_prefix_attn_run(b2b_attn_t p, int32_t batch, int64_t prefix, in
     a.ldo = O.row_stride;
     a.hso = O.head_stride;
     a.rows = batch;
-    const Split s = prefix ? plan_tiles(p, 1, batch, prefix, false) : Split{0, 0};
+    const Split s = prefix ? plan_tiles(p, 1, batch, prefix, false, 256) : Split{0, 0};
     const int own_parts = own ? plan_own(p, batch, own) : 0, slots = s.splits + own_parts;
     a.part = (float*)workspace;
     a.part_lse = a.part + (size_t)slots * batch * p->heads * dim;
     const int64_t grid_p = s.tiles * p->kv_heads * s.splits;
     const int64_t row_tiles = ceil_div(p->heads / p->kv_heads, 32);
     const int64_t grid_o = (int64_t)batch * row_tiles * p->kv_heads * own_parts;
-    if (grid_p > INT32_MAX || grid_o > INT32_MAX) return B2B_ERROR_INVALID_VALUE;
+    if (grid_p + grid_o > INT32_MAX) return B2B_ERROR_INVALID_VALUE;
+    a.splits = std::max(s.splits, 1);
+    a.tiles = (int32_t)s.tiles;
+    a.seqs = 1;
+    b2bk::AttnArgs o = a;
     if (prefix) {
         a.K = dev(Kp, dim);
         a.V = dev(Vp, dim);
         a.keys = prefix;
-        a.seqs = 1;
-        a.splits = s.splits;
-        a.tiles = (int32_t)s.tiles;
-        if (L.tile(a, true, (unsigned)grid_p, stream) != hipSuccess) return B2B_ERROR_HIP;
     }
     if (own) {
-        a.K = dev(K, dim);
-        a.V = dev(V, dim);
-        a.lens = lens;
-        a.k_stride = k_stride;
-        a.v_stride = v_stride;
-        a.keys = own;
-        a.seqs = batch;
-        a.splits = own_parts;
-        a.slot0 = s.splits;
-        a.tiles = (int32_t)row_tiles;
-        if (L.rows(a, (unsigned)grid_o, stream) != hipSuccess) return B2B_ERROR_HIP;
+        o.K = dev(K, dim);
+        o.V = dev(V, dim);
+        o.lens = lens;
+        o.k_stride = k_stride;
+        o.v_stride = v_stride;
+        o.keys = own;
+        o.seqs = batch;
+        o.splits = own_parts;
+        o.slot0 = s.splits;
+        o.tiles = (int32_t)row_tiles;
     }
+    if (grid_p + grid_o && L.prefix(a, o, (unsigned)grid_p, (unsigned)grid_o, stream) != hipSuccess) return B2B_ERROR_HIP;
     return L.join(a, slots, stream) == hipSuccess ? B2B_SUCCESS : B2B_ERROR_HIP;
 }
 

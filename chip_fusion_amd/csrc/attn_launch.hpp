@@ -11,7 +11,9 @@ constexpr int kAttnRows = b2bk::AttnCfg<b2bk::DT_F16, 2, false>::BM;   // row ti
 struct AttnLaunch {
     // grid workgroups of the many-rows kernel (part: partial results)
     hipError_t (*tile)(const b2bk::AttnArgs&, bool part, unsigned grid, hipStream_t);
-    hipError_t (*rows)(const b2bk::AttnArgs&, unsigned grid, hipStream_t);
+    // prefix_grid workgroups of the prefix's keys and own_grid of the requests' own
+    hipError_t (*prefix)(const b2bk::AttnArgs& p, const b2bk::AttnArgs& own, unsigned prefix_grid, unsigned own_grid,
+                         hipStream_t);
     hipError_t (*join)(const b2bk::AttnArgs&, int slots, hipStream_t);
 };
 
@@ -35,24 +37,24 @@ struct AttnLaunchers {
         if (a.dim <= 96) return tile_db<3>(a, part, grid, s);
         return tile_db<4>(a, part, grid, s);
     }
-    template <int DB>
-    static hipError_t rows_db(const b2bk::AttnArgs& a, unsigned grid, hipStream_t s) {
-        using C = b2bk::AttnRowsCfg<DT, DB>;
-        hipLaunchKernelGGL(b2bk::attn_rows_kernel<C>, dim3(grid), dim3(C::THREADS), 0, s, a);
+    static hipError_t prefix(const b2bk::AttnArgs& p, const b2bk::AttnArgs& own, unsigned prefix_grid, unsigned own_grid,
+                             hipStream_t s) {
+        auto go = [&](auto db) {
+            hipLaunchKernelGGL((b2bk::attn_prefix_kernel<DT, decltype(db)::value>), dim3(prefix_grid + own_grid), dim3(256), 0,
+                               s, p, own, (int)prefix_grid);
+        };
+        if (p.dim <= 64) go(std::integral_constant<int, 2>{});
+        else if (p.dim <= 96) go(std::integral_constant<int, 3>{});
+        else go(std::integral_constant<int, 4>{});
         return hipGetLastError();
-    }
-    static hipError_t rows(const b2bk::AttnArgs& a, unsigned grid, hipStream_t s) {
-        if (a.dim <= 64) return rows_db<2>(a, grid, s);
-        if (a.dim <= 96) return rows_db<3>(a, grid, s);
-        return rows_db<4>(a, grid, s);
     }
     static hipError_t join(const b2bk::AttnArgs& a, int slots, hipStream_t s) {
         const int64_t n = a.rows * a.heads;
-        hipLaunchKernelGGL(b2bk::attn_join_kernel<DT>, dim3((unsigned)((n + 3) / 4)), dim3(256), 0, s, a, slots);
+        hipLaunchKernelGGL(b2bk::attn_join_kernel<DT>, dim3((unsigned)((n + 15) / 16)), dim3(256), 0, s, a, slots);
         return hipGetLastError();
     }
     static const AttnLaunch& table() {
-        static const AttnLaunch t = {&tile, &rows, &join};
+        static const AttnLaunch t = {&tile, &prefix, &join};
         return t;
     }
 };

@@ -21,10 +21,12 @@ def _rows(t, name, dtype, shape):
     size) whose last three dimensions are rows of heads that the kernels can
     address; its b2b_rows_t."""
     try:                                        # what nearly every call passes, in one look
-        rows, heads, dim = t.shape
-        ld, hs, one = t.stride()
-        p = t.data_ptr()
-        if (t.dtype is dtype and rows and heads == shape[1] and dim == shape[2] and (shape[0] is None or rows == shape[0])
+        size, stride, p = t.shape, t.stride(), t.data_ptr()
+        rows, heads, dim = size[-3:]
+        ld, hs, one = stride[-3:]
+        if (t.dtype is dtype and p and rows and heads == shape[-2] and dim == shape[-1]
+                and (shape[-3] is None or rows == shape[-3]) and len(size) == len(shape)
+                and (len(size) == 3 or size[0] == shape[0])
                 and one == 1 and ld >= dim and not (ld & 7 or hs & 7 or p & 15)):
             return Rows(p, ld, hs)
     except (AttributeError, TypeError, ValueError):

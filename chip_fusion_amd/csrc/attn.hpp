@@ -65,49 +65,61 @@ struct AttnArgs {
 // ---------------------------------------------------------------------------
 struct SeqTile {
     int seq, local, tiles;   // sequence, tile within it, tiles it has
-    int64_t q0;              // first row of Q
-    int nq;                  // rows (tokens)
+    int q0, nq;              // first row of Q, rows (tokens)
+    int k0, nk;              // first key, keys
 };
 
 // Sequence starts come from device memory: clamped to the rows there are, so
 // that no values of theirs lead outside the tensors.
-__device__ inline void seq_range(const int32_t* cu, int s, int64_t total, int64_t* start, int* n) {
-    int64_t a = cu[s], b = cu[s + 1];
+__device__ __forceinline__ void seq_range(const int32_t* cu, int s, int total, int* start, int* n) {
+    int a = cu[s], b = cu[s + 1];
     a = a < 0 ? 0 : (a > total ? total : a);
     b = b < a ? a : (b > total ? total : b);
     *start = a;
-    *n = (int)(b - a);
+    *n = b - a;
 }
 
-// The sequence and place of row tile `tile`, tiles of bm rows of n * group:
-// every wave scans the starts 64 at a time.
-__device__ inline bool find_tile(const int32_t* cu, int seqs, int64_t rows, int group, int bm, int tile, SeqTile* out) {
+// Sum over this lane and those below it.
+__device__ __forceinline__ int lanes_sum(int x) {
+    x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false);   // row_shr:1, 2, 4, 8: sums within 16 lanes
+    x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);   // row_bcast:15 into rows 1 and 3
+    x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);   // row_bcast:31 into rows 2 and 3
+    return x;
+}
+
+// The sequence and place of tile `tile`, a sequence of n tokens having
+// ceil(n * group / bm) tiles, and at least `least`: every wave scans the
+// starts 64 at a time.  cu_k may be null.
+__device__ __forceinline__ bool find_tile(const int32_t* cu_q, const int32_t* cu_k, int seqs, int rows, int keys, int group,
+                                          int bm, int least, int tile, SeqTile* out) {
     const int lane = threadIdx.x & 63;
     int before = 0;
     for (int s0 = 0; s0 < seqs; s0 += 64) {
         const int s = s0 + lane;
-        int64_t start = 0;
-        int n = 0;
-        if (s < seqs) seq_range(cu, s, rows, &start, &n);
-        const int mine = (int)(((int64_t)n * group + bm - 1) / bm);
-        int sum = mine;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int o = __shfl_up(sum, d);
-            if (lane >= d) sum += o;
+        int q0 = 0, n = 0, k0 = 0, nk = 0, mine = 0;
+        if (s < seqs) {
+            seq_range(cu_q, s, rows, &q0, &n);
+            if (cu_k) seq_range(cu_k, s, keys, &k0, &nk);
+            mine = (int)(((unsigned)n * (unsigned)group + (unsigned)bm - 1) / (unsigned)bm);
+            mine = mine < least ? least : mine;
         }
+        const int sum = lanes_sum(mine);
         const unsigned long long hit = __ballot(before + sum > tile);
         if (hit) {
             const int at = __ffsll(hit) - 1;
-            out->seq = __builtin_amdgcn_readfirstlane(s0 + at);
-            out->tiles = __builtin_amdgcn_readfirstlane(__shfl(mine, at));
-            out->local = __builtin_amdgcn_readfirstlane(tile - before - __shfl(sum, at)) + out->tiles;
-            out->nq = __builtin_amdgcn_readfirstlane(__shfl(n, at));
-            const unsigned lo = __builtin_amdgcn_readfirstlane(__shfl((int)(unsigned)start, at));
-            out->q0 = (int64_t)lo;     // rows fit 31 bits
+            out->seq = s0 + at;
+            out->tiles = __builtin_amdgcn_readlane(mine, at);
+            out->local = tile - before - __builtin_amdgcn_readlane(sum, at) + out->tiles;
+            out->q0 = __builtin_amdgcn_readlane(q0, at);
+            out->nq = __builtin_amdgcn_readlane(n, at);
+            out->k0 = __builtin_amdgcn_readlane(k0, at);
+            out->nk = __builtin_amdgcn_readlane(nk, at);
             return true;
         }
-        before += __builtin_amdgcn_readfirstlane(__shfl(sum, 63));
+        before += __builtin_amdgcn_readlane(sum, 63);
     }
     return false;
 }
@@ -319,19 +331,17 @@ __device__ __forceinline__ void attn_tile_body(const AttnArgs& a, unsigned char*
     const int split = rest % a.splits;
     SeqTile w;
     if (a.cu_q) {
-        if (!find_tile(a.cu_q, a.seqs, a.rows, a.group, C::BM, rest / a.splits, &w)) return;
+        if (!find_tile(a.cu_q, a.cu_k, a.seqs, (int)a.rows, (int)a.keys, a.group, C::BM, 0, rest / a.splits, &w)) return;
     } else {
         // all rows are one sequence's
-        w.seq = 0;
-        w.q0 = 0;
+        w.q0 = w.k0 = 0;
         w.nq = (int)a.rows;
+        w.nk = (int)a.keys;
         w.tiles = a.tiles;
         w.local = rest / a.splits;
     }
-    int64_t k0 = 0;
-    int nk = (int)a.keys;
-    if (a.cu_k) seq_range(a.cu_k, w.seq, a.keys, &k0, &nk);
-    nk = __builtin_amdgcn_readfirstlane(nk);
+    const int64_t k0 = w.k0;
+    const int nk = w.nk;
     // the last tile of a causal sequence sees the most keys: it starts first
     const int row0 = (a.causal ? w.tiles - 1 - w.local : w.local) * C::BM;
     const int rows = w.nq * a.group, shift = nk - w.nq;
@@ -351,7 +361,6 @@ __device__ __forceinline__ void attn_tile_body(const AttnArgs& a, unsigned char*
     u4_t q[C::KS];
     f16x_t o[C::DB];
     RowState st;
-    attn_load_q<C::KS>(q, a, w.q0, kvh, rr, rows, lane);
     st.init();
 #pragma unroll
     for (int t = 0; t < C::DB; ++t) o[t] = f16x_t{};
@@ -410,9 +419,14 @@ __device__ __forceinline__ void attn_tile_body(const AttnArgs& a, unsigned char*
     f16x_t sa[2], sb[2];
     if (t0 < t1) {
         copy_k(t0);
+        attn_load_q<C::KS>(q, a, w.q0, kvh, rr, rows, lane);
+        barrier_vm<0>();
+        // the queries are taken here, where the compiler's own wait for them
+        // costs nothing: behind the copies below it would wait for those too
+#pragma unroll
+        for (int j = 0; j < C::KS; ++j) asm volatile("" : "+v"(q[j]));
         if (t0 + 1 < t1) copy_k(t0 + 1);
         copy_v(t0);
-        barrier_vm<0>();
         scores(t0, sa);
         if (t0 >= clear) attn_mask<2>(sa, lim - t0 * C::BN);
         mx = attn_max<2>(sa);

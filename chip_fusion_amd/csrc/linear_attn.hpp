@@ -51,40 +51,6 @@ __device__ __forceinline__ float lin_pow(float g2, int d) {
     return d <= 0 ? 1.f : __builtin_amdgcn_exp2f((float)d * g2);
 }
 
-// Segment `tile`: as find_tile, a sequence without tokens counting as one
-// empty segment (its state still passes through).
-__device__ inline bool find_segment(const LinArgs& a, int tile, SeqTile* out) {
-    const int lane = threadIdx.x & 63;
-    int before = 0;
-    for (int s0 = 0; s0 < a.seqs; s0 += 64) {
-        const int s = s0 + lane;
-        int64_t start = 0;
-        int n = 0, mine = 0;
-        if (s < a.seqs) {
-            seq_range(a.cu, s, a.rows, &start, &n);
-            mine = n > a.seg ? (int)(((int64_t)n + a.seg - 1) / a.seg) : 1;
-        }
-        int sum = mine;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int o = __shfl_up(sum, d);
-            if (lane >= d) sum += o;
-        }
-        const unsigned long long hit = __ballot(before + sum > tile);
-        if (hit) {
-            const int at = __ffsll(hit) - 1;
-            out->seq = __builtin_amdgcn_readfirstlane(s0 + at);
-            out->tiles = __builtin_amdgcn_readfirstlane(__shfl(mine, at));
-            out->local = __builtin_amdgcn_readfirstlane(tile - before - __shfl(sum, at)) + out->tiles;
-            out->nq = __builtin_amdgcn_readfirstlane(__shfl(n, at));
-            out->q0 = __builtin_amdgcn_readfirstlane(__shfl((int)start, at));
-            return true;
-        }
-        before += __builtin_amdgcn_readfirstlane(__shfl(sum, 63));
-    }
-    return false;
-}
-
 // STATE: only the segments' own states (from zero), for the pass before the
 // outputs of sequences that are split.
 // LDS: two slots of keys, then values (STATE: two slots), then queries, then
@@ -186,7 +152,8 @@ __device__ __forceinline__ void lin_body(const LinArgs& a) {
     const int h = lane >> 5, m = lane & 31;
     const int head = blockIdx.x % a.heads, tile = blockIdx.x / a.heads, kvh = head / a.group;
     SeqTile w;
-    if (!find_segment(a, tile, &w)) return;
+    // (a sequence without tokens counts as one empty segment: its state still passes through)
+    if (!find_tile(a.cu, nullptr, a.seqs, (int)a.rows, 0, 1, a.seg, 1, tile, &w)) return;
     const bool last = w.local + 1 == w.tiles;
     if (C::STATE && last) return;       // nobody reads what follows the last segment
     const int64_t row0 = w.q0 + (int64_t)w.local * a.seg;
@@ -397,16 +364,13 @@ __global__ __launch_bounds__(256) void lin_scan_kernel(LinArgs a) {
     int first = 0, tiles = 0;
     for (int s0 = 0; s0 <= seq; s0 += 64) {
         const int s = s0 + lane;
-        int64_t start;
-        int n = 0, mine = 0;
+        int start, n, mine = 0;
         if (s <= seq) {
-            seq_range(a.cu, s, a.rows, &start, &n);
-            mine = n > a.seg ? (int)(((int64_t)n + a.seg - 1) / a.seg) : 1;
+            seq_range(a.cu, s, (int)a.rows, &start, &n);
+            mine = n > a.seg ? (n + a.seg - 1) / a.seg : 1;
         }
-        if (s0 + 64 > seq) tiles = __shfl(mine, seq - s0);
-        int sum = s < seq ? mine : 0;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
+        if (s0 + 64 > seq) tiles = __builtin_amdgcn_readlane(mine, seq - s0);
+        const int sum = __builtin_amdgcn_readlane(lanes_sum(s < seq ? mine : 0), 63);
         first += sum;
     }
     if (tiles < 2) return;

@@ -317,7 +317,7 @@ template <int DT_, int DB_, bool PART_>
 struct AttnCfg {
     static constexpr int DT = DT_, DB = DB_, WAVES = 4, THREADS = 64 * WAVES;
     static constexpr bool PART = PART_;
-    static constexpr int BM = 32 * WAVES, BN = 64;
+    static constexpr int BM = 32 * WAVES, BN = 32;
     static constexpr int KS = 2 * DB;                       // K-steps of the first product
     static constexpr int TILE = BN * DB * 64, LDS_BYTES = 4 * TILE;
     static_assert(LDS_BYTES <= 160 * 1024, "LDS");
@@ -369,84 +369,51 @@ __device__ __forceinline__ void attn_tile_body(const AttnArgs& a, unsigned char*
     // tiles from `done` on show this wave nothing
     const int wlast = (wrow + 32 < rows ? wrow + 32 : rows) - 1;
     const int done = wrow < rows ? (sees(wlast) + C::BN - 1) / C::BN : 0;
-    const int64_t khead = (int64_t)kvh * a.K.hs, vhead = (int64_t)kvh * a.V.hs;
-    // Slots 0 and 1 hold keys, 2 and 3 values, of even and odd tiles.
-    auto copy_k = [&](int t) {
+    // Slots 0 and 1 hold even and odd tiles, keys then values; two waves copy
+    // the keys, two the values.
+    const bool keys = wave < 2;
+    const AttnRows& src = keys ? a.K : a.V;
+    const int64_t head_at = (int64_t)kvh * src.hs;
+    auto copy = [&](int t) __attribute__((always_inline)) {
         const int n = nk - t * C::BN < C::BN ? nk - t * C::BN : C::BN;
-        attn_copy<C::DB, C::BN, true>(lds + (t & 1) * C::TILE,
-                                      attn_rsrc(a.K.p, k0 + (int64_t)t * C::BN, a.K.ld, khead, n, a.dim),
-                                      (int)a.K.ld * 2, a.dim, wave, lane);
-    };
-    auto copy_v = [&](int t) {
-        const int n = nk - t * C::BN < C::BN ? nk - t * C::BN : C::BN;
-        attn_copy<C::DB, C::BN, false>(lds + (2 + (t & 1)) * C::TILE,
-                                       attn_rsrc(a.V.p, k0 + (int64_t)t * C::BN, a.V.ld, vhead, n, a.dim),
-                                       (int)a.V.ld * 2, a.dim, wave, lane);
+        const unsigned char* dst = lds + (2 * (t & 1) + (keys ? 0 : 1)) * C::TILE;
+        const auto rs = attn_rsrc(src.p, k0 + (int64_t)t * C::BN, src.ld, head_at, n, a.dim);
+        if (keys) attn_copy<C::DB, C::BN, true>(dst, rs, (int)src.ld * 2, a.dim, wave, lane);
+        else attn_copy<C::DB, C::BN, false>(dst, rs, (int)src.ld * 2, a.dim, wave - 2, lane);
     };
     const int kb0 = attn_kbase(lane, 0), kb1 = attn_kbase(lane, 1), vb = attn_vbase(lane);
-    auto scores = [&](int t, f16x_t (&s)[2]) __attribute__((always_inline)) {
-        const unsigned char* kt = lds + (t & 1) * C::TILE;
-        s[0] = s[1] = f16x_t{};
+    if (t0 < t1) copy(t0);
+    attn_load_q<C::KS>(q, a, w.q0, kvh, rr, rows, lane);
+    for (int t = t0; t < t1; ++t) {
+        barrier_vm<0>();          // tile t is in LDS, and everyone is done with tile t - 1
+        // the queries are taken here, where the compiler's own wait for them
+        // costs nothing: behind the next copies it would wait for those too
+        if (t == t0)
+#pragma unroll
+            for (int j = 0; j < C::KS; ++j) asm volatile("" : "+v"(q[j]));
+        if (t + 1 < t1) copy(t + 1);
+        if (t >= done) continue;
+        const unsigned char* kt = lds + 2 * (t & 1) * C::TILE;
+        const unsigned char* vt = kt + C::TILE;
+        f16x_t s[1] = {f16x_t{}};
 #pragma unroll
         for (int j = 0; j < C::KS; ++j)
+            s[0] = M::mma(*(const u4_t*)(kt + ((j & 1) ? kb1 : kb0) + (j >> 1) * C::BN * 64), q[j], s[0]);
+        if (t >= clear) attn_mask<1>(s, lim - t * C::BN);
+        attn_move_max<C::DB>(attn_max<1>(s), st, o, a.sc);
+        attn_probs<1>(s, st, a.sc);
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-                s[k] = M::mma(*(const u4_t*)(kt + ((j & 1) ? kb1 : kb0) + (j >> 1) * C::BN * 64 + k * 2048), q[j], s[k]);
-    };
-    // One tile: its scores s become probabilities while the matrix cores
-    // compute the next tile's, then meet the values.
-    float mx = 0.f;
-    auto step = [&](int t, f16x_t (&s)[2], f16x_t (&next)[2], auto MASK) __attribute__((always_inline)) {
-        barrier_vm<0>();          // keys t + 1 and values t are in LDS, and everyone is done with tile t - 1's
-        if (t + 2 < t1) copy_k(t + 2);
-        if (t + 1 < t1) copy_v(t + 1);
-        if (t >= done) return;
-        attn_move_max<C::DB>(mx, st, o, a.sc);
-        scores(t + 1, next);      // past the end: of whatever the slot holds, and dropped
-        u4_t p[4];
-        attn_probs<2>(s, st, a.sc);
+        for (int k = 0; k < 2; ++k) {
+            const u4_t p = attn_pack<C::DT>(s[0], k);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) p[k] = attn_pack<C::DT>(s[k >> 1], k & 1);
-        const unsigned char* vt = lds + (2 + (t & 1)) * C::TILE;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-            for (int b = 0; b < C::DB; ++b)
-                o[b] = M::mma(attn_vfrag<C::BN>(vt, vb, b, k), p[k], o[b]);
-        if constexpr (MASK.value) attn_mask<2>(next, lim - (t + 1) * C::BN);
-        mx = attn_max<2>(next);
-    };
-    f16x_t sa[2], sb[2];
-    if (t0 < t1) {
-        copy_k(t0);
-        attn_load_q<C::KS>(q, a, w.q0, kvh, rr, rows, lane);
-        barrier_vm<0>();
-        // the queries are taken here, where the compiler's own wait for them
-        // costs nothing: behind the copies below it would wait for those too
-#pragma unroll
-        for (int j = 0; j < C::KS; ++j) asm volatile("" : "+v"(q[j]));
-        if (t0 + 1 < t1) copy_k(t0 + 1);
-        copy_v(t0);
-        scores(t0, sa);
-        if (t0 >= clear) attn_mask<2>(sa, lim - t0 * C::BN);
-        mx = attn_max<2>(sa);
-        int t = t0;
-        for (; t + 2 < clear && t + 2 < t1; t += 2) {     // tiles t + 1 and t + 2 need no mask
-            step(t, sa, sb, std::false_type{});
-            step(t + 1, sb, sa, std::false_type{});
-        }
-        for (;;) {
-            step(t, sa, sb, std::true_type{});
-            if (++t >= t1) break;
-            step(t, sb, sa, std::true_type{});
-            if (++t >= t1) break;
+            for (int b = 0; b < C::DB; ++b) o[b] = M::mma(attn_vfrag<C::BN>(vt, vb, b, k), p, o[b]);
         }
     }
     attn_store<C::DT, C::DB, C::PART>(a, o, st, w.q0, kvh, rr, rows, a.slot0 + split, lane);
 }
 
 template <class C>
-__global__ __launch_bounds__(C::THREADS, 2) void attn_tile_kernel(AttnArgs a) {
+__global__ __launch_bounds__(C::THREADS, 3) void attn_tile_kernel(AttnArgs a) {
     __shared__ __attribute__((aligned(1024))) unsigned char lds[C::LDS_BYTES];
     attn_tile_body<C>(a, lds, blockIdx.x);
 }
@@ -455,16 +422,17 @@ __global__ __launch_bounds__(C::THREADS, 2) void attn_tile_kernel(AttnArgs a) {
 // Few rows (up to 32 a workgroup): the waves take different keys
 // ---------------------------------------------------------------------------
 // What bounds it is the bytes of K and V.  Each wave streams tiles of 32 keys
-// of its own through its own LDS, without a barrier until the end: the next
-// keys are on their way once the scores are computed, the next values once
-// the products are.  The four waves' results are joined in LDS.
+// of its own through its own LDS, without a barrier until the end.  Keys and
+// values take the same 32 rows of LDS in turn (values are asked for once the
+// scores are computed, the next keys once the products are), which leaves
+// room for three workgroups a compute unit; their waves cover each other's
+// waits.  The four waves' results are joined in LDS.
 template <int DT_, int DB_>
 struct AttnRowsCfg {
     static constexpr int DT = DT_, DB = DB_, WAVES = 4, THREADS = 64 * WAVES, BN = 32, KS = 2 * DB;
-    static constexpr int TILE = BN * DB * 64, WAVE_BYTES = 2 * TILE, JOIN = WAVES * WAVE_BYTES;
+    static constexpr int TILE = BN * DB * 64, JOIN = WAVES * TILE;
     static constexpr int LDS_BYTES = JOIN + 2 * WAVES * 32 * 4;
-    static constexpr int LOADS = 2 * DB;      // copies of a tile of keys, or of values
-    static_assert(WAVES == 4 && BN * DB * 128 <= WAVE_BYTES, "the join: four waves, 32 rows of floats each");
+    static_assert(WAVES == 4, "the join: a quarter of the columns' sums at a time");
 };
 
 template <class C>
@@ -489,43 +457,36 @@ __device__ __forceinline__ void attn_rows_body(const AttnArgs& a, unsigned char*
     st.init();
 #pragma unroll
     for (int t = 0; t < C::DB; ++t) o[t] = f16x_t{};
-    unsigned char* mine = lds + wave * C::WAVE_BYTES;
+    unsigned char* mine = lds + wave * C::TILE;
     const int64_t khead = (int64_t)kvh * a.K.hs + seq * a.k_stride, vhead = (int64_t)kvh * a.V.hs + seq * a.v_stride;
-    auto copy = [&](const AttnRows& x, int64_t at, int t, int slot, auto SWZ) __attribute__((always_inline)) {
-        // past the end: the same number of copies, of nothing
-        const int n = t < t1 ? (nk - t * C::BN < C::BN ? nk - t * C::BN : C::BN) : 0;
-        const auto rs = attn_rsrc(x.p, t < t1 ? (int64_t)t * C::BN : 0, x.ld, at, n, a.dim);
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");    // what the slot held has been read
+    auto copy = [&](const AttnRows& x, int64_t at, int t, auto SWZ) __attribute__((always_inline)) {
+        const int n = nk - t * C::BN < C::BN ? nk - t * C::BN : C::BN;
+        const auto rs = attn_rsrc(x.p, (int64_t)t * C::BN, x.ld, at, n, a.dim);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");    // what the rows held has been read
 #pragma unroll
-        for (int rg = 0; rg < 2; ++rg)
-            attn_copy<C::DB, C::BN, SWZ.value>(mine + slot * C::TILE, rs, (int)x.ld * 2, a.dim, rg, lane);
+        for (int rg = 0; rg < 2; ++rg) attn_copy<C::DB, C::BN, SWZ.value>(mine, rs, (int)x.ld * 2, a.dim, rg, lane);
     };
-    auto copy_k = [&](int t) { copy(a.K, khead, t, 0, std::true_type{}); };
-    auto copy_v = [&](int t) { copy(a.V, vhead, t, 1, std::false_type{}); };
     const int kb0 = attn_kbase(lane, 0), kb1 = attn_kbase(lane, 1), vb = attn_vbase(lane);
-    if (t0 + wave < t1) {
-        copy_k(t0 + wave);
-        copy_v(t0 + wave);
-    }
+    if (t0 + wave < t1) copy(a.K, khead, t0 + wave, std::true_type{});
     for (int t = t0 + wave; t < t1; t += C::WAVES) {
-        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(C::LOADS) : "memory");      // the keys are there
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         f16x_t s[1] = {f16x_t{}};
 #pragma unroll
         for (int j = 0; j < C::KS; ++j)
             s[0] = M::mma(*(const u4_t*)(mine + ((j & 1) ? kb1 : kb0) + (j >> 1) * C::BN * 64), q[j], s[0]);
-        copy_k(t + C::WAVES);
+        copy(a.V, vhead, t, std::false_type{});
         if ((t + 1) * C::BN > nk) attn_mask<1>(s, nk - t * C::BN - 4 * (lane >> 5));
         attn_move_max<C::DB>(attn_max<1>(s), st, o, a.sc);
         attn_probs<1>(s, st, a.sc);
         u4_t p[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) p[k] = attn_pack<C::DT>(s[0], k);
-        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(C::LOADS) : "memory");      // the values are
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 #pragma unroll
         for (int b = 0; b < C::DB; ++b)
 #pragma unroll
-            for (int k = 0; k < 2; ++k) o[b] = M::mma(attn_vfrag<C::BN>(mine + C::TILE, vb, b, k), p[k], o[b]);
-        copy_v(t + C::WAVES);
+            for (int k = 0; k < 2; ++k) o[b] = M::mma(attn_vfrag<C::BN>(mine, vb, b, k), p[k], o[b]);
+        if (t + C::WAVES < t1) copy(a.K, khead, t + C::WAVES, std::true_type{});
     }
     // join: every wave's maximum and sum, then its rows, scaled to the common maximum
     float* ms = (float*)(lds + C::JOIN);           // [maximum, sum][wave][row]
@@ -534,7 +495,6 @@ __device__ __forceinline__ void attn_rows_body(const AttnArgs& a, unsigned char*
         ms[wave * 32 + lane] = st.m;
         ms[(C::WAVES + wave) * 32 + lane] = l;
     }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");     // copies of nothing still write zeros
     __syncthreads();
     float m = kLowest, sum = 0.f;
 #pragma unroll
@@ -543,29 +503,35 @@ __device__ __forceinline__ void attn_rows_body(const AttnArgs& a, unsigned char*
     for (int v = 0; v < C::WAVES; ++v)
         sum += ms[(C::WAVES + v) * 32 + (lane & 31)] * __builtin_amdgcn_exp2f(ms[v * 32 + (lane & 31)] - m);
     const float f = __builtin_amdgcn_exp2f(st.m - m) * (sum == 0.f ? 0.f : 1.f / sum);
-    float* mo = (float*)mine;      // [column quad][row]: 4 floats of a row, 16 bytes a lane
-#pragma unroll
-    for (int b = 0; b < C::DB; ++b)
-#pragma unroll
-        for (int g = 0; g < 4; ++g)
-            *(f4_t*)(mo + ((8 * b + 2 * g + (lane >> 5)) * 32 + (lane & 31)) * 4) =
-                f4_t{o[b][4 * g] * f, o[b][4 * g + 1] * f, o[b][4 * g + 2] * f, o[b][4 * g + 3] * f};
-    __syncthreads();
     const int64_t at0 = ((int64_t)(a.slot0 + split) * a.rows + seq) * a.heads + kvh * a.group;
     if (wave == 0 && lane < 32 && rr < rows)
         a.part_lse[at0 + rr] = sum == 0.f ? -__builtin_inff() : m + __builtin_amdgcn_logf(sum);
     const int live = rows - 32 * tile < 32 ? rows - 32 * tile : 32;
-    for (int i = threadIdx.x; i < live * 8 * C::DB; i += C::THREADS) {
-        const int row = i / (8 * C::DB), c = i % (8 * C::DB);
-        if (4 * c >= a.dim) continue;
-        f4_t v = {0.f, 0.f, 0.f, 0.f};
+    // half of the columns at a time: a wave's tile of LDS holds 32 rows of
+    // 16 DB floats, [column quad][row]
+    float* mo = (float*)mine;
 #pragma unroll
-        for (int x = 0; x < C::WAVES; ++x) {
-            const f4_t y = *(const f4_t*)((const float*)(lds + x * C::WAVE_BYTES) + (c * 32 + row) * 4);
+    for (int half = 0; half < 2; ++half) {
+        __syncthreads();
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] += y[e];
+        for (int x = 0; x < 2 * C::DB; ++x) {
+            const int y = half * 2 * C::DB + x, b = y / 4, g = y % 4;        // column quads 2y and 2y + 1
+            *(f4_t*)(mo + ((2 * x + (lane >> 5)) * 32 + (lane & 31)) * 4) =
+                f4_t{o[b][4 * g] * f, o[b][4 * g + 1] * f, o[b][4 * g + 2] * f, o[b][4 * g + 3] * f};
         }
-        *(f4_t*)(a.part + (at0 + 32 * tile + row) * a.dim + 4 * c) = v;
+        __syncthreads();
+        for (int i = threadIdx.x; i < live * 4 * C::DB; i += C::THREADS) {
+            const int row = i / (4 * C::DB), c = i % (4 * C::DB), col = 4 * (half * 4 * C::DB + c);
+            if (col >= a.dim) continue;
+            f4_t v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int x = 0; x < C::WAVES; ++x) {
+                const f4_t y = *(const f4_t*)((const float*)(lds + x * C::TILE) + (c * 32 + row) * 4);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] += y[e];
+            }
+            *(f4_t*)(a.part + (at0 + 32 * tile + row) * a.dim + col) = v;
+        }
     }
 }
 
@@ -573,7 +539,7 @@ __device__ __forceinline__ void attn_rows_body(const AttnArgs& a, unsigned char*
 // first workgroups take the prefix (bound by the matrix cores), the others
 // the requests' own keys (bound by memory); they fit a compute unit together.
 template <int DT, int DB>
-__global__ __launch_bounds__(256, 2) void attn_prefix_kernel(AttnArgs p, AttnArgs own, int prefix_blocks) {
+__global__ __launch_bounds__(256, 3) void attn_prefix_kernel(AttnArgs p, AttnArgs own, int prefix_blocks) {
     using C = AttnCfg<DT, DB, true>;
     using R = AttnRowsCfg<DT, DB>;
     __shared__ __attribute__((aligned(1024))) unsigned char lds[C::LDS_BYTES > R::LDS_BYTES ? C::LDS_BYTES : R::LDS_BYTES];

@@ -45,14 +45,31 @@ struct Split {
     int64_t tiles;     // row tiles at most
     int splits;        // parts of the keys
 };
-// fill: workgroups wanted
-Split plan_tiles(const b2b_attn_plan* p, int64_t seqs, int64_t rows, int64_t keys, bool packed, int64_t fill) {
+Split plan_tiles(const b2b_attn_plan* p, int64_t seqs, int64_t rows, int64_t keys) {
+    const int64_t fill = 512;      // workgroups: two a compute unit
     const int64_t group = p->heads / p->kv_heads;
     Split s;
-    s.tiles = packed ? rows * group / b2b::kAttnRows + seqs : ceil_div(rows * group, b2b::kAttnRows);
-    const int64_t wgs = s.tiles * p->kv_heads;
-    // too few workgroups: the keys in parts of 256 or more
-    s.splits = (int)std::max<int64_t>(1, std::min<int64_t>({fill / wgs, keys / seqs / 256, 64}));
+    s.tiles = rows * group / b2b::kAttnRows + seqs;
+    const int64_t wgs = s.tiles * p->kv_heads, each = keys / seqs;
+    // Parts of the keys.  Too few workgroups for `fill`: parts of 256 keys or
+    // more.  Where most keys come before the rows (pieces of prompts), contexts
+    // differ and one workgroup's may be twice the average while all of them run
+    // at once: up to three workgroups a slot, parts of 800 or more, so that
+    // writing and joining partial results stays below what the balance gains
+    // (2500 rows behind 0..4096 keys, 24 heads of 96: 119 us whole, 96 in two
+    // parts, 91 in three).
+    int64_t parts = std::min(fill / wgs, each / 256);
+    if (keys >= 2 * rows) parts = std::max(parts, std::min(3 * fill / wgs, each / 800));
+    s.splits = (int)std::max<int64_t>(1, std::min<int64_t>(parts, 64));
+    return s;
+}
+// A prefix: 1.5 workgroups a compute unit, beside those of the requests' own
+// keys (128 requests behind 32768 tokens, 32 heads of 128: 140 us at 1, 125 at
+// 1.5, 133 at 2, 147 at 3).
+Split plan_prefix(const b2b_attn_plan* p, int64_t batch, int64_t prefix) {
+    Split s;
+    s.tiles = ceil_div(batch * (p->heads / p->kv_heads), b2b::kAttnRows);
+    s.splits = (int)std::max<int64_t>(1, std::min<int64_t>({384 / (s.tiles * p->kv_heads), prefix / 256, 64}));
     return s;
 }
 // the many-requests kernel's parts of a request's own keys
@@ -120,7 +137,7 @@ b2b_status_t b2b_attn_workspace(b2b_attn_t p, int32_t seqs, int64_t rows, int64_
     if (!p || !bytes || !sizes_ok(p, seqs, rows, keys)) return B2B_ERROR_INVALID_VALUE;
     *bytes = 0;
     if (!seqs || !rows) return B2B_SUCCESS;
-    const Split s = plan_tiles(p, seqs, rows, keys, true, 512);
+    const Split s = plan_tiles(p, seqs, rows, keys);
     if (s.splits > 1) *bytes = part_bytes(p, s.splits, rows);
     return B2B_SUCCESS;
 }
@@ -134,7 +151,7 @@ b2b_status_t b2b_attn_run(b2b_attn_t p, int32_t seqs, int64_t rows, int64_t keys
     if (!rows_ok(Q, rows, dim) || !rows_ok(O, rows, dim) || !cu_q || !cu_k) return B2B_ERROR_INVALID_VALUE;
     if (keys && (!rows_ok(K, keys, dim) || !rows_ok(V, keys, dim))) return B2B_ERROR_INVALID_VALUE;
     if (O.data == Q.data || O.data == K.data || O.data == V.data || (uintptr_t)lse % 4) return B2B_ERROR_INVALID_VALUE;
-    const Split s = plan_tiles(p, seqs, rows, keys, true, 512);
+    const Split s = plan_tiles(p, seqs, rows, keys);
     size_t need = s.splits > 1 ? part_bytes(p, s.splits, rows) : 0;
     if (need && (!workspace || (uintptr_t)workspace % 16 || workspace_bytes < need)) return B2B_ERROR_INVALID_VALUE;
     b2bk::AttnArgs a = base_args(p);
@@ -168,7 +185,7 @@ b2b_status_t b2b_prefix_attn_workspace(b2b_attn_t p, int32_t batch, int64_t pref
         return B2B_ERROR_INVALID_VALUE;
     *bytes = 0;
     if (!batch) return B2B_SUCCESS;
-    const int64_t slots = (prefix ? plan_tiles(p, 1, batch, prefix, false, 256).splits : 0) + (own ? plan_own(p, batch, own) : 0);
+    const int64_t slots = (prefix ? plan_prefix(p, batch, prefix).splits : 0) + (own ? plan_own(p, batch, own) : 0);
     *bytes = part_bytes(p, slots, batch);
     return B2B_SUCCESS;
 }
@@ -197,7 +214,7 @@ b2b_status_t b2b_prefix_attn_run(b2b_attn_t p, int32_t batch, int64_t prefix, in
     a.ldo = O.row_stride;
     a.hso = O.head_stride;
     a.rows = batch;
-    const Split s = prefix ? plan_tiles(p, 1, batch, prefix, false, 256) : Split{0, 0};
+    const Split s = prefix ? plan_prefix(p, batch, prefix) : Split{0, 0};
     const int own_parts = own ? plan_own(p, batch, own) : 0, slots = s.splits + own_parts;
     a.part = (float*)workspace;
     a.part_lse = a.part + (size_t)slots * batch * p->heads * dim;

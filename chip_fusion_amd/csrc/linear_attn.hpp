@@ -3,23 +3,26 @@
 //     S_t = lambda S_{t-1} + k_t v_t^T        (S: D x D, float32)
 //     o_t = scale q_t^T S_t.
 //
-// Prompts go 64 tokens at a time.  With S the state before a chunk and i, j
+// Prompts go 32 tokens at a time.  With S the state before a chunk and i, j
 // its tokens (0 ..),
 //     o_i = scale ( lambda^(i+1) q_i^T S + sum_{j<=i} lambda^(i-j) (q_i.k_j) v_j )
 //     S'  = lambda^n S + sum_j lambda^(n-1-j) k_j v_j^T
-// -- three cascades whose intermediates stay in registers (the relabelled K
-// order of the attention kernels):
+// -- three cascades whose intermediates stay on chip (the relabelled K order
+// of the attention kernels):
 //   * scores are computed transposed, S^T = K.Q^T, so decayed and rounded
 //     they are the operand of V^T.P^T as they lie;
 //   * the state's accumulators (lane: value column, registers: key columns,
 //     their order set by the order in which the keys' columns are read) are,
-//     rounded, the operand of S^T.Q^T as they lie, so the state never leaves
-//     its wave's registers;
+//     rounded, the operand of S^T.Q^T as they lie;
 //   * both end in O^T with one query row a lane, so the factor
 //     scale lambda^(i+1) is one multiplication a register.
-// Every wave owns 32 value columns: its part of the state (D x 32 floats, 64
-// registers at D = 128) and of the output.  Scores are recomputed by each
-// wave (24 of its ~90 matrix instructions a chunk) rather than exchanged.
+// A sequence's head is one workgroup walking its chunks in order, so what
+// counts is the time of a chunk.  Half of the waves keep the state, half
+// compute outputs, one of each on a SIMD, 32 value columns a wave: while a
+// state wave takes in chunk c, an output wave answers chunk c's queries from
+// the copy of the state that the state wave left in LDS a step before.  (All
+// waves doing both in turn took 4.1 us for 64 tokens of a head of 128, two
+// barriers and one wave a SIMD; 2.9 so.)
 //
 // The state is float32 and so are its terms: lambda^(n-1-j) v_j is split into
 // parts of the 16-bit type that together hold its 24 bits (bf16: three; fp16:
@@ -52,22 +55,27 @@ __device__ __forceinline__ float lin_pow(float g2, int d) {
 }
 
 // STATE: only the segments' own states (from zero), for the pass before the
-// outputs of sequences that are split.
-// LDS: two slots of keys, then values (STATE: two slots), then queries, then
-// decays: of the chunk's tokens up to its end, and of the scores.
+// outputs of sequences that are split: no output waves, no queries.
+// LDS: SLOTS chunks of keys, values (and queries), copied by the state waves
+// SLOTS - 1 chunks ahead; two copies of the state; two chunks of outputs on
+// their way out; the copies' exponents (fp16).
 template <int DT_, int D_, bool STATE_>
 struct LinCfg {
-    static constexpr int DT = DT_, D = D_, DB = D / 32, WAVES = DB, THREADS = 64 * WAVES, C = 64;
+    static constexpr int DT = DT_, D = D_, DB = D / 32, C = 32;
     static constexpr bool STATE = STATE_;
-    static constexpr int KS = 2 * DB, TILE = C * DB * 64, FALL = 4 * TILE, DECAYS = FALL + 256;
-    static constexpr int LDS_BYTES = DECAYS + (STATE ? 0 : 8192);
-    static constexpr int PARTS = DT == DT_BF16 ? 3 : 2;
+    static constexpr int WAVES = STATE ? DB : 2 * DB, THREADS = 64 * WAVES;
+    static constexpr int KS = 2 * DB, TILE = C * DB * 64, OPS = STATE ? 2 : 3, SLOTS = STATE ? 4 : 3;
+    static constexpr int COPY = SLOTS * OPS * TILE, COPY_BYTES = DB * KS * 1024;      // a copy of the state
+    static constexpr int OUT = COPY + (STATE ? 0 : 2 * COPY_BYTES);                   // two chunks of outputs
+    static constexpr int EXPS = OUT + (STATE ? 0 : 2 * TILE), LDS_BYTES = EXPS + (STATE ? 0 : 64);
+    static constexpr int PARTS = DT == DT_BF16 ? 3 : 2, PIECES = TILE / 1024 / DB;      // copies of a tile by a state wave
+    static_assert(LDS_BYTES <= 160 * 1024 && (SLOTS - 2) * OPS * PIECES <= 63, "config");
 };
 
 // A transposed fragment of the swizzled key tile: 32 columns of block t,
 // K-step ks of its rows; tb[e]: the lane's bases.  Of each 16 columns the
 // second and third four trade places: the product's result then has, in lane
-// half h and register r, column 16*(r/8) + 8h + r%8 of the block (lin_column),
+// half h and register r, column 16*(r/8) + 8h + r%8 of the block (lin_row),
 // which makes eight registers of the state an operand in the natural order.
 __device__ __forceinline__ void lin_tbase(int lane, int (&tb)[2]) {
     const int g = lane >> 4, i = lane & 15;
@@ -78,7 +86,7 @@ __device__ __forceinline__ void lin_tbase(int lane, int (&tb)[2]) {
         tb[e] = 512 * e + (4 * (g >> 1) + (i >> 2)) * 64 + chunk * 16 + (q & 1) * 8;
     }
 }
-__device__ __forceinline__ int lin_column(int r, int h) { return 16 * (r >> 3) + 8 * h + (r & 7); }
+__device__ __forceinline__ int lin_row(int r, int h) { return 16 * (r >> 3) + 8 * h + (r & 7); }
 template <int R>
 __device__ __forceinline__ u4_t lin_tfrag(const unsigned char* p, const int (&tb)[2], int t, int ks) {
     u4_t out;
@@ -159,193 +167,258 @@ __device__ __forceinline__ void lin_body(const LinArgs& a) {
     const int64_t row0 = w.q0 + (int64_t)w.local * a.seg;
     const int n = last ? w.nq - w.local * a.seg : a.seg;
     const float g2 = a.log_decay[head] * kLog2e;
-
-    // this wave's columns of the state
-    f16x_t S[C::DB];
-    const int col = 32 * wave + m;
-    auto state_at = [&](float* base, int64_t slot) { return base + ((slot * a.heads + head) * C::D) * C::D + col; };
-    const float* from = nullptr;
-    if constexpr (!C::STATE) {
-        if (w.tiles > 1) from = state_at(a.part, tile);
-        else if (a.s0) from = state_at(const_cast<float*>(a.s0), w.seq);
-    }
-#pragma unroll
-    for (int t = 0; t < C::DB; ++t)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) S[t][r] = from ? from[(32 * t + lin_column(r, h)) * C::D] : 0.f;
-
     const int chunks = (n + C::C - 1) / C::C;
-    const int64_t qat = (int64_t)head * a.Q.hs, kat = (int64_t)kvh * a.K.hs, vat = (int64_t)kvh * a.V.hs;
-    auto copy = [&](const AttnRows& x, int64_t at, int c, int slot, auto SWZ) __attribute__((always_inline)) {
-        const auto rs = attn_rsrc(x.p, row0 + (int64_t)c * C::C, x.ld, at, n - c * C::C < C::C ? n - c * C::C : C::C, C::D);
-#pragma unroll
-        for (int rg = wave; rg < 4; rg += C::WAVES)
-            attn_copy<C::DB, C::C, SWZ.value>(lds + slot * C::TILE, rs, (int)x.ld * 2, C::D, rg, lane);
-    };
-    auto copy_k = [&](int c) { copy(a.K, kat, c, c & 1, std::true_type{}); };
-    auto copy_v = [&](int c) { copy(a.V, vat, c, C::STATE ? 2 + (c & 1) : 2, std::false_type{}); };
-    auto copy_q = [&](int c) { copy(a.Q, qat, c, 3, std::true_type{}); };
-    const int kb[2] = {attn_kbase(lane, 0), attn_kbase(lane, 1)};
-    int tb[2];
-    lin_tbase(lane, tb);
-    auto rows32 = [&](int off, int s) __attribute__((always_inline)) {     // a fragment of 32 rows, K-step s
-        return *(const u4_t*)(lds + off + kb[s & 1] + (s >> 1) * C::C * 64);
-    };
-    const int vb = attn_vbase(lane);
-    // decays of the scores: of a pair of tokens in the same half of the chunk
-    // (0 where the key comes later) and of a query in the second half with a
-    // key in the first
-    // -- in LDS, 16 of each a lane: in registers they would cost two waves a SIMD
-    float into[2];
-    if constexpr (!C::STATE) {
-        for (int g = wave; g < 8; g += C::WAVES) {
-            f4_t d;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int j = 8 * (g & 3) + 4 * h + r;
-                d[r] = g >= 4 ? a.scale * lin_pow(g2, 32 + m - j) : (j > m ? 0.f : a.scale * lin_pow(g2, m - j));
-            }
-            *(f4_t*)(lds + C::DECAYS + g * 1024 + lane * 16) = d;
-        }
-        into[0] = a.scale * lin_pow(g2, m + 1);
-        into[1] = a.scale * lin_pow(g2, m + 33);
-    }
-    float* fall = (float*)(lds + C::FALL);       // lambda^(n-1-j) of token j of the chunk
-    if (wave == 0) fall[lane] = lin_pow(g2, 63 - lane);
 
-    if (chunks > 0) {
-        copy_k(0);
-        copy_v(0);
-        if constexpr (!C::STATE) copy_q(0);
-    }
-    for (int c = 0; c < chunks; ++c) {
-        barrier_vm<0>();       // chunk c is in LDS, and everyone is done with chunk c - 1
-        if (c + 1 < chunks) copy_k(c + 1);
-        const unsigned char* kt = lds + (c & 1) * C::TILE;
-        const int left = n - c * C::C < C::C ? n - c * C::C : C::C;
-        u4_t v[4];
+    const int vb = attn_vbase(lane);
+    const int part = wave % C::DB, col = 32 * part + m;        // this wave's value columns
+    auto slot = [&](int c) __attribute__((always_inline)) {      // where the c-th chunk taken in lies
+        return lds + __builtin_amdgcn_readfirstlane(c % C::SLOTS * C::OPS * C::TILE);
+    };
+
+    if (wave < C::DB) {
+        // ---- the state ----
+        // this wave's pieces of a tile: 16 rows x 64 bytes of a block
+        // The i-th chunk taken in is c = i, or (STATE: the contributions of
+        // chunks are summed with their decays, in any order) from the last
+        // back: a head whose decay has run out of float32's range is done early,
+        // and what the pass reads last, the next pass reads first.
+        auto chunk_of = [&](int i) __attribute__((always_inline)) { return C::STATE ? chunks - 1 - i : i; };
+        auto copy = [&](const AttnRows& x, int64_t at, int i, int op, bool swz) __attribute__((always_inline)) {
+            // past the end: as many copies, of nothing
+            const int c = i < chunks ? chunk_of(i) : 0, live = i < chunks;
+            const int left = n - c * C::C < C::C ? n - c * C::C : C::C;
+            const auto rs = attn_rsrc(x.p, row0 + (int64_t)c * C::C, x.ld, at, live ? left : 0, C::D);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = attn_vfrag<C::C>(lds + (C::STATE ? 2 + (c & 1) : 2) * C::TILE, vb, wave, k);
-        if constexpr (C::STATE) {
-            if (c + 1 < chunks) copy_v(c + 1);
-        } else {
-            // the state as an operand
-            u4_t sp[C::KS];
-            int e = 0;
-            if constexpr (C::DT == DT_F16) e = lin_exponent(S);
-            if (e != 0) {
-                const float down = __builtin_ldexpf(1.f, -e);
-#pragma unroll
-                for (int s = 0; s < C::KS; ++s) {
-                    f16x_t x = S[s >> 1];
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) x[r] *= down;
-                    sp[s] = attn_pack<C::DT>(x, s & 1);
-                }
-            } else {
-#pragma unroll
-                for (int s = 0; s < C::KS; ++s) sp[s] = attn_pack<C::DT>(S[s >> 1], s & 1);
+            for (int j = 0; j < C::PIECES; ++j) {
+                const int piece = wave * C::PIECES + j, row = 16 * (piece & 1) + (lane >> 2);
+                const int chunk = swz ? (lane & 3) ^ ((row >> 2) & 3) : lane & 3;
+                lds_dma16<false>(rs, slot(i) + op * C::TILE + piece * 1024,
+                                 row * (int)x.ld * 2 + chunk * 16 + 64 * (piece >> 1));
             }
-            const float up = __builtin_ldexpf(1.f, e);
+        };
+        auto copy_chunk = [&](int i) __attribute__((always_inline)) {
+            copy(a.K, (int64_t)kvh * a.K.hs, i, 0, true);
+            copy(a.V, (int64_t)kvh * a.V.hs, i, 1, false);
+            if constexpr (!C::STATE) copy(a.Q, (int64_t)head * a.Q.hs, i, 2, true);
+        };
+        if (chunks > 0)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                u4_t q[C::KS];
-#pragma unroll
-                for (int s = 0; s < C::KS; ++s) q[s] = rows32(3 * C::TILE + i * 2048, s);
-                if (i == 1) {
-                    // the last chunk's tokens count up to its own end
-                    if (left < C::C && wave == 0) fall[lane] = lin_pow(g2, left - 1 - lane);
-                    barrier_lds();       // everyone has read this chunk's values and queries
-                    if (c + 1 < chunks) {
-                        copy_v(c + 1);
-                        copy_q(c + 1);
-                    }
-                }
-                // from the state
-                f16x_t o = f16x_t{};
-#pragma unroll
-                for (int s = 0; s < C::KS; ++s) o = M::mma(sp[s], q[s], o);
-                const float f = into[i] * up;
-#pragma unroll
-                for (int r = 0; r < 16; ++r) o[r] *= f;
-                // from the chunk's own tokens
-#pragma unroll
-                for (int k = 0; k <= i; ++k) {
-                    f16x_t p = f16x_t{};
-#pragma unroll
-                    for (int s = 0; s < C::KS; ++s) p = M::mma(rows32((c & 1) * C::TILE + k * 2048, s), q[s], p);
-#pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        const f4_t d = *(const f4_t*)(lds + C::DECAYS + ((i == k ? 0 : 4) + g) * 1024 + lane * 16);
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) p[4 * g + r] *= d[r];
-                    }
-#pragma unroll
-                    for (int s = 0; s < 2; ++s) o = M::mma(v[2 * k + s], attn_pack<C::DT>(p, s), o);
-                }
-                const int row = 32 * i + m;
-                char* op = (char*)a.O + ((row0 + (int64_t)c * C::C + row) * a.ldo + (int64_t)head * a.hso + 32 * wave) * 2;
-#pragma unroll
-                for (int q4 = 0; q4 < 4; q4 += 2) {
-                    unsigned x0 = Ty<C::DT>::pack(o[4 * q4], o[4 * q4 + 1]);
-                    unsigned x1 = Ty<C::DT>::pack(o[4 * q4 + 2], o[4 * q4 + 3]);
-                    unsigned y0 = Ty<C::DT>::pack(o[4 * q4 + 4], o[4 * q4 + 5]);
-                    unsigned y1 = Ty<C::DT>::pack(o[4 * q4 + 6], o[4 * q4 + 7]);
-                    swap32(x0, y0);
-                    swap32(x1, y1);
-                    if (row < left) *(u4_t*)(op + 16 * (q4 + h)) = u4_t{x0, x1, y0, y1};
-                }
-                __builtin_amdgcn_sched_barrier(0);   // the two halves' registers in turn
-            }
+            for (int c = 0; c < C::SLOTS - 1; ++c) copy_chunk(c);
+        int tb[2];
+        lin_tbase(lane, tb);
+        f16x_t S[C::DB];
+        auto state_at = [&](float* base, int64_t at) {
+            return base + (at * a.heads + head) * C::D * C::D + col;
+        };
+        const float* from = nullptr;
+        if constexpr (!C::STATE) {
+            if (w.tiles > 1) from = state_at(a.part, tile);
+            else if (a.s0) from = state_at(const_cast<float*>(a.s0), w.seq);
         }
-        // the state after the chunk
-        u4_t vp[C::PARTS][4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const f4_t w = *(const f4_t*)(fall + 16 * k + 8 * x + 4 * h);
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    const unsigned two = v[k][2 * x + y];
-                    unsigned out[C::PARTS];
-                    lin_split<C::DT>(lin_unpack<C::DT>(two, 0) * w[2 * y], lin_unpack<C::DT>(two, 1) * w[2 * y + 1], out);
-#pragma unroll
-                    for (int p = 0; p < C::PARTS; ++p) vp[p][k][2 * x + y] = out[p];
-                }
-            }
-        const float keep = lin_pow(g2, left);
-#pragma unroll
-        for (int t = 0; t < C::DB; ++t) {
-            u4_t f[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) f[k] = lin_tfrag<C::C>(kt, tb, t, k);
-            if constexpr (C::DT == DT_F16) {
-                f16x_t low = f16x_t{};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) low = M::mma(f[k], vp[1][k], low);
-#pragma unroll
-                for (int r = 0; r < 16; ++r) S[t][r] = __builtin_fmaf(low[r], 1.f / 2048, S[t][r] * keep);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) S[t] = M::mma(f[k], vp[0][k], S[t]);
-            } else {
-#pragma unroll
-                for (int r = 0; r < 16; ++r) S[t][r] *= keep;
-#pragma unroll
-                for (int p = C::PARTS - 1; p >= 0; --p)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) S[t] = M::mma(f[k], vp[p][k], S[t]);
-            }
-        }
-    }
-    float* to = nullptr;
-    if constexpr (C::STATE) to = state_at(a.part, tile);
-    else if (last && a.s1) to = state_at(a.s1, w.seq);
-    if (to)
 #pragma unroll
         for (int t = 0; t < C::DB; ++t)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) to[(32 * t + lin_column(r, h)) * C::D] = S[t][r];
+            for (int r = 0; r < 16; ++r) S[t][r] = from ? from[(32 * t + lin_row(r, h)) * C::D] : 0.f;
+        // leaves a copy for the output waves, behind their next barrier
+        auto leave = [&](int c) __attribute__((always_inline)) {
+            if constexpr (!C::STATE) {
+                unsigned char* to = lds + C::COPY + (c & 1) * C::COPY_BYTES + part * C::KS * 1024 + lane * 16;
+                if constexpr (C::DT == DT_F16) {
+                    const int e = lin_exponent(S);
+                    const float down = __builtin_ldexpf(1.f, -e);
+                    if (lane == 0) ((float*)(lds + C::EXPS))[(c & 1) * 4 + part] = __builtin_ldexpf(1.f, e);
+                    if (e != 0) {
+#pragma unroll
+                        for (int s = 0; s < C::KS; ++s) {
+                            f16x_t x = S[s >> 1];
+#pragma unroll
+                            for (int r = 0; r < 16; ++r) x[r] *= down;
+                            *(u4_t*)(to + s * 1024) = attn_pack<C::DT>(x, s & 1);
+                        }
+                        return;
+                    }
+                }
+#pragma unroll
+                for (int s = 0; s < C::KS; ++s) *(u4_t*)(to + s * 1024) = attn_pack<C::DT>(S[s >> 1], s & 1);
+            }
+        };
+        // lambda^(n-1-j) of the chunk's tokens j = 16k + 8*(i/4) + 4h + i%4
+        float fall[2][8];
+        auto fall_to = [&](int left) __attribute__((always_inline)) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) fall[k][i] = lin_pow(g2, left - 1 - (16 * k + 8 * (i >> 2) + 4 * h + (i & 3)));
+        };
+        fall_to(C::C);
+        float keep = lin_pow(g2, C::C);
+        if (chunks > 0) leave(0);
+        for (int c = 0; c < chunks; ++c) {
+            // what lies between the chunk and the segment's end
+            const float after = C::STATE ? lin_pow(g2, C::C * c) : 1.f;
+            if (C::STATE && __builtin_amdgcn_readfirstlane(after == 0.f)) break;
+            barrier_vm<(C::SLOTS - 2) * C::OPS * C::PIECES>();   // chunk c is in LDS, and everyone is done with chunk c - 1
+            copy_chunk(c + C::SLOTS - 1);
+            const unsigned char* kt = slot(c);
+            if (!C::STATE && n - c * C::C < C::C) {
+                fall_to(n - c * C::C);
+                keep = lin_pow(g2, n - c * C::C);
+            }
+            u4_t v[2], f[C::DB][2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                v[k] = attn_vfrag<C::C>(kt + C::TILE, vb, part, k);
+#pragma unroll
+                for (int t = 0; t < C::DB; ++t) f[t][k] = lin_tfrag<C::C>(kt, tb, t, k);
+            }
+            // K-step by K-step, so that one's matrix instructions run under the
+            // other's arithmetic
+            u4_t vp[2][C::PARTS];
+            // bf16 has float32's range, so there a chunk's decay to the
+            // segment's end goes into the split values; fp16's products are
+            // decayed as a whole
+            const float in = C::DT == DT_BF16 ? after : 1.f;
+            auto split = [&](int k) __attribute__((always_inline)) {
+#pragma unroll
+                for (int d = 0; d < 4; ++d) {
+                    unsigned out[C::PARTS];
+                    float w0 = fall[k][2 * d], w1 = fall[k][2 * d + 1];
+                    if constexpr (C::STATE && C::DT == DT_BF16) {
+                        w0 *= in;
+                        w1 *= in;
+                    }
+                    lin_split<C::DT>(lin_unpack<C::DT>(v[k][d], 0) * w0, lin_unpack<C::DT>(v[k][d], 1) * w1, out);
+#pragma unroll
+                    for (int p = 0; p < C::PARTS; ++p) vp[k][p][d] = out[p];
+                }
+            };
+            if constexpr (C::DT == DT_F16) {
+                f16x_t low[C::DB];
+#pragma unroll
+                for (int t = 0; t < C::DB; ++t) low[t] = f16x_t{};
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    split(k);
+#pragma unroll
+                    for (int t = 0; t < C::DB; ++t) low[t] = M::mma(f[t][k], vp[k][1], low[t]);
+                }
+                if constexpr (C::STATE) {
+#pragma unroll
+                    for (int t = 0; t < C::DB; ++t)
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) low[t][r] *= 1.f / 2048;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+#pragma unroll
+                        for (int t = 0; t < C::DB; ++t) low[t] = M::mma(f[t][k], vp[k][0], low[t]);
+#pragma unroll
+                    for (int t = 0; t < C::DB; ++t)
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) S[t][r] = __builtin_fmaf(low[t][r], after, S[t][r]);
+                } else {
+#pragma unroll
+                    for (int t = 0; t < C::DB; ++t)
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) S[t][r] = __builtin_fmaf(low[t][r], 1.f / 2048, S[t][r] * keep);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+#pragma unroll
+                        for (int t = 0; t < C::DB; ++t) S[t] = M::mma(f[t][k], vp[k][0], S[t]);
+                }
+            } else {
+                if constexpr (!C::STATE)
+#pragma unroll
+                    for (int t = 0; t < C::DB; ++t)
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) S[t][r] *= keep;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    split(k);
+#pragma unroll
+                    for (int p = C::PARTS - 1; p >= 0; --p)
+#pragma unroll
+                        for (int t = 0; t < C::DB; ++t) S[t] = M::mma(f[t][k], vp[k][p], S[t]);
+                }
+            }
+            leave(c + 1);
+        }
+        if (!C::STATE && chunks > 0) barrier_lds();      // the output waves' last
+        float* to = nullptr;
+        if constexpr (C::STATE) to = state_at(a.part, tile);
+        else if (last && a.s1) to = state_at(a.s1, w.seq);
+        if (to)
+#pragma unroll
+            for (int t = 0; t < C::DB; ++t)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) to[(32 * t + lin_row(r, h)) * C::D] = S[t][r];
+    } else if constexpr (!C::STATE) {
+        // ---- the outputs ----
+        const int kb[2] = {attn_kbase(lane, 0), attn_kbase(lane, 1)};
+        float same[16];                        // decays of the scores, 0 where the key comes later
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const int j = 8 * (r >> 2) + 4 * h + (r & 3);
+            same[r] = j > m ? 0.f : a.scale * lin_pow(g2, m - j);
+        }
+        const float into = a.scale * lin_pow(g2, m + 1);
+        // Outputs leave through LDS, a step later, as whole rows: in 32-byte
+        // pieces straight from the registers they took 42 of 123 us (32768 tokens of
+        // 16 heads of 128 whose 402 MB of reads take 81).
+        constexpr int CH = 4 * C::DB, RW = 64 / CH;               // 16-byte chunks of a row; rows of a store
+        auto out_at = [&](int c, int row, int chunk) __attribute__((always_inline)) {
+            return lds + C::OUT + (c & 1) * C::TILE + row * CH * 16 + ((chunk ^ (row & (CH - 1))) << 4);
+        };
+        auto flush = [&](int c) __attribute__((always_inline)) {
+            const int left = n - c * C::C < C::C ? n - c * C::C : C::C;
+            const auto rs = attn_rsrc(a.O, row0 + (int64_t)c * C::C, a.ldo, (int64_t)head * a.hso, left, C::D);
+#pragma unroll
+            for (int i = 0; i < C::C / C::DB / RW; ++i) {
+                const int row = part * (C::C / C::DB) + i * RW + lane / CH, chunk = lane % CH;
+                st128(rs, row * (int)a.ldo * 2 + chunk * 16, *(const u4_t*)out_at(c, row, chunk));
+            }
+        };
+        for (int c = 0; c < chunks; ++c) {
+            barrier_lds();
+            if (c > 0) flush(c - 1);
+            const unsigned char* kt = slot(c);
+            auto rows32 = [&](const unsigned char* p, int s) __attribute__((always_inline)) {
+                return *(const u4_t*)(p + kb[s & 1] + (s >> 1) * C::C * 64);
+            };
+            f16x_t p = f16x_t{}, y = f16x_t{};
+            const unsigned char* sp = lds + C::COPY + (c & 1) * C::COPY_BYTES + part * C::KS * 1024 + lane * 16;
+#pragma unroll
+            for (int s = 0; s < C::KS; ++s) {
+                const u4_t q = rows32(kt + 2 * C::TILE, s);
+                p = M::mma(rows32(kt, s), q, p);
+                y = M::mma(*(const u4_t*)(sp + s * 1024), q, y);
+            }
+            float f = into;
+            if constexpr (C::DT == DT_F16) f *= ((const float*)(lds + C::EXPS))[(c & 1) * 4 + part];
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                y[r] *= f;
+                p[r] *= same[r];
+            }
+#pragma unroll
+            for (int s = 0; s < 2; ++s) y = M::mma(attn_vfrag<C::C>(kt + C::TILE, vb, part, s), attn_pack<C::DT>(p, s), y);
+#pragma unroll
+            for (int q4 = 0; q4 < 4; q4 += 2) {
+                unsigned x0 = Ty<C::DT>::pack(y[4 * q4], y[4 * q4 + 1]);
+                unsigned x1 = Ty<C::DT>::pack(y[4 * q4 + 2], y[4 * q4 + 3]);
+                unsigned y0 = Ty<C::DT>::pack(y[4 * q4 + 4], y[4 * q4 + 5]);
+                unsigned y1 = Ty<C::DT>::pack(y[4 * q4 + 6], y[4 * q4 + 7]);
+                swap32(x0, y0);
+                swap32(x1, y1);
+                *(u4_t*)out_at(c, m, 4 * part + q4 + h) = u4_t{x0, x1, y0, y1};
+            }
+        }
+        if (chunks > 0) {
+            barrier_lds();
+            flush(chunks - 1);
+        }
+    }
+    // copies of nothing still write zeros: not into LDS that is another workgroup's by then
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
 
 template <class C>

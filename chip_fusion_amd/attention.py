@@ -53,35 +53,39 @@ def _rows(t, name, dtype, shape):
 
 
 def _starts(cu, name, seqs=None):
-    if not isinstance(cu, torch.Tensor) or cu.dtype != torch.int32 or cu.dim() != 1 or not cu.is_contiguous():
+    if not isinstance(cu, torch.Tensor) or cu.dtype is not torch.int32 or cu.dim() != 1 or not cu.is_contiguous():
         raise ValueError(f"{name}: a contiguous 1-D int32 tensor is expected")
-    if cu.numel() < 1 or (seqs is not None and cu.numel() != seqs + 1):
+    n = cu.numel() - 1
+    if n < 0 or (seqs is not None and n != seqs):
         raise ValueError(f"{name}: {'at least one value' if seqs is None else f'{seqs + 1} values'} expected, "
-                         f"got {cu.numel()}")
-    return cu.numel() - 1
+                         f"got {n + 1}")
+    return n
 
 
 def _device_of(names, *tensors):
     """The CUDA device that holds all the tensors (None among them: not given)."""
     index = tensors[0].get_device()
-    if index < 0 or any(t is not None and t.get_device() != index for t in tensors):
-        first = None
-        for name, t in zip(names.split(), tensors):
-            if t is None:
-                continue
-            if t.device.type != "cuda":
-                raise ValueError(f"{name}: a device (cuda) tensor is expected, got one on {t.device}")
-            if first is not None and t.device != first:
-                raise ValueError(f"{name}: on {t.device}, the others on {first}")
-            first = t.device
-    return index
+    for t in tensors:
+        if index < 0 or (t is not None and t.get_device() != index):
+            break
+    else:
+        return index
+    first = None
+    for name, t in zip(names.split(), tensors):
+        if t is None:
+            continue
+        if t.device.type != "cuda":
+            raise ValueError(f"{name}: a device (cuda) tensor is expected, got one on {t.device}")
+        if first is not None and t.device != first:
+            raise ValueError(f"{name}: on {t.device}, the others on {first}")
+        first = t.device
 
 
 def _on(index, stream, call):
     """call(handle) with the tensors' device current and `stream` (or that
     device's current stream) the one that allocations belong to; handle: its
     hipStream_t."""
-    if stream is None and torch.cuda.current_device() == index:
+    if stream is None and torch._C._cuda_getDevice() == index:
         return call(torch._C._cuda_getCurrentRawStream(index))
     with torch.cuda.device(index):
         s = torch.cuda.current_stream() if stream is None else stream
@@ -91,15 +95,33 @@ def _on(index, stream, call):
             return call(s.cuda_stream)
 
 
-def _workspace(call, handle, like, *sizes):
-    """A workspace for one run (torch's allocator keeps it until the stream is
-    past it): the tensor, its address and its bytes."""
-    n = ctypes.c_size_t()
-    _check(call(handle, *sizes, ctypes.byref(n)), call.__name__)
-    if n.value == 0:
-        return None, None, 0
-    t = like.new_empty(n.value, dtype=torch.uint8)
-    return t, t.data_ptr(), n.value
+class _Workspaces:
+    """Workspaces for one run each, from torch's allocator, which keeps one
+    until the stream is past its run; the bytes that a call of some sizes needs
+    are asked for once."""
+
+    def __init__(self, call, handle):
+        self._call, self._handle, self._bytes = call, handle, {}
+
+    def get(self, like, *sizes):
+        """The workspace (a tensor, or None), its address and its bytes."""
+        n = self._bytes.get(sizes)
+        if n is None:
+            out = ctypes.c_size_t()
+            _check(self._call(self._handle, *sizes, ctypes.byref(out)), self._call.__name__)
+            n = out.value
+            if len(self._bytes) >= 4096:
+                self._bytes.clear()
+            self._bytes[sizes] = n
+        if n == 0:
+            return None, None, 0
+        t = like.new_empty(n, dtype=torch.uint8)
+        return t, t.data_ptr(), n
+
+
+def _new(t):
+    """An uninitialised dense tensor like t."""
+    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
 
 
 def _ptr(t):
@@ -119,6 +141,7 @@ class _Heads:
                "b2b_attn_create")
         self._h = h
         self.dtype = TORCH_DTYPES[code]
+        self._workspaces = _Workspaces(getattr(lib(), self._workspace_call), h)
 
     def close(self):
         if getattr(self, "_h", None):
@@ -137,6 +160,8 @@ class Attention(_Heads):
     for each sequence and head, causal (aligned to the last key) or full.
 
     scale: of the scores, dim ** -0.5 by default."""
+
+    _workspace_call = "b2b_attn_workspace"
 
     def __init__(self, dtype, heads, kv_heads, head_dim, causal=True, scale=None):
         super().__init__(dtype, heads, kv_heads, head_dim, scale, ATTN_CAUSAL if causal else 0)
@@ -166,12 +191,11 @@ class Attention(_Heads):
         def call(stream):
             out, ls = O, LSE
             if out is None:
-                out = Q.new_empty(Q.shape)
+                out = _new(Q)
             if want and ls is None:
                 ls = Q.new_empty((rows, self.heads), dtype=torch.float32)
-            L = lib()
-            keep, wp, n = _workspace(L.b2b_attn_workspace, self._h, Q, seqs, rows, keys)
-            st = L.b2b_attn_run(self._h, seqs, rows, keys, q, k, v,
+            keep, wp, n = self._workspaces.get(Q, seqs, rows, keys)
+            st = lib().b2b_attn_run(self._h, seqs, rows, keys, q, k, v,
                                 o if O is not None else Rows(out.data_ptr(), self.heads * self.dim, self.dim),
                                 cu_q.data_ptr(), cu_k.data_ptr(), _ptr(ls), wp, n, stream)
             _check(st, "b2b_attn_run")
@@ -183,6 +207,8 @@ class Attention(_Heads):
 class PrefixAttention(_Heads):
     """Attention of one new token a request, all requests behind one shared
     prefix (b2b_prefix_attn_run): the prefix is read once for the batch."""
+
+    _workspace_call = "b2b_prefix_attn_workspace"
 
     def __init__(self, dtype, heads, kv_heads, head_dim, scale=None):
         super().__init__(dtype, heads, kv_heads, head_dim, scale, 0)
@@ -202,7 +228,7 @@ class PrefixAttention(_Heads):
         ks, vs = (K.stride(0), V.stride(0)) if batch > 1 and own else (0, 0)
         if ks % 8 or vs % 8:
             raise ValueError(f"{'K' if ks % 8 else 'V'}: requests must start on 16-byte boundaries")
-        if not isinstance(lens, torch.Tensor) or lens.dtype != torch.int32 or tuple(lens.shape) != (batch,) \
+        if not isinstance(lens, torch.Tensor) or lens.dtype is not torch.int32 or lens.shape != (batch,) \
                 or not lens.is_contiguous():
             raise ValueError(f"lens: a contiguous int32 tensor [{batch}] is expected")
         if O is not None:
@@ -210,10 +236,9 @@ class PrefixAttention(_Heads):
         index = _device_of("Q Kp Vp K V lens O", Q, Kp, Vp, K, V, lens, O)
 
         def call(stream):
-            out = Q.new_empty(Q.shape) if O is None else O
-            L = lib()
-            keep, wp, n = _workspace(L.b2b_prefix_attn_workspace, self._h, Q, batch, prefix, own)
-            st = L.b2b_prefix_attn_run(self._h, batch, prefix, own, q, kp, vp, k, ks, v, vs, lens.data_ptr(),
+            out = _new(Q) if O is None else O
+            keep, wp, n = self._workspaces.get(Q, batch, prefix, own)
+            st = lib().b2b_prefix_attn_run(self._h, batch, prefix, own, q, kp, vp, k, ks, v, vs, lens.data_ptr(),
                                        o if O is not None else Rows(out.data_ptr(), self.heads * self.dim, self.dim),
                                        wp, n, stream)
             _check(st, "b2b_prefix_attn_run")
@@ -239,6 +264,7 @@ class LinearAttention:
                "b2b_linear_attn_create")
         self._h = h
         self.dtype = TORCH_DTYPES[code]
+        self._workspaces = _Workspaces(lib().b2b_linear_attn_workspace, h)
 
     def _operands(self, Q, K, V, log_decay, O):
         q = _rows(Q, "Q", self.dtype, (None, self.heads, self.dim))
@@ -246,8 +272,8 @@ class LinearAttention:
         v = _rows(V, "V", self.dtype, (Q.shape[0], self.kv_heads, self.dim))
         if O is not None:
             _rows(O, "O", self.dtype, tuple(Q.shape))
-        if not isinstance(log_decay, torch.Tensor) or log_decay.dtype != torch.float32 \
-                or tuple(log_decay.shape) != (self.heads,) or not log_decay.is_contiguous():
+        if not isinstance(log_decay, torch.Tensor) or log_decay.dtype is not torch.float32 \
+                or log_decay.shape != (self.heads,) or not log_decay.is_contiguous():
             raise ValueError(f"log_decay: a contiguous float32 tensor [{self.heads}] is expected")
         return q, k, v
 
@@ -255,7 +281,7 @@ class LinearAttention:
         if t is None:
             return
         want = (n, self.heads, self.dim, self.dim)
-        if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or tuple(t.shape) != want \
+        if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32 or t.shape != want \
                 or not t.is_contiguous() or t.data_ptr() % 16:
             raise ValueError(f"{name}: a contiguous, 16-byte aligned float32 tensor {list(want)} is expected")
 
@@ -272,13 +298,12 @@ class LinearAttention:
         index = _device_of("Q K V log_decay cu state O state_out", Q, K, V, log_decay, cu, state, O, state_out)
 
         def call(stream):
-            out = Q.new_empty(Q.shape) if O is None else O
+            out = _new(Q) if O is None else O
             after = state_out
             if after is None:
                 after = Q.new_empty((seqs, self.heads, self.dim, self.dim), dtype=torch.float32)
-            L = lib()
-            keep, wp, n = _workspace(L.b2b_linear_attn_workspace, self._h, Q, seqs, rows)
-            st = L.b2b_linear_attn_run(self._h, seqs, rows, q, k, v, self._out(out, O is None), log_decay.data_ptr(),
+            keep, wp, n = self._workspaces.get(Q, seqs, rows)
+            st = lib().b2b_linear_attn_run(self._h, seqs, rows, q, k, v, self._out(out, O is None), log_decay.data_ptr(),
                                        cu.data_ptr(), _ptr(state), after.data_ptr(), wp, n, stream)
             _check(st, "b2b_linear_attn_run")
             return out, after
@@ -298,7 +323,7 @@ class LinearAttention:
         index = _device_of("Q K V log_decay state O state_out", Q, K, V, log_decay, state, O, state_out)
 
         def call(stream):
-            out = Q.new_empty(Q.shape) if O is None else O
+            out = _new(Q) if O is None else O
             after = torch.empty_like(state) if state_out is None else state_out
             st = lib().b2b_linear_attn_step(self._h, rows, q, k, v, self._out(out, O is None), log_decay.data_ptr(),
                                             state.data_ptr(), after.data_ptr(), stream)

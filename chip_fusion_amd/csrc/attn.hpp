@@ -190,6 +190,18 @@ __device__ __forceinline__ float other_half(float x) {
     return __builtin_bit_cast(float, l ? a : b);
 }
 
+// One of the two values in a word.
+template <int DT>
+__device__ __forceinline__ float attn_unpack(unsigned w, int hi) {
+    if constexpr (DT == DT_BF16) {
+        const unsigned x = hi ? (w & 0xFFFF0000u) : (w << 16);
+        return __builtin_bit_cast(float, x);
+    } else {
+        const h2_t v = __builtin_bit_cast(h2_t, w);
+        return hi ? (float)v[1] : (float)v[0];
+    }
+}
+
 // Query rows as the first product's operand: lane l holds row l%32, columns
 // 16s + 8*(l/32) + u; columns past D read as zero.
 template <int KS>
@@ -366,6 +378,71 @@ __device__ __forceinline__ void attn_store(const AttnArgs& a, const f16x_t (&o)[
     }
 }
 
+// Infinities and NaN among the values, causal.  A tile of the second product
+// multiplies the probability 0 of an unseen key by that key's value, which
+// gives NaN where the value is not finite.  So a wave whose results are not all
+// finite (looked at once, behind the last tile) computes its rows again from
+// the keys that they see and no others: lanes take keys for the scores, then
+// columns for the sums.  Some 30 times the tiles' time, and only there.
+template <class C>
+__device__ __forceinline__ bool attn_finite(const f16x_t (&o)[C::DB]) {
+    float z = 0.f;
+#pragma unroll
+    for (int b = 0; b < C::DB; ++b)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) z = __builtin_fmaf(o[b][r], 0.f, z);
+    return !__any(z != 0.f);
+}
+
+// st: the rows' maxima and sums; key range [from, to) of those at k0.
+template <class C>
+__device__ __forceinline__ void attn_careful(const AttnArgs& a, const RowState& st, int64_t q0, int64_t k0, int kvh, int wrow,
+                                             int rows, int shift, int from, int to, int slot, int lane) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");      // what the tiles gave has been written
+    const float l_all = st.l + other_half(st.l);
+    const char* K = (const char*)a.K.p + (k0 * a.K.ld + kvh * a.K.hs) * 2;
+    const char* V = (const char*)a.V.p + (k0 * a.V.ld + kvh * a.V.hs) * 2;
+    for (int r = 0; r < 32 && wrow + r < rows; ++r) {
+        const int pos = (wrow + r) / a.group, head = kvh * a.group + (wrow + r - pos * a.group);
+        const int end = pos + 1 + shift < to ? pos + 1 + shift : to;
+        const float m = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, st.m), r));
+        const float l = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, l_all), r));
+        const char* q = (const char*)a.Q.p + ((q0 + pos) * a.Q.ld + (int64_t)head * a.Q.hs) * 2;
+        float o0 = 0.f, o1 = 0.f;
+        for (int j = from; j < end; j += 64) {
+            float p = 0.f;
+            if (j + lane < end) {
+                const char* k = K + (int64_t)(j + lane) * a.K.ld * 2;
+                float s = 0.f;
+                for (int c = 0; c < a.dim; c += 2) {
+                    const unsigned x = *(const unsigned*)(q + 2 * c), y = *(const unsigned*)(k + 2 * c);
+                    s = __builtin_fmaf(attn_unpack<C::DT>(x, 0), attn_unpack<C::DT>(y, 0), s);
+                    s = __builtin_fmaf(attn_unpack<C::DT>(x, 1), attn_unpack<C::DT>(y, 1), s);
+                }
+                p = __builtin_amdgcn_exp2f(__builtin_fmaf(s, a.sc, -m));
+            }
+            const int n = end - j < 64 ? end - j : 64;
+            for (int i = 0; i < n; ++i) {
+                const float pi = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, p), i));
+                const unsigned v = 2 * lane < a.dim ? *(const unsigned*)(V + ((int64_t)(j + i) * a.V.ld + 2 * lane) * 2) : 0u;
+                o0 = __builtin_fmaf(pi, attn_unpack<C::DT>(v, 0), o0);
+                o1 = __builtin_fmaf(pi, attn_unpack<C::DT>(v, 1), o1);
+            }
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        if (2 * lane < a.dim) {
+            if constexpr (C::PART) {
+                float* x = a.part + (((int64_t)slot * a.rows + q0 + pos) * a.heads + head) * a.dim + 2 * lane;
+                x[0] = o0 * inv;
+                x[1] = o1 * inv;
+            } else {
+                *(unsigned*)((char*)a.O + ((q0 + pos) * a.ldo + (int64_t)head * a.hso + 2 * lane) * 2) =
+                    Ty<C::DT>::pack(o0 * inv, o1 * inv);
+            }
+        }
+    }
+}
+
 // ---------------------------------------------------------------------------
 // Many rows: a workgroup's waves take 32 rows each and share the key tiles
 // ---------------------------------------------------------------------------
@@ -470,6 +547,8 @@ __device__ __forceinline__ void attn_tile_body(const AttnArgs& a, unsigned char*
         }
     }
     attn_store<C::DT, C::DB, C::PART>(a, o, st, w.q0, kvh, rr, rows, a.slot0 + split, lane);
+    if (a.causal && !attn_finite<C>(o))
+        attn_careful<C>(a, st, w.q0, k0, kvh, wrow, rows, shift, t0 * C::BN, t1 * C::BN, a.slot0 + split, lane);
 }
 
 template <class C>

@@ -101,17 +101,6 @@ __device__ __forceinline__ u4_t lin_tfrag(const unsigned char* p, const int (&tb
     return out;
 }
 
-template <int DT>
-__device__ __forceinline__ float lin_unpack(unsigned w, int hi) {
-    if constexpr (DT == DT_BF16) {
-        const unsigned x = hi ? (w & 0xFFFF0000u) : (w << 16);
-        return __builtin_bit_cast(float, x);
-    } else {
-        const h2_t v = __builtin_bit_cast(h2_t, w);
-        return hi ? (float)v[1] : (float)v[0];
-    }
-}
-
 // Two values as PARTS 16-bit parts each, packed: their sum holds 24 bits
 // (fp16: the second part is scaled by 2^11).
 template <int DT, int PARTS>
@@ -125,8 +114,8 @@ __device__ __forceinline__ void lin_split(float x, float y, unsigned (&out)[PART
             // for those bits and twice for the remainder (seen: one value in
             // thousands, a step apart at a tie).
             asm("" : "+v"(out[p]));
-            x -= lin_unpack<DT>(out[p], 0);
-            y -= lin_unpack<DT>(out[p], 1);
+            x -= attn_unpack<DT>(out[p], 0);
+            y -= attn_unpack<DT>(out[p], 1);
             if constexpr (DT == DT_F16) {
                 x *= 2048.f;
                 y *= 2048.f;
@@ -148,27 +137,75 @@ __device__ __forceinline__ int lin_exponent(const f16x_t (&s)[NT]) {
     if (!__any(m > 16384.f) && __any(m > 0.25f)) return 0;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) m = __builtin_fmaxf(m, __shfl_xor(m, d));
-    if (!(m > 0.f) || m > 3e38f) return 0;
+    if (m > 3e38f) {       // an infinity sets no scale for the others
+        m = 0.f;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const float x = __builtin_fabsf(s[t][r]);
+                m = x <= 3e38f ? __builtin_fmaxf(m, x) : m;
+            }
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) m = __builtin_fmaxf(m, __shfl_xor(m, d));
+    }
+    if (!(m > 0.f)) return 0;
     return __builtin_amdgcn_readfirstlane(__builtin_amdgcn_frexp_expf(m) - 13);
 }
 
-template <class C>
-__device__ __forceinline__ void lin_body(const LinArgs& a) {
-    __shared__ __attribute__((aligned(1024))) unsigned char lds[C::LDS_BYTES];
+// Whether one of a lane's packed values is not finite.
+typedef unsigned short us2_t __attribute__((ext_vector_type(2)));
+template <int DT, int N>
+__device__ __forceinline__ bool lin_odd(const u4_t (&x)[N]) {
+    us2_t m[4] = {};
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            m[i] = __builtin_elementwise_max(m[i], __builtin_bit_cast(us2_t, x[n][i] & 0x7FFF7FFFu));
+    const us2_t y = __builtin_elementwise_max(__builtin_elementwise_max(m[0], m[1]), __builtin_elementwise_max(m[2], m[3]));
+    constexpr unsigned short inf = DT == DT_BF16 ? 0x7F80 : 0x7C00;
+    return y[0] >= inf || y[1] >= inf;
+}
+
+// acc, or NaN if one of eight packed values is not finite (0 times it).
+template <int DT>
+__device__ __forceinline__ float lin_watch(const u4_t& w, float acc) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if constexpr (DT == DT_BF16)
+            acc = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf2_t, (unsigned)w[i]), bf2_t{}, acc, false);
+        else
+            acc = __builtin_amdgcn_fdot2(__builtin_bit_cast(h2_t, (unsigned)w[i]), h2_t{}, acc, false);
+    return acc;
+}
+
+// Infinities and NaN.  A product of 32 tokens multiplies the 0 of a key that
+// comes after a row by that key's value, and makes NaN of rows before one that
+// is not finite.  The outputs are watched (8 of some 90 vector instructions a
+// step); a workgroup that has seen one that is not finite leaves its states
+// unwritten and returns true, and goes again with CAREFUL: there a chunk with
+// such values or scores adds them row by row, each over its own keys.  (With
+// that branch in the only loop a step took 5 % longer.)
+template <class C, bool CAREFUL>
+__device__ __forceinline__ bool lin_body(const LinArgs& a, unsigned char* lds) {
     using M = Ty32<C::DT>;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int h = lane >> 5, m = lane & 31;
     const int head = blockIdx.x % a.heads, tile = blockIdx.x / a.heads, kvh = head / a.group;
     SeqTile w;
     // (a sequence without tokens counts as one empty segment: its state still passes through)
-    if (!find_tile(a.cu, nullptr, a.seqs, (int)a.rows, 0, 1, a.seg, 1, tile, &w)) return;
+    if (!find_tile(a.cu, nullptr, a.seqs, (int)a.rows, 0, 1, a.seg, 1, tile, &w)) return false;
     const bool last = w.local + 1 == w.tiles;
-    if (C::STATE && last) return;       // nobody reads what follows the last segment
+    if (C::STATE && last) return false;       // nobody reads what follows the last segment
     const int64_t row0 = w.q0 + (int64_t)w.local * a.seg;
     const int n = last ? w.nq - w.local * a.seg : a.seg;
     const float g2 = a.log_decay[head] * kLog2e;
     const int chunks = (n + C::C - 1) / C::C;
 
+    bool again = false;
+    int* flag = (int*)(lds + C::EXPS) + 8;      // an output that is not finite (behind the exponents)
+    if (!C::STATE && threadIdx.x == 0) *flag = 0;
     const int vb = attn_vbase(lane);
     const int part = wave % C::DB, col = 32 * part + m;        // this wave's value columns
     auto slot = [&](int c) __attribute__((always_inline)) {      // where the c-th chunk taken in lies
@@ -287,7 +324,7 @@ __device__ __forceinline__ void lin_body(const LinArgs& a) {
                         w0 *= in;
                         w1 *= in;
                     }
-                    lin_split<C::DT>(lin_unpack<C::DT>(v[k][d], 0) * w0, lin_unpack<C::DT>(v[k][d], 1) * w1, out);
+                    lin_split<C::DT>(attn_unpack<C::DT>(v[k][d], 0) * w0, attn_unpack<C::DT>(v[k][d], 1) * w1, out);
 #pragma unroll
                     for (int p = 0; p < C::PARTS; ++p) vp[k][p][d] = out[p];
                 }
@@ -342,11 +379,14 @@ __device__ __forceinline__ void lin_body(const LinArgs& a) {
             }
             leave(c + 1);
         }
-        if (!C::STATE && chunks > 0) barrier_lds();      // the output waves' last
+        if (!C::STATE && chunks > 0) {
+            barrier_lds();      // the output waves' last
+            again = !CAREFUL && __builtin_amdgcn_readfirstlane(*flag);
+        }
         float* to = nullptr;
         if constexpr (C::STATE) to = state_at(a.part, tile);
         else if (last && a.s1) to = state_at(a.s1, w.seq);
-        if (to)
+        if (to && !again)
 #pragma unroll
             for (int t = 0; t < C::DB; ++t)
 #pragma unroll
@@ -369,7 +409,8 @@ __device__ __forceinline__ void lin_body(const LinArgs& a) {
             return lds + C::OUT + (c & 1) * C::TILE + row * CH * 16 + ((chunk ^ (row & (CH - 1))) << 4);
         };
         auto flush = [&](int c) __attribute__((always_inline)) {
-            const int left = n - c * C::C < C::C ? n - c * C::C : C::C;
+            // (nothing has gone before the first chunk: a resource of no bytes takes no stores)
+            const int left = c < 0 ? 0 : (n - c * C::C < C::C ? n - c * C::C : C::C);
             const auto rs = attn_rsrc(a.O, row0 + (int64_t)c * C::C, a.ldo, (int64_t)head * a.hso, left, C::D);
 #pragma unroll
             for (int i = 0; i < C::C / C::DB / RW; ++i) {
@@ -377,53 +418,93 @@ __device__ __forceinline__ void lin_body(const LinArgs& a) {
                 st128(rs, row * (int)a.ldo * 2 + chunk * 16, *(const u4_t*)out_at(c, row, chunk));
             }
         };
+        float odd = 0.f;
         for (int c = 0; c < chunks; ++c) {
             barrier_lds();
-            if (c > 0) flush(c - 1);
+            flush(c - 1);
             const unsigned char* kt = slot(c);
             auto rows32 = [&](const unsigned char* p, int s) __attribute__((always_inline)) {
                 return *(const u4_t*)(p + kb[s & 1] + (s >> 1) * C::C * 64);
             };
-            f16x_t p = f16x_t{}, y = f16x_t{};
+            f16x_t p, y;
             const unsigned char* sp = lds + C::COPY + (c & 1) * C::COPY_BYTES + part * C::KS * 1024 + lane * 16;
-#pragma unroll
-            for (int s = 0; s < C::KS; ++s) {
-                const u4_t q = rows32(kt + 2 * C::TILE, s);
-                p = M::mma(rows32(kt, s), q, p);
-                y = M::mma(*(const u4_t*)(sp + s * 1024), q, y);
-            }
             float f = into;
             if constexpr (C::DT == DT_F16) f *= ((const float*)(lds + C::EXPS))[(c & 1) * 4 + part];
+            auto firsts = [&]() __attribute__((always_inline)) {
+                p = y = f16x_t{};
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                y[r] *= f;
-                p[r] *= same[r];
+                for (int s = 0; s < C::KS; ++s) {
+                    const u4_t q = rows32(kt + 2 * C::TILE, s);
+                    p = M::mma(rows32(kt, s), q, p);
+                    y = M::mma(*(const u4_t*)(sp + s * 1024), q, y);
+                }
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    y[r] *= f;
+                    p[r] *= same[r];
+                }
+            };
+            firsts();
+            // the chunk's values and scores
+            u4_t vp[4];
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                vp[s] = attn_vfrag<C::C>(kt + C::TILE, vb, part, s);
+                vp[2 + s] = attn_pack<C::DT>(p, s);
             }
 #pragma unroll
-            for (int s = 0; s < 2; ++s) y = M::mma(attn_vfrag<C::C>(kt + C::TILE, vb, part, s), attn_pack<C::DT>(p, s), y);
+            for (int s = 0; s < 2; ++s) y = M::mma(vp[s], vp[2 + s], y);
+            if (CAREFUL && __any(lin_odd<C::DT>(vp))) {
+                firsts();
+                // the scores, rounded, where this wave's outputs will lie: a lane's
+                // own row, read by the two lanes that hold it
 #pragma unroll
-            for (int q4 = 0; q4 < 4; q4 += 2) {
-                unsigned x0 = Ty<C::DT>::pack(y[4 * q4], y[4 * q4 + 1]);
-                unsigned x1 = Ty<C::DT>::pack(y[4 * q4 + 2], y[4 * q4 + 3]);
-                unsigned y0 = Ty<C::DT>::pack(y[4 * q4 + 4], y[4 * q4 + 5]);
-                unsigned y1 = Ty<C::DT>::pack(y[4 * q4 + 6], y[4 * q4 + 7]);
+                for (int x = 0; x < 4; ++x) {
+                    const u4_t w = attn_pack<C::DT>(p, x >> 1);
+                    *(u2_t*)(out_at(c, m, 4 * part + x) + 8 * h) = u2_t{w[2 * (x & 1)], w[2 * (x & 1) + 1]};
+                }
+                for (int j = 0; j <= m; ++j) {
+                    const float pj = attn_unpack<C::DT>(*(const unsigned short*)(out_at(c, m, 4 * part + (j >> 3)) + 2 * (j & 7)), 0);
+                    const unsigned char* v = kt + C::TILE + part * C::C * 64 + j * 64 + 8 * h;
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const u2_t w = *(const u2_t*)(v + 16 * x);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            y[4 * x + e] = __builtin_fmaf(pj, attn_unpack<C::DT>(w[e >> 1], e & 1), y[4 * x + e]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const u4_t w = attn_pack<C::DT>(y, x);
+                unsigned x0 = w[0], x1 = w[1], y0 = w[2], y1 = w[3];
                 swap32(x0, y0);
                 swap32(x1, y1);
-                *(u4_t*)out_at(c, m, 4 * part + q4 + h) = u4_t{x0, x1, y0, y1};
+                *(u4_t*)out_at(c, m, 4 * part + 2 * x + h) = u4_t{x0, x1, y0, y1};
+                if constexpr (!CAREFUL) odd = lin_watch<C::DT>(w, odd);
             }
         }
         if (chunks > 0) {
+            if (!CAREFUL && __any(odd != 0.f) && lane == 0) *flag = 1;
             barrier_lds();
+            again = !CAREFUL && __builtin_amdgcn_readfirstlane(*flag);
             flush(chunks - 1);
         }
     }
     // copies of nothing still write zeros: not into LDS that is another workgroup's by then
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    return again;
 }
 
 template <class C>
 __global__ __launch_bounds__(C::THREADS, 2) void lin_kernel(LinArgs a) {
-    lin_body<C>(a);
+    __shared__ __attribute__((aligned(1024))) unsigned char lds[C::LDS_BYTES];
+    if (!lin_body<C, false>(a, lds)) return;
+    if constexpr (!C::STATE) {
+        barrier_lds();
+        lin_body<C, true>(a, lds);
+    }
 }
 
 // Segments' own states -> the state before each segment, in place.  One
@@ -487,12 +568,12 @@ __global__ __launch_bounds__(256) void lin_step_kernel(LinArgs a) {
 #pragma unroll
     for (int i = 0; i < N; ++i) S[i] = *(const f4_t*)(a.s0 + at + (r0 + ROWS * i) * D + c);
     const float lam = __builtin_amdgcn_exp2f(a.log_decay[head] * kLog2e);
-    const float v[4] = {lin_unpack<DT>(vw[0], 0), lin_unpack<DT>(vw[0], 1), lin_unpack<DT>(vw[1], 0),
-                        lin_unpack<DT>(vw[1], 1)};
+    const float v[4] = {attn_unpack<DT>(vw[0], 0), attn_unpack<DT>(vw[0], 1), attn_unpack<DT>(vw[1], 0),
+                        attn_unpack<DT>(vw[1], 1)};
     float o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const float kk = lin_unpack<DT>(k[r0 + ROWS * i], 0), qq = lin_unpack<DT>(q[r0 + ROWS * i], 0);
+        const float kk = attn_unpack<DT>(k[r0 + ROWS * i], 0), qq = attn_unpack<DT>(q[r0 + ROWS * i], 0);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             S[i][e] = __builtin_fmaf(S[i][e], lam, kk * v[e]);

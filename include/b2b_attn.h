@@ -66,7 +66,10 @@ b2b_status_t b2b_attn_create(b2b_attn_t* plan, b2b_dtype_t dtype, int32_t heads,
  *     O_i = sum_j p_ij V_j,  p_ij = exp(scale Q_i.K_j) / sum_j' exp(scale Q_i.K_j')
  * over the keys that row i sees: all of its sequence, or with
  * B2B_ATTN_CAUSAL those up to its own place counted from the end (a prompt's
- * piece behind earlier keys).  A row that sees no key gets 0.
+ * piece behind earlier keys).  A row that sees no key gets 0.  Infinities and
+ * NaN reach the rows that see them and no others (a tile of 32 rows whose
+ * results are not all finite is computed again, key by key, which takes
+ * longer).
  *   seqs        sequences; cu_q and cu_k hold seqs + 1 values (device); cu_k
  *               may be cu_q
  *   rows, keys  rows that Q and O, and K and V, hold: cu values past them are
@@ -121,8 +124,10 @@ b2b_status_t b2b_linear_attn_create(b2b_linear_attn_t* plan, b2b_dtype_t dtype, 
                                     int32_t head_dim, float scale);
 
 /*
- * Packed prompts: rows cu[s] .. cu[s+1]-1 are sequence s, 64 tokens at a time.
- *   log_decay   device float32 [heads], 0 or below
+ * Packed prompts: rows cu[s] .. cu[s+1]-1 are sequence s, 32 tokens at a time.
+ * Infinities and NaN reach no earlier rows and no columns but their own (a
+ * sequence's head, or its piece, that holds some is computed twice).
+ *   log_decay   device float32 [heads], 0 or below (-inf: nothing is kept)
  *   state_in    device float32 [seqs, heads, head_dim, head_dim], the states
  *               before the sequences, or NULL (zero); 16-byte aligned
  *   state_out   the states after them, or NULL; may be state_in.  A sequence

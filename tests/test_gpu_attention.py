@@ -162,6 +162,25 @@ def test_nan_and_infinities_where_they_are_seen():
     assert not nan[:40, 1].any() and bool(nan[40:, 1].all())
 
 
+@pytest.mark.parametrize("dtype,D,n,keys", [("f16", 72, 150, 150), ("bf16", 128, 150, 150), ("bf16", 64, 40, 3000)])
+def test_values_that_are_not_finite_reach_only_rows_that_see_them(dtype, D, n, keys):
+    """Infinities and NaN among the values: rows before them in the same tile
+    stay finite, rows that see them get them (both signs: NaN)."""
+    q, k, v = _case(dtype, 4, 2, D, [n], [keys], seed=55)
+    old = keys - n                  # keys before the first row's own
+    v[old + 33, 0, 5], v[old + 37, 0, 5] = math.inf, -math.inf
+    v[old + 20, 1, 56], v[keys - 1, 1, 0], v[old, 1, 7] = -math.inf, math.nan, math.inf
+    _flush(f"attention odd values {dtype} {n} {keys}")
+    got = cf.Attention(dtype, 4, 2, D).run(q, k, v, _cu([n]), _cu([keys]))
+    torch.cuda.synchronize()
+    odd = ~torch.isfinite(v)
+    want, _, b, _ = R.attention(q, k, torch.where(odd, 0.0, v), [0, n], [0, keys], True, D ** -0.5)
+    for h in range(4):
+        for j, d in odd[:, h // 2].nonzero().tolist():
+            want[max(j - old, 0):, h, d] += v[j, h // 2, d].double().cpu()
+    R.check(got, want, b)
+
+
 def test_empty_calls():
     plan = cf.Attention("f16", 2, 2, 64)
     e = torch.empty((0, 2, 64), dtype=torch.float16, device="cuda")

@@ -175,6 +175,31 @@ def test_fp16_states_out_of_fp16_range(size):
     R.check(after, ws, bs)
 
 
+@pytest.mark.parametrize("dtype,D,n", [("f16", 64, 150), ("bf16", 128, 150), ("f16", 128, 1300), ("bf16", 64, 1300)])
+def test_values_that_are_not_finite_reach_only_later_rows(dtype, D, n):
+    """A value that is not finite spoils its column from its token on, a key
+    all of them; the rows before it in the same chunk, and other columns, stay."""
+    H, Hkv = 2, 2
+    _flush(f"linear odd values {dtype} {D} {n}")
+    q, k, v, g, s0 = _case(dtype, H, Hkv, D, [n], seed=61)
+    at = n - 50
+    v[at, 0, 5], v[at + 3, 0, 40], v[at + 20, 0, D - 1] = math.inf, math.nan, -math.inf
+    k[at + 21, 1, 9] = math.nan
+    got, after = cf.LinearAttention(dtype, H, Hkv, D).run(q, k, v, g, _cu([n]), state=s0)
+    torch.cuda.synchronize()
+    odd = torch.zeros((n, H, D), dtype=torch.bool)
+    odd[at:, 0, 5] = odd[at + 3:, 0, 40] = odd[at + 20:, 0, D - 1] = True
+    odd[at + 21:, 1] = True
+    clean = [torch.where(torch.isfinite(x), x, 0.0) for x in (k, v)]
+    want, b, ws, bs = recurrence(q, clean[0], clean[1], g, [0, n], s0, D ** -0.5)
+    got, after, gone = got.cpu(), after.cpu(), torch.zeros((1, H, D, D), dtype=torch.bool)
+    assert not torch.isfinite(got[odd]).any()
+    R.check(torch.where(odd, 0.0, got), torch.where(odd, 0.0, want), b, "O")
+    gone[:, 0, :, [5, 40, D - 1]] = gone[:, 1, 9] = True
+    assert not torch.isfinite(after[gone]).any()
+    R.check(torch.where(gone, 0.0, after), torch.where(gone, 0.0, ws), bs, "state")
+
+
 def test_layouts_and_rows_outside():
     H, Hkv, D, n = 4, 2, 64, 130
     fused = _randn(51, (n, (H + 2 * Hkv) * D), torch.float16)

@@ -153,7 +153,7 @@ __device__ __forceinline__ bool find_tile_by_size(const int32_t* cu_q, const int
     }
     const int tiles = (int)(((unsigned)n * (unsigned)group + (unsigned)bm - 1) / (unsigned)bm);
     // 1 .. 2^24: the level of the sequence's last (causal) or every tile
-    const int64_t seen = (int64_t)(causal ? nk : nk / 16) * group / bm + 1;
+    const int64_t seen = causal ? (int64_t)nk * group / bm + 1 : nk / 32 + 1;
     const int top = tiles ? (seen > (1 << 24) ? 1 << 24 : (int)seen) : 0;
     auto above = [&](int level) __attribute__((always_inline)) {      // this lane's tiles at `level` and above
         const int c = top - level + 1;

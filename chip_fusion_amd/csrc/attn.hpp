@@ -36,6 +36,22 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLowest = -3.402823466e38f;
 constexpr float kMaxLag = 8.f;     // how far (log2) a running maximum may lag behind
 
+// Division of n < 2^31 by a number that the call fixes: with l = ceil(log2 d)
+// and m = floor(2^(31+l) / d) + 1, which 32 bits hold, n / d is n m / 2^(31+l)
+// rounded down.  (A prologue has half a dozen of them, 20 to 140 instructions
+// each as the compiler writes them.)
+struct FastDiv {
+    uint32_t m;
+    int32_t l, d;
+    void set(int32_t by) {
+        d = by;
+        l = 0;
+        while (((int64_t)1 << l) < d) ++l;
+        m = (uint32_t)(((uint64_t)1 << (31 + l)) / (uint64_t)d + 1);
+    }
+    __device__ __forceinline__ int operator()(int n) const { return (int)(__umulhi(2u * (unsigned)n, m) >> l); }
+};
+
 // One operand: rows of heads, strides in elements, head_dim contiguous.
 struct AttnRows {
     const void* p;
@@ -54,10 +70,17 @@ struct AttnArgs {
     float* lse;             // [rows, heads], natural logarithm, or null
     float* part;            // partial results [slots, rows, heads, D], and their
     float* part_lse;        // [slots, rows, heads] log2-sum-exp2
-    int32_t seqs, heads, kv_heads, group, dim, causal;
-    int32_t splits, slot0;  // parts of the keys; the first one's slot
+    int32_t seqs, heads, dim, causal;
+    int32_t slot0;          // the first part's slot
+    FastDiv kv_heads, group, splits;    // splits: parts of the keys
     int32_t tiles;          // row tiles (the grid's bound)
     float sc;               // scale * log2 e
+    // where part i of n key tiles begins (n <= 2^25, at most 64 parts; n splits as
+    // whole * parts + rest, so that nothing leaves 31 bits)
+    __device__ __forceinline__ int part_at(int n, int i) const {
+        const int whole = splits(n), rest = n - whole * splits.d;
+        return whole * i + splits(rest * i);
+    }
 };
 
 // ---------------------------------------------------------------------------
@@ -153,26 +176,28 @@ __device__ __forceinline__ bool find_tile_by_size(const int32_t* cu_q, const int
     }
     const int tiles = (int)(((unsigned)n * (unsigned)group + (unsigned)bm - 1) / (unsigned)bm);
     // 1 .. 2^24: the level of the sequence's last (causal) or every tile
-    const int64_t seen = causal ? (int64_t)nk * group / bm + 1 : nk / 32 + 1;
-    const int top = tiles ? (seen > (1 << 24) ? 1 << 24 : (int)seen) : 0;
+    int64_t seen = nk / 32 + 1;
+    if (causal) {
+        seen = (int64_t)nk * group / bm + 1;
+        seen = seen < tiles ? tiles : seen;
+    }
+    const int top = tiles ? (seen > (1 << 24) ? 1 << 24 : (int)seen) : 0, whole = causal ? tiles : 1;
     auto above = [&](int level) __attribute__((always_inline)) {      // this lane's tiles at `level` and above
         const int c = top - level + 1;
-        if (!causal) return c > 0 ? tiles : 0;
-        return c < 0 ? 0 : (c > tiles || level <= 1 ? tiles : c);
+        return c <= 0 ? 0 : (c >= whole ? tiles : c);
     };
-    if (tile >= __builtin_amdgcn_readlane(lanes_sum(tiles), 63)) return false;
     int level = 0;
     for (int bit = 1 << (31 - __clz(__builtin_amdgcn_readlane(lanes_max(top), 63) | 1)); bit; bit >>= 1)
         if (__builtin_amdgcn_readlane(lanes_sum(above(level | bit)), 63) > tile) level |= bit;
+    if (!level) return false;       // not even all tiles are that many
     // tiles of this lane on that level, and the place among them
-    const int mine = above(level) - above(level + 1), upto = lanes_sum(mine);
-    const int place = tile - __builtin_amdgcn_readlane(lanes_sum(above(level + 1)), 63);
+    const int higher = above(level + 1), mine = above(level) - higher, upto = lanes_sum(mine);
+    const int place = tile - __builtin_amdgcn_readlane(lanes_sum(higher), 63);
     const int at = __ffsll(__ballot(upto > place)) - 1;
     out->seq = at;
     out->tiles = __builtin_amdgcn_readlane(tiles, at);
     // counted from the sequence's last tile
-    const int last = __builtin_amdgcn_readlane(causal ? above(level + 1) : 0, at);
-    out->local = last + place - (__builtin_amdgcn_readlane(upto, at) - __builtin_amdgcn_readlane(mine, at));
+    out->local = __builtin_amdgcn_readlane(higher - upto + mine, at) + place;
     out->q0 = __builtin_amdgcn_readlane(q0, at);
     out->nq = __builtin_amdgcn_readlane(n, at);
     out->k0 = __builtin_amdgcn_readlane(k0, at);
@@ -208,13 +233,18 @@ template <int KS>
 __device__ __forceinline__ void attn_load_q(u4_t (&q)[KS], const AttnArgs& a, int64_t q0, int kvh, int rr, int rows,
                                             int lane) {
     const int h = lane >> 5;
-    const int pos = rr / a.group, g = rr - pos * a.group;
-    const char* p = (const char*)a.Q.p + ((q0 + pos) * a.Q.ld + (int64_t)(kvh * a.group + g) * a.Q.hs) * 2;
+    const int pos = a.group(rr), g = rr - pos * a.group.d;
+    const char* p = (const char*)a.Q.p + ((q0 + pos) * a.Q.ld + (int64_t)(kvh * a.group.d + g) * a.Q.hs + 8 * h) * 2;
 #pragma unroll
-    for (int s = 0; s < KS; ++s) {
-        const int c = 16 * s + 8 * h;
-        q[s] = u4_t{0, 0, 0, 0};
-        if (rr < rows && c < a.dim) q[s] = *(const u4_t*)(p + 2 * c);
+    for (int s = 0; s < KS; ++s) q[s] = u4_t{0, 0, 0, 0};
+    if (rr >= rows) return;
+    if (a.dim == 16 * KS) {
+#pragma unroll
+        for (int s = 0; s < KS; ++s) q[s] = *(const u4_t*)(p + 32 * s);
+    } else {
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+            if (16 * s + 8 * h < a.dim) q[s] = *(const u4_t*)(p + 32 * s);
     }
 }
 
@@ -341,41 +371,49 @@ __device__ __forceinline__ void attn_store(const AttnArgs& a, const f16x_t (&o)[
     const float l = st.l + other_half(st.l);
     // l: a NaN (from a NaN among the row's scores) goes through to the output
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    const int pos = rr / a.group, head = kvh * a.group + (rr - pos * a.group);
+    const int pos = a.group(rr), head = kvh * a.group.d + (rr - pos * a.group.d);
     const int64_t row = q0 + pos;
     const bool live = rr < rows;
     const float lse2 = l == 0.f ? -__builtin_inff() : st.m + __builtin_amdgcn_logf(l);
-    if constexpr (PART) {
-        const int64_t at = ((int64_t)slot * a.rows + row) * a.heads + head;
-        if (live) {
+    // `FULL`: no columns past D
+    auto columns = [&](auto FULL) __attribute__((always_inline)) {
+        if constexpr (PART) {
+            const int64_t at = ((int64_t)slot * a.rows + row) * a.heads + head;
+            if (!live) return;
             if (h == 0) a.part_lse[at] = lse2;
 #pragma unroll
             for (int t = 0; t < DB; ++t)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const int c = 32 * t + 8 * q + 4 * h;
-                    if (c < a.dim)
+                    if (FULL.value || c < a.dim)
                         *(f4_t*)(a.part + at * a.dim + c) = f4_t{o[t][4 * q] * inv, o[t][4 * q + 1] * inv,
                                                                  o[t][4 * q + 2] * inv, o[t][4 * q + 3] * inv};
                 }
+        } else {
+            if (live && h == 0 && a.lse) a.lse[row * a.heads + head] = lse2 * kLn2;
+            char* p = (char*)a.O + (row * a.ldo + (int64_t)head * a.hso) * 2;
+            u4_t w[2 * DB];
+#pragma unroll
+            for (int t = 0; t < DB; ++t)
+#pragma unroll
+                for (int q = 0; q < 4; q += 2) {
+                    unsigned x0 = Ty<DT>::pack(o[t][4 * q] * inv, o[t][4 * q + 1] * inv);
+                    unsigned x1 = Ty<DT>::pack(o[t][4 * q + 2] * inv, o[t][4 * q + 3] * inv);
+                    unsigned y0 = Ty<DT>::pack(o[t][4 * q + 4] * inv, o[t][4 * q + 5] * inv);
+                    unsigned y1 = Ty<DT>::pack(o[t][4 * q + 6] * inv, o[t][4 * q + 7] * inv);
+                    swap32(x0, y0);
+                    swap32(x1, y1);
+                    w[2 * t + q / 2] = u4_t{x0, x1, y0, y1};
+                }
+            if (!live) return;
+#pragma unroll
+            for (int i = 0; i < 2 * DB; ++i)
+                if (FULL.value || 16 * i + 8 * h < a.dim) *(u4_t*)(p + 2 * (16 * i + 8 * h)) = w[i];
         }
-    } else {
-        if (live && h == 0 && a.lse) a.lse[row * a.heads + head] = lse2 * kLn2;
-        char* p = (char*)a.O + (row * a.ldo + (int64_t)head * a.hso) * 2;
-#pragma unroll
-        for (int t = 0; t < DB; ++t)
-#pragma unroll
-            for (int q = 0; q < 4; q += 2) {
-                unsigned x0 = Ty<DT>::pack(o[t][4 * q] * inv, o[t][4 * q + 1] * inv);
-                unsigned x1 = Ty<DT>::pack(o[t][4 * q + 2] * inv, o[t][4 * q + 3] * inv);
-                unsigned y0 = Ty<DT>::pack(o[t][4 * q + 4] * inv, o[t][4 * q + 5] * inv);
-                unsigned y1 = Ty<DT>::pack(o[t][4 * q + 6] * inv, o[t][4 * q + 7] * inv);
-                swap32(x0, y0);
-                swap32(x1, y1);
-                const int c = 32 * t + 8 * (q + h);
-                if (live && c < a.dim) *(u4_t*)(p + 2 * c) = u4_t{x0, x1, y0, y1};
-            }
-    }
+    };
+    if (a.dim == 32 * DB) columns(std::true_type{});
+    else columns(std::false_type{});
 }
 
 // Infinities and NaN among the values, causal.  A tile of the second product
@@ -403,7 +441,7 @@ __device__ __forceinline__ void attn_careful(const AttnArgs& a, const RowState& 
     const char* K = (const char*)a.K.p + (k0 * a.K.ld + kvh * a.K.hs) * 2;
     const char* V = (const char*)a.V.p + (k0 * a.V.ld + kvh * a.V.hs) * 2;
     for (int r = 0; r < 32 && wrow + r < rows; ++r) {
-        const int pos = (wrow + r) / a.group, head = kvh * a.group + (wrow + r - pos * a.group);
+        const int pos = a.group(wrow + r), head = kvh * a.group.d + (wrow + r - pos * a.group.d);
         const int end = pos + 1 + shift < to ? pos + 1 + shift : to;
         const float m = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, st.m), r));
         const float l = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, l_all), r));
@@ -460,14 +498,14 @@ template <class C>
 __device__ __forceinline__ void attn_tile_body(const AttnArgs& a, unsigned char* lds, int block) {
     using M = Ty32<C::DT>;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int kvh = block % a.kv_heads, rest = block / a.kv_heads;
-    const int split = rest % a.splits;
+    const int rest = a.kv_heads(block), kvh = block - rest * a.kv_heads.d;
+    const int tile = C::PART ? a.splits(rest) : rest, split = rest - tile * a.splits.d;
     SeqTile w;
     if (a.cu_q) {
-        const bool found = a.seqs <= 64 ? find_tile_by_size(a.cu_q, a.cu_k, a.seqs, (int)a.rows, (int)a.keys, a.group, C::BM,
-                                                            a.causal, rest / a.splits, &w)
-                                        : find_tile(a.cu_q, a.cu_k, a.seqs, (int)a.rows, (int)a.keys, a.group, C::BM, 0,
-                                                    rest / a.splits, &w);
+        const bool found = a.seqs <= 64 ? find_tile_by_size(a.cu_q, a.cu_k, a.seqs, (int)a.rows, (int)a.keys, a.group.d, C::BM,
+                                                            a.causal, tile, &w)
+                                        : find_tile(a.cu_q, a.cu_k, a.seqs, (int)a.rows, (int)a.keys, a.group.d, C::BM, 0,
+                                                    tile, &w);
         if (!found) return;
     } else {
         // all rows are one sequence's
@@ -475,23 +513,23 @@ __device__ __forceinline__ void attn_tile_body(const AttnArgs& a, unsigned char*
         w.nq = (int)a.rows;
         w.nk = (int)a.keys;
         w.tiles = a.tiles;
-        w.local = rest / a.splits;
+        w.local = tile;
     }
     const int64_t k0 = w.k0;
     const int nk = w.nk;
     // the last tile of a causal sequence sees the most keys: it starts first
     const int row0 = (a.causal ? w.tiles - 1 - w.local : w.local) * C::BM;
-    const int rows = w.nq * a.group, shift = nk - w.nq;
+    const int rows = w.nq * a.group.d, shift = nk - w.nq;
     auto sees = [&](int rr) -> int {     // keys that row rr sees
         if (rr >= rows) return 0;
         if (!a.causal) return nk;
-        const int n = rr / a.group + 1 + shift;
+        const int n = a.group(rr) + 1 + shift;
         return n < 0 ? 0 : n;
     };
     const int last = (row0 + C::BM < rows ? row0 + C::BM : rows) - 1;
     const int end = sees(last);                               // keys the workgroup needs
     const int nt = (end + C::BN - 1) / C::BN;
-    const int t0 = (int)((int64_t)nt * split / a.splits), t1 = (int)((int64_t)nt * (split + 1) / a.splits);
+    const int t0 = C::PART ? a.part_at(nt, split) : 0, t1 = C::PART ? a.part_at(nt, split + 1) : nt;
     const int wrow = row0 + 32 * wave;                        // this wave's first row
     const int rr = wrow + (lane & 31);
     const int lim = sees(rr) - 4 * (lane >> 5);
@@ -578,17 +616,15 @@ template <class C>
 __device__ __forceinline__ void attn_rows_body(const AttnArgs& a, unsigned char* lds, int block) {
     using M = Ty32<C::DT>;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int kvh = block % a.kv_heads;
-    int rest = block / a.kv_heads;
-    const int split = rest % a.splits;
-    rest /= a.splits;
-    const int tile = rest % a.tiles, seq = rest / a.tiles;    // tiles: row tiles of a sequence
-    const int rows = a.group, rr = 32 * tile + (lane & 31);
+    const int rest = a.kv_heads(block), kvh = block - rest * a.kv_heads.d;
+    const int row_tile = a.splits(rest), split = rest - row_tile * a.splits.d;
+    const int seq = row_tile / a.tiles, tile = row_tile - seq * a.tiles;    // tiles: row tiles of a sequence
+    const int rows = a.group.d, rr = 32 * tile + (lane & 31);
     int nk = a.lens[seq];
     nk = nk < 0 ? 0 : (nk > (int)a.keys ? (int)a.keys : nk);
     nk = __builtin_amdgcn_readfirstlane(nk);
     const int nt = (nk + C::BN - 1) / C::BN;
-    const int t0 = (int)((int64_t)nt * split / a.splits), t1 = (int)((int64_t)nt * (split + 1) / a.splits);
+    const int t0 = a.part_at(nt, split), t1 = a.part_at(nt, split + 1);
     u4_t q[C::KS];
     f16x_t o[C::DB];
     RowState st;
@@ -642,7 +678,7 @@ __device__ __forceinline__ void attn_rows_body(const AttnArgs& a, unsigned char*
     for (int v = 0; v < C::WAVES; ++v)
         sum += ms[(C::WAVES + v) * 32 + (lane & 31)] * __builtin_amdgcn_exp2f(ms[v * 32 + (lane & 31)] - m);
     const float f = __builtin_amdgcn_exp2f(st.m - m) * (sum == 0.f ? 0.f : 1.f / sum);
-    const int64_t at0 = ((int64_t)(a.slot0 + split) * a.rows + seq) * a.heads + kvh * a.group;
+    const int64_t at0 = ((int64_t)(a.slot0 + split) * a.rows + seq) * a.heads + kvh * a.group.d;
     if (wave == 0 && lane < 32 && rr < rows)
         a.part_lse[at0 + rr] = sum == 0.f ? -__builtin_inff() : m + __builtin_amdgcn_logf(sum);
     const int live = rows - 32 * tile < 32 ? rows - 32 * tile : 32;

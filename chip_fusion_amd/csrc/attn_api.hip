@@ -87,7 +87,7 @@ size_t part_bytes(const b2b_attn_plan* p, int64_t slots, int64_t rows) {
 }
 
 bool sizes_ok(const b2b_attn_plan* p, int64_t seqs, int64_t rows, int64_t keys) {
-    return seqs >= 0 && rows >= 0 && keys >= 0 && rows * (int64_t)p->heads <= INT32_MAX && rows <= INT32_MAX &&
+    return seqs >= 0 && rows >= 0 && keys >= 0 && rows <= INT32_MAX && rows * (int64_t)p->heads <= INT32_MAX - 1024 &&
            keys <= INT32_MAX / 2 && seqs <= INT32_MAX / 2;
 }
 
@@ -98,11 +98,11 @@ const b2b::AttnLaunch& launchers(const b2b_attn_plan* p) {
 b2bk::AttnArgs base_args(const b2b_attn_plan* p) {
     b2bk::AttnArgs a = {};
     a.heads = p->heads;
-    a.kv_heads = p->kv_heads;
-    a.group = p->heads / p->kv_heads;
+    a.kv_heads.set(p->kv_heads);
+    a.group.set(p->heads / p->kv_heads);
     a.dim = p->dim;
     a.sc = p->scale * b2bk::kLog2e;
-    a.splits = 1;
+    a.splits.set(1);
     return a;
 }
 
@@ -172,7 +172,7 @@ b2b_status_t b2b_attn_run(b2b_attn_t p, int32_t seqs, int64_t rows, int64_t keys
     a.lse = lse;
     a.seqs = seqs;
     a.causal = p->causal;
-    a.splits = s.splits;
+    a.splits.set(s.splits);
     a.tiles = (int32_t)s.tiles;
     a.part = (float*)workspace;
     a.part_lse = a.part + (size_t)s.splits * rows * p->heads * dim;
@@ -226,7 +226,7 @@ b2b_status_t b2b_prefix_attn_run(b2b_attn_t p, int32_t batch, int64_t prefix, in
     const int64_t row_tiles = ceil_div(p->heads / p->kv_heads, 32);
     const int64_t grid_o = (int64_t)batch * row_tiles * p->kv_heads * own_parts;
     if (grid_p + grid_o > INT32_MAX) return B2B_ERROR_INVALID_VALUE;
-    a.splits = std::max(s.splits, 1);
+    a.splits.set(std::max(s.splits, 1));
     a.tiles = (int32_t)s.tiles;
     a.seqs = 1;
     b2bk::AttnArgs o = a;
@@ -243,7 +243,7 @@ b2b_status_t b2b_prefix_attn_run(b2b_attn_t p, int32_t batch, int64_t prefix, in
         o.v_stride = v_stride;
         o.keys = own;
         o.seqs = batch;
-        o.splits = own_parts;
+        o.splits.set(own_parts);
         o.slot0 = s.splits;
         o.tiles = (int32_t)row_tiles;
     }

@@ -25,12 +25,19 @@ struct b2b_linear_attn_plan {
 namespace {
 
 constexpr int64_t kMaxStride = (int64_t)1 << 23;    // 64 rows' offsets stay below 2^30 bytes
+constexpr int64_t kMaxFar = (int64_t)1 << 40;       // from head to head, request to request: past any memory
 
 // Rows of heads that the kernels can address: n rows, 16-byte pieces.
 bool rows_ok(const b2b_rows_t& r, int64_t n, int dim) {
     if (!r.data || (uintptr_t)r.data % 16) return false;
-    if (r.row_stride % 8 || r.head_stride % 8 || r.head_stride < 0) return false;
+    if (r.row_stride % 8 || r.head_stride % 8 || r.head_stride < 0 || r.head_stride > kMaxFar) return false;
     return n <= 1 || (r.row_stride >= dim && r.row_stride <= kMaxStride);
+}
+// Rows that are written: no two of their (row, head) share an element.
+bool out_ok(const b2b_rows_t& r, int64_t n, int heads, int dim) {
+    if (!rows_ok(r, n, dim) || (heads > 1 && r.head_stride < dim)) return false;
+    return n <= 1 || heads <= 1 || r.row_stride >= (heads - 1) * r.head_stride + dim ||
+           r.head_stride >= (n - 1) * r.row_stride + dim;
 }
 b2bk::AttnRows dev(const b2b_rows_t& r, int dim) {
     // a single row's stride is never stepped by; the kernels still size resources with it
@@ -152,7 +159,7 @@ b2b_status_t b2b_attn_run(b2b_attn_t p, int32_t seqs, int64_t rows, int64_t keys
     if (!p || !sizes_ok(p, seqs, rows, keys)) return B2B_ERROR_INVALID_VALUE;
     if (!seqs || !rows) return B2B_SUCCESS;
     const int dim = p->dim;
-    if (!rows_ok(Q, rows, dim) || !rows_ok(O, rows, dim) || !cu_q || !cu_k) return B2B_ERROR_INVALID_VALUE;
+    if (!rows_ok(Q, rows, dim) || !out_ok(O, rows, p->heads, dim) || !cu_q || !cu_k) return B2B_ERROR_INVALID_VALUE;
     if (keys && (!rows_ok(K, keys, dim) || !rows_ok(V, keys, dim))) return B2B_ERROR_INVALID_VALUE;
     if (O.data == Q.data || O.data == K.data || O.data == V.data || (uintptr_t)lse % 4) return B2B_ERROR_INVALID_VALUE;
     const Split s = plan_tiles(p, seqs, rows, keys);
@@ -204,11 +211,11 @@ b2b_status_t b2b_prefix_attn_run(b2b_attn_t p, int32_t batch, int64_t prefix, in
     if (st != B2B_SUCCESS) return st;
     if (!batch) return B2B_SUCCESS;
     const int dim = p->dim;
-    if (!rows_ok(Q, batch, dim) || !rows_ok(O, batch, dim) || O.data == Q.data) return B2B_ERROR_INVALID_VALUE;
+    if (!rows_ok(Q, batch, dim) || !out_ok(O, batch, p->heads, dim) || O.data == Q.data) return B2B_ERROR_INVALID_VALUE;
     if (prefix && (!rows_ok(Kp, prefix, dim) || !rows_ok(Vp, prefix, dim) || O.data == Kp.data || O.data == Vp.data))
         return B2B_ERROR_INVALID_VALUE;
     if (own && (!rows_ok(K, own, dim) || !rows_ok(V, own, dim) || !lens || k_stride < 0 || v_stride < 0 ||
-                k_stride % 8 || v_stride % 8 || O.data == K.data || O.data == V.data))
+                k_stride > kMaxFar || v_stride > kMaxFar || k_stride % 8 || v_stride % 8 || O.data == K.data || O.data == V.data))
         return B2B_ERROR_INVALID_VALUE;
     if (need && (!workspace || (uintptr_t)workspace % 16 || workspace_bytes < need)) return B2B_ERROR_INVALID_VALUE;
     const b2b::AttnLaunch& L = launchers(p);
@@ -320,8 +327,8 @@ b2bk::LinArgs lin_args(const b2b_linear_attn_plan* p, const b2b_rows_t& Q, const
 }
 bool lin_operands_ok(const b2b_linear_attn_plan* p, int64_t rows, const b2b_rows_t& Q, const b2b_rows_t& K,
                      const b2b_rows_t& V, const b2b_rows_t& O) {
-    return rows_ok(Q, rows, p->dim) && rows_ok(K, rows, p->dim) && rows_ok(V, rows, p->dim) && rows_ok(O, rows, p->dim) &&
-           O.data != Q.data && O.data != K.data && O.data != V.data;
+    return rows_ok(Q, rows, p->dim) && rows_ok(K, rows, p->dim) && rows_ok(V, rows, p->dim) &&
+           out_ok(O, rows, p->heads, p->dim) && O.data != Q.data && O.data != K.data && O.data != V.data;
 }
 
 }  // namespace
@@ -357,6 +364,7 @@ b2b_status_t b2b_linear_attn_run(b2b_linear_attn_t p, int32_t seqs, int64_t rows
     a.seg = (int32_t)seg;
     const b2b::LinLaunch& L = p->dtype == B2B_DTYPE_F16 ? b2b::lin_f16() : b2b::lin_bf16();
     const int64_t segs = split ? rows / seg + seqs : seqs;
+    a.slots = (int32_t)segs;
     if (split) {
         if (L.run(a, p->dim, true, segs, stream) != hipSuccess) return B2B_ERROR_HIP;
         if (L.scan(a, p->dim, stream) != hipSuccess) return B2B_ERROR_HIP;

@@ -45,7 +45,7 @@ struct LinArgs {
     float* part;                // [tiles, heads, D, D]: a segment's own state, then the state before it
     int64_t rows;
     int32_t seqs, heads, kv_heads, group;
-    int32_t seg;                // tokens of a segment
+    int32_t seg, slots;         // tokens of a segment; the segments that `part` holds
     float scale;
 };
 
@@ -527,6 +527,9 @@ __global__ __launch_bounds__(256) void lin_scan_kernel(LinArgs a) {
         const int sum = __builtin_amdgcn_readlane(lanes_sum(s < seq ? mine : 0), 63);
         first += sum;
     }
+    // (starts that go back and forth would ask for more segments than there is room for)
+    if (first >= a.slots) return;
+    tiles = tiles < a.slots - first ? tiles : a.slots - first;
     if (tiles < 2) return;
     const float keep = lin_pow(a.log_decay[head] * kLog2e, a.seg);
     const int64_t step = (int64_t)a.heads * D * D;

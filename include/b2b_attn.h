@@ -79,7 +79,8 @@ b2b_status_t b2b_attn_create(b2b_attn_t* plan, b2b_dtype_t dtype, int32_t heads,
  *   workspace   device, 16-byte aligned, at least b2b_attn_workspace bytes
  *               (NULL where that is 0)
  * INVALID_VALUE for bad sizes, strides, alignment or pointers, O at an
- * input's address, or a workspace too small.
+ * input's address or with rows or heads that overlap, or a workspace too small.
+ * O must not overlap the inputs.
  */
 b2b_status_t b2b_attn_workspace(b2b_attn_t plan, int32_t seqs, int64_t rows, int64_t keys, size_t* bytes);
 b2b_status_t b2b_attn_run(b2b_attn_t plan, int32_t seqs, int64_t rows, int64_t keys, b2b_rows_t Q, b2b_rows_t K,

@@ -54,6 +54,9 @@ def _rows(p=P, ld=256, hs=64):
     (dict(Q=_rows(ld=56)), INVALID), (dict(K=_rows(hs=4)), INVALID), (dict(K=_rows(hs=-64)), INVALID),
     (dict(V=_rows(ld=(1 << 23) + 8)), INVALID), (dict(V=_rows(None)), INVALID),
     (dict(O=_rows()), INVALID),                             # O at Q's address
+    (dict(O=_rows(P * 4, hs=0)), INVALID), (dict(O=_rows(P * 4, hs=56)), INVALID),      # heads of O overlap
+    (dict(O=_rows(P * 4, ld=192)), INVALID), (dict(O=_rows(P * 4, ld=64, hs=192)), INVALID),
+    (dict(Q=_rows(hs=1 << 41)), INVALID),
     (dict(cu_q=None), INVALID), (dict(cu_k=None), INVALID), (dict(lse=P + 2), INVALID),
     (dict(ws=None), INVALID), (dict(ws=P + 8), INVALID), (dict(ws_bytes=15), INVALID),
     (dict(plan=None), INVALID),
@@ -76,6 +79,7 @@ def test_run_refuses(kw, status):
     (dict(batch=-1), INVALID), (dict(prefix=-1), INVALID), (dict(own=-1), INVALID), (dict(own=1 << 31), INVALID),
     (dict(batch=0), OK), (dict(Q=_rows(None)), INVALID), (dict(Kp=_rows(None)), INVALID), (dict(V=_rows(ld=8)), INVALID),
     (dict(ks=12), INVALID), (dict(vs=-8), INVALID), (dict(lens=None), INVALID), (dict(O=_rows()), INVALID),
+    (dict(O=_rows(P * 6, hs=0)), INVALID), (dict(ks=1 << 41), INVALID),
     (dict(ws=None), INVALID), (dict(ws_bytes=16), INVALID), (dict(causal=True), INVALID),
 ])
 def test_prefix_run_refuses(kw, status):
@@ -157,6 +161,7 @@ def test_linear_create(kw, status):
 @pytest.mark.parametrize("kw,status", [
     (dict(seqs=-1), INVALID), (dict(rows=-1), INVALID), (dict(rows=1 << 30), INVALID), (dict(seqs=0), OK),
     (dict(Q=_rows(None)), INVALID), (dict(K=_rows(ld=100)), INVALID), (dict(V=_rows(P + 4)), INVALID), (dict(O=_rows()), INVALID),
+    (dict(O=_rows(P * 4, ld=128)), INVALID),
     (dict(g=None), INVALID), (dict(cu=None), INVALID), (dict(s0=P + 4), INVALID), (dict(s1=P + 8), INVALID),
     (dict(ws=None), INVALID), (dict(ws_bytes=64), INVALID), (dict(ws=P + 8), INVALID), (dict(plan=None), INVALID),
 ])

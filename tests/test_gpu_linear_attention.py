@@ -11,6 +11,7 @@ state, every term of it is counted with u and 2^-24 for each of its sums (D
 products of a score, 64 keys, one multiplication a chunk) and 2^-21 for its
 powers of lambda.  States: the same sum without q, every term in float32 with
 2^-23 a chunk for its factor."""
+import ctypes
 import math
 
 import pytest
@@ -83,6 +84,7 @@ CASES = [
     ("f16", 2, 2, 64, [1300], True),             # cut into segments
     ("bf16", 3, 1, 128, [1200, 1, 700, 512], True),
     ("f16", 1, 1, 128, [1025], False),
+    ("bf16", 1, 1, 64, [3, 0] * 35 + [1300, 9, 700], True),      # more sequences than a wave scans at once, some cut
 ]
 
 
@@ -219,6 +221,27 @@ def test_layouts_and_rows_outside():
     o1, s1 = plan.step(q[:3], k[:3], v[:3], g, s0)
     o2, s2 = plan.step(*(hm(x[:3]) for x in (q, k, v)), g, s0)
     assert torch.equal(o1, o2) and torch.equal(s1, s2)
+
+
+def test_starts_that_go_back_stay_inside():
+    """Starts that are out of order ask for more segments than the workspace
+    holds: nothing outside it or the tensors is written."""
+    H, D, n = 2, 64, 4000
+    _flush("linear starts out of order")
+    q, k, v, g, _ = _case("f16", H, H, D, [n], seed=71, state=False)
+    cu = torch.tensor([0, n, 0, n, -5, 2 * n, 7], dtype=torch.int32, device="cuda")
+    seqs = cu.numel() - 1
+    plan, L, need = cf.LinearAttention("f16", H, H, D), cf.lib(), ctypes.c_size_t()
+    assert L.b2b_linear_attn_workspace(plan._h, seqs, n, ctypes.byref(need)) == 0 and need.value > 0
+    guard = 1 << 20
+    ws = torch.full((need.value // 4 + 12 * guard,), 7.0, device="cuda")
+    O = torch.full((n + 64, H, D), 7.0, dtype=torch.float16, device="cuda")
+    after = torch.empty((seqs, H, D, D), device="cuda")
+    rows = lambda t: cf.Rows(t.data_ptr(), t.stride(0), t.stride(1))
+    assert L.b2b_linear_attn_run(plan._h, seqs, n, rows(q), rows(k), rows(v), rows(O), g.data_ptr(), cu.data_ptr(), None,
+                                 after.data_ptr(), ws.data_ptr(), need.value, torch.cuda.current_stream().cuda_stream) == 0
+    torch.cuda.synchronize()
+    assert bool((ws[need.value // 4:] == 7).all()) and bool((O[n:] == 7).all())
 
 
 def test_empty_calls():

@@ -83,6 +83,23 @@ def test_many_sequences(seqs):
     R.check(got, want, b)
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("seqs", [40, 64])
+def test_sequences_of_all_sizes(causal, seqs):
+    """Every tile of every sequence is taken, in whatever order they start: rows
+    and keys of very different numbers, more rows than keys among them."""
+    lq = [(37 * i * i) % 241 if i % 5 else 0 for i in range(seqs)]
+    lk = [(53 * i) % 401 if i % 7 else 0 for i in range(seqs)]
+    _flush(f"attention {seqs} sequences of all sizes, causal {causal}")
+    q, k, v = _case("f16", 6, 2, 40, lq, lk, seed=13)
+    O = torch.full_like(q, math.nan)
+    got, lse = cf.Attention("f16", 6, 2, 40, causal=causal).run(q, k, v, _cu(lq), _cu(lk), O=O, lse=True)
+    torch.cuda.synchronize()
+    want, want_lse, b, bl = R.attention(q, k, v, R.starts(lq), R.starts(lk), causal, 40 ** -0.5)
+    R.check(got, want, b, "O")
+    R.check(lse, want_lse, bl, "LSE")
+
+
 @pytest.mark.parametrize("scale", [None, 0.02, 3.0])
 def test_scale_and_large_scores(scale):
     """Scores from nearly equal to one key taking all of the weight."""
@@ -128,6 +145,32 @@ def test_layouts():
     assert torch.equal(O, want)
     ref, _, b, _ = R.attention(q, k, v, [0, 100, 140], [0, 100, 140], True, 0.125)
     R.check(want, ref, b)
+
+
+def test_offsets_past_32_bits():
+    """Keys and values whose rows, and whose requests, lie gigabytes apart."""
+    H, D, n, far = 2, 64, 2200, 1 << 20
+    T = torch.bfloat16
+    q, k, v = _case("bf16", H, 1, D, [5], [n], seed=17)
+    room = torch.zeros((n * far,), dtype=T, device="cuda")           # 4.6 GB; K and V in turn along its rows
+    K, V = room.as_strided((n, 1, D), (far, D, 1)), room.as_strided((n, 1, D), (far, D, 1), far // 2)
+    K.copy_(k), V.copy_(v)
+    _flush("attention far rows")
+    got = cf.Attention("bf16", H, 1, D).run(q, K, V, _cu([5]), _cu([n]))
+    torch.cuda.synchronize()
+    want, _, b, _ = R.attention(q, k, v, [0, 5], [0, n], True, D ** -0.5)
+    R.check(got, want, b)
+    _flush("prefix far requests")
+    B, S = 11, 200                                                    # request i from row 200 i on
+    K4, V4 = K[:B * S].as_strided((B, S, 1, D), (S * far, far, D, 1)), V.as_strided((B, S, 1, D), (S * far, far, D, 1))
+    q = _randn(3, (B, H, D), T, 1.5)
+    lens = torch.full((B,), S, dtype=torch.int32, device="cuda")
+    got = cf.PrefixAttention("bf16", H, 1, D).run(q, k[:3], v[:3], K4, V4, lens)
+    torch.cuda.synchronize()
+    ks = torch.cat([torch.cat([k[:3], k[i * S:(i + 1) * S]]) for i in range(B)])
+    vs = torch.cat([torch.cat([v[:3], v[i * S:(i + 1) * S]]) for i in range(B)])
+    want, _, b, _ = R.attention(q, ks, vs, list(range(B + 1)), R.starts([S + 3] * B), False, D ** -0.5)
+    R.check(got, want, b + 2.0 ** -20 * want.abs())
 
 
 def test_rows_outside_the_sequences_stay():
@@ -263,6 +306,38 @@ def test_prefix_attention(case):
     want, _, b, _ = R.attention(q, K, V, list(range(B + 1)), R.starts([P + n for n in lens]), False, D ** -0.5)
     # joining parts: a few more roundings in 32 bits
     R.check(got, want, b + 2.0 ** -20 * want.abs(), "O")
+
+
+def test_prefix_graph_replays():
+    """Captured twice and replayed with new keys and lengths in turn, eager calls
+    in between."""
+    H, Hkv, D, B, P, S = 8, 2, 128, 6, 1500, 300
+    T = torch.bfloat16
+    plan = cf.PrefixAttention("bf16", H, Hkv, D)
+    mk = lambda i: (_randn(i, (B, H, D), T, 1.5), _randn(i + 1, (P, Hkv, D), T), _randn(i + 2, (P, Hkv, D), T),
+                    _randn(i + 3, (B, S, Hkv, D), T), _randn(i + 4, (B, S, Hkv, D), T),
+                    (torch.arange(B, device="cuda", dtype=torch.int32) * 61 + 7 * i) % (S + 1))
+    args = mk(1)
+    _flush("prefix graph")
+    plan.run(*args)
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(plan.run(*args))
+        graphs.append(g)
+    for rep in range(3):
+        new = mk(20 + 10 * rep)
+        for a, b in zip(args, new):
+            a.copy_(b)
+        torch.cuda.synchronize()
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        want = plan.run(*new)
+        for o in outs:
+            assert torch.equal(o, want), rep
 
 
 def test_prompt_then_tokens():

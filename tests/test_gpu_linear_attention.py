@@ -244,6 +244,21 @@ def test_starts_that_go_back_stay_inside():
     assert bool((ws[need.value // 4:] == 7).all()) and bool((O[n:] == 7).all())
 
 
+def test_offsets_past_32_bits():
+    """Rows that lie gigabytes apart, inputs and outputs."""
+    H, D, n, far = 1, 64, 1200, 1 << 21
+    _flush("linear far rows")
+    q, k, v, g, s0 = _case("bf16", H, H, D, [n], seed=81)
+    room = torch.zeros((n * far,), dtype=torch.bfloat16, device="cuda")           # 5 GB
+    Q, K, V, O = [room.as_strided((n, H, D), (far, D, 1), i * far // 4) for i in range(4)]
+    Q.copy_(q), K.copy_(k), V.copy_(v)
+    got, after = cf.LinearAttention("bf16", H, H, D).run(Q, K, V, g, _cu([n]), state=s0, O=O)
+    torch.cuda.synchronize()
+    want, b, ws, bs = recurrence(q, k, v, g, [0, n], s0, D ** -0.5)
+    R.check(got, want, b, "O")
+    R.check(after, ws, bs, "state")
+
+
 def test_empty_calls():
     plan = cf.LinearAttention("bf16", 2, 1, 64)
     e = lambda h: torch.empty((0, h, 64), dtype=torch.bfloat16, device="cuda")

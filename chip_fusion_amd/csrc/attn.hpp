@@ -162,7 +162,7 @@ __device__ __forceinline__ bool find_tile(const int32_t* cu_q, const int32_t* cu
 // As find_tile, up to 64 sequences, the tiles that see the most keys first:
 // workgroups are taken in order, so the launch ends on short ones (17
 // sequences of up to 800 tokens, 8 key heads: 73 us in the sequences' order,
-// 66 in this).  A tile's level is about how many tiles' worth of tokens its
+// 66 in this; 24 of up to 644 without a mask, 16 heads: 40 and 35).  A tile's level is about how many tiles' worth of tokens its
 // last row sees.  Causal: one level a tile, the last tile of a sequence on
 // top; else all tiles of a sequence share one.  The level is found bit by bit
 // from how many tiles lie at or above one.
@@ -484,6 +484,21 @@ __device__ __forceinline__ void attn_careful(const AttnArgs& a, const RowState& 
 // ---------------------------------------------------------------------------
 // Many rows: a workgroup's waves take 32 rows each and share the key tiles
 // ---------------------------------------------------------------------------
+// Tiles of 32 keys, two slots of LDS, a wave's queries in registers: 168
+// registers and 32 KB at D = 128, which leaves room for three workgroups a
+// compute unit.  One's matrix instructions run under the others' softmax (a
+// tile of 32 x 32 scores: 512 cycles of matrix instructions, some 350 of vector
+// ones, at D = 128).  Two workgroups with tiles of 64 keys and the next tile's
+// scores computed ahead did as well on one long sequence and lost on short ones
+// (8001 packed tokens: 77 us, 72 so), whose time is a workgroup's start: its
+// place found, first keys and queries waited for (some 12 of its 38 thousand
+// cycles).
+// Measured: 16384 causal tokens, 32 heads of 128 (8 key heads), bf16: 1.92 ms,
+// 1145 TFLOP/s of the 1222 that a product of 8192^3 reaches (matrix cores busy
+// 0.66 of the cycles, the clock held down by power); 8001 tokens in 17
+// sequences: 62 us; head dim 64, half of the matrix work for the same softmax:
+// 9000 tokens of 16 heads in 24 sequences 32 us (545 TFLOP/s), bound by vector
+// instructions and by what does not fill the card at its end.
 template <int DT_, int DB_, bool PART_>
 struct AttnCfg {
     static constexpr int DT = DT_, DB = DB_, WAVES = 4, THREADS = 64 * WAVES;
@@ -713,6 +728,11 @@ __device__ __forceinline__ void attn_rows_body(const AttnArgs& a, unsigned char*
 // One launch for both kinds of keys of a batch behind a shared prefix: its
 // first workgroups take the prefix (bound by the matrix cores), the others
 // the requests' own keys (bound by memory); they fit a compute unit together.
+// 128 requests behind 32768 tokens, up to 1000 own keys, 32 heads of 128: 119 us
+// on the device (the products alone 58, the bytes alone 77: a prefix tile a
+// wave takes about 1.1 us however few its neighbours are, so the two hide each
+// other in part only; own workgroups spread among the prefix's: 137 at best).
+// 32 behind 4097, up to 512 own: 15.5 us and 5.9 for the join.
 template <int DT, int DB>
 __global__ __launch_bounds__(256, 3) void attn_prefix_kernel(AttnArgs p, AttnArgs own, int prefix_blocks) {
     using C = AttnCfg<DT, DB, true>;
@@ -727,6 +747,8 @@ __global__ __launch_bounds__(256, 3) void attn_prefix_kernel(AttnArgs p, AttnArg
 // ---------------------------------------------------------------------------
 // O = sum_s w_s O_s / sum_s w_s with w_s = 2^(lse_s - max); parts that saw no
 // key have lse = -inf and weight 0.  Four parts' loads are in flight at once.
+// Bound by the parts' bytes: 2500 rows of 24 heads of 96 in three parts, 70 MB
+// read, 13.5 us (5.2 TB/s).
 template <int DT>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int slots) {
     const int lane = threadIdx.x & 15;

@@ -61,21 +61,22 @@ Split plan_tiles(const b2b_attn_plan* p, int64_t seqs, int64_t rows, int64_t key
     // Parts of the keys.  Too few workgroups for `fill`: parts of 256 keys or
     // more.  Where most keys come before the rows (pieces of prompts), contexts
     // differ and one workgroup's may be twice the average while all of them run
-    // at once: up to three workgroups a slot, parts of 800 or more, so that
+    // at once: up to two workgroups a slot, parts of 800 or more, so that
     // writing and joining partial results stays below what the balance gains
-    // (2500 rows behind 0..4096 keys, 24 heads of 96: 119 us whole, 96 in two
-    // parts, 91 in three).
+    // (2500 rows behind 0..4096 keys, 24 heads of 96: 102 us whole, 82 in two
+    // parts or three, 88 in four; 8001 rows of 32 heads, their own keys only: 63
+    // us whole, 165 in two).
     int64_t parts = std::min(fill / wgs, each / 256);
-    if (keys >= 2 * rows) parts = std::max(parts, std::min(3 * fill / wgs, each / 800));
+    if (keys >= 2 * rows) parts = std::max(parts, std::min(2 * fill / wgs, each / 800));
     s.splits = (int)std::max<int64_t>(1, std::min<int64_t>(parts, 64));
     return s;
 }
 // A prefix: 1.5 workgroups a compute unit, beside those of the requests' own
-// keys (128 requests behind 32768 tokens, 32 heads of 128: 140 us at 1, 125 at
-// 1.5, 133 at 2, 147 at 3), and parts of 256 keys or more, of a few rows 64
+// keys (128 requests behind 32768 tokens, 32 heads of 128: 141 us at 1, 124 at
+// 1.5, 128 at 2, 146 at 3), and parts of 256 keys or more, of a few rows 64
 // (partial results cost little then: 3 requests of 8 heads behind 300 tokens
 // take 6.2 us on the device instead of 10.6; 32 requests of 32 heads behind 4097
-// took 26 us in parts of 128 and 21 in parts of 256).
+// took 26 us in parts of 128, 20 in parts of 256 and 23 in parts of 512).
 Split plan_prefix(const b2b_attn_plan* p, int64_t batch, int64_t prefix) {
     Split s;
     s.tiles = ceil_div(batch * (p->heads / p->kv_heads), b2b::kAttnRows);
@@ -289,9 +290,9 @@ namespace {
 // Tokens of a segment.  A workgroup, one a compute unit, takes a sequence's
 // head; where those are fewer than compute units, sequences are cut into
 // segments of 512 tokens or more, at the price of reading K and V twice (8200
-// tokens in 9 sequences of 32 heads, 288 workgroups: 87 us whole, 123 to 134
-// in segments of 512 to 1024; one of 32768 with 16 heads: 198 us in 16
-// segments, 235 in 24, 211 in 32, 287 in 8).
+// tokens in 9 sequences of 32 heads, 288 workgroups: 82 us whole, 124 to 126
+// in segments of 512 to 1024; one of 32768 with 16 heads: 1258 us whole, 282 in
+// 8 segments, 183 in 16, 193 in 32, 222 in 64).
 int64_t lin_segment(const b2b_linear_attn_plan* p, int64_t seqs, int64_t rows) {
     const int64_t want = std::max(1, 256 / p->heads);
     if (seqs >= want) return INT32_MAX;

@@ -22,13 +22,20 @@
 // state wave takes in chunk c, an output wave answers chunk c's queries from
 // the copy of the state that the state wave left in LDS a step before.  (All
 // waves doing both in turn took 4.1 us for 64 tokens of a head of 128, two
-// barriers and one wave a SIMD; 2.9 so.)
+// barriers and one wave a SIMD; two steps of 32 take 2.6 so.)  A state wave
+// bounds the step: 24 matrix instructions (bf16) and 220 vector ones that wait
+// for one another; two sets of state waves with half of the rows each were
+// slower, their split values being computed twice.
+// Measured: 8200 bf16 tokens in 9 sequences, 32 heads of 128: 82 us (3.7 TB/s of
+// its own bytes), the time of the longest sequence's steps; 32768 fp16 tokens of
+// 16 heads: 183 us (segments' states 71, joined in 8, outputs 122; K and V are
+// read twice, 5.12 TB/s would take 157).
 //
 // The state is float32 and so are its terms: lambda^(n-1-j) v_j is split into
 // parts of the 16-bit type that together hold its 24 bits (bf16: three; fp16:
 // two, the second scaled by 2^11), each a pass of matrix instructions with the
-// exact k_j.  Only the operands that end in the 16-bit output are rounded to
-// its type: the scores and, as q's partner, a copy of the state.
+// exact k_j.  What ends in the 16-bit output alone is held in its type: the
+// scores in two parts, and, as q's partner, a copy of the state, rounded once.
 #pragma once
 #include "attn.hpp"
 
@@ -122,6 +129,20 @@ __device__ __forceinline__ void lin_split(float x, float y, unsigned (&out)[PART
             }
         }
     }
+}
+
+// What rounding left of eight values of x: their second parts.
+template <int DT>
+__device__ __forceinline__ u4_t lin_rest(const f16x_t& x, int k, u4_t& first) {
+    u4_t out;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        unsigned w = first[i];
+        asm("" : "+v"(w));          // as in lin_split
+        first[i] = w;
+        out[i] = Ty<DT>::pack(x[8 * k + 2 * i] - attn_unpack<DT>(w, 0), x[8 * k + 2 * i + 1] - attn_unpack<DT>(w, 1));
+    }
+    return out;
 }
 
 // The exponent e for which the state's largest magnitude times 2^-e is about
@@ -452,11 +473,16 @@ __device__ __forceinline__ bool lin_body(const LinArgs& a, unsigned char* lds) {
                 vp[s] = attn_vfrag<C::C>(kt + C::TILE, vb, part, s);
                 vp[2 + s] = attn_pack<C::DT>(p, s);
             }
+            // The scores in two parts of the type: rounded once, they cost a row
+            // of few tokens as much precision as its output's own rounding.  (The
+            // output waves wait for the state waves, two passes more or not.)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) y = M::mma(vp[s], lin_rest<C::DT>(p, s, vp[2 + s]), y);
 #pragma unroll
             for (int s = 0; s < 2; ++s) y = M::mma(vp[s], vp[2 + s], y);
             if (CAREFUL && __any(lin_odd<C::DT>(vp))) {
                 firsts();
-                // the scores, rounded, where this wave's outputs will lie: a lane's
+                // the scores' first parts, where this wave's outputs will lie: a lane's
                 // own row, read by the two lanes that hold it
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {

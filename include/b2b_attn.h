@@ -116,8 +116,9 @@ typedef struct b2b_linear_attn_plan* b2b_linear_attn_t;   /* opaque, owned by th
  *     S_t = lambda_h S_{t-1} + k_t v_t^T        (head_dim x head_dim, row: key element)
  *     o_t = scale q_t^T S_t,    lambda_h = exp(log_decay[h])
  *   dtype       B2B_DTYPE_F16 or B2B_DTYPE_BF16: Q, K, V and O; states are
- *               float32 and updated in float32 precision; the scores q.k and
- *               the copy of the state that meets q are rounded to dtype
+ *               float32 and updated in float32 precision; the scores q.k are
+ *               held in two parts of dtype, the copy of the state that meets q
+ *               is rounded to it
  *   head_dim    64 or 128
  *   scale       finite and positive (0: head_dim ^ -1/2)
  */

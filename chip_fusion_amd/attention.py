@@ -15,22 +15,29 @@ import torch
 
 from . import ATTN_CAUSAL, DTYPES, Rows, TORCH_DTYPES, _check, lib
 
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _heads3(t, name, dtype, rows, heads, dim):
+    """As _rows for [rows, heads, dim] (rows None: any number): what nearly
+    every call passes, in one look, the rest in _rows."""
+    try:
+        n, h, d = t.shape
+        ld, hs, one = t.stride()
+        p = t.data_ptr()
+        if (t.dtype is dtype and p and n and h == heads and d == dim and (rows is None or n == rows)
+                and one == 1 and ld >= dim and not (ld | hs | p >> 1) & 7):
+            return Rows(p, ld, hs)
+    except (AttributeError, TypeError, ValueError):
+        pass
+    return _rows(t, name, dtype, (rows, heads, dim))
+
 
 def _rows(t, name, dtype, shape):
     """ValueError unless t is a tensor of that dtype and shape (None: any
     size) whose last three dimensions are rows of heads that the kernels can
     address; its b2b_rows_t."""
-    try:                                        # what nearly every call passes, in one look
-        size, stride, p = t.shape, t.stride(), t.data_ptr()
-        rows, heads, dim = size[-3:]
-        ld, hs, one = stride[-3:]
-        if (t.dtype is dtype and p and rows and heads == shape[-2] and dim == shape[-1]
-                and (shape[-3] is None or rows == shape[-3]) and len(size) == len(shape)
-                and (len(size) == 3 or size[0] == shape[0])
-                and one == 1 and ld >= dim and not (ld & 7 or hs & 7 or p & 15)):
-            return Rows(p, ld, hs)
-    except (AttributeError, TypeError, ValueError):
-        pass
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name}: a torch tensor is expected, got {type(t).__name__}")
     if t.dtype != dtype:
@@ -65,11 +72,12 @@ def _starts(cu, name, seqs=None):
 def _device_of(names, *tensors):
     """The CUDA device that holds all the tensors (None among them: not given)."""
     index = tensors[0].get_device()
-    for t in tensors:
-        if index < 0 or (t is not None and t.get_device() != index):
-            break
-    else:
-        return index
+    if index >= 0:
+        for t in tensors:
+            if t is not None and t.get_device() != index:
+                break
+        else:
+            return index
     first = None
     for name, t in zip(names.split(), tensors):
         if t is None:
@@ -81,18 +89,18 @@ def _device_of(names, *tensors):
         first = t.device
 
 
-def _on(index, stream, call):
-    """call(handle) with the tensors' device current and `stream` (or that
-    device's current stream) the one that allocations belong to; handle: its
-    hipStream_t."""
-    if stream is None and torch._C._cuda_getDevice() == index:
-        return call(torch._C._cuda_getCurrentRawStream(index))
+def _on(index, stream, call, *args):
+    """call(handle, *args) with the tensors' device current and `stream` (or
+    that device's current stream) the one that allocations belong to; handle:
+    its hipStream_t."""
+    if stream is None and _current_device() == index:
+        return call(_raw_stream(index), *args)
     with torch.cuda.device(index):
         s = torch.cuda.current_stream() if stream is None else stream
         if s.device.index != index:
             raise ValueError(f"stream: on {s.device}, the tensors on cuda:{index}")
         with torch.cuda.stream(s):
-            return call(s.cuda_stream)
+            return call(s.cuda_stream, *args)
 
 
 class _Workspaces:
@@ -165,6 +173,7 @@ class Attention(_Heads):
 
     def __init__(self, dtype, heads, kv_heads, head_dim, causal=True, scale=None):
         super().__init__(dtype, heads, kv_heads, head_dim, scale, ATTN_CAUSAL if causal else 0)
+        self._call = lib().b2b_attn_run
 
     def run(self, Q, K, V, cu_q, cu_k=None, O=None, lse=False, stream=None):
         """Q [rows, heads, dim], K and V [keys, kv_heads, dim]; sequence s has
@@ -176,32 +185,30 @@ class Attention(_Heads):
         seqs = _starts(cu_q, "cu_q")
         if cu_k is not cu_q:
             _starts(cu_k, "cu_k", seqs)
-        q = _rows(Q, "Q", self.dtype, (None, self.heads, self.dim))
-        k = _rows(K, "K", self.dtype, (None, self.kv_heads, self.dim))
+        dtype, heads, kv_heads, dim = self.dtype, self.heads, self.kv_heads, self.dim
+        q = _heads3(Q, "Q", dtype, None, heads, dim)
+        k = _heads3(K, "K", dtype, None, kv_heads, dim)
         rows, keys = Q.shape[0], K.shape[0]
-        v = _rows(V, "V", self.dtype, (keys, self.kv_heads, self.dim))
+        v = _heads3(V, "V", dtype, keys, kv_heads, dim)
         want = lse is not False and lse is not None
         LSE = lse if isinstance(lse, torch.Tensor) else None
-        if O is not None:
-            o = _rows(O, "O", self.dtype, (rows, self.heads, self.dim))
+        o = None if O is None else _heads3(O, "O", dtype, rows, heads, dim)
         if LSE is not None and (LSE.dtype != torch.float32 or LSE.shape != Q.shape[:2] or not LSE.is_contiguous()):
             raise ValueError("lse: a contiguous float32 tensor [rows, heads] is expected")
         index = _device_of("Q K V cu_q cu_k O lse", Q, K, V, cu_q, cu_k, O, LSE)
+        return _on(index, stream, self._run, seqs, rows, keys, q, k, v, o, Q, O, cu_q, cu_k, want, LSE)
 
-        def call(stream):
-            out, ls = O, LSE
-            if out is None:
-                out = _new(Q)
-            if want and ls is None:
-                ls = Q.new_empty((rows, self.heads), dtype=torch.float32)
-            keep, wp, n = self._workspaces.get(Q, seqs, rows, keys)
-            st = lib().b2b_attn_run(self._h, seqs, rows, keys, q, k, v,
-                                o if O is not None else Rows(out.data_ptr(), self.heads * self.dim, self.dim),
-                                cu_q.data_ptr(), cu_k.data_ptr(), _ptr(ls), wp, n, stream)
+    def _run(self, stream, seqs, rows, keys, q, k, v, o, Q, O, cu_q, cu_k, want, LSE):
+        if O is None:
+            O = _new(Q)
+            o = Rows(O.data_ptr(), self.heads * self.dim, self.dim)
+        if want and LSE is None:
+            LSE = Q.new_empty((rows, self.heads), dtype=torch.float32)
+        keep, wp, n = self._workspaces.get(Q, seqs, rows, keys)
+        st = self._call(self._h, seqs, rows, keys, q, k, v, o, cu_q.data_ptr(), cu_k.data_ptr(), _ptr(LSE), wp, n, stream)
+        if st:
             _check(st, "b2b_attn_run")
-            return (out, ls) if want else out
-
-        return _on(index, stream, call)
+        return (O, LSE) if want else O
 
 
 class PrefixAttention(_Heads):
@@ -212,39 +219,55 @@ class PrefixAttention(_Heads):
 
     def __init__(self, dtype, heads, kv_heads, head_dim, scale=None):
         super().__init__(dtype, heads, kv_heads, head_dim, scale, 0)
+        self._call = lib().b2b_prefix_attn_run
 
     def run(self, Q, Kp, Vp, K, V, lens, O=None, stream=None):
         """Q [batch, heads, dim]; Kp, Vp [prefix, kv_heads, dim], the shared
         keys and values; K, V [batch, own, kv_heads, dim], of which request b
         has the first lens[b] (device int32).  Returns O [batch, heads, dim]."""
-        q = _rows(Q, "Q", self.dtype, (None, self.heads, self.dim))
+        dtype, heads, kv_heads, dim = self.dtype, self.heads, self.kv_heads, self.dim
+        q = _heads3(Q, "Q", dtype, None, heads, dim)
         batch = Q.shape[0]
-        kp = _rows(Kp, "Kp", self.dtype, (None, self.kv_heads, self.dim))
+        kp = _heads3(Kp, "Kp", dtype, None, kv_heads, dim)
         prefix = Kp.shape[0]
-        vp = _rows(Vp, "Vp", self.dtype, (prefix, self.kv_heads, self.dim))
-        k = _rows(K, "K", self.dtype, (batch, None, self.kv_heads, self.dim))
+        vp = _heads3(Vp, "Vp", dtype, prefix, kv_heads, dim)
+        k, ks = self._own(K, "K", batch, None)
         own = K.shape[1]
-        v = _rows(V, "V", self.dtype, (batch, own, self.kv_heads, self.dim))
-        ks, vs = (K.stride(0), V.stride(0)) if batch > 1 and own else (0, 0)
-        if ks % 8 or vs % 8:
-            raise ValueError(f"{'K' if ks % 8 else 'V'}: requests must start on 16-byte boundaries")
+        v, vs = self._own(V, "V", batch, own)
         if not isinstance(lens, torch.Tensor) or lens.dtype is not torch.int32 or lens.shape != (batch,) \
                 or not lens.is_contiguous():
             raise ValueError(f"lens: a contiguous int32 tensor [{batch}] is expected")
-        if O is not None:
-            o = _rows(O, "O", self.dtype, (batch, self.heads, self.dim))
+        o = None if O is None else _heads3(O, "O", dtype, batch, heads, dim)
         index = _device_of("Q Kp Vp K V lens O", Q, Kp, Vp, K, V, lens, O)
+        return _on(index, stream, self._run, batch, prefix, own, q, kp, vp, k, ks, v, vs, o, Q, O, lens)
 
-        def call(stream):
-            out = _new(Q) if O is None else O
-            keep, wp, n = self._workspaces.get(Q, batch, prefix, own)
-            st = lib().b2b_prefix_attn_run(self._h, batch, prefix, own, q, kp, vp, k, ks, v, vs, lens.data_ptr(),
-                                       o if O is not None else Rows(out.data_ptr(), self.heads * self.dim, self.dim),
-                                       wp, n, stream)
+    def _own(self, t, name, batch, own):
+        """Requests' own keys or values [batch, own, kv_heads, dim]: their
+        b2b_rows_t and the stride from one request's to the next one's."""
+        try:
+            b, n, h, d = t.shape
+            far, ld, hs, one = t.stride()
+            p = t.data_ptr()
+            if (t.dtype is self.dtype and p and n and b == batch and h == self.kv_heads and d == self.dim
+                    and (own is None or n == own) and one == 1 and ld >= d and not (far | ld | hs | p >> 1) & 7):
+                return Rows(p, ld, hs), far
+        except (AttributeError, TypeError, ValueError):
+            pass
+        r = _rows(t, name, self.dtype, (batch, own, self.kv_heads, self.dim))
+        far = t.stride(0) if batch > 1 and t.shape[1] else 0
+        if far % 8:
+            raise ValueError(f"{name}: requests must start on 16-byte boundaries")
+        return r, far
+
+    def _run(self, stream, batch, prefix, own, q, kp, vp, k, ks, v, vs, o, Q, O, lens):
+        if O is None:
+            O = _new(Q)
+            o = Rows(O.data_ptr(), self.heads * self.dim, self.dim)
+        keep, wp, n = self._workspaces.get(Q, batch, prefix, own)
+        st = self._call(self._h, batch, prefix, own, q, kp, vp, k, ks, v, vs, lens.data_ptr(), o, wp, n, stream)
+        if st:
             _check(st, "b2b_prefix_attn_run")
-            return out
-
-        return _on(index, stream, call)
+        return O
 
 
 class LinearAttention:
@@ -267,15 +290,16 @@ class LinearAttention:
         self._workspaces = _Workspaces(lib().b2b_linear_attn_workspace, h)
 
     def _operands(self, Q, K, V, log_decay, O):
-        q = _rows(Q, "Q", self.dtype, (None, self.heads, self.dim))
-        k = _rows(K, "K", self.dtype, (Q.shape[0], self.kv_heads, self.dim))
-        v = _rows(V, "V", self.dtype, (Q.shape[0], self.kv_heads, self.dim))
-        if O is not None:
-            _rows(O, "O", self.dtype, tuple(Q.shape))
+        dtype, dim = self.dtype, self.dim
+        q = _heads3(Q, "Q", dtype, None, self.heads, dim)
+        rows = Q.shape[0]
+        k = _heads3(K, "K", dtype, rows, self.kv_heads, dim)
+        v = _heads3(V, "V", dtype, rows, self.kv_heads, dim)
+        o = None if O is None else _heads3(O, "O", dtype, rows, self.heads, dim)
         if not isinstance(log_decay, torch.Tensor) or log_decay.dtype is not torch.float32 \
                 or log_decay.shape != (self.heads,) or not log_decay.is_contiguous():
             raise ValueError(f"log_decay: a contiguous float32 tensor [{self.heads}] is expected")
-        return q, k, v
+        return rows, q, k, v, o
 
     def _state(self, t, name, n):
         if t is None:
@@ -290,52 +314,51 @@ class LinearAttention:
         cu[s] .. cu[s+1]-1 being sequence s (device int32); state: the states
         before them [seqs, heads, dim, dim] (zero by default).  Returns O and
         the states after them (state_out, which may be `state`)."""
-        q, k, v = self._operands(Q, K, V, log_decay, O)
+        rows, q, k, v, o = self._operands(Q, K, V, log_decay, O)
         seqs = _starts(cu, "cu")
         self._state(state, "state", seqs)
         self._state(state_out, "state_out", seqs)
-        rows = Q.shape[0]
         index = _device_of("Q K V log_decay cu state O state_out", Q, K, V, log_decay, cu, state, O, state_out)
+        return _on(index, stream, self._run, seqs, rows, q, k, v, o, Q, O, log_decay, cu, state, state_out)
 
-        def call(stream):
-            out = _new(Q) if O is None else O
-            after = state_out
-            if after is None:
-                after = Q.new_empty((seqs, self.heads, self.dim, self.dim), dtype=torch.float32)
-            keep, wp, n = self._workspaces.get(Q, seqs, rows)
-            st = lib().b2b_linear_attn_run(self._h, seqs, rows, q, k, v, self._out(out, O is None), log_decay.data_ptr(),
-                                       cu.data_ptr(), _ptr(state), after.data_ptr(), wp, n, stream)
+    def _run(self, stream, seqs, rows, q, k, v, o, Q, O, log_decay, cu, state, after):
+        if O is None:
+            O, o = self._new_out(Q)
+        if after is None:
+            after = Q.new_empty((seqs, self.heads, self.dim, self.dim), dtype=torch.float32)
+        keep, wp, n = self._workspaces.get(Q, seqs, rows)
+        st = lib().b2b_linear_attn_run(self._h, seqs, rows, q, k, v, o, log_decay.data_ptr(), cu.data_ptr(), _ptr(state),
+                                       after.data_ptr(), wp, n, stream)
+        if st:
             _check(st, "b2b_linear_attn_run")
-            return out, after
-
-        return _on(index, stream, call)
+        return O, after
 
     def step(self, Q, K, V, log_decay, state, O=None, state_out=None, stream=None):
         """One token of each request: row b of Q, K and V on state b
         [batch, heads, dim, dim].  Returns O and the states after it
         (state_out, which may be `state`)."""
-        q, k, v = self._operands(Q, K, V, log_decay, O)
+        rows, q, k, v, o = self._operands(Q, K, V, log_decay, O)
         if state is None:
             raise ValueError("state: a tensor is expected")
-        self._state(state, "state", Q.shape[0])
-        self._state(state_out, "state_out", Q.shape[0])
-        rows = Q.shape[0]
+        self._state(state, "state", rows)
+        self._state(state_out, "state_out", rows)
         index = _device_of("Q K V log_decay state O state_out", Q, K, V, log_decay, state, O, state_out)
+        return _on(index, stream, self._step, rows, q, k, v, o, Q, O, log_decay, state, state_out)
 
-        def call(stream):
-            out = _new(Q) if O is None else O
-            after = torch.empty_like(state) if state_out is None else state_out
-            st = lib().b2b_linear_attn_step(self._h, rows, q, k, v, self._out(out, O is None), log_decay.data_ptr(),
-                                            state.data_ptr(), after.data_ptr(), stream)
+    def _step(self, stream, rows, q, k, v, o, Q, O, log_decay, state, after):
+        if O is None:
+            O, o = self._new_out(Q)
+        if after is None:
+            after = torch.empty_like(state)
+        st = lib().b2b_linear_attn_step(self._h, rows, q, k, v, o, log_decay.data_ptr(), state.data_ptr(), after.data_ptr(),
+                                        stream)
+        if st:
             _check(st, "b2b_linear_attn_step")
-            return out, after
+        return O, after
 
-        return _on(index, stream, call)
-
-    def _out(self, t, made):
-        if made:
-            return Rows(t.data_ptr(), self.heads * self.dim, self.dim)
-        return _rows(t, "O", self.dtype, tuple(t.shape))
+    def _new_out(self, Q):
+        O = _new(Q)
+        return O, Rows(O.data_ptr(), self.heads * self.dim, self.dim)
 
     def close(self):
         if getattr(self, "_h", None):

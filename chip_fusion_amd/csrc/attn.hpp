@@ -732,7 +732,7 @@ __device__ __forceinline__ void attn_rows_body(const AttnArgs& a, unsigned char*
 // on the device (the products alone 58, the bytes alone 77: a prefix tile a
 // wave takes about 1.1 us however few its neighbours are, so the two hide each
 // other in part only; own workgroups spread among the prefix's: 137 at best).
-// 32 behind 4097, up to 512 own: 15.5 us and 5.9 for the join.
+// 32 behind 4097, up to 512 own: 15.4 us and 4.6 for the join.
 template <int DT, int DB>
 __global__ __launch_bounds__(256, 3) void attn_prefix_kernel(AttnArgs p, AttnArgs own, int prefix_blocks) {
     using C = AttnCfg<DT, DB, true>;
@@ -743,34 +743,41 @@ __global__ __launch_bounds__(256, 3) void attn_prefix_kernel(AttnArgs p, AttnArg
 }
 
 // ---------------------------------------------------------------------------
-// Joining partial results: a quarter of a wave a (row, head), 8 columns a lane
+// Joining partial results: 16 lanes a (row, head), 8 columns a lane
 // ---------------------------------------------------------------------------
 // O = sum_s w_s O_s / sum_s w_s with w_s = 2^(lse_s - max); parts that saw no
-// key have lse = -inf and weight 0.  Four parts' loads are in flight at once.
-// Bound by the parts' bytes: 2500 rows of 24 heads of 96 in three parts, 70 MB
-// read, 13.5 us (5.2 TB/s).
-template <int DT>
+// key have lse = -inf and weight 0.  One pass with a running maximum, four
+// parts' loads in flight.  SUB = 4: the quarters of a wave take every fourth
+// part of one (row, head) each, for few rows of many parts, whose time is the
+// loads' latency (32 rows of 32 heads in 17 parts: 6.0 us by 16 lanes, 4.6 so);
+// else it is the parts' bytes (2500 rows of 24 heads of 96 in two parts, 47 MB
+// read: 10 us).
+template <int DT, int SUB>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int slots) {
-    const int lane = threadIdx.x & 15;
-    const int64_t n = a.rows * a.heads, at = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+    const int lane = threadIdx.x & 15, sub = SUB == 1 ? 0 : (threadIdx.x >> 4) & (SUB - 1);
+    const int64_t n = a.rows * a.heads, at = (int64_t)blockIdx.x * (16 / SUB) + threadIdx.x / (16 * SUB);
     if (at >= n) return;
     const int64_t row = at / a.heads;
     const int head = (int)(at - row * a.heads);
-    float m = -__builtin_inff();
-    for (int s = lane; s < slots; s += 16) m = __builtin_fmaxf(m, a.part_lse[s * n + at]);
-#pragma unroll
-    for (int d = 1; d < 16; d <<= 1) m = __builtin_fmaxf(m, __shfl_xor(m, d));
-    const float m0 = m == -__builtin_inff() ? 0.f : m;
-    float sum = 0.f, x[8] = {};
+    float m = -__builtin_inff(), sum = 0.f, x[8] = {};
     const bool live = 8 * lane < a.dim;
     const float* p = a.part + at * a.dim + 8 * lane;
-    for (int s0 = 0; s0 < slots; s0 += 4) {
-        float w[4];
+    // to a new maximum (0 for -inf: nothing has been seen)
+    auto scale_to = [&](float m1) __attribute__((always_inline)) {
+        const float f = __builtin_amdgcn_exp2f(m - m1);
+        sum *= f;
+        // a weight of 0 leaves its part out, whatever that holds
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = f == 0.f ? 0.f : x[e] * f;
+    };
+    for (int s0 = sub; s0 < slots; s0 += 4 * SUB) {
+        float w[4], m1 = m;
         f4_t v[4][2];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int s = s0 + i < slots ? s0 + i : slots - 1;
-            w[i] = s0 + i < slots ? a.part_lse[s * n + at] : -__builtin_inff();
+            const bool in = s0 + i * SUB < slots;
+            const int s = in ? s0 + i * SUB : s0;
+            w[i] = in ? a.part_lse[s * n + at] : -__builtin_inff();
             v[i][0] = v[i][1] = f4_t{0.f, 0.f, 0.f, 0.f};
             if (live) {
                 v[i][0] = *(const f4_t*)(p + s * n * a.dim);
@@ -778,20 +785,38 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int slots) {
             }
         }
 #pragma unroll
+        for (int i = 0; i < 4; ++i) m1 = __builtin_fmaxf(m1, w[i]);
+        const float m0 = m1 == -__builtin_inff() ? 0.f : m1;
+        scale_to(m0);
+        m = m1;
+#pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float f = __builtin_amdgcn_exp2f(w[i] - m0);
             sum += f;
-            // a weight of 0 leaves its part out, whatever that holds
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] = f == 0.f ? x[e] : __builtin_fmaf(f, v[i][e >> 2][e & 3], x[e]);
         }
+    }
+    if constexpr (SUB > 1) {
+        float m1 = m;
+#pragma unroll
+        for (int d = 16; d < 16 * SUB; d <<= 1) m1 = __builtin_fmaxf(m1, __shfl_xor(m1, d));
+        scale_to(m1 == -__builtin_inff() ? 0.f : m1);
+        m = m1;
+#pragma unroll
+        for (int d = 16; d < 16 * SUB; d <<= 1) {
+            sum += __shfl_xor(sum, d);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] += __shfl_xor(x[e], d);
+        }
+        if (sub) return;
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     if (live)
         *(u4_t*)((char*)a.O + (row * a.ldo + (int64_t)head * a.hso + 8 * lane) * 2) =
             u4_t{Ty<DT>::pack(x[0] * inv, x[1] * inv), Ty<DT>::pack(x[2] * inv, x[3] * inv),
                  Ty<DT>::pack(x[4] * inv, x[5] * inv), Ty<DT>::pack(x[6] * inv, x[7] * inv)};
-    if (lane == 0 && a.lse) a.lse[at] = sum == 0.f ? -__builtin_inff() : (m0 + __builtin_amdgcn_logf(sum)) * kLn2;
+    if (lane == 0 && a.lse) a.lse[at] = sum == 0.f ? -__builtin_inff() : (m + __builtin_amdgcn_logf(sum)) * kLn2;
 }
 
 }  // namespace b2bk

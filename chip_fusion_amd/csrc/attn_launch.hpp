@@ -50,7 +50,10 @@ struct AttnLaunchers {
     }
     static hipError_t join(const b2bk::AttnArgs& a, int slots, hipStream_t s) {
         const int64_t n = a.rows * a.heads;
-        hipLaunchKernelGGL(b2bk::attn_join_kernel<DT>, dim3((unsigned)((n + 15) / 16)), dim3(256), 0, s, a, slots);
+        if (slots >= 4)
+            hipLaunchKernelGGL((b2bk::attn_join_kernel<DT, 4>), dim3((unsigned)((n + 3) / 4)), dim3(256), 0, s, a, slots);
+        else
+            hipLaunchKernelGGL((b2bk::attn_join_kernel<DT, 1>), dim3((unsigned)((n + 15) / 16)), dim3(256), 0, s, a, slots);
         return hipGetLastError();
     }
     static const AttnLaunch& table() {

@@ -383,12 +383,7 @@ __device__ __forceinline__ bool lin_body(const LinArgs& a, unsigned char* lds) {
 #pragma unroll
                         for (int t = 0; t < C::DB; ++t) S[t] = M::mma(f[t][k], vp[k][0], S[t]);
                 }
-            } else {
-                if constexpr (!C::STATE)
-#pragma unroll
-                    for (int t = 0; t < C::DB; ++t)
-#pragma unroll
-                        for (int r = 0; r < 16; ++r) S[t][r] *= keep;
+            } else if constexpr (C::STATE) {
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     split(k);
@@ -397,8 +392,26 @@ __device__ __forceinline__ bool lin_body(const LinArgs& a, unsigned char* lds) {
 #pragma unroll
                         for (int t = 0; t < C::DB; ++t) S[t] = M::mma(f[t][k], vp[k][p], S[t]);
                 }
+            } else {
+                // one tile of the state after the other: its copy is rounded and left
+                // under the next one's matrix instructions (3 % of the launch
+                // against all tiles in step; the parts' order makes no such difference)
+                split(0);
+                split(1);
+                unsigned char* to = lds + C::COPY + ((c + 1) & 1) * C::COPY_BYTES + part * C::KS * 1024 + lane * 16;
+#pragma unroll
+                for (int t = 0; t < C::DB; ++t) {
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) S[t][r] *= keep;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+#pragma unroll
+                        for (int p = C::PARTS - 1; p >= 0; --p) S[t] = M::mma(f[t][k], vp[k][p], S[t]);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) *(u4_t*)(to + (2 * t + k) * 1024) = attn_pack<C::DT>(S[t], k);
+                }
             }
-            leave(c + 1);
+            if constexpr (!C::STATE && C::DT == DT_F16) leave(c + 1);
         }
         if (!C::STATE && chunks > 0) {
             barrier_lds();      // the output waves' last

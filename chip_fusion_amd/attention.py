@@ -5,9 +5,11 @@ Tensors are taken as they lie: [rows, heads, dim] with any row and head
 strides that are multiples of 8 elements, dim contiguous -- slices of a fused
 projection, or [heads, rows, dim] storage seen transposed.  Everything runs
 on the device that holds the tensors, on `stream` or on that device's current
-stream; outputs and workspaces that a call allocates come from torch's
-allocator on that stream, so overlapping calls and captured graphs each have
-their own.
+stream (inputs made on another stream are the caller's to wait for and to
+keep, as for torch's own operators); outputs and workspaces that a call
+allocates come from torch's allocator on that stream, so overlapping calls
+and captured graphs each have their own.  Forward only, as all of the
+library: outputs carry no gradients.
 """
 import ctypes
 

@@ -191,6 +191,32 @@ def test_rows_outside_the_sequences_stay():
     assert torch.equal(got, O[:60])
 
 
+def test_starts_and_lengths_are_clamped():
+    """Starts below 0 and past the rows, lengths below 0 and past the own keys:
+    as if they were the nearest that fit, and nothing outside is touched."""
+    H, Hkv, D, n = 4, 2, 64, 300
+    T = torch.float16
+    q, k, v = _case("f16", H, Hkv, D, [n], [n], seed=91)
+    O = torch.full((n + 40, H, D), 7.0, dtype=T, device="cuda")
+    at = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    _flush("starts clamped")
+    plan = cf.Attention("f16", H, Hkv, D)
+    plan.run(q, k, v, at([-9, 100, 90, 2 * n]), at([-1, 120, 2 * n, 1 << 30]), O=O[:n])
+    # 0..100 on keys 0..120; none on the rest; 90.. has no keys left
+    want = plan.run(q, k, v, at([0, 100, 100, 100]), at([0, 120, 120, 120]))
+    torch.cuda.synchronize()
+    assert torch.equal(O[:90], want[:90]) and bool((O[100:n] == 0).all()) and bool((O[n:] == 7).all())
+    B, S = 3, 20
+    q, k, v = _randn(1, (B, H, D), T), _randn(2, (B, S, Hkv, D), T), _randn(3, (B, S, Hkv, D), T)
+    e = k[0, :0]
+    plan = cf.PrefixAttention("f16", H, Hkv, D)
+    _flush("lengths clamped")
+    got = plan.run(q, e, e, k, v, at([-5, S + 100, 7]))
+    want = plan.run(q, e, e, k, v, at([0, S, 7]))
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and bool((got[0] == 0).all())
+
+
 def test_nan_and_infinities_where_they_are_seen():
     """A NaN among a row's keys makes that row NaN and no other; a query's NaN
     its own row; an infinite score ends in NaN as the definition does."""

@@ -445,6 +445,7 @@ __device__ __forceinline__ void attn_careful(const AttnArgs& a, const RowState& 
         const int end = pos + 1 + shift < to ? pos + 1 + shift : to;
         const float m = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, st.m), r));
         const float l = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, l_all), r));
+        if (l != l) continue;       // a NaN among the row's scores: all of it is NaN, as written
         const char* q = (const char*)a.Q.p + ((q0 + pos) * a.Q.ld + (int64_t)head * a.Q.hs) * 2;
         float o0 = 0.f, o1 = 0.f;
         for (int j = from; j < end; j += 64) {

@@ -15,6 +15,10 @@ import ctypes
 
 import torch
 
+try:
+    from . import _attn
+except ImportError as e:
+    raise ImportError("chip_fusion_amd/_attn.so is missing: run python -m chip_fusion_amd.build") from e
 from . import ATTN_CAUSAL, DTYPES, Rows, TORCH_DTYPES, _check, lib
 
 _current_device = torch._C._cuda_getDevice
@@ -138,6 +142,13 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _usual(handle, heads, kv_heads, dim, dtype, workspace, run, step=None):
+    """The plan's usual calls (pyattn.cpp): on the current stream, tensors of the
+    common layouts; they return None where the checks here are to be made."""
+    at = lambda f: 0 if f is None else ctypes.cast(f, ctypes.c_void_p).value
+    return _attn.Call(handle.value, at(workspace), at(run), at(step), heads, kv_heads, dim, dtype, torch)
+
+
 class _Heads:
     """A plan of the attention of a model's heads (b2b_attn_create)."""
 
@@ -151,10 +162,13 @@ class _Heads:
                "b2b_attn_create")
         self._h = h
         self.dtype = TORCH_DTYPES[code]
-        self._workspaces = _Workspaces(getattr(lib(), self._workspace_call), h)
+        self._call, workspace = getattr(lib(), self._run_call), getattr(lib(), self._workspace_call)
+        self._workspaces = _Workspaces(workspace, h)
+        self._usual = _usual(h, heads, kv_heads, head_dim, self.dtype, workspace, self._call)
 
     def close(self):
         if getattr(self, "_h", None):
+            self._usual.close()
             lib().b2b_attn_destroy(self._h)
             self._h = None
 
@@ -171,11 +185,10 @@ class Attention(_Heads):
 
     scale: of the scores, dim ** -0.5 by default."""
 
-    _workspace_call = "b2b_attn_workspace"
+    _run_call, _workspace_call = "b2b_attn_run", "b2b_attn_workspace"
 
     def __init__(self, dtype, heads, kv_heads, head_dim, causal=True, scale=None):
         super().__init__(dtype, heads, kv_heads, head_dim, scale, ATTN_CAUSAL if causal else 0)
-        self._call = lib().b2b_attn_run
 
     def run(self, Q, K, V, cu_q, cu_k=None, O=None, lse=False, stream=None):
         """Q [rows, heads, dim], K and V [keys, kv_heads, dim]; sequence s has
@@ -183,6 +196,10 @@ class Attention(_Heads):
         (device int32; cu_k defaults to cu_q).  Returns O, or (O, LSE) with
         `lse` (True, or a float32 tensor [rows, heads] to write).  Rows that
         belong to no sequence are not written."""
+        if stream is None:
+            out = self._usual.attention(Q, K, V, cu_q, cu_k, O, lse)
+            if out is not None:
+                return out
         cu_k = cu_q if cu_k is None else cu_k
         seqs = _starts(cu_q, "cu_q")
         if cu_k is not cu_q:
@@ -217,16 +234,19 @@ class PrefixAttention(_Heads):
     """Attention of one new token a request, all requests behind one shared
     prefix (b2b_prefix_attn_run): the prefix is read once for the batch."""
 
-    _workspace_call = "b2b_prefix_attn_workspace"
+    _run_call, _workspace_call = "b2b_prefix_attn_run", "b2b_prefix_attn_workspace"
 
     def __init__(self, dtype, heads, kv_heads, head_dim, scale=None):
         super().__init__(dtype, heads, kv_heads, head_dim, scale, 0)
-        self._call = lib().b2b_prefix_attn_run
 
     def run(self, Q, Kp, Vp, K, V, lens, O=None, stream=None):
         """Q [batch, heads, dim]; Kp, Vp [prefix, kv_heads, dim], the shared
         keys and values; K, V [batch, own, kv_heads, dim], of which request b
         has the first lens[b] (device int32).  Returns O [batch, heads, dim]."""
+        if stream is None:
+            out = self._usual.prefix(Q, Kp, Vp, K, V, lens, O)
+            if out is not None:
+                return out
         dtype, heads, kv_heads, dim = self.dtype, self.heads, self.kv_heads, self.dim
         q = _heads3(Q, "Q", dtype, None, heads, dim)
         batch = Q.shape[0]
@@ -289,7 +309,10 @@ class LinearAttention:
                "b2b_linear_attn_create")
         self._h = h
         self.dtype = TORCH_DTYPES[code]
-        self._workspaces = _Workspaces(lib().b2b_linear_attn_workspace, h)
+        L = lib()
+        self._workspaces = _Workspaces(L.b2b_linear_attn_workspace, h)
+        self._usual = _usual(h, heads, kv_heads, head_dim, self.dtype, L.b2b_linear_attn_workspace, L.b2b_linear_attn_run,
+                             L.b2b_linear_attn_step)
 
     def _operands(self, Q, K, V, log_decay, O):
         dtype, dim = self.dtype, self.dim
@@ -316,6 +339,10 @@ class LinearAttention:
         cu[s] .. cu[s+1]-1 being sequence s (device int32); state: the states
         before them [seqs, heads, dim, dim] (zero by default).  Returns O and
         the states after them (state_out, which may be `state`)."""
+        if stream is None:
+            out = self._usual.linear(Q, K, V, log_decay, cu, state, O, state_out)
+            if out is not None:
+                return out
         rows, q, k, v, o = self._operands(Q, K, V, log_decay, O)
         seqs = _starts(cu, "cu")
         self._state(state, "state", seqs)
@@ -339,6 +366,10 @@ class LinearAttention:
         """One token of each request: row b of Q, K and V on state b
         [batch, heads, dim, dim].  Returns O and the states after it
         (state_out, which may be `state`)."""
+        if stream is None:
+            out = self._usual.linear_step(Q, K, V, log_decay, state, O, state_out)
+            if out is not None:
+                return out
         rows, q, k, v, o = self._operands(Q, K, V, log_decay, O)
         if state is None:
             raise ValueError("state: a tensor is expected")
@@ -364,6 +395,7 @@ class LinearAttention:
 
     def close(self):
         if getattr(self, "_h", None):
+            self._usual.close()
             lib().b2b_linear_attn_destroy(self._h)
             self._h = None
 

@@ -7,12 +7,14 @@ import os
 import re
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libb2b.so")
+PYATTN = os.path.join(HERE, "_attn.so")      # the attention plans' usual calls (CPython's API)
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-Wall",
@@ -101,6 +103,11 @@ def build(jobs=None, remarks=False, verbose=False):
     subprocess.check_call([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp] + sorted(objs)
                           + ["-L/opt/rocm/lib", "-lamdhip64"])
     os.replace(tmp, LIB)
+    tmp = PYATTN + ".tmp%d" % os.getpid()
+    subprocess.check_call(["g++", "-std=c++17", "-O2", "-fPIC", "-Wall", "-shared", "-D__HIP_PLATFORM_AMD__=1",
+                           "-I", os.path.join(ROOT, "include"), "-isystem", "/opt/rocm/include",
+                           "-isystem", sysconfig.get_paths()["include"], os.path.join(CSRC, "pyattn.cpp"), "-o", tmp])
+    os.replace(tmp, PYATTN)
     if verbose or remarks:
         for s, log in sorted(logs.items()):
             if log.strip():

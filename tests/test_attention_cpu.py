@@ -210,3 +210,21 @@ def test_binding_checks_linear():
             plan.step(q, k, k, g, **kw)
     with pytest.raises(cf.B2BError, match="not supported"):
         cf.LinearAttention("f16", 4, 2, 96)
+
+
+def test_usual_calls_leave_the_rest_to_python():
+    """The compiled binding takes no call whose tensors are not on a device, and
+    none of a plan that is closed; whatever it is given, it raises nothing."""
+    from chip_fusion_amd import _attn
+    plan, lin = cf.Attention("f16", 4, 2, 64), cf.LinearAttention("f16", 4, 2, 64)
+    q, k, cu, g = _t(10, 4, 64), _t(10, 2, 64), _cu(0, 10), _t(4, dtype=torch.float32)
+    u = plan._usual
+    for args in [(q, k, k, cu, None, None, False), (q, k, k, cu, cu, q, True), (None,) * 7, (1, 2, 3, 4, 5, 6, 7), (q, k), (),
+                 (q.numpy(), k, k, cu, None, None, False)]:
+        assert u.attention(*args) is None and u.prefix(*args) is None and u.linear_step(*args) is None
+        assert u.linear(*args) is None and u.linear(*args, None) is None
+    assert lin._usual.linear(q, k, k, g, cu, None, None, None) is None
+    plan.close()
+    assert u.attention(q, k, k, cu, None, None, False) is None
+    with pytest.raises(TypeError):
+        _attn.Call(1, 2)

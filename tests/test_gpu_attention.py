@@ -2,6 +2,7 @@
 definition in 64 bits, at the sizes, masks and layouts where it can go wrong."""
 import itertools
 import math
+import sys
 
 import pytest
 import torch
@@ -248,6 +249,52 @@ def test_values_that_are_not_finite_reach_only_rows_that_see_them(dtype, D, n, k
         for j, d in odd[:, h // 2].nonzero().tolist():
             want[max(j - old, 0):, h, d] += v[j, h // 2, d].double().cpu()
     R.check(got, want, b)
+
+
+def test_calls_in_python_and_compiled_agree():
+    """The same checks and results whether the compiled binding takes a call or
+    the one in Python does (here: because a stream is named); no references are
+    kept or lost."""
+    H, Hkv, D, n = 4, 2, 64, 70
+    T = torch.bfloat16
+    q, k, v = _case("bf16", H, Hkv, D, [n], [n], seed=23)
+    cu, lens = _cu([n]), torch.tensor([5, 0, 9], dtype=torch.int32, device="cuda")
+    k4, v4 = _randn(4, (3, 9, Hkv, D), T), _randn(5, (3, 9, Hkv, D), T)
+    g = torch.full((H,), -0.1, device="cuda")
+    s1, s3 = _randn(6, (1, H, D, D), torch.float32), _randn(7, (3, H, D, D), torch.float32)
+    pa, pp, pl = cf.Attention("bf16", H, Hkv, D), cf.PrefixAttention("bf16", H, Hkv, D), cf.LinearAttention("bf16", H, Hkv, D)
+    calls = [lambda **x: pa.run(q, k, v, cu, **x), lambda **x: pa.run(q, k, v, cu, cu, lse=True, **x),
+             lambda **x: pa.run(q[:3], k, v, _cu([3]), cu, O=torch.empty_like(q[:3]), **x),
+             lambda **x: pp.run(q[:3], k, v, k4, v4, lens, **x),
+             lambda **x: pl.run(q, k, v, g, cu, **x), lambda **x: pl.run(q, k, v, g, cu, state=s1, **x),
+             lambda **x: pl.step(q[:3], k[:3], v[:3], g, s3, **x)]
+    _flush("both bindings")
+    here = torch.cuda.current_stream()
+    for call in calls:
+        a, b = call(), call(stream=here)
+        a, b = (x if isinstance(x, tuple) else (x,) for x in (a, b))
+        assert len(a) == len(b) and all(torch.equal(x, y) and x.stride() == y.stride() for x, y in zip(a, b))
+    assert pa._usual.attention(q, k, v, cu, None, None, False) is not None
+    assert pp._usual.prefix(q[:3], k, v, k4, v4, lens, None) is not None
+    assert pl._usual.linear(q, k, v, g, cu, s1, None, None) is not None
+    assert pl._usual.linear_step(q[:3], k[:3], v[:3], g, s3, None, None) is not None
+    held = [q, k, v, cu, k4, v4, lens, g, s1, s3, torch.float32, pa, pp, pl]
+    before = [sys.getrefcount(x) for x in held]
+    for _ in range(50):
+        for call in calls:
+            call()
+    assert [sys.getrefcount(x) for x in held] == before
+    for bad, match in [(dict(Q=q.half()), "Q: dtype"), (dict(K=k[:, :1]), "K: shape"), (dict(V=v[1:]), "V: shape"),
+                       (dict(cu_q=cu.long()), "cu_q"), (dict(O=q[:, :, :32]), "O: shape"), (dict(cu_k=_cu([1, 2])), "cu_k"),
+                       (dict(V=v.cpu()), "V: a device")]:
+        with pytest.raises(ValueError, match=match):
+            pa.run(**{**dict(Q=q, K=k, V=v, cu_q=cu), **bad})
+    with pytest.raises(cf.B2BError):
+        pa.run(q, k, v, cu, O=q)                  # O at Q's address
+    pa.close()
+    with pytest.raises(cf.B2BError):
+        pa.run(q, k, v, cu)
+    torch.cuda.synchronize()
 
 
 def test_empty_calls():

@@ -159,6 +159,18 @@ __device__ __forceinline__ bool find_tile(const int32_t* cu_q, const int32_t* cu
     return false;
 }
 
+// As find_tile where there is one sequence: nothing to look for (77 tokens of 8
+// heads of 64: 6.0 us on the device with the search, 5.5 so).
+__device__ __forceinline__ bool only_tile(const int32_t* cu_q, const int32_t* cu_k, int rows, int keys, int group, int bm,
+                                          int tile, SeqTile* out) {
+    seq_range(cu_q, 0, rows, &out->q0, &out->nq);
+    seq_range(cu_k, 0, keys, &out->k0, &out->nk);
+    out->seq = 0;
+    out->local = tile;
+    out->tiles = (int)(((unsigned)out->nq * (unsigned)group + (unsigned)bm - 1) / (unsigned)bm);
+    return tile < out->tiles;
+}
+
 // As find_tile, up to 64 sequences, the tiles that see the most keys first:
 // workgroups are taken in order, so the launch ends on short ones (17
 // sequences of up to 800 tokens, 8 key heads: 73 us in the sequences' order,
@@ -543,7 +555,8 @@ __device__ __forceinline__ void attn_tile_body(const AttnArgs& a, unsigned char*
     const int tile = C::PART ? a.splits(rest) : rest, split = rest - tile * a.splits.d;
     SeqTile w;
     if (a.cu_q) {
-        const bool found = a.seqs <= 64 ? find_tile_by_size(a.cu_q, a.cu_k, a.seqs, (int)a.rows, (int)a.keys, a.group.d, C::BM,
+        const bool found = a.seqs == 1 ? only_tile(a.cu_q, a.cu_k, (int)a.rows, (int)a.keys, a.group.d, C::BM, tile, &w)
+                           : a.seqs <= 64 ? find_tile_by_size(a.cu_q, a.cu_k, a.seqs, (int)a.rows, (int)a.keys, a.group.d, C::BM,
                                                             a.causal, tile, &w)
                                         : find_tile(a.cu_q, a.cu_k, a.seqs, (int)a.rows, (int)a.keys, a.group.d, C::BM, 0,
                                                     tile, &w);

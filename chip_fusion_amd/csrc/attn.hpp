@@ -315,6 +315,29 @@ __device__ __forceinline__ int attn_kbase(int lane, int odd) {
     return row * 64 + ((c ^ ((row >> 2) & 3)) << 4);
 }
 
+// Whether any sequence holds this lane's row, which 16 lanes share; every lane
+// of the wave is active.  from, to: where lane's sequence of the first 64 starts
+// and ends, which the caller has asked for early.  (Starts may be in any order,
+// so it takes a look at each sequence.)
+__device__ __forceinline__ bool in_a_sequence(const AttnArgs& a, int row, int from, int to) {
+    const int lane = threadIdx.x & 63;
+    bool in = false;
+    for (int s0 = 0;;) {
+        // (a row is 0 .. rows - 1, so clamping changes nothing here)
+        const bool have = s0 + lane < a.seqs;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const int r = __builtin_amdgcn_readlane(row, 16 * g);
+            in |= __ballot(have && r >= from && r < to) && lane >> 4 == g;
+        }
+        s0 += 64;
+        if (s0 >= a.seqs || __all(in)) return in;
+        const int s = s0 + lane < a.seqs ? s0 + lane : a.seqs - 1;
+        from = a.cu_q[s];
+        to = a.cu_q[s + 1];
+    }
+}
+
 // The softmax state of one query row a lane.
 struct RowState {
     float m, l;
@@ -791,12 +814,21 @@ __global__ __launch_bounds__(256, 3) void attn_prefix_kernel(AttnArgs p, AttnArg
 // loads' latency (32 rows of 32 heads in 17 parts: 6.0 us by 16 lanes, 4.6 so);
 // else it is the parts' bytes (2500 rows of 24 heads of 96 in two parts, 47 MB
 // read: 10 us).
+// A row that belongs to no sequence has no partial results, and its output stays
+// as it is.
 template <int DT, int SUB>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int slots) {
     const int lane = threadIdx.x & 15, sub = SUB == 1 ? 0 : (threadIdx.x >> 4) & (SUB - 1);
-    const int64_t n = a.rows * a.heads, at = (int64_t)blockIdx.x * (16 / SUB) + threadIdx.x / (16 * SUB);
-    if (at >= n) return;
+    const int64_t n = a.rows * a.heads, mine = (int64_t)blockIdx.x * (16 / SUB) + threadIdx.x / (16 * SUB);
+    // places past the last stay, as copies of it that write nothing: every lane looks at sequences
+    const int64_t at = mine < n ? mine : n - 1;
     const int64_t row = at / a.heads;
+    int from = 0, to = 0;
+    if (a.cu_q) {
+        const int s = (int)(threadIdx.x & 63) < a.seqs ? threadIdx.x & 63 : a.seqs - 1;
+        from = a.cu_q[s];
+        to = a.cu_q[s + 1];
+    }
     const int head = (int)(at - row * a.heads);
     float m = -__builtin_inff(), sum = 0.f, x[8] = {};
     const bool live = 8 * lane < a.dim;
@@ -848,8 +880,8 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int slots) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] += __shfl_xor(x[e], d);
         }
-        if (sub) return;
     }
+    if ((a.cu_q && !in_a_sequence(a, (int)row, from, to)) || mine >= n || sub) return;
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     if (live)
         *(u4_t*)((char*)a.O + (row * a.ldo + (int64_t)head * a.hso + 8 * lane) * 2) =

@@ -147,7 +147,9 @@ __device__ __forceinline__ u4_t lin_rest(const f16x_t& x, int k, u4_t& first) {
 
 // The exponent e for which the state's largest magnitude times 2^-e is about
 // 2^13: fp16 copies of larger or much smaller states would leave its range.
-// Uniform over the wave; 0 for states that are in range as they are.
+// Uniform over the wave; 0 for states that are in range as they are; -126 or
+// above, so that 2^e and 2^-e are both finite and normal (smaller states have
+// few bits left, and their copy holds them all).
 template <int NT>
 __device__ __forceinline__ int lin_exponent(const f16x_t (&s)[NT]) {
     float m = 0.f;
@@ -171,7 +173,8 @@ __device__ __forceinline__ int lin_exponent(const f16x_t (&s)[NT]) {
         for (int d = 1; d < 64; d <<= 1) m = __builtin_fmaxf(m, __shfl_xor(m, d));
     }
     if (!(m > 0.f)) return 0;
-    return __builtin_amdgcn_readfirstlane(__builtin_amdgcn_frexp_expf(m) - 13);
+    const int e = __builtin_amdgcn_readfirstlane(__builtin_amdgcn_frexp_expf(m) - 13);
+    return e < -126 ? -126 : e;
 }
 
 // Whether one of a lane's packed values is not finite.

@@ -1,0 +1,90 @@
+"""Linear attention in fp16 where something leaves fp16's range, or falls below
+it, while the operands and the results do not: states, scores, a chunk's decayed
+values.  Against the recurrence in 64 bits.
+
+Bounds (u = 2^-11, A = scale sum_j lambda^(i-j) sum_d |q_id k_jd| |v_j| over all
+keys and the first state, y: the same sum without q and scale).  Outputs: a
+score is held in two parts (2^-21 of its row's largest in the chunk or better,
+and every tested row's values are of one size: 32 keys, 2^-16 A), the state's
+copy is rounded once (u A), the result once (u of itself; 2^-25 where it is
+subnormal), the rest is float32: D products and 72 sums of 2^-24, 2^-22 a chunk
+for the powers of lambda, 2^-20 more.  States: float32 terms, 72 sums of 2^-24, 2^-22
+a chunk, 2^-21; values below float32's normal range (2^-126) count as nothing."""
+import math
+
+import pytest
+import torch
+
+import attn_ref as R
+import chip_fusion_amd as cf
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -11
+
+
+def _flush(msg):
+    print(f"\n[case] {msg}", flush=True)
+
+
+def _randn(seed, shape, std=1.0, dtype=torch.float16):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(shape, generator=g, device="cuda") * std).to(dtype)
+
+
+def _cu(lens):
+    return torch.tensor(R.starts(lens), dtype=torch.int32, device="cuda")
+
+
+def recurrence(q, k, v, decay, state, scale):
+    """One sequence: O, its bound, the state after it and its bound."""
+    n, H, D = q.shape
+    q, k, v, g = (x.detach().cpu().double() for x in (q, k, v, decay))
+    lam = torch.exp(g)[:, None, None]
+    x = torch.zeros((H, D, D), dtype=torch.float64) if state is None else state.detach().cpu().double()[0]
+    y = x.abs()
+    out, bound = torch.zeros_like(q), torch.zeros_like(q)
+    for t in range(n):
+        term = k[t][:, :, None] * v[t][:, None, :]
+        x, y = lam * x + term, lam * y + term.abs()
+        out[t] = scale * (q[t][:, None] @ x)[:, 0]
+        A = scale * (q[t].abs()[:, None] @ y)[:, 0]
+        rel = (D + 72) * R.E32 + (t // 32 + 1) * 2.0 ** -22 + 2.0 ** -20 + 2.0 ** -16
+        bound[t] = (U * (1 + U) + rel) * A + U * out[t].abs() + 2.0 ** -25
+    return out, bound, x[None], ((72 * R.E32 + (n // 32 + 1) * 2.0 ** -22 + 2.0 ** -21) * y + 2.0 ** -126)[None]
+
+
+def _check(what, q, k, v, decay, state, scale=None):
+    n, H, D = q.shape
+    plan = cf.LinearAttention("f16", H, H, D, scale=scale)
+    got, after = plan.run(q, k, v, decay, _cu([n]), state=state)
+    torch.cuda.synchronize()
+    want, b, ws, bs = recurrence(q, k, v, decay, state, D ** -0.5 if scale is None else scale)
+    assert bool((want.abs() < 65504).all())
+    R.check(got, want, b, f"{what}: O")
+    R.check(after, ws, bs, f"{what}: state")
+    return got, after
+
+
+@pytest.mark.parametrize("D,n", [(64, 400), (128, 900), (64, 1700)])
+@pytest.mark.parametrize("zero", ["k", "v"])
+def test_states_that_decay_to_nothing(D, n, zero):
+    """Hundreds of masked tokens (zero keys or values) after a state: it decays
+    through all of float32's range, whole and cut into segments, and on behind
+    them tokens count as before."""
+    decay = torch.tensor([-0.7, -0.25, -0.06, 0.0], device="cuda")
+    _flush(f"decaying state {D} {n} {zero}")
+    q, k, v = _randn(1, (n, 4, D)), _randn(2, (n, 4, D), 0.7), _randn(3, (n, 4, D))
+    (k if zero == "k" else v)[:n - 20] = 0
+    _check("decayed", q, k, v, decay, _randn(4, (1, 4, D, D), 4.0, torch.float32))
+
+
+@pytest.mark.parametrize("size", [1e-36, 1e-40, 2.0 ** -120, 2.0 ** -149, 1e30])
+@pytest.mark.parametrize("n", [40, 600])
+def test_states_of_any_size(size, n):
+    _flush(f"state of {size}, {n} tokens")
+    q, k, v = _randn(1, (n, 2, 64)), torch.zeros((n, 2, 64), dtype=torch.float16, device="cuda"), _randn(3, (n, 2, 64))
+    state = torch.full((1, 2, 64, 64), size, device="cuda")
+    state[:, :, ::3] = 0
+    # (large states: outputs in range, by the scale)
+    _check("tiny", q, k, v, torch.tensor([-0.01, -0.3], device="cuda"), state, None if size < 1 else 1e-30)

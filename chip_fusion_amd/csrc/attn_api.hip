@@ -318,7 +318,7 @@ b2bk::LinArgs lin_args(const b2b_linear_attn_plan* p, const b2b_rows_t& Q, const
     a.K = dev(K, p->dim);
     a.V = dev(V, p->dim);
     a.O = const_cast<void*>(O.data);
-    a.ldo = O.row_stride;
+    a.ldo = dev(O, p->dim).ld;      // a chunk's stores step by it past a single row too
     a.hso = O.head_stride;
     a.heads = p->heads;
     a.kv_heads = p->kv_heads;

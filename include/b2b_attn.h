@@ -117,7 +117,8 @@ typedef struct b2b_linear_attn_plan* b2b_linear_attn_t;   /* opaque, owned by th
  *   dtype       B2B_DTYPE_F16 or B2B_DTYPE_BF16: Q, K, V and O; states are
  *               float32 and updated in float32 precision; the scores q.k are
  *               held in two parts of dtype, the copy of the state that meets q
- *               is rounded to it
+ *               is rounded to it (fp16: a row's scores and the copy are scaled
+ *               by powers of two, so both may be of any size)
  *   head_dim    64 or 128
  *   scale       finite and positive (0: head_dim ^ -1/2)
  */

@@ -88,3 +88,68 @@ def test_states_of_any_size(size, n):
     state[:, :, ::3] = 0
     # (large states: outputs in range, by the scale)
     _check("tiny", q, k, v, torch.tensor([-0.01, -0.3], device="cuda"), state, None if size < 1 else 1e-30)
+
+
+def test_scores_past_fp16():
+    """Scores past 65504 of operands and results that fit."""
+    D, n = 128, 100
+    decay = torch.tensor([-0.5, -0.02], device="cuda")
+    big = torch.full((n, 2, D), 100.0, dtype=torch.float16, device="cuda")
+    _flush("scores past fp16: all alike")
+    _check("alike", big, big, torch.full_like(big, 0.001), decay, None)
+    _flush("scores past fp16: scale 1")
+    q, k = _randn(1, (n, 2, D), 30.0), _randn(2, (n, 2, D), 30.0)
+    q, k = (x + 25 * torch.sign(x) for x in (q, k))
+    k[::2] = q[::2]                                     # large at the token itself
+    v = torch.sign(_randn(3, (n, 2, D))) * 0.01
+    state = _randn(4, (1, 2, D, D), 0.1, torch.float32)
+    got, after = _check("scale 1", q, k, v, decay, state, 1.0)
+    # a prompt's first token is what a step gives
+    one, s = cf.LinearAttention("f16", 2, 2, D, scale=1.0).step(q[:1], k[:1], v[:1], decay, state)
+    want, b, ws, bs = recurrence(q[:1], k[:1], v[:1], decay, state, 1.0)
+    R.check(one, want, b)
+    R.check(got[:1], want, b)
+
+
+def test_scores_past_fp16_beside_infinities():
+    """The same where a later value is infinite: rows before it, whose scores
+    are large, stay right."""
+    D, n = 64, 70
+    _flush("scores past fp16 beside an infinity")
+    q = torch.full((n, 1, D), 200.0, dtype=torch.float16, device="cuda")
+    v = torch.full((n, 1, D), 0.001, dtype=torch.float16, device="cuda")
+    decay = torch.tensor([-1.0], device="cuda")
+    want, b, _, _ = recurrence(q, q, v, decay, None, 0.125)
+    v[50, 0, 7] = math.inf
+    got, after = cf.LinearAttention("f16", 1, 1, D).run(q, q, v, decay, _cu([n]))
+    torch.cuda.synchronize()
+    assert not torch.isfinite(got[50:, 0, 7]).any() and not torch.isfinite(after[0, 0, :, 7]).any()
+    keep = torch.ones((n, 1, D), dtype=torch.bool)
+    keep[50:, 0, 7] = False
+    # (the careful pass takes each score's first part alone: U of A more)
+    R.check(got.cpu()[keep], want[keep], (b + U * want.abs())[keep])
+
+
+def test_zero_queries_on_large_states():
+    """Rows of zeros stay zeros, however large the state is."""
+    _flush("zero queries")
+    q, k, v = (torch.zeros((40, 2, 64), dtype=torch.float16, device="cuda") for _ in range(3))
+    k[20:], v[20:] = 1.0, 2.0
+    state = _randn(4, (1, 2, 64, 64), 1e38, torch.float32).clamp(-3e38, 3e38)
+    for scale in (None, 1e6):
+        got, _ = cf.LinearAttention("f16", 2, 2, 64, scale=scale).run(q, k, v, torch.tensor([0.0, -0.1], device="cuda"),
+                                                                      _cu([40]), state=state)
+        torch.cuda.synchronize()
+        assert bool((got == 0).all())
+
+
+def test_scores_below_fp16():
+    """Scores of 2^-20 and below with values of thousands."""
+    D, n = 64, 100
+    decay = torch.tensor([-0.5, -0.02], device="cuda")
+    for std in (1e-3, 1e-4):
+        _flush(f"scores below fp16: {std}")
+        q, k = _randn(1, (n, 2, D), std), _randn(2, (n, 2, D), std)
+        k[::2] = q[::2]
+        v = torch.sign(_randn(3, (n, 2, D))) * 30000.0
+        _check("small scores", q, k, v, decay, None)

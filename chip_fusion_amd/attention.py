@@ -144,9 +144,10 @@ def _ptr(t):
 
 def _usual(handle, heads, kv_heads, dim, dtype, workspace, run, step=None):
     """The plan's usual calls (pyattn.cpp): on the current stream, tensors of the
-    common layouts; they return None where the checks here are to be made."""
+    common layouts; they return None, with nothing launched, where the checks here
+    are to be made."""
     at = lambda f: 0 if f is None else ctypes.cast(f, ctypes.c_void_p).value
-    return _attn.Call(handle.value, at(workspace), at(run), at(step), heads, kv_heads, dim, dtype, torch)
+    return _attn.Call(handle.value, at(workspace), at(run), at(step), heads, kv_heads, dim, dtype, torch, _check)
 
 
 class _Heads:

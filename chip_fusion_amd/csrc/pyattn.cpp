@@ -2,6 +2,8 @@
 // nearly every call passes (tensors of the plan's type and heads on the current
 // device, the current stream) is checked, allocated and launched here; anything
 // else returns None, and the binding's own checks in Python take it from there.
+// None means that nothing has been launched: a status of the run itself is
+// raised, since a run that is made again would take states in place twice.
 // 77 tokens take 6.4 us a call so, about what the device takes for them, and 10.0
 // with all of it in Python.
 //
@@ -24,7 +26,7 @@ struct Call {
     void *handle, *workspace, *run, *step;
     long heads, kv_heads, dim;
     // borrowed from the torch module for as long as it lives, held all the same
-    PyObject *dtype, *f32, *i32, *u8, *tensor, *empty_like, *get_device, *raw_stream;
+    PyObject *dtype, *f32, *i32, *u8, *tensor, *empty_like, *get_device, *raw_stream, *check;
 };
 
 struct Ref {       // an owned reference
@@ -166,6 +168,13 @@ PyObject* other() {
     Py_RETURN_NONE;
 }
 
+// What a run that was not accepted ends in: check(status, name), which raises.
+PyObject* failed(Call* c, int status, const char* name) {
+    Ref r(PyObject_CallFunction(c->check, "is", status, name));
+    if (r.o) PyErr_Format(PyExc_RuntimeError, "%s: status %d", name, status);
+    return nullptr;
+}
+
 PyObject* call_attention(PyObject* self, PyObject* const* a, Py_ssize_t na) {
     Call* c = (Call*)self;
     if (na != 7 || !c->handle) return other();
@@ -194,7 +203,7 @@ PyObject* call_attention(PyObject* self, PyObject* const* a, Py_ssize_t na) {
     st = ((decltype(&b2b_attn_run))c->run)((b2b_attn_t)c->handle, (int32_t)(nq - 1), rows, keys, q, k, v, o, (int32_t*)pq,
                                            (int32_t*)pk, (float*)l, w, bytes, (hipStream_t)s);
     Py_END_ALLOW_THREADS
-    if (st) return other();
+    if (st) return failed(c, st, "b2b_attn_run");
     return lse.o ? PyTuple_Pack(2, out.o, lse.o) : out.take();
 }
 
@@ -222,7 +231,7 @@ PyObject* call_prefix(PyObject* self, PyObject* const* a, Py_ssize_t na) {
     st = ((decltype(&b2b_prefix_attn_run))c->run)((b2b_attn_t)c->handle, (int32_t)batch, prefix, own, q, kp, vp, k, ks, v, vs,
                                                   (int32_t*)lens, o, w, bytes, (hipStream_t)s);
     Py_END_ALLOW_THREADS
-    return st ? other() : out.take();
+    return st ? failed(c, st, "b2b_prefix_attn_run") : out.take();
 }
 
 // Q, K, V, log_decay: what prompts and steps have alike
@@ -260,7 +269,7 @@ PyObject* call_linear(PyObject* self, PyObject* const* a, Py_ssize_t na) {
     st = ((decltype(&b2b_linear_attn_run))c->run)((b2b_linear_attn_t)c->handle, (int32_t)(ncu - 1), rows, q, k, v, o, (float*)g,
                                                   (int32_t*)cu, (float*)s0, (float*)s1, w, bytes, (hipStream_t)s);
     Py_END_ALLOW_THREADS
-    return st ? other() : PyTuple_Pack(2, out.o, after.o);
+    return st ? failed(c, st, "b2b_linear_attn_run") : PyTuple_Pack(2, out.o, after.o);
 }
 
 PyObject* call_linear_step(PyObject* self, PyObject* const* a, Py_ssize_t na) {
@@ -286,7 +295,7 @@ PyObject* call_linear_step(PyObject* self, PyObject* const* a, Py_ssize_t na) {
     st = ((decltype(&b2b_linear_attn_step))c->step)((b2b_linear_attn_t)c->handle, (int32_t)rows, q, k, v, o, (float*)g, (float*)s0,
                                                     (float*)s1, (hipStream_t)s);
     Py_END_ALLOW_THREADS
-    return st ? other() : PyTuple_Pack(2, out.o, after.o);
+    return st ? failed(c, st, "b2b_linear_attn_step") : PyTuple_Pack(2, out.o, after.o);
 }
 
 PyObject* call_close(PyObject* self, PyObject*) {
@@ -295,17 +304,19 @@ PyObject* call_close(PyObject* self, PyObject*) {
 }
 
 PyObject** const held(Call* c, int i) {
-    PyObject** all[] = {&c->dtype, &c->f32, &c->i32, &c->u8, &c->tensor, &c->empty_like, &c->get_device, &c->raw_stream};
-    return i < 8 ? all[i] : nullptr;
+    PyObject** all[] = {&c->dtype, &c->f32, &c->i32, &c->u8, &c->tensor, &c->empty_like, &c->get_device, &c->raw_stream,
+                        &c->check};
+    return i < 9 ? all[i] : nullptr;
 }
 
-// Call(handle, workspace, run, step, heads, kv_heads, dim, dtype, torch): addresses of
-// the plan and of the library's functions, as integers.
+// Call(handle, workspace, run, step, heads, kv_heads, dim, dtype, torch, check): addresses
+// of the plan and of the library's functions, as integers; check(status, name)
+// raises for a status that is not 0.
 PyObject* call_new(PyTypeObject* type, PyObject* args, PyObject*) {
     unsigned long long handle, workspace, run, step;
     long heads, kv, dim;
-    PyObject *dtype, *torch;
-    if (!PyArg_ParseTuple(args, "KKKKlllOO", &handle, &workspace, &run, &step, &heads, &kv, &dim, &dtype, &torch))
+    PyObject *dtype, *torch, *check;
+    if (!PyArg_ParseTuple(args, "KKKKlllOOO", &handle, &workspace, &run, &step, &heads, &kv, &dim, &dtype, &torch, &check))
         return nullptr;
     Call* c = (Call*)type->tp_alloc(type, 0);
     if (!c) return nullptr;
@@ -318,6 +329,8 @@ PyObject* call_new(PyTypeObject* type, PyObject* args, PyObject*) {
     c->dim = dim;
     Py_INCREF(dtype);
     c->dtype = dtype;
+    Py_INCREF(check);
+    c->check = check;
     Ref C(PyObject_GetAttrString(torch, "_C"));
     c->f32 = PyObject_GetAttrString(torch, "float32");
     c->i32 = PyObject_GetAttrString(torch, "int32");

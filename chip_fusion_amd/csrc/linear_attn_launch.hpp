@@ -2,6 +2,7 @@
 #pragma once
 #include <hip/hip_runtime.h>
 
+#include "attn_launch.hpp"
 #include "linear_attn.hpp"
 
 namespace b2b {
@@ -21,28 +22,19 @@ struct LinLaunchers {
     static hipError_t run(const b2bk::LinArgs& a, int dim, bool state, int64_t segs, hipStream_t s) {
         auto go = [&](auto c) {
             using C = decltype(c);
-            hipLaunchKernelGGL(b2bk::lin_kernel<C>, dim3((unsigned)(segs * a.heads)), dim3(C::THREADS), 0, s, a);
+            return launch(b2bk::lin_kernel<C>, (unsigned)(segs * a.heads), C::THREADS, s, a);
         };
-        if (dim == 64) {
-            if (state) go(b2bk::LinCfg<DT, 64, true>{});
-            else go(b2bk::LinCfg<DT, 64, false>{});
-        } else {
-            if (state) go(b2bk::LinCfg<DT, 128, true>{});
-            else go(b2bk::LinCfg<DT, 128, false>{});
-        }
-        return hipGetLastError();
+        if (dim == 64) return state ? go(b2bk::LinCfg<DT, 64, true>{}) : go(b2bk::LinCfg<DT, 64, false>{});
+        return state ? go(b2bk::LinCfg<DT, 128, true>{}) : go(b2bk::LinCfg<DT, 128, false>{});
     }
     static hipError_t scan(const b2bk::LinArgs& a, int dim, hipStream_t s) {
         const unsigned grid = (unsigned)((int64_t)a.seqs * a.heads * (dim * dim / 1024));
-        if (dim == 64) hipLaunchKernelGGL(b2bk::lin_scan_kernel<64>, dim3(grid), dim3(256), 0, s, a);
-        else hipLaunchKernelGGL(b2bk::lin_scan_kernel<128>, dim3(grid), dim3(256), 0, s, a);
-        return hipGetLastError();
+        return dim == 64 ? launch(b2bk::lin_scan_kernel<64>, grid, 256, s, a) : launch(b2bk::lin_scan_kernel<128>, grid, 256, s, a);
     }
     static hipError_t step(const b2bk::LinArgs& a, int dim, hipStream_t s) {
-        const dim3 grid((unsigned)(a.rows * a.heads));
-        if (dim == 64) hipLaunchKernelGGL((b2bk::lin_step_kernel<DT, 64>), grid, dim3(256), 0, s, a);
-        else hipLaunchKernelGGL((b2bk::lin_step_kernel<DT, 128>), grid, dim3(256), 0, s, a);
-        return hipGetLastError();
+        const unsigned grid = (unsigned)(a.rows * a.heads);
+        return dim == 64 ? launch(b2bk::lin_step_kernel<DT, 64>, grid, 256, s, a)
+                         : launch(b2bk::lin_step_kernel<DT, 128>, grid, 256, s, a);
     }
     static const LinLaunch& table() {
         static const LinLaunch t = {&run, &scan, &step};

@@ -117,6 +117,11 @@ class _Workspaces:
     def __init__(self, call, handle):
         self._call, self._handle, self._bytes = call, handle, {}
 
+    def close(self):
+        """The plan is gone: asking is an error."""
+        self._handle = None
+        self._bytes.clear()
+
     def get(self, like, *sizes):
         """The workspace (a tensor, or None), its address and its bytes."""
         n = self._bytes.get(sizes)
@@ -170,6 +175,7 @@ class _Heads:
     def close(self):
         if getattr(self, "_h", None):
             self._usual.close()
+            self._workspaces.close()
             lib().b2b_attn_destroy(self._h)
             self._h = None
 
@@ -397,6 +403,7 @@ class LinearAttention:
     def close(self):
         if getattr(self, "_h", None):
             self._usual.close()
+            self._workspaces.close()
             lib().b2b_linear_attn_destroy(self._h)
             self._h = None
 

@@ -101,3 +101,22 @@ def test_what_is_refused_before_the_run_is_left_to_python():
     """(A step asks for no workspace.)"""
     for plan, name, call in _calls(Plan(0, 1, three=True), Plan(0, 1))[:3]:
         assert call() is None and plan.runs == 0, name
+
+
+@pytest.mark.parametrize("make,sizes", [
+    (lambda: cf.Attention("f16", H, KV, D), (1, 4, 4096)), (lambda: cf.PrefixAttention("bf16", H, KV, D), (4, 100, 10)),
+    (lambda: cf.LinearAttention("f16", H, KV, D), (1, 5000)),
+])
+@pytest.mark.parametrize("asked", [False, True])
+def test_a_closed_plan_is_asked_for_nothing(make, sizes, asked):
+    """Its memory is freed: sizes of a workspace, new ones and ones that it was
+    asked for before, are an error."""
+    plan = make()
+    like = Tensor((1,), "f16")
+    like.new_empty = lambda n, dtype: Tensor((n,), dtype)
+    if asked:
+        assert plan._workspaces.get(like, *sizes)[2] > 0
+    plan.close()
+    with pytest.raises(cf.B2BError):
+        plan._workspaces.get(like, *sizes)
+    plan.close()

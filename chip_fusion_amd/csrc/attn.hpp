@@ -808,8 +808,8 @@ __global__ __launch_bounds__(256, 3) void attn_prefix_kernel(AttnArgs p, AttnArg
 // Joining partial results: 16 lanes a (row, head), 8 columns a lane
 // ---------------------------------------------------------------------------
 // O = sum_s w_s O_s / sum_s w_s with w_s = 2^(lse_s - max); parts that saw no
-// key have lse = -inf and weight 0.  One pass with a running maximum, four
-// parts' loads in flight.  SUB = 4: the quarters of a wave take every fourth
+// key have lse = -inf and weight 0.  One pass with a running maximum, three or
+// four parts' loads in flight.  SUB = 4: the quarters of a wave take every fourth
 // part of one (row, head) each, for few rows of many parts, whose time is the
 // loads' latency (32 rows of 32 heads in 17 parts: 6.0 us by 16 lanes, 4.6 so);
 // else it is the parts' bytes (2500 rows of 24 heads of 96 in two parts, 47 MB
@@ -818,21 +818,24 @@ __global__ __launch_bounds__(256, 3) void attn_prefix_kernel(AttnArgs p, AttnArg
 // as it is.
 template <int DT, int SUB>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int slots) {
+    constexpr int PER = SUB == 1 ? 3 : 4;       // parts' loads in flight
     const int lane = threadIdx.x & 15, sub = SUB == 1 ? 0 : (threadIdx.x >> 4) & (SUB - 1);
-    const int64_t n = a.rows * a.heads, mine = (int64_t)blockIdx.x * (16 / SUB) + threadIdx.x / (16 * SUB);
+    // (rows x heads stays below 2^31)
+    const int n = (int)a.rows * a.heads, mine = (int)blockIdx.x * (16 / SUB) + (int)threadIdx.x / (16 * SUB);
     // places past the last stay, as copies of it that write nothing: every lane looks at sequences
-    const int64_t at = mine < n ? mine : n - 1;
-    const int64_t row = at / a.heads;
+    const int at = mine < n ? mine : n - 1, row = at / a.heads;
     int from = 0, to = 0;
     if (a.cu_q) {
         const int s = (int)(threadIdx.x & 63) < a.seqs ? threadIdx.x & 63 : a.seqs - 1;
         from = a.cu_q[s];
         to = a.cu_q[s + 1];
     }
-    const int head = (int)(at - row * a.heads);
+    const int head = at - row * a.heads;
     float m = -__builtin_inff(), sum = 0.f, x[8] = {};
     const bool live = 8 * lane < a.dim;
-    const float* p = a.part + at * a.dim + 8 * lane;
+    const float* p = a.part + (int64_t)at * a.dim + 8 * lane;
+    const int64_t slot = (int64_t)n * a.dim;
+    float least = __builtin_inff();     // of the parts that saw keys
     // to a new maximum (0 for -inf: nothing has been seen)
     auto scale_to = [&](float m1) __attribute__((always_inline)) {
         const float f = __builtin_amdgcn_exp2f(m - m1);
@@ -841,29 +844,30 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int slots) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = f == 0.f ? 0.f : x[e] * f;
     };
-    for (int s0 = sub; s0 < slots; s0 += 4 * SUB) {
-        float w[4], m1 = m;
-        f4_t v[4][2];
+    for (int s0 = sub; s0 < slots; s0 += PER * SUB) {
+        float w[PER], m1 = m;
+        f4_t v[PER][2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < PER; ++i) {
             const bool in = s0 + i * SUB < slots;
             const int s = in ? s0 + i * SUB : s0;
-            w[i] = in ? a.part_lse[s * n + at] : -__builtin_inff();
+            w[i] = in ? a.part_lse[(int64_t)s * n + at] : -__builtin_inff();
             v[i][0] = v[i][1] = f4_t{0.f, 0.f, 0.f, 0.f};
             if (live) {
-                v[i][0] = *(const f4_t*)(p + s * n * a.dim);
-                v[i][1] = *(const f4_t*)(p + s * n * a.dim + 4);
+                v[i][0] = *(const f4_t*)(p + s * slot);
+                v[i][1] = *(const f4_t*)(p + s * slot + 4);
             }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) m1 = __builtin_fmaxf(m1, w[i]);
+        for (int i = 0; i < PER; ++i) m1 = __builtin_fmaxf(m1, w[i]);
         const float m0 = m1 == -__builtin_inff() ? 0.f : m1;
         scale_to(m0);
         m = m1;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < PER; ++i) {
             const float f = __builtin_amdgcn_exp2f(w[i] - m0);
             sum += f;
+            least = __builtin_fminf(least, w[i] == -__builtin_inff() ? __builtin_inff() : w[i]);
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] = f == 0.f ? x[e] : __builtin_fmaf(f, v[i][e >> 2][e & 3], x[e]);
         }
@@ -881,10 +885,21 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int slots) {
             for (int e = 0; e < 8; ++e) x[e] += __shfl_xor(x[e], d);
         }
     }
-    if ((a.cu_q && !in_a_sequence(a, (int)row, from, to)) || mine >= n || sub) return;
+    if (__any(least - m < -126.f)) {
+        // a part's weight may have been 0: its infinities and NaN are not left out
+#pragma unroll 1
+        for (int s = 0; s < slots; ++s)
+            if (live && a.part_lse[(int64_t)s * n + at] != -__builtin_inff())
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float y = p[s * slot + e];
+                    if (!(__builtin_fabsf(y) <= -kLowest)) x[e] += y;
+                }
+    }
+    if ((a.cu_q && !in_a_sequence(a, row, from, to)) || mine >= n || sub) return;
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     if (live)
-        *(u4_t*)((char*)a.O + (row * a.ldo + (int64_t)head * a.hso + 8 * lane) * 2) =
+        *(u4_t*)((char*)a.O + ((int64_t)row * a.ldo + (int64_t)head * a.hso + 8 * lane) * 2) =
             u4_t{Ty<DT>::pack(x[0] * inv, x[1] * inv), Ty<DT>::pack(x[2] * inv, x[3] * inv),
                  Ty<DT>::pack(x[4] * inv, x[5] * inv), Ty<DT>::pack(x[6] * inv, x[7] * inv)};
     if (lane == 0 && a.lse) a.lse[at] = sum == 0.f ? -__builtin_inff() : (m + __builtin_amdgcn_logf(sum)) * kLn2;

@@ -68,7 +68,8 @@ b2b_status_t b2b_attn_create(b2b_attn_t* plan, b2b_dtype_t dtype, int32_t heads,
  * B2B_ATTN_CAUSAL those up to its own place counted from the end (a prompt's
  * piece behind earlier keys).  A row that sees no key gets 0.  Infinities and
  * NaN reach the rows that see them and no others (32 rows whose results are
- * not all finite are computed again, which takes some 15 times as long).
+ * not all finite are computed again, which takes some 15 times as long); an
+ * infinity whose probability is below float32's range may come out as NaN.
  *   seqs        sequences; cu_q and cu_k hold seqs + 1 values (device); cu_k
  *               may be cu_q
  *   rows, keys  rows that Q and O, and K and V, hold: cu values past them are

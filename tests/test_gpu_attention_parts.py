@@ -101,3 +101,39 @@ def test_graph_replays_with_fewer_rows():
         lo, hi = a[0], a[-1]
         R.check(O[lo:hi], want[lo:hi], bound[lo:hi] + 2.0 ** -20 * want[lo:hi].abs())
         assert bool((O[:lo] == 7.0).all()) and bool((O[hi:] == 7.0).all())
+
+
+@pytest.mark.parametrize("dtype,D", [("f16", 64), ("bf16", 128)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_infinities_of_little_weight_stay(dtype, D, causal):
+    """An infinite value among keys whose weight is far below float32's range
+    beside another part's (their scores differ by 300): its column is infinite
+    as the definition has it, whichever part comes first."""
+    n, keys, H = 9, 3000, 2
+    for at, big in ((10, keys - 40), (keys - 40, 10)):
+        _flush(f"infinity of little weight {dtype} {D} {causal} {at}")
+        q = torch.ones((n, H, D), dtype=DT[dtype], device="cuda")
+        k, v = torch.zeros((keys, H, D), dtype=DT[dtype], device="cuda"), _randn(3, (keys, H, D), DT[dtype])
+        k[big] = 300.0 / D
+        v[at, 0, 5], v[at, 1, 3], v[at, 1, 4] = math.inf, -math.inf, math.nan
+        plan = cf.Attention(dtype, H, H, D, causal=causal, scale=1.0)
+        assert _is_split(plan, 1, n, keys)
+        got = plan.run(q, k, v, _at([0, n]), _at([0, keys]))
+        torch.cuda.synchronize()
+        want, _, b, _ = R.attention(q, k, torch.where(torch.isfinite(v), v, 0.0), [0, n], [0, keys], causal, 1.0)
+        want[:, 0, 5], want[:, 1, 3], want[:, 1, 4] = math.inf, -math.inf, math.nan
+        R.check(got, want, b + 2.0 ** -20)
+
+
+def test_infinities_of_little_weight_in_a_prefix_stay():
+    H, D, P, S, T = 2, 64, 1000, 40, torch.bfloat16
+    _flush("infinity of little weight, prefix")
+    q, k = torch.ones((3, H, D), dtype=T, device="cuda"), torch.zeros((3, S, H, D), dtype=T, device="cuda")
+    k[:, 7] = 300.0 / D
+    kp, vp, v = torch.zeros((P, H, D), dtype=T, device="cuda"), _randn(2, (P, H, D), T), _randn(3, (3, S, H, D), T)
+    vp[500, 0, 5], vp[20, 1, 7] = math.inf, -math.inf
+    lens = _at([S, 0, 8])
+    got = cf.PrefixAttention("bf16", H, H, D, scale=1.0).run(q, kp, vp, k, v, lens)
+    torch.cuda.synchronize()
+    odd = ~torch.isfinite(got)
+    assert bool(odd[:, 0, 5].all()) and bool(odd[:, 1, 7].all()) and int(odd.sum()) == 6

@@ -33,8 +33,8 @@
 //
 // The state is float32 and so are its terms: lambda^(n-1-j) v_j is split into
 // parts of the 16-bit type that together hold its 24 bits (bf16: three; fp16:
-// two, the second scaled by 2^11), each a pass of matrix instructions with the
-// exact k_j.  What ends in the 16-bit output alone is held in its type: the
+// two, of values scaled into its range), each a pass of matrix instructions with
+// the exact k_j.  What ends in the 16-bit output alone is held in its type: the
 // scores in two parts, and, as q's partner, a copy of the state, rounded once.
 // fp16 holds neither over its range: a row's scores, and the copy, are scaled by
 // powers of two that the float32 accumulators take out again.
@@ -110,8 +110,8 @@ __device__ __forceinline__ u4_t lin_tfrag(const unsigned char* p, const int (&tb
     return out;
 }
 
-// Two values as PARTS 16-bit parts each, packed: their sum holds 24 bits
-// (fp16: the second part is scaled by 2^11).
+// Two values as PARTS 16-bit parts each, packed: their sum holds 24 bits (fp16:
+// of values that are scaled into its range).
 template <int DT, int PARTS>
 __device__ __forceinline__ void lin_split(float x, float y, unsigned (&out)[PARTS]) {
 #pragma unroll
@@ -125,10 +125,6 @@ __device__ __forceinline__ void lin_split(float x, float y, unsigned (&out)[PART
             asm("" : "+v"(out[p]));
             x -= attn_unpack<DT>(out[p], 0);
             y -= attn_unpack<DT>(out[p], 1);
-            if constexpr (DT == DT_F16) {
-                x *= 2048.f;
-                y *= 2048.f;
-            }
         }
     }
 }
@@ -179,20 +175,24 @@ __device__ __forceinline__ int lin_exponent(const f16x_t (&s)[NT]) {
     return e < -126 ? -126 : e;
 }
 
-// The power of two that takes the largest of a row's scores (the row's two lanes
-// hold 16 each) to 2^13 .. 2^14, and its inverse: fp16 operands then hold scores
-// of any size, to 2^-38 of the row's largest in two parts.  A largest below 2^-14
-// counts as 2^-14: scores are then held to 2^-52, and 32 times that times any fp16
-// value is below a result's smallest step.  NaN are passed over, an infinity
-// stays one.  (32768 tokens of 16 heads: 188 us without, 189 so.)
+// The power of two that takes m (2^-100 or more) to 2^13 .. 2^14, and its
+// inverse.
+__device__ __forceinline__ float lin_scale(float m, float* back) {
+    const unsigned e = __builtin_bit_cast(unsigned, m) & 0x7F800000u;
+    *back = __builtin_bit_cast(float, e - (13u << 23));
+    return __builtin_bit_cast(float, (267u << 23) - e);
+}
+
+// That of a row's scores (its two lanes hold 16 each): fp16 operands then hold
+// scores of any size, to 2^-38 of the row's largest in two parts.  A largest
+// below 2^-14 counts as 2^-14: scores are then held to 2^-52, and 32 times that
+// times any fp16 value is below a result's smallest step.  NaN are passed over, an
+// infinity stays one.  (32768 tokens of 16 heads: 188 us without, 189 so.)
 __device__ __forceinline__ float lin_row_scale(const f16x_t& p, float* up) {
     float m = 0x1p-14f;
 #pragma unroll
     for (int r = 0; r < 16; ++r) m = __builtin_fmaxf(m, __builtin_fabsf(p[r]));
-    m = __builtin_fmaxf(m, other_half(m));
-    const unsigned e = __builtin_bit_cast(unsigned, m) & 0x7F800000u;
-    *up = __builtin_bit_cast(float, e - (13u << 23));
-    return __builtin_bit_cast(float, (267u << 23) - e);
+    return lin_scale(__builtin_fmaxf(m, other_half(m)), up);
 }
 
 // Whether one of a lane's packed values is not finite.
@@ -355,16 +355,29 @@ __device__ __forceinline__ bool lin_body(const LinArgs& a, unsigned char* lds) {
             u4_t vp[2][C::PARTS];
             // bf16 has float32's range, so there a chunk's decay to the
             // segment's end goes into the split values; fp16's products are
-            // decayed as a whole
-            const float in = C::DT == DT_BF16 ? after : 1.f;
+            // decayed as a whole, and its values scaled by a power of two a
+            // column (a lane): two parts then hold them to 2^-38 of the column's
+            // largest and 2^-23 of themselves, whatever the decays and the tokens
+            // that are masked have left of them.  (Unscaled they were held to 2^-36,
+            // and what the matrix instruction adds subnormal values to, to 2^-38.)
+            float by = C::STATE && C::DT == DT_BF16 ? after : 1.f, back = 1.f;
+            if constexpr (C::DT == DT_F16) {
+                float most = 0x1p-100f;
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        most = __builtin_fmaxf(most, __builtin_fabsf(attn_unpack<C::DT>(v[k][i >> 1], i & 1) * fall[k][i]));
+                by = lin_scale(__builtin_fmaxf(most, other_half(most)), &back);
+            }
             auto split = [&](int k) __attribute__((always_inline)) {
 #pragma unroll
                 for (int d = 0; d < 4; ++d) {
                     unsigned out[C::PARTS];
                     float w0 = fall[k][2 * d], w1 = fall[k][2 * d + 1];
-                    if constexpr (C::STATE && C::DT == DT_BF16) {
-                        w0 *= in;
-                        w1 *= in;
+                    if constexpr (C::STATE || C::DT == DT_F16) {
+                        w0 *= by;
+                        w1 *= by;
                     }
                     lin_split<C::DT>(attn_unpack<C::DT>(v[k][d], 0) * w0, attn_unpack<C::DT>(v[k][d], 1) * w1, out);
 #pragma unroll
@@ -372,38 +385,22 @@ __device__ __forceinline__ bool lin_body(const LinArgs& a, unsigned char* lds) {
                 }
             };
             if constexpr (C::DT == DT_F16) {
-                f16x_t low[C::DB];
+                f16x_t u[C::DB];
 #pragma unroll
-                for (int t = 0; t < C::DB; ++t) low[t] = f16x_t{};
+                for (int t = 0; t < C::DB; ++t) u[t] = f16x_t{};
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     split(k);
 #pragma unroll
-                    for (int t = 0; t < C::DB; ++t) low[t] = M::mma(f[t][k], vp[k][1], low[t]);
+                    for (int p = C::PARTS - 1; p >= 0; --p)
+#pragma unroll
+                        for (int t = 0; t < C::DB; ++t) u[t] = M::mma(f[t][k], vp[k][p], u[t]);
                 }
-                if constexpr (C::STATE) {
+                const float into = C::STATE ? back * after : back;
 #pragma unroll
-                    for (int t = 0; t < C::DB; ++t)
+                for (int t = 0; t < C::DB; ++t)
 #pragma unroll
-                        for (int r = 0; r < 16; ++r) low[t][r] *= 1.f / 2048;
-#pragma unroll
-                    for (int k = 0; k < 2; ++k)
-#pragma unroll
-                        for (int t = 0; t < C::DB; ++t) low[t] = M::mma(f[t][k], vp[k][0], low[t]);
-#pragma unroll
-                    for (int t = 0; t < C::DB; ++t)
-#pragma unroll
-                        for (int r = 0; r < 16; ++r) S[t][r] = __builtin_fmaf(low[t][r], after, S[t][r]);
-                } else {
-#pragma unroll
-                    for (int t = 0; t < C::DB; ++t)
-#pragma unroll
-                        for (int r = 0; r < 16; ++r) S[t][r] = __builtin_fmaf(low[t][r], 1.f / 2048, S[t][r] * keep);
-#pragma unroll
-                    for (int k = 0; k < 2; ++k)
-#pragma unroll
-                        for (int t = 0; t < C::DB; ++t) S[t] = M::mma(f[t][k], vp[k][0], S[t]);
-                }
+                    for (int r = 0; r < 16; ++r) S[t][r] = __builtin_fmaf(u[t][r], into, C::STATE ? S[t][r] : S[t][r] * keep);
             } else if constexpr (C::STATE) {
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {

@@ -153,3 +153,27 @@ def test_scores_below_fp16():
         k[::2] = q[::2]
         v = torch.sign(_randn(3, (n, 2, D))) * 30000.0
         _check("small scores", q, k, v, decay, None)
+
+
+@pytest.mark.parametrize("D,n", [(64, 43), (128, 64 + 11), (64, 1600)])
+@pytest.mark.parametrize("rate", [-0.3, -0.7, -2.0])
+def test_terms_that_decay_within_a_chunk(D, n, rate):
+    """Tokens early in a chunk whose others are masked: their terms are small
+    at its end, and the state, which is float32, holds nothing else."""
+    _flush(f"decayed terms {D} {n} {rate}")
+    q, k, v = _randn(1, (n, 2, D)), _randn(2, (n, 2, D), 0.7), _randn(3, (n, 2, D))
+    decay = torch.tensor([rate, rate / 2], device="cuda")
+    at = torch.arange(n, device="cuda")
+    masked = at % 32 >= 11
+    masked[:n // 3] = False
+    masked[-10:] = True                               # and none behind them
+    v[masked] = 0
+    _check("masked", q, k, v, decay, None)
+
+
+@pytest.mark.parametrize("n", [50, 1100])
+def test_small_values(n):
+    """Values near fp16's smallest: a decayed one still has float32's bits."""
+    _flush(f"small values {n}")
+    q, k, v = _randn(1, (n, 2, 64)), _randn(2, (n, 2, 64), 0.7), _randn(3, (n, 2, 64), 1e-5)
+    _check("small", q, k, v, torch.tensor([-0.2, -0.03], device="cuda"), None)

@@ -17,8 +17,8 @@ import torch
 
 try:
     from . import _attn
-except ImportError as e:
-    raise ImportError("chip_fusion_amd/_attn.so is missing: run python -m chip_fusion_amd.build") from e
+except ImportError:         # a shortcut: every call is made in Python without it
+    _attn = None
 from . import ATTN_CAUSAL, DTYPES, Rows, TORCH_DTYPES, _check, lib
 
 _current_device = torch._C._cuda_getDevice
@@ -147,10 +147,24 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+class _NotCompiled:
+    """Usual calls where there is no compiled binding: none."""
+
+    def close(self):
+        pass
+
+    def attention(self, *args):
+        return None
+
+    prefix = linear = linear_step = attention
+
+
 def _usual(handle, heads, kv_heads, dim, dtype, workspace, run, step=None):
     """The plan's usual calls (pyattn.cpp): on the current stream, tensors of the
     common layouts; they return None, with nothing launched, where the checks here
     are to be made."""
+    if _attn is None:
+        return _NotCompiled()
     at = lambda f: 0 if f is None else ctypes.cast(f, ctypes.c_void_p).value
     return _attn.Call(handle.value, at(workspace), at(run), at(step), heads, kv_heads, dim, dtype, torch, _check)
 

@@ -84,6 +84,25 @@ def _compile(src, remarks):
     return obj, r.stderr if remarks else ""
 
 
+def binding():
+    """The attention plans' compiled calls.  They are a shortcut past Python, which
+    makes every call without them: where they cannot be compiled (no g++, no
+    Python.h), a line says so and the build goes on.  Their path, or None."""
+    tmp = PYATTN + ".tmp%d" % os.getpid()
+    try:
+        subprocess.check_call(["g++", "-std=c++17", "-O2", "-fPIC", "-Wall", "-shared", "-D__HIP_PLATFORM_AMD__=1",
+                               "-I", os.path.join(ROOT, "include"), "-isystem", "/opt/rocm/include",
+                               "-isystem", sysconfig.get_paths()["include"], os.path.join(CSRC, "pyattn.cpp"), "-o", tmp])
+    except (subprocess.CalledProcessError, OSError) as e:
+        for f in (tmp, PYATTN):         # (one of an earlier build may not fit the library)
+            if os.path.exists(f):
+                os.remove(f)
+        sys.stderr.write(f"{os.path.basename(PYATTN)} is not built ({e}): attention calls are made in Python\n")
+        return None
+    os.replace(tmp, PYATTN)
+    return PYATTN
+
+
 def build(jobs=None, remarks=False, verbose=False):
     os.makedirs(BUILD, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.hip")))
@@ -103,11 +122,7 @@ def build(jobs=None, remarks=False, verbose=False):
     subprocess.check_call([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp] + sorted(objs)
                           + ["-L/opt/rocm/lib", "-lamdhip64"])
     os.replace(tmp, LIB)
-    tmp = PYATTN + ".tmp%d" % os.getpid()
-    subprocess.check_call(["g++", "-std=c++17", "-O2", "-fPIC", "-Wall", "-shared", "-D__HIP_PLATFORM_AMD__=1",
-                           "-I", os.path.join(ROOT, "include"), "-isystem", "/opt/rocm/include",
-                           "-isystem", sysconfig.get_paths()["include"], os.path.join(CSRC, "pyattn.cpp"), "-o", tmp])
-    os.replace(tmp, PYATTN)
+    binding()
     if verbose or remarks:
         for s, log in sorted(logs.items()):
             if log.strip():

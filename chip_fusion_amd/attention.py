@@ -169,16 +169,25 @@ def _usual(handle, heads, kv_heads, dim, dtype, workspace, run, step=None):
     return _attn.Call(handle.value, at(workspace), at(run), at(step), heads, kv_heads, dim, dtype, torch, _check)
 
 
+def _scale(scale):
+    """A plan's scale in float32 (None: 0, the library's default)."""
+    if scale is None:
+        return 0.0
+    value = ctypes.c_float(scale).value
+    if not value > 0:
+        raise ValueError("scale: a positive number (of float32) is expected")
+    return value
+
+
 class _Heads:
     """A plan of the attention of a model's heads (b2b_attn_create)."""
 
     def __init__(self, dtype, heads, kv_heads, head_dim, scale, flags):
         code = DTYPES[dtype] if isinstance(dtype, str) else int(dtype)
-        if scale is not None and not scale > 0:
-            raise ValueError("scale: a positive number is expected")
+        scale = _scale(scale)
         self.heads, self.kv_heads, self.dim = heads, kv_heads, head_dim
         h = ctypes.c_void_p()
-        _check(lib().b2b_attn_create(ctypes.byref(h), code, heads, kv_heads, head_dim, scale or 0.0, flags),
+        _check(lib().b2b_attn_create(ctypes.byref(h), code, heads, kv_heads, head_dim, scale, flags),
                "b2b_attn_create")
         self._h = h
         self.dtype = TORCH_DTYPES[code]
@@ -322,11 +331,10 @@ class LinearAttention:
 
     def __init__(self, dtype, heads, kv_heads, head_dim, scale=None):
         code = DTYPES[dtype] if isinstance(dtype, str) else int(dtype)
-        if scale is not None and not scale > 0:
-            raise ValueError("scale: a positive number is expected")
+        scale = _scale(scale)
         self.heads, self.kv_heads, self.dim = heads, kv_heads, head_dim
         h = ctypes.c_void_p()
-        _check(lib().b2b_linear_attn_create(ctypes.byref(h), code, heads, kv_heads, head_dim, scale or 0.0),
+        _check(lib().b2b_linear_attn_create(ctypes.byref(h), code, heads, kv_heads, head_dim, scale),
                "b2b_linear_attn_create")
         self._h = h
         self.dtype = TORCH_DTYPES[code]

@@ -125,7 +125,7 @@ b2b_status_t b2b_attn_create(b2b_attn_t* plan, b2b_dtype_t dtype, int32_t heads,
     if (heads < 1 || kv_heads < 1 || heads % kv_heads || heads > 65536 || head_dim < 1 ||
         (flags & ~(uint32_t)B2B_ATTN_CAUSAL))
         return B2B_ERROR_INVALID_VALUE;
-    if (!(scale >= 0.f) || !std::isfinite(scale)) return B2B_ERROR_INVALID_VALUE;
+    if (!(scale >= 0.f) || !std::isfinite(scale * b2bk::kLog2e)) return B2B_ERROR_INVALID_VALUE;
     if ((dtype != B2B_DTYPE_F16 && dtype != B2B_DTYPE_BF16) || head_dim % 8 || head_dim > 128)
         return B2B_ERROR_NOT_SUPPORTED;
     b2b_attn_plan* p = new (std::nothrow) b2b_attn_plan();

@@ -53,7 +53,7 @@ enum {
  *               probabilities are rounded to dtype for the second product
  *   heads       query heads; kv_heads divides it
  *   head_dim    a multiple of 8, up to 128
- *   scale       of the scores, positive and finite (0: head_dim ^ -1/2)
+ *   scale       of the scores, positive, up to 2^127 (0: head_dim ^ -1/2)
  * INVALID_VALUE for sizes or flags outside these, NOT_SUPPORTED for another
  * dtype or head_dim.
  */

@@ -20,3 +20,12 @@ def test_a_scale_that_rounds_to_0_is_refused(make):
     for scale in (1e39, float("inf")):
         with pytest.raises(cf.B2BError, match="invalid"):
             make(scale)
+
+
+@pytest.mark.parametrize("scale,status", [(2.3e38, 0), (2.4e38, 1), (3.4e38, 1)])
+def test_a_scale_whose_base_2_form_is_infinite_is_refused(scale, status):
+    """(Scores of 0 would be 0 times infinity.)"""
+    h = ctypes.c_void_p()
+    assert cf.lib().b2b_attn_create(ctypes.byref(h), 0, 2, 2, 64, scale, 0) == status
+    assert bool(h.value) == (status == 0)
+    cf.lib().b2b_attn_destroy(h)

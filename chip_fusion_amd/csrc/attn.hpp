@@ -554,12 +554,15 @@ __device__ __forceinline__ void attn_again(const AttnArgs& a, f16x_t (&o)[C::DB]
 // (8001 packed tokens: 77 us, 72 so), whose time is a workgroup's start: its
 // place found, first keys and queries waited for (some 12 of its 38 thousand
 // cycles).
-// Measured: 16384 causal tokens, 32 heads of 128 (8 key heads), bf16: 1.92 ms,
-// 1145 TFLOP/s of the 1222 that a product of 8192^3 reaches (matrix cores busy
-// 0.66 of the cycles, the clock held down by power); 8001 tokens in 17
-// sequences: 62 us; head dim 64, half of the matrix work for the same softmax:
-// 9000 tokens of 16 heads in 24 sequences 32 us (545 TFLOP/s), bound by vector
-// instructions and by what does not fill the card at its end.
+// A third slot of LDS, keys asked for two tiles ahead, was slower (packed tokens
+// 65.6 us -> 67.1, 16384 tokens 2015 -> 2023).
+// Measured: 16384 causal tokens, 32 heads of 128 (8 key heads), bf16: 1.94 to 2.0
+// ms by the card, 1105 to 1143 TFLOP/s of the 1154 to 1228 that a product of 8192^3
+// reaches there (matrix cores busy 0.66 of the cycles, the clock held down by
+// power); 8001 tokens in 17 sequences: 66 to 68 us; head dim 64, half of the matrix
+// work for the same softmax: 9000 tokens of 16 heads in 24 sequences 34 to 35 us
+// (500 to 520 TFLOP/s), bound by the longest sequences' chains of tiles at the
+// launch's end (compute units busy 0.70) and, while busy, by vector instructions.
 template <int DT_, int DB_, bool PART_>
 struct AttnCfg {
     static constexpr int DT = DT_, DB = DB_, WAVES = 4, THREADS = 64 * WAVES;
@@ -790,11 +793,11 @@ __device__ __forceinline__ void attn_rows_body(const AttnArgs& a, unsigned char*
 // One launch for both kinds of keys of a batch behind a shared prefix: its
 // first workgroups take the prefix (bound by the matrix cores), the others
 // the requests' own keys (bound by memory); they fit a compute unit together.
-// 128 requests behind 32768 tokens, up to 1000 own keys, 32 heads of 128: 119 us
+// 128 requests behind 32768 tokens, up to 1000 own keys, 32 heads of 128: 124 us
 // on the device (the products alone 58, the bytes alone 77: a prefix tile a
 // wave takes about 1.1 us however few its neighbours are, so the two hide each
 // other in part only; own workgroups spread among the prefix's: 137 at best).
-// 32 behind 4097, up to 512 own: 15.4 us and 4.6 for the join.
+// 32 behind 4097, up to 512 own: 15.3 us and 4.5 for the join.
 template <int DT, int DB>
 __global__ __launch_bounds__(256, 3) void attn_prefix_kernel(AttnArgs p, AttnArgs own, int prefix_blocks) {
     using C = AttnCfg<DT, DB, true>;
@@ -813,7 +816,7 @@ __global__ __launch_bounds__(256, 3) void attn_prefix_kernel(AttnArgs p, AttnArg
 // part of one (row, head) each, for few rows of many parts, whose time is the
 // loads' latency (32 rows of 32 heads in 17 parts: 6.0 us by 16 lanes, 4.6 so);
 // else it is the parts' bytes (2500 rows of 24 heads of 96 in two parts, 47 MB
-// read: 10 us).
+// read: 10.7 us).
 // A row that belongs to no sequence has no partial results, and its output stays
 // as it is.
 template <int DT, int SUB>

@@ -63,8 +63,8 @@ Split plan_tiles(const b2b_attn_plan* p, int64_t seqs, int64_t rows, int64_t key
     // differ and one workgroup's may be twice the average while all of them run
     // at once: up to two workgroups a slot, parts of 800 or more, so that
     // writing and joining partial results stays below what the balance gains
-    // (2500 rows behind 0..4096 keys, 24 heads of 96: 102 us whole, 82 in two
-    // parts or three, 88 in four; 8001 rows of 32 heads, their own keys only: 63
+    // (2500 rows behind 0..4096 keys, 24 heads of 96: 106 us whole, 85 in two
+    // parts, 88 in three, 111 in four; 8001 rows of 32 heads, their own keys only: 63
     // us whole, 165 in two).
     int64_t parts = std::min(fill / wgs, each / 256);
     if (keys >= 2 * rows) parts = std::max(parts, std::min(2 * fill / wgs, each / 800));
@@ -291,8 +291,8 @@ namespace {
 // head; where those are fewer than compute units, sequences are cut into
 // segments of 512 tokens or more, at the price of reading K and V twice (8200
 // tokens in 9 sequences of 32 heads, 288 workgroups: 82 us whole, 124 to 126
-// in segments of 512 to 1024; one of 32768 with 16 heads: 1258 us whole, 282 in
-// 8 segments, 183 in 16, 193 in 32, 222 in 64).
+// in segments of 512 to 1024; one of 32768 with 16 heads, fp16: 1364 us whole,
+// 290 in 8 segments, 195 in 16, 207 in 32, 234 in 64).
 int64_t lin_segment(const b2b_linear_attn_plan* p, int64_t seqs, int64_t rows) {
     const int64_t want = std::max(1, 256 / p->heads);
     if (seqs >= want) return INT32_MAX;

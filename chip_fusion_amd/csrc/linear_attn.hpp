@@ -26,10 +26,10 @@
 // bounds the step: 24 matrix instructions (bf16) and 220 vector ones that wait
 // for one another; two sets of state waves with half of the rows each were
 // slower, their split values being computed twice.
-// Measured: 8200 bf16 tokens in 9 sequences, 32 heads of 128: 82 us (3.7 TB/s of
-// its own bytes), the time of the longest sequence's steps; 32768 fp16 tokens of
-// 16 heads: 183 us (segments' states 71, joined in 8, outputs 122; K and V are
-// read twice, 5.12 TB/s would take 157).
+// Measured: 8200 bf16 tokens in 9 sequences, 32 heads of 128: 83 to 87 us by the
+// card (3.6 TB/s of its own bytes), the time of the longest sequence's steps;
+// 32768 fp16 tokens of 16 heads: 194 to 200 us (segments' states 61, joined in 8,
+// outputs 125; K and V are read twice, 5.11 TB/s would take 158).
 //
 // The state is float32 and so are its terms: lambda^(n-1-j) v_j is split into
 // parts of the 16-bit type that together hold its 24 bits (bf16: three; fp16:
@@ -37,7 +37,9 @@
 // the exact k_j.  What ends in the 16-bit output alone is held in its type: the
 // scores in two parts, and, as q's partner, a copy of the state, rounded once.
 // fp16 holds neither over its range: a row's scores, and the copy, are scaled by
-// powers of two that the float32 accumulators take out again.
+// powers of two that the float32 accumulators take out again, and so are a
+// chunk's decayed values.  (The scaling of scores and values takes 2 % of the time
+// of the 32768 tokens, and 4 % of that of the 8200 in fp16: 93 us, 97 so.)
 #pragma once
 #include "attn.hpp"
 

@@ -4,7 +4,7 @@
 // else returns None, and the binding's own checks in Python take it from there.
 // None means that nothing has been launched: a status of the run itself is
 // raised, since a run that is made again would take states in place twice.
-// 77 tokens take 6.4 us a call so, about what the device takes for them, and 10.0
+// 77 tokens take 6.0 us a call so, about what the device takes for them, and 10.0
 // with all of it in Python.
 //
 // CPython's API only: tensors are asked for their shape, strides and address

@@ -9,8 +9,9 @@
  * elements contiguous, with a stride from row to row and one from head to
  * head (b2b_rows_t), so [tokens, heads, dim], [heads, tokens, dim] and slices
  * of a fused projection are all taken as they lie.  Base pointers are
- * 16-byte aligned and strides are multiples of 8 elements.  Query head h
- * reads key/value head h / (heads / kv_heads).
+ * 16-byte aligned and strides are multiples of 8 elements, from row to row up
+ * to 2^23 (a single row's is not looked at).  Query head h reads key/value head
+ * h / (heads / kv_heads).
  *
  * Sequence starts (cu_*) and lengths (lens) are read on the device, so a
  * captured graph replays with new ones; the kernels clamp them to the rows
@@ -50,7 +51,8 @@ enum {
  * Plans the attention of a model's heads.
  *   dtype       B2B_DTYPE_F16 or B2B_DTYPE_BF16: Q, K, V and O; sums, the
  *               softmax's statistics and partial results are float32, the
- *               probabilities are rounded to dtype for the second product
+ *               probabilities are rounded to dtype for the second product (fp16:
+ *               below 2^-25 of the row's largest they count in its sum alone)
  *   heads       query heads; kv_heads divides it
  *   head_dim    a multiple of 8, up to 128
  *   scale       of the scores, positive, up to 2^127 (0: head_dim ^ -1/2)
@@ -118,8 +120,10 @@ typedef struct b2b_linear_attn_plan* b2b_linear_attn_t;   /* opaque, owned by th
  *   dtype       B2B_DTYPE_F16 or B2B_DTYPE_BF16: Q, K, V and O; states are
  *               float32 and updated in float32 precision; the scores q.k are
  *               held in two parts of dtype, the copy of the state that meets q
- *               is rounded to it (fp16: a row's scores and the copy are scaled
- *               by powers of two, so both may be of any size)
+ *               is rounded to it (fp16: a row's scores and, where its largest value
+ *               is below 0.25 or above 2^14, the copy of 32 value columns are scaled
+ *               by powers of two, so both may be of any size; else the copy's values
+ *               below 2^-14 are held to 2^-25)
  *   head_dim    64 or 128
  *   scale       finite and positive (0: head_dim ^ -1/2)
  */
@@ -129,14 +133,17 @@ b2b_status_t b2b_linear_attn_create(b2b_linear_attn_t* plan, b2b_dtype_t dtype, 
 /*
  * Packed prompts: rows cu[s] .. cu[s+1]-1 are sequence s, 32 tokens at a time.
  * Infinities and NaN reach no earlier rows and no columns but their own (a
- * sequence's head, or its piece, that holds some is computed twice).
+ * sequence's head, or its piece, that holds some is computed twice); of a sequence
+ * cut into pieces, later pieces may be without those that the decay has taken
+ * below float32's range.
  *   log_decay   device float32 [heads], 0 or below (-inf: nothing is kept)
  *   state_in    device float32 [seqs, heads, head_dim, head_dim], the states
  *               before the sequences, or NULL (zero); 16-byte aligned
- *   state_out   the states after them, or NULL; may be state_in.  A sequence
- *               without tokens keeps its state
+ *   state_out   the states after them, or NULL; may be state_in, and else must
+ *               not overlap it.  A sequence without tokens keeps its state
  *   workspace   as for b2b_attn_run (b2b_linear_attn_workspace)
- * Rows of O that belong to no sequence are not written.
+ * Rows of O that belong to no sequence are not written.  O must not overlap the
+ * inputs.
  */
 b2b_status_t b2b_linear_attn_workspace(b2b_linear_attn_t plan, int32_t seqs, int64_t rows, size_t* bytes);
 b2b_status_t b2b_linear_attn_run(b2b_linear_attn_t plan, int32_t seqs, int64_t rows, b2b_rows_t Q, b2b_rows_t K,

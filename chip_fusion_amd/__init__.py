@@ -34,13 +34,22 @@ BENCH_EXPORTS = ("b2b_bench_mfma", "b2b_bench_copy", "b2b_bench_stream")
 # attention operators (b2b_attn.h)
 ATTN_EXPORTS = ("b2b_attn_create", "b2b_attn_workspace", "b2b_attn_run", "b2b_prefix_attn_workspace",
                 "b2b_prefix_attn_run", "b2b_attn_destroy", "b2b_linear_attn_create", "b2b_linear_attn_workspace",
-                "b2b_linear_attn_run", "b2b_linear_attn_step", "b2b_linear_attn_destroy")
+                "b2b_linear_attn_run", "b2b_linear_attn_step", "b2b_linear_attn_destroy",
+                "b2b_attn_create_window", "b2b_paged_attn_create", "b2b_paged_attn_workspace", "b2b_paged_attn_run",
+                "b2b_rotary_create", "b2b_rotary_run", "b2b_rotary_append", "b2b_rotary_destroy")
 ATTN_CAUSAL = 1
+ROTARY_NORM, ROTARY_INTERLEAVED = 1, 2
 
 
 class Rows(ctypes.Structure):
     """b2b_rows_t: rows of heads in device memory, strides in elements."""
     _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class Pages(ctypes.Structure):
+    """b2b_pages_t: the pages of a cache in device memory, strides in elements."""
+    _fields_ = [("data", ctypes.c_void_p), ("page_stride", ctypes.c_int64), ("row_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
 
 
 class B2BError(RuntimeError):
@@ -99,6 +108,16 @@ def lib():
         L.b2b_linear_attn_run.argtypes = [vp, i32, i64, Rows, Rows, Rows, Rows, vp, vp, vp, vp, vp, sz, vp]
         L.b2b_linear_attn_step.argtypes = [vp, i32, Rows, Rows, Rows, Rows, vp, vp, vp, vp]
         L.b2b_linear_attn_destroy.argtypes = [vp]
+        L.b2b_attn_create_window.argtypes = [ctypes.POINTER(vp), i32, i32, i32, i32, ctypes.c_float, i32, i32]
+        L.b2b_paged_attn_create.argtypes = [ctypes.POINTER(vp), i32, i32, i32, i32, i32, ctypes.c_float, i32, i32]
+        L.b2b_paged_attn_workspace.argtypes = [vp, i32, i64, i32, szp]
+        L.b2b_paged_attn_run.argtypes = [vp, i32, i64, Rows, Pages, Pages, i32, vp, i32, i64, vp, vp, Rows, vp, vp, sz, vp]
+        L.b2b_rotary_create.argtypes = [ctypes.POINTER(vp), i32, i32, i32, i32, i32, ctypes.POINTER(ctypes.c_double),
+                                        ctypes.POINTER(i32), i32, ctypes.c_float, u32]
+        L.b2b_rotary_run.argtypes = [vp, i64, Rows, Rows, Rows, Rows, vp, i64, vp, vp, vp]
+        L.b2b_rotary_append.argtypes = [vp, i32, i64, Rows, Rows, Rows, Rows, Pages, Pages, i32, i32, vp, i32, i64, vp, vp,
+                                        vp, i64, vp, vp, vp]
+        L.b2b_rotary_destroy.argtypes = [vp]
         for n in EXPORTS + BENCH_EXPORTS + ATTN_EXPORTS:
             if n not in ("b2b_status_string",):
                 getattr(L, n).restype = i32
@@ -461,7 +480,7 @@ def to_host(t):
 
 def __getattr__(name):
     """The attention plans (chip_fusion_amd.attention), imported when first named."""
-    if name in ("Attention", "PrefixAttention", "LinearAttention"):
+    if name in ("Attention", "PrefixAttention", "LinearAttention", "PagedAttention", "NormRotary"):
         from . import attention
         return getattr(attention, name)
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -19,7 +19,7 @@ try:
     from . import _attn
 except ImportError:         # a shortcut: every call is made in Python without it
     _attn = None
-from . import ATTN_CAUSAL, DTYPES, Rows, TORCH_DTYPES, _check, lib
+from . import ATTN_CAUSAL, DTYPES, Pages, ROTARY_INTERLEAVED, ROTARY_NORM, Rows, TORCH_DTYPES, _check, lib
 
 _current_device = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream
@@ -182,13 +182,14 @@ def _scale(scale):
 class _Heads:
     """A plan of the attention of a model's heads (b2b_attn_create)."""
 
-    def __init__(self, dtype, heads, kv_heads, head_dim, scale, flags):
+    _create_call = "b2b_attn_create"
+
+    def __init__(self, dtype, heads, kv_heads, head_dim, *rest):
+        """rest: what the create call takes after head_dim."""
         code = DTYPES[dtype] if isinstance(dtype, str) else int(dtype)
-        scale = _scale(scale)
         self.heads, self.kv_heads, self.dim = heads, kv_heads, head_dim
         h = ctypes.c_void_p()
-        _check(lib().b2b_attn_create(ctypes.byref(h), code, heads, kv_heads, head_dim, scale, flags),
-               "b2b_attn_create")
+        _check(getattr(lib(), self._create_call)(ctypes.byref(h), code, heads, kv_heads, head_dim, *rest), self._create_call)
         self._h = h
         self.dtype = TORCH_DTYPES[code]
         self._call, workspace = getattr(lib(), self._run_call), getattr(lib(), self._workspace_call)
@@ -209,16 +210,36 @@ class _Heads:
             pass
 
 
+def _window(window, sinks):
+    """A window and its sinks as the library takes them (0: none)."""
+    for name, n, least in (("window", 1 if window is None else window, 1), ("sinks", sinks, 0)):
+        if isinstance(n, bool) or not isinstance(n, int) or not least <= n <= 1 << 30:
+            raise ValueError(f"{name}: a whole number from {least} to 2^30 is expected, got {n!r}")
+    if window is None and sinks:
+        raise ValueError("sinks: without a window every earlier key is visible")
+    return window or 0, sinks
+
+
 class Attention(_Heads):
     """Attention over packed sequences (b2b_attn_run): softmax(scale Q.K^T).V
     for each sequence and head, causal (aligned to the last key) or full.
 
-    scale: of the scores, dim ** -0.5 by default."""
+    scale: of the scores, dim ** -0.5 by default.
+    window: causal rows see their last `window` keys only, and the sequence's
+    first `sinks` (b2b_attn_create_window)."""
 
     _run_call, _workspace_call = "b2b_attn_run", "b2b_attn_workspace"
 
-    def __init__(self, dtype, heads, kv_heads, head_dim, causal=True, scale=None):
-        super().__init__(dtype, heads, kv_heads, head_dim, scale, ATTN_CAUSAL if causal else 0)
+    def __init__(self, dtype, heads, kv_heads, head_dim, causal=True, scale=None, window=None, sinks=0):
+        scale = _scale(scale)
+        window, sinks = _window(window, sinks)
+        if window:
+            if not causal:
+                raise ValueError("window: causal attention only")
+            self._create_call = "b2b_attn_create_window"
+            super().__init__(dtype, heads, kv_heads, head_dim, scale, window, sinks)
+        else:
+            super().__init__(dtype, heads, kv_heads, head_dim, scale, ATTN_CAUSAL if causal else 0)
 
     def run(self, Q, K, V, cu_q, cu_k=None, O=None, lse=False, stream=None):
         """Q [rows, heads, dim], K and V [keys, kv_heads, dim]; sequence s has
@@ -267,7 +288,7 @@ class PrefixAttention(_Heads):
     _run_call, _workspace_call = "b2b_prefix_attn_run", "b2b_prefix_attn_workspace"
 
     def __init__(self, dtype, heads, kv_heads, head_dim, scale=None):
-        super().__init__(dtype, heads, kv_heads, head_dim, scale, 0)
+        super().__init__(dtype, heads, kv_heads, head_dim, _scale(scale), 0)
 
     def run(self, Q, Kp, Vp, K, V, lens, O=None, stream=None):
         """Q [batch, heads, dim]; Kp, Vp [prefix, kv_heads, dim], the shared
@@ -320,6 +341,236 @@ class PrefixAttention(_Heads):
         if st:
             _check(st, "b2b_prefix_attn_run")
         return O
+
+
+def _pages(t, name, dtype, pages, size, heads, dim):
+    """ValueError unless t is a cache's pages [pages, size, heads, dim] that the
+    kernels can address; its b2b_pages_t."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name}: a torch tensor is expected, got {type(t).__name__}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: dtype {dtype} expected, got {t.dtype}")
+    want = (pages, size, heads, dim)
+    if t.dim() != 4 or any(n is not None and n != m for n, m in zip(want, t.shape)):
+        raise ValueError(f"{name}: shape [{', '.join('any' if n is None else str(n) for n in want)}] expected, "
+                         f"got {list(t.shape)}")
+    if t.numel() == 0:
+        return Pages(None, 0, 0, 0)
+    strides = [st if n > 1 else 0 for st, n in zip(t.stride(), t.shape)]      # 0: never stepped by
+    if t.stride(3) != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    if any(st % 8 for st in strides[:3]) or t.data_ptr() % 16:
+        raise ValueError(f"{name}: pages, rows and heads must start on 16-byte boundaries")
+    return Pages(t.data_ptr(), *strides[:3])
+
+
+def _ints(t, name, shape):
+    """ValueError unless t is a contiguous int32 tensor of that shape."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous int32 tensor {list(shape)} is expected")
+
+
+def _table(table, lens, cu, rows):
+    """The sequences, the table's width and its row stride."""
+    if not isinstance(table, torch.Tensor) or table.dtype is not torch.int32 or table.dim() != 2 \
+            or (table.shape[1] > 1 and table.stride(1) != 1) or (table.shape[0] > 1 and table.stride(0) < table.shape[1]):
+        raise ValueError("table: an int32 tensor [seqs, width] with contiguous rows is expected")
+    seqs, width = table.shape
+    _ints(lens, "lens", (seqs,))
+    if cu is not None:
+        _starts(cu, "cu", seqs)
+    elif rows != seqs:
+        raise ValueError(f"cu: without it every sequence has one row, got {rows} rows and {seqs} sequences")
+    return seqs, width, table.stride(0) if seqs > 1 else width
+
+
+class PagedAttention(_Heads):
+    """Causal attention of new tokens over a paged cache (b2b_paged_attn_run):
+    one token of a sequence or a chunk of them, each sequence as it comes.
+
+    page_size: keys a page, any number.
+    window, sinks: as for Attention."""
+
+    _create_call, _run_call, _workspace_call = "b2b_paged_attn_create", "b2b_paged_attn_run", "b2b_paged_attn_workspace"
+
+    def __init__(self, dtype, heads, kv_heads, head_dim, page_size, scale=None, window=None, sinks=0):
+        window, sinks = _window(window, sinks)
+        super().__init__(dtype, heads, kv_heads, head_dim, page_size, _scale(scale), window, sinks)
+        self.page_size = page_size
+
+    def run(self, Q, K, V, table, lens, cu=None, O=None, lse=False, stream=None):
+        """Q [rows, heads, dim]: rows cu[s] .. cu[s+1]-1 (device int32; None: row
+        s) are the last tokens of sequence s, which has lens[s] keys with theirs.
+        K, V [pages, page_size, kv_heads, dim], any strides that are multiples of
+        8; key j of sequence s is in page table[s, j // page_size] (device int32
+        [seqs, width]).  Returns O, or (O, LSE) with `lse` (True, or a float32
+        tensor [rows, heads] to write).  Rows that belong to no sequence are
+        not written."""
+        dtype, heads, kv_heads, dim = self.dtype, self.heads, self.kv_heads, self.dim
+        q = _heads3(Q, "Q", dtype, None, heads, dim)
+        rows = Q.shape[0]
+        k = _pages(K, "K", dtype, None, self.page_size, kv_heads, dim)
+        v = _pages(V, "V", dtype, K.shape[0], self.page_size, kv_heads, dim)
+        seqs, width, table_ld = _table(table, lens, cu, rows)
+        want = lse is not False and lse is not None
+        LSE = lse if isinstance(lse, torch.Tensor) else None
+        o = None if O is None else _heads3(O, "O", dtype, rows, heads, dim)
+        if LSE is not None and (LSE.dtype != torch.float32 or LSE.shape != Q.shape[:2] or not LSE.is_contiguous()):
+            raise ValueError("lse: a contiguous float32 tensor [rows, heads] is expected")
+        index = _device_of("Q K V table lens cu O lse", Q, K, V, table, lens, cu, O, LSE)
+        return _on(index, stream, self._run, seqs, rows, q, k, v, K.shape[0], table, width, table_ld, lens, cu, o, Q, O, want,
+                   LSE)
+
+    def _run(self, stream, seqs, rows, q, k, v, pages, table, width, table_ld, lens, cu, o, Q, O, want, LSE):
+        if O is None:
+            O = _new(Q)
+            o = Rows(O.data_ptr(), self.heads * self.dim, self.dim)
+        if want and LSE is None:
+            LSE = Q.new_empty((rows, self.heads), dtype=torch.float32)
+        keep, wp, n = self._workspaces.get(Q, seqs, rows, width)
+        st = self._call(self._h, seqs, rows, q, k, v, pages, table.data_ptr(), width, table_ld, lens.data_ptr(), _ptr(cu), o,
+                        _ptr(LSE), wp, n, stream)
+        if st:
+            _check(st, "b2b_paged_attn_run")
+        return (O, LSE) if want else O
+
+
+class NormRotary:
+    """Norms of queries and keys for each head and their rotation by the
+    position, in one pass (b2b_rotary_create), and the same for new tokens
+    whose keys and values go into the pages of a cache.
+
+    rotary_dim: how many of a head's first elements turn (all by default; 0: none).
+    base, freqs: pair i turns by freqs[i] radians a position, base ** (-2 i /
+    rotary_dim) by default.
+    sections: how many of the pairs, in order, follow each axis of the positions
+    (time, height, width ...); or axes_of: every pair's axis.
+    interleaved: pair i is elements 2i and 2i + 1 (else i and i + rotary_dim / 2).
+    eps: of the norm; None: no norm."""
+
+    def __init__(self, dtype, heads, kv_heads, head_dim, rotary_dim=None, base=10000.0, freqs=None, sections=None, axes_of=None,
+                 interleaved=False, eps=1e-6):
+        code = DTYPES[dtype] if isinstance(dtype, str) else int(dtype)
+        rotary_dim = head_dim if rotary_dim is None else rotary_dim
+        pairs = rotary_dim // 2
+        if freqs is None:
+            freqs = [base ** (-2.0 * i / rotary_dim) for i in range(pairs)]
+        freqs = [float(f) for f in freqs]
+        if len(freqs) != pairs:
+            raise ValueError(f"freqs: {pairs} values expected, got {len(freqs)}")
+        if sections is not None:
+            if axes_of is not None:
+                raise ValueError("axes_of: either it or sections")
+            if any(n < 0 for n in sections) or sum(sections) != pairs:
+                raise ValueError(f"sections: {pairs} pairs in all expected, got {list(sections)}")
+            axes_of = [axis for axis, n in enumerate(sections) for _ in range(n)]
+        elif axes_of is None:
+            axes_of = [0] * pairs
+        axes_of = [int(x) for x in axes_of]
+        if len(axes_of) != pairs:
+            raise ValueError(f"axes_of: {pairs} values expected, got {len(axes_of)}")
+        axes = len(sections) if sections else max(axes_of, default=0) + 1
+        flags = (0 if eps is None else ROTARY_NORM) | (ROTARY_INTERLEAVED if interleaved else 0)
+        h = ctypes.c_void_p()
+        _check(lib().b2b_rotary_create(ctypes.byref(h), code, heads, kv_heads, head_dim, rotary_dim,
+                                       (ctypes.c_double * pairs)(*freqs), (ctypes.c_int * pairs)(*axes_of), axes,
+                                       0.0 if eps is None else eps, flags), "b2b_rotary_create")
+        self._h = h
+        self.dtype = TORCH_DTYPES[code]
+        self.heads, self.kv_heads, self.dim, self.rotary_dim, self.axes, self.norm = \
+            heads, kv_heads, head_dim, rotary_dim, axes, eps is not None
+
+    def _common(self, Q, K, positions, q_weight, k_weight, Q_out):
+        dtype, dim = self.dtype, self.dim
+        q = _heads3(Q, "Q", dtype, None, self.heads, dim)
+        rows = Q.shape[0]
+        k = _heads3(K, "K", dtype, rows, self.kv_heads, dim)
+        qo = None if Q_out is None else _heads3(Q_out, "Q_out", dtype, rows, self.heads, dim)
+        for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+            if w is None:
+                continue
+            if not self.norm:
+                raise ValueError(f"{name}: the plan has no norm")
+            if not isinstance(w, torch.Tensor) or w.dtype is not dtype or w.shape != (dim,) or not w.is_contiguous() \
+                    or w.data_ptr() % 16:
+                raise ValueError(f"{name}: a contiguous, 16-byte aligned {dtype} tensor [{dim}] is expected")
+        far = 0
+        if positions is not None:
+            if not isinstance(positions, torch.Tensor) or positions.dtype is not torch.int32 \
+                    or positions.shape != ((rows,) if self.axes == 1 and positions.dim() == 1 else (self.axes, rows)) \
+                    or (rows > 1 and positions.stride(-1) != 1):
+                want = f"[{rows}] or [1, {rows}]" if self.axes == 1 else f"[{self.axes}, {rows}]"
+                raise ValueError(f"positions: an int32 tensor {want} with contiguous rows is expected")
+            far = positions.stride(0) if self.axes > 1 else rows
+        return rows, q, k, qo, far
+
+    def run(self, Q, K, positions=None, q_weight=None, k_weight=None, Q_out=None, K_out=None, stream=None):
+        """Q [rows, heads, dim], K [rows, kv_heads, dim]; positions: device int32
+        [rows], or [axes, rows] with several axes (None only where rotary_dim is
+        0); weights: [dim], 1 by default.  Returns Q_out and K_out, which may be
+        Q and K."""
+        rows, q, k, qo, far = self._common(Q, K, positions, q_weight, k_weight, Q_out)
+        if positions is None and self.rotary_dim:
+            raise ValueError("positions: a tensor is expected")
+        ko = None if K_out is None else _heads3(K_out, "K_out", self.dtype, rows, self.kv_heads, self.dim)
+        index = _device_of("Q K positions q_weight k_weight Q_out K_out", Q, K, positions, q_weight, k_weight, Q_out, K_out)
+        return _on(index, stream, self._run, rows, q, k, qo, ko, positions, far, q_weight, k_weight, Q, K, Q_out, K_out)
+
+    def _run(self, stream, rows, q, k, qo, ko, positions, far, q_weight, k_weight, Q, K, Q_out, K_out):
+        if Q_out is None:
+            Q_out = _new(Q)
+            qo = Rows(Q_out.data_ptr(), self.heads * self.dim, self.dim)
+        if K_out is None:
+            K_out = _new(K)
+            ko = Rows(K_out.data_ptr(), self.kv_heads * self.dim, self.dim)
+        st = lib().b2b_rotary_run(self._h, rows, q, k, qo, ko, _ptr(positions), far, _ptr(q_weight), _ptr(k_weight), stream)
+        if st:
+            _check(st, "b2b_rotary_run")
+        return Q_out, K_out
+
+    def append(self, Q, K, V, k_cache, v_cache, table, lens, cu=None, positions=None, q_weight=None, k_weight=None,
+               Q_out=None, stream=None):
+        """New tokens: rows cu[s] .. cu[s+1]-1 (None: row s) of Q, K and V are the
+        last ones of sequence s, which has lens[s] keys with theirs.  Their keys,
+        normed and turned, and their values are written into the pages k_cache
+        and v_cache [pages, page_size, kv_heads, dim] at the rows' places, where
+        PagedAttention.run finds them with the same table, lens and cu.
+        positions: the rows' places in their sequences by default.  Returns Q_out,
+        which may be Q."""
+        rows, q, k, qo, far = self._common(Q, K, positions, q_weight, k_weight, Q_out)
+        v = _heads3(V, "V", self.dtype, rows, self.kv_heads, self.dim)
+        kc = _pages(k_cache, "k_cache", self.dtype, None, None, self.kv_heads, self.dim)
+        pages, size = k_cache.shape[:2]
+        vc = _pages(v_cache, "v_cache", self.dtype, pages, size, self.kv_heads, self.dim)
+        if size < 1:
+            raise ValueError("k_cache: a page holds at least one key")
+        seqs, width, table_ld = _table(table, lens, cu, rows)
+        index = _device_of("Q K V k_cache v_cache table lens cu positions q_weight k_weight Q_out", Q, K, V, k_cache, v_cache,
+                           table, lens, cu, positions, q_weight, k_weight, Q_out)
+        return _on(index, stream, self._append, seqs, rows, q, k, v, qo, kc, vc, pages, size, table, width, table_ld, lens, cu,
+                   positions, far, q_weight, k_weight, Q, Q_out)
+
+    def _append(self, stream, seqs, rows, q, k, v, qo, kc, vc, pages, size, table, width, table_ld, lens, cu, positions, far,
+                q_weight, k_weight, Q, Q_out):
+        if Q_out is None:
+            Q_out = _new(Q)
+            qo = Rows(Q_out.data_ptr(), self.heads * self.dim, self.dim)
+        st = lib().b2b_rotary_append(self._h, seqs, rows, q, k, v, qo, kc, vc, pages, size, table.data_ptr(), width, table_ld,
+                                     lens.data_ptr(), _ptr(cu), _ptr(positions), far, _ptr(q_weight), _ptr(k_weight), stream)
+        if st:
+            _check(st, "b2b_rotary_append")
+        return Q_out
+
+    def close(self):
+        if getattr(self, "_h", None):
+            lib().b2b_rotary_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
 
 
 class LinearAttention:

@@ -7,15 +7,8 @@
 #include <cmath>
 #include <new>
 
-#include "attn_launch.hpp"
-#include "b2b_attn.h"
+#include "attn_plan.hpp"
 #include "linear_attn_launch.hpp"
-
-struct b2b_attn_plan {
-    int dtype, heads, kv_heads, dim;
-    float scale;
-    bool causal;
-};
 
 struct b2b_linear_attn_plan {
     int dtype, heads, kv_heads, dim;
@@ -24,27 +17,7 @@ struct b2b_linear_attn_plan {
 
 namespace {
 
-constexpr int64_t kMaxStride = (int64_t)1 << 23;    // 64 rows' offsets stay below 2^30 bytes
-constexpr int64_t kMaxFar = (int64_t)1 << 40;       // from head to head, request to request: past any memory
-
-// Rows of heads that the kernels can address: n rows, 16-byte pieces.
-bool rows_ok(const b2b_rows_t& r, int64_t n, int dim) {
-    if (!r.data || (uintptr_t)r.data % 16) return false;
-    if (r.row_stride % 8 || r.head_stride % 8 || r.head_stride < 0 || r.head_stride > kMaxFar) return false;
-    return n <= 1 || (r.row_stride >= dim && r.row_stride <= kMaxStride);
-}
-// Rows that are written: no two of their (row, head) share an element.
-bool out_ok(const b2b_rows_t& r, int64_t n, int heads, int dim) {
-    if (!rows_ok(r, n, dim) || (heads > 1 && r.head_stride < dim)) return false;
-    return n <= 1 || heads <= 1 || r.row_stride >= (heads - 1) * r.head_stride + dim ||
-           r.head_stride >= (n - 1) * r.row_stride + dim;
-}
-b2bk::AttnRows dev(const b2b_rows_t& r, int dim) {
-    // a single row's stride is never stepped by; the kernels still size resources with it
-    return {r.data, r.row_stride >= dim && r.row_stride <= kMaxStride ? r.row_stride : dim, r.head_stride};
-}
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+using namespace b2b;
 
 // How a call with this many query rows a key head (in all, and a sequence on
 // average) and keys is laid over workgroups.
@@ -94,37 +67,15 @@ size_t part_bytes(const b2b_attn_plan* p, int64_t slots, int64_t rows) {
     return (size_t)slots * rows * p->heads * (p->dim + 1) * 4;
 }
 
-bool sizes_ok(const b2b_attn_plan* p, int64_t seqs, int64_t rows, int64_t keys) {
-    return seqs >= 0 && rows >= 0 && keys >= 0 && rows <= INT32_MAX && rows * (int64_t)p->heads <= INT32_MAX - 1024 &&
-           keys <= INT32_MAX / 2 && seqs <= INT32_MAX / 2;
-}
-
 const b2b::AttnLaunch& launchers(const b2b_attn_plan* p) {
     return p->dtype == B2B_DTYPE_F16 ? b2b::attn_f16() : b2b::attn_bf16();
 }
 
-b2bk::AttnArgs base_args(const b2b_attn_plan* p) {
-    b2bk::AttnArgs a = {};
-    a.heads = p->heads;
-    a.kv_heads.set(p->kv_heads);
-    a.group.set(p->heads / p->kv_heads);
-    a.dim = p->dim;
-    a.sc = p->scale * b2bk::kLog2e;
-    a.splits.set(1);
-    return a;
-}
-
 }  // namespace
 
-extern "C" {
-
-b2b_status_t b2b_attn_create(b2b_attn_t* plan, b2b_dtype_t dtype, int32_t heads, int32_t kv_heads, int32_t head_dim,
-                             float scale, uint32_t flags) {
-    if (!plan) return B2B_ERROR_INVALID_VALUE;
-    *plan = nullptr;
-    if (heads < 1 || kv_heads < 1 || heads % kv_heads || heads > 65536 || head_dim < 1 ||
-        (flags & ~(uint32_t)B2B_ATTN_CAUSAL))
-        return B2B_ERROR_INVALID_VALUE;
+b2b_status_t b2b::create_attn(b2b_attn_t* plan, b2b_dtype_t dtype, int32_t heads, int32_t kv_heads, int32_t head_dim,
+                              float scale, bool causal, int32_t window, int32_t sinks, int32_t page) {
+    if (heads < 1 || kv_heads < 1 || heads % kv_heads || heads > 65536 || head_dim < 1) return B2B_ERROR_INVALID_VALUE;
     if (!(scale >= 0.f) || !std::isfinite(scale * b2bk::kLog2e)) return B2B_ERROR_INVALID_VALUE;
     if ((dtype != B2B_DTYPE_F16 && dtype != B2B_DTYPE_BF16) || head_dim % 8 || head_dim > 128)
         return B2B_ERROR_NOT_SUPPORTED;
@@ -135,9 +86,22 @@ b2b_status_t b2b_attn_create(b2b_attn_t* plan, b2b_dtype_t dtype, int32_t heads,
     p->kv_heads = kv_heads;
     p->dim = head_dim;
     p->scale = scale > 0.f ? scale : (float)(1.0 / std::sqrt((double)head_dim));
-    p->causal = (flags & B2B_ATTN_CAUSAL) != 0;
+    p->causal = causal;
+    p->window = window;
+    p->sinks = sinks;
+    p->page = page;
     *plan = p;
     return B2B_SUCCESS;
+}
+
+extern "C" {
+
+b2b_status_t b2b_attn_create(b2b_attn_t* plan, b2b_dtype_t dtype, int32_t heads, int32_t kv_heads, int32_t head_dim,
+                             float scale, uint32_t flags) {
+    if (!plan) return B2B_ERROR_INVALID_VALUE;
+    *plan = nullptr;
+    if (flags & ~(uint32_t)B2B_ATTN_CAUSAL) return B2B_ERROR_INVALID_VALUE;
+    return create_attn(plan, dtype, heads, kv_heads, head_dim, scale, (flags & B2B_ATTN_CAUSAL) != 0, 0, 0, 0);
 }
 
 b2b_status_t b2b_attn_destroy(b2b_attn_t plan) {
@@ -146,7 +110,8 @@ b2b_status_t b2b_attn_destroy(b2b_attn_t plan) {
 }
 
 b2b_status_t b2b_attn_workspace(b2b_attn_t p, int32_t seqs, int64_t rows, int64_t keys, size_t* bytes) {
-    if (!p || !bytes || !sizes_ok(p, seqs, rows, keys)) return B2B_ERROR_INVALID_VALUE;
+    if (!p || !bytes || p->page || !sizes_ok(p, seqs, rows, keys)) return B2B_ERROR_INVALID_VALUE;
+    if (p->window) return window_workspace(p, seqs, rows, keys, bytes);
     *bytes = 0;
     if (!seqs || !rows) return B2B_SUCCESS;
     const Split s = plan_tiles(p, seqs, rows, keys);
@@ -157,16 +122,19 @@ b2b_status_t b2b_attn_workspace(b2b_attn_t p, int32_t seqs, int64_t rows, int64_
 b2b_status_t b2b_attn_run(b2b_attn_t p, int32_t seqs, int64_t rows, int64_t keys, b2b_rows_t Q, b2b_rows_t K,
                           b2b_rows_t V, b2b_rows_t O, const int32_t* cu_q, const int32_t* cu_k, float* lse,
                           void* workspace, size_t workspace_bytes, hipStream_t stream) {
-    if (!p || !sizes_ok(p, seqs, rows, keys)) return B2B_ERROR_INVALID_VALUE;
+    if (!p || p->page || !sizes_ok(p, seqs, rows, keys)) return B2B_ERROR_INVALID_VALUE;
     if (!seqs || !rows) return B2B_SUCCESS;
     const int dim = p->dim;
     if (!rows_ok(Q, rows, dim) || !out_ok(O, rows, p->heads, dim) || !cu_q || !cu_k) return B2B_ERROR_INVALID_VALUE;
     if (keys && (!rows_ok(K, keys, dim) || !rows_ok(V, keys, dim))) return B2B_ERROR_INVALID_VALUE;
     if (O.data == Q.data || O.data == K.data || O.data == V.data || (uintptr_t)lse % 4) return B2B_ERROR_INVALID_VALUE;
+    if (p->window)
+        return window_run(p, seqs, rows, keys, Q, K, V, O, cu_q, cu_k, lse, workspace, workspace_bytes, stream);
     const Split s = plan_tiles(p, seqs, rows, keys);
     size_t need = s.splits > 1 ? part_bytes(p, s.splits, rows) : 0;
     if (need && (!workspace || (uintptr_t)workspace % 16 || workspace_bytes < need)) return B2B_ERROR_INVALID_VALUE;
-    b2bk::AttnArgs a = base_args(p);
+    b2bk::AttnArgs a = {};
+    base_args(p, a);
     a.Q = dev(Q, dim);
     a.K = dev(K, dim);
     a.V = dev(V, dim);
@@ -207,7 +175,7 @@ b2b_status_t b2b_prefix_attn_run(b2b_attn_t p, int32_t batch, int64_t prefix, in
                                  int64_t v_stride, const int32_t* lens, b2b_rows_t O, void* workspace,
                                  size_t workspace_bytes, hipStream_t stream) {
     size_t need = 0;
-    if (!p || p->causal) return B2B_ERROR_INVALID_VALUE;
+    if (!p || p->causal) return B2B_ERROR_INVALID_VALUE;      // (nor a window or pages, which are causal)
     const b2b_status_t st = b2b_prefix_attn_workspace(p, batch, prefix, own, &need);
     if (st != B2B_SUCCESS) return st;
     if (!batch) return B2B_SUCCESS;
@@ -220,7 +188,8 @@ b2b_status_t b2b_prefix_attn_run(b2b_attn_t p, int32_t batch, int64_t prefix, in
         return B2B_ERROR_INVALID_VALUE;
     if (need && (!workspace || (uintptr_t)workspace % 16 || workspace_bytes < need)) return B2B_ERROR_INVALID_VALUE;
     const b2b::AttnLaunch& L = launchers(p);
-    b2bk::AttnArgs a = base_args(p);
+    b2bk::AttnArgs a = {};
+    base_args(p, a);
     a.Q = dev(Q, dim);
     a.O = const_cast<void*>(O.data);
     a.ldo = O.row_stride;

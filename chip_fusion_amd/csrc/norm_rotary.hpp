@@ -1,0 +1,272 @@
+// Norms of queries and keys for each head and their rotation, in one pass over
+// the heads; for new tokens, keys and values into the pages of a cache.
+//
+//   y = x / sqrt(mean(x^2) + eps) * weight,   pair (a, b) of y -> (a cos t - b sin t, b cos t + a sin t)
+//
+// What bounds it is the bytes: every head is read once and written once.  L
+// lanes hold a head, 8 elements each (L = 8 up to 64 elements, 16 up to 128): one
+// 16-byte load and store a lane, the sum of squares by exchanges inside L lanes.
+// The partner of element i is rotary_dim / 2 away, a whole number of 4-element
+// halves of a lane's piece, which lanes fetch from each other.
+//
+// A row's angles are the same for all of its heads: a workgroup of R rows works
+// out R x rotary_dim / 2 sines and cosines once, in LDS, and a lane keeps those of
+// its 8 elements in registers over the heads it takes.  An angle is position x
+// frequency / 2 pi in float64, of which only the fraction of a turn counts: off by
+// 2^-25 of a turn at positions of 2^31.
+#pragma once
+#include "paged_attn.hpp"
+
+namespace b2bk {
+
+struct RotaryArgs {
+    AttnRows Q, K, V;               // V: append only
+    void *Qo, *Ko;
+    int64_t ldqo, hqo, ldko, hko;
+    Pages ck, cv;                   // append: where keys and values go
+    const int32_t *table, *lens, *cu;
+    int64_t table_ld;
+    const int32_t* positions;       // [axes, rows]; null: a row's place in its sequence
+    int64_t position_ld;
+    const void *qw, *kw;
+    double turns[64];               // frequency / 2 pi of each pair
+    uint8_t axis[64];
+    FastDiv page, per_row;          // per_row: workgroups that share R rows' heads
+    int32_t rows, seqs, pages, width, heads, kv_heads, dim, rotary, row_log;    // R = 1 << row_log
+    float eps;
+};
+
+// Sum over the L lanes (8 or 16) that hold a head, in each of them.
+template <int L>
+__device__ __forceinline__ float head_sum(float x) {
+    auto add = [&](int y) { x += __builtin_bit_cast(float, y); };
+    auto me = [&] { return __builtin_bit_cast(int, x); };
+    add(__builtin_amdgcn_update_dpp(0, me(), 0xB1, 0xf, 0xf, false));       // lane ^ 1
+    add(__builtin_amdgcn_update_dpp(0, me(), 0x4E, 0xf, 0xf, false));       // lane ^ 2
+    add(__builtin_amdgcn_update_dpp(0, me(), 0x141, 0xf, 0xf, false));      // 7 - lane of 8
+    if constexpr (L == 16) add(__builtin_amdgcn_update_dpp(0, me(), 0x140, 0xf, 0xf, false));   // 15 - lane of 16
+    return x;
+}
+template <int L>
+__device__ __forceinline__ double head_sum(double x) {
+#pragma unroll
+    for (int d = 1; d < L; d <<= 1) x += __shfl_xor(x, d);
+    return x;
+}
+
+template <int DT>
+__device__ __forceinline__ void unpack8(u4_t w, float (&x)[8]) {
+#pragma unroll
+    for (int u = 0; u < 8; ++u) x[u] = attn_unpack<DT>(w[u >> 1], u & 1);
+}
+
+// APPEND: keys and values go to the pages.  NORM, INTER: the plan's flags.
+template <int DT, int L, bool APPEND, bool NORM, bool INTER>
+__global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a) {
+    constexpr int GROUPS = 256 / L, BATCH = 4;      // heads in flight a lane
+    __shared__ float turn[4][64][2];                // [row][pair][cos, sin]
+    __shared__ int place[4], row_seq[4];            // append: a row's place in its sequence, which one (-1: none)
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int R = 1 << a.row_log, block = a.per_row((int)blockIdx.x), share = (int)blockIdx.x - block * a.per_row.d;
+    const int row0 = block << a.row_log;
+    const int group = threadIdx.x / L, c = threadIdx.x & (L - 1);
+    const int r = group & (R - 1), row = row0 + r;
+    // this lane's heads: Q's, then K's, then V's, `step` apart
+    const int items = a.heads + (APPEND ? 2 : 1) * a.kv_heads, step = (GROUPS >> a.row_log) * a.per_row.d;
+    const int first = (group >> a.row_log) + share * (GROUPS >> a.row_log);
+    const bool live = row < a.rows && 8 * c < a.dim;
+    auto source = [&](int i) __attribute__((always_inline)) {
+        const bool q = i < a.heads, k = !APPEND || i < a.heads + a.kv_heads;
+        const AttnRows& x = q ? a.Q : k ? a.K : a.V;
+        const int h = q ? i : k ? i - a.heads : i - a.heads - a.kv_heads;
+        return (const u4_t*)((const char*)x.p + (row * x.ld + h * x.hs + 8 * c) * 2);
+    };
+    u4_t raw[BATCH];
+    auto fetch = [&](int i0) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) {
+            raw[j] = u4_t{0, 0, 0, 0};
+            if (live && i0 + j * step < items) raw[j] = *source(i0 + j * step);
+        }
+    };
+    fetch(first);
+    // the pieces of the weights that this lane and its partners hold
+    const int half = a.rotary >> 1;
+    int from[2];                // lane (of L) with the partner of each half of the piece
+    const int other = (half >> 2) & 1;      // whether it is in the other half of that lane's piece
+    bool turned[2], lower[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int v = 2 * c + h;            // 4-element unit
+        turned[h] = 4 * v < a.rotary;
+        lower[h] = 4 * v < half;
+        from[h] = turned[h] ? (lower[h] ? v + (half >> 2) : v - (half >> 2)) >> 1 : c;
+    }
+    u4_t qw = {0, 0, 0, 0}, kw = qw;
+    if constexpr (NORM) {
+        if (a.qw && 8 * c < a.dim) qw = *((const u4_t*)a.qw + c);
+        if (a.kw && 8 * c < a.dim) kw = *((const u4_t*)a.kw + c);
+    }
+    if constexpr (APPEND) {
+        // one wave a row: which sequence holds it
+        const int mine = row0 + wave;
+        if (wave < R && mine < a.rows) {
+            int seq = -1, at = 0;
+            if (!a.cu) {
+                seq = mine;
+                at = (a.lens[mine] > 0 ? a.lens[mine] : 0) - 1;
+            } else {
+                for (int s0 = 0; s0 < a.seqs && seq < 0; s0 += 64) {
+                    const int s = s0 + lane;
+                    int q0 = 0, n = 0, len = 0;
+                    if (s < a.seqs) {
+                        seq_range(a.cu, s, a.rows, &q0, &n);
+                        len = a.lens[s] > 0 ? a.lens[s] : 0;
+                    }
+                    const unsigned long long hit = __ballot(mine >= q0 && mine < q0 + n);
+                    if (hit) {
+                        const int l = __ffsll(hit) - 1;
+                        seq = s0 + l;
+                        at = __builtin_amdgcn_readlane(len, l) - (__builtin_amdgcn_readlane(q0, l) + __builtin_amdgcn_readlane(n, l) - mine);
+                    }
+                }
+            }
+            if (lane == 0) {
+                row_seq[wave] = seq;
+                place[wave] = at;
+            }
+        }
+        __syncthreads();
+    }
+    for (int i = threadIdx.x; i < half << a.row_log; i += 256) {
+        const int rr = i & (R - 1), p = i >> a.row_log;
+        if (row0 + rr >= a.rows) continue;
+        const int at = APPEND && !a.positions ? place[rr] : a.positions[a.axis[p] * a.position_ld + row0 + rr];
+        const double turns = at * a.turns[p];
+        float s, co;
+        sincospif(2.f * (float)(turns - __builtin_rint(turns)), &s, &co);
+        turn[rr][p][0] = co;
+        turn[rr][p][1] = s;
+    }
+    __syncthreads();
+    float cosine[8], sine[8];       // the sine with the sign that the element's partner comes with
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+        const int e = 8 * c + u;
+        const int p = INTER ? e >> 1 : (lower[u >> 2] ? e : e - half);
+        cosine[u] = turned[u >> 2] ? turn[r][p & 63][0] : 1.f;
+        const float s = turned[u >> 2] ? turn[r][p & 63][1] : 0.f;
+        sine[u] = (INTER ? !(u & 1) : lower[u >> 2]) ? -s : s;
+    }
+    char *kp = nullptr, *vp = nullptr;      // append: where head 0's piece of the row goes
+    bool writes = live;
+    if constexpr (APPEND) {
+        const int seq = writes ? row_seq[r] : -1, at = writes ? place[r] : -1;
+        writes = seq >= 0;                  // (a row of no sequence writes nothing)
+        const int pg = at >= 0 ? a.page(at) : 0;
+        if (writes && at >= 0 && pg < a.width) {
+            const int entry = a.table[seq * a.table_ld + pg];
+            if (entry >= 0 && entry < a.pages) {
+                const int in = at - pg * a.page.d;
+                kp = (char*)a.ck.p + (entry * a.ck.ps + in * a.ck.ld + 8 * c) * 2;
+                vp = (char*)a.cv.p + (entry * a.cv.ps + in * a.cv.ld + 8 * c) * 2;
+            }
+        }
+    }
+    auto partner = [&](u4_t w, u4_t& out) __attribute__((always_inline)) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const unsigned x = other ? w[2 * (h ^ 1) + j] : w[2 * h + j];
+                out[2 * h + j] = __shfl(x, from[h], L);
+            }
+    };
+    u4_t qwp = qw, kwp = kw;
+    if constexpr (NORM && !INTER) {
+        partner(qw, qwp);
+        partner(kw, kwp);
+    }
+    const float per = 1.f / a.dim;
+    for (int i0 = first; i0 < items; i0 += BATCH * step) {
+        u4_t now[BATCH];
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) now[j] = raw[j];
+        fetch(i0 + BATCH * step);
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) {
+            const int i = i0 + j * step;
+            if (i >= items) break;
+            const bool q = i < a.heads, k = !q && (!APPEND || i < a.heads + a.kv_heads);
+            u4_t out = now[j];
+            if (q || k) {
+                float x[8], y[8];
+                unpack8<DT>(now[j], x);
+                if constexpr (INTER) {
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) y[u] = x[u ^ 1];
+                } else {
+                    u4_t p;
+                    partner(now[j], p);
+                    unpack8<DT>(p, y);
+                }
+                if constexpr (NORM) {
+                    float sum = 0.f;
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) sum = __builtin_fmaf(x[u], x[u], sum);
+                    sum = head_sum<L>(sum);
+                    const float inv = __builtin_amdgcn_rsqf(__builtin_fmaf(sum, per, a.eps));
+                    // squares that leave float32's range (the sum infinite, or so small that terms are lost)
+                    const bool far = !(sum < 0x1p126f && sum > 0x1p-100f) && sum == sum;
+                    if (__any(far)) {
+                        double d = 0.0;
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) d += (double)x[u] * x[u];
+                        d = 1.0 / sqrt(head_sum<L>(d) / a.dim + (double)a.eps);
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) {
+                            x[u] = far ? (float)(x[u] * d) : x[u] * inv;
+                            y[u] = far ? (float)(y[u] * d) : y[u] * inv;
+                        }
+                    } else {
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) {
+                            x[u] *= inv;
+                            y[u] *= inv;
+                        }
+                    }
+                    if (q ? a.qw : a.kw) {
+                        float w[8];
+                        unpack8<DT>(q ? qw : kw, w);
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) x[u] *= w[u];
+                        if constexpr (INTER) {
+#pragma unroll
+                            for (int u = 0; u < 8; ++u) y[u] *= w[u ^ 1];
+                        } else {
+                            unpack8<DT>(q ? qwp : kwp, w);
+#pragma unroll
+                            for (int u = 0; u < 8; ++u) y[u] *= w[u];
+                        }
+                    }
+                }
+                // (an element that is not turned keeps its value whatever its neighbour holds)
+#pragma unroll
+                for (int u = 0; u < 8; ++u) x[u] = turned[u >> 2] ? __builtin_fmaf(y[u], sine[u], x[u] * cosine[u]) : x[u];
+                out = u4_t{Ty<DT>::pack(x[0], x[1]), Ty<DT>::pack(x[2], x[3]), Ty<DT>::pack(x[4], x[5]), Ty<DT>::pack(x[6], x[7])};
+            }
+            if (!writes) continue;
+            if (q) {
+                *(u4_t*)((char*)a.Qo + (row * a.ldqo + i * a.hqo + 8 * c) * 2) = out;
+            } else if constexpr (APPEND) {
+                char* p = k ? kp : vp;
+                const int h = i - a.heads - (k ? 0 : a.kv_heads);
+                if (p) *(u4_t*)(p + h * (k ? a.ck.hs : a.cv.hs) * 2) = out;
+            } else {
+                *(u4_t*)((char*)a.Ko + (row * a.ldko + (i - a.heads) * a.hko + 8 * c) * 2) = out;
+            }
+        }
+    }
+}
+
+}  // namespace b2bk

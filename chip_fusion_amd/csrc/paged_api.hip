@@ -1,0 +1,167 @@
+// C ABI of attention under a window and over pages (b2b_attn.h): checks, how a
+// call is laid over workgroups, launches.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "attn_plan.hpp"
+#include "paged_attn_launch.hpp"
+
+namespace {
+
+using namespace b2b;
+
+// Workgroups that a call's key tiles are cut for: two a compute unit.
+constexpr int kTarget = 512;
+// Key tiles of a part, at least.
+constexpr int kLeast = 8;
+
+struct Layout {
+    int64_t tiles;          // row tiles a key head, at most
+    int64_t items;          // workgroups a key head, at most
+    int64_t slots;          // partial results a key head, at most (0: nothing is cut)
+    int32_t slot_rows;
+    size_t bytes;
+};
+
+// cu: whether sequences have starts (else one row each)
+Layout lay_out(const b2b_attn_plan* p, int64_t seqs, int64_t rows, int64_t keys) {
+    const int64_t group = p->heads / p->kv_heads;
+    Layout l = {};
+    l.tiles = rows * group / b2bk::kKeyRows + seqs;
+    // key tiles of a row tile, at most
+    int64_t most = ceil_div(keys, 32);
+    if (p->window) most = std::min<int64_t>(most, ((int64_t)p->window + b2bk::kKeyRows) / 32 + ceil_div(p->sinks, 32) + 2);
+    // Under a window no row tile has many more key tiles than another: once there
+    // are as many as workgroups are wanted nothing is gained by cutting them.
+    const bool enough = p->window && rows * group / b2bk::kKeyRows * p->kv_heads >= kTarget;
+    l.items = l.tiles;
+    if (most > kLeast && !enough) {
+        l.items += kTarget / p->kv_heads;
+        l.slots = std::min<int64_t>(l.items, 2 * kTarget / p->kv_heads);
+    }
+    l.slot_rows = (int32_t)std::min<int64_t>(b2bk::kKeyRows, rows * group);
+    l.bytes = (size_t)l.slots * p->kv_heads * l.slot_rows * (p->dim + 1) * 4;
+    return l;
+}
+
+bool key_sizes_ok(const b2b_attn_plan* p, int64_t seqs, int64_t rows, int64_t keys) {
+    // (rows and keys of 2^30 at most keep every place less a window in 32 bits)
+    return sizes_ok(p, seqs, rows, keys) && rows <= INT32_MAX / 2;
+}
+
+bool ready(const Layout& l, const b2b_attn_plan* p, const void* workspace, size_t bytes) {
+    if (l.bytes && (!workspace || (uintptr_t)workspace % 16 || bytes < l.bytes)) return false;
+    return std::max(l.items, 4 * l.tiles) * p->kv_heads <= INT32_MAX;
+}
+
+b2b_status_t launch_keys(b2b_attn_t p, const Layout& l, b2bk::KeyArgs& a, int kind, void* workspace, hipStream_t stream) {
+    a.causal = 1;
+    a.window = (int32_t)std::min<int64_t>(p->window, std::max<int64_t>(a.keys, 1));
+    a.sinks = (int32_t)std::min<int64_t>(p->sinks, a.keys);
+    a.split = l.slots > 0;
+    a.least = kLeast;
+    a.per = (float)p->kv_heads / kTarget;
+    a.slots = (int32_t)l.slots;
+    a.slot_rows = l.slot_rows;
+    a.part = (float*)workspace;
+    a.part_lse = a.part + (size_t)l.slots * p->kv_heads * l.slot_rows * p->dim;
+    const KeyLaunch& L = p->dtype == B2B_DTYPE_F16 ? key_attn_f16() : key_attn_bf16();
+    if (L.run(a, kind, (unsigned)(l.items * p->kv_heads), stream) != hipSuccess) return B2B_ERROR_HIP;
+    if (a.split && L.join(a, kind, (unsigned)(4 * l.tiles * p->kv_heads), stream) != hipSuccess) return B2B_ERROR_HIP;
+    return B2B_SUCCESS;
+}
+
+b2bk::KeyArgs key_args(const b2b_attn_plan* p, int32_t seqs, int64_t rows, int64_t keys, const b2b_rows_t& Q,
+                       const b2b_rows_t& O, const int32_t* cu_q, float* lse) {
+    b2bk::KeyArgs a = {};
+    base_args(p, a);
+    a.Q = dev(Q, p->dim);
+    a.O = const_cast<void*>(O.data);
+    a.ldo = O.row_stride;
+    a.hso = O.head_stride;
+    a.cu_q = cu_q;
+    a.rows = rows;
+    a.keys = keys;
+    a.lse = lse;
+    a.seqs = seqs;
+    return a;
+}
+
+}  // namespace
+
+b2b_status_t b2b::window_workspace(b2b_attn_t p, int32_t seqs, int64_t rows, int64_t keys, size_t* bytes) {
+    if (!key_sizes_ok(p, seqs, rows, keys)) return B2B_ERROR_INVALID_VALUE;
+    *bytes = seqs && rows ? lay_out(p, seqs, rows, keys).bytes : 0;
+    return B2B_SUCCESS;
+}
+
+b2b_status_t b2b::window_run(b2b_attn_t p, int32_t seqs, int64_t rows, int64_t keys, const b2b_rows_t& Q, const b2b_rows_t& K,
+                             const b2b_rows_t& V, const b2b_rows_t& O, const int32_t* cu_q, const int32_t* cu_k, float* lse,
+                             void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    if (!key_sizes_ok(p, seqs, rows, keys)) return B2B_ERROR_INVALID_VALUE;
+    const Layout l = lay_out(p, seqs, rows, keys);
+    if (!ready(l, p, workspace, workspace_bytes)) return B2B_ERROR_INVALID_VALUE;
+    b2bk::KeyArgs a = key_args(p, seqs, rows, keys, Q, O, cu_q, lse);
+    a.K = b2b::dev(K, p->dim);
+    a.V = b2b::dev(V, p->dim);
+    a.cu_k = cu_k;
+    return launch_keys(p, l, a, KEYS_WINDOW, workspace, stream);
+}
+
+extern "C" {
+
+b2b_status_t b2b_attn_create_window(b2b_attn_t* plan, b2b_dtype_t dtype, int32_t heads, int32_t kv_heads, int32_t head_dim,
+                                    float scale, int32_t window, int32_t sinks) {
+    if (!plan) return B2B_ERROR_INVALID_VALUE;
+    *plan = nullptr;
+    if (window < 1 || window > 1 << 30 || sinks < 0 || sinks > 1 << 30) return B2B_ERROR_INVALID_VALUE;
+    return create_attn(plan, dtype, heads, kv_heads, head_dim, scale, true, window, sinks, 0);
+}
+
+b2b_status_t b2b_paged_attn_create(b2b_attn_t* plan, b2b_dtype_t dtype, int32_t heads, int32_t kv_heads, int32_t head_dim,
+                                   int32_t page_size, float scale, int32_t window, int32_t sinks) {
+    if (!plan) return B2B_ERROR_INVALID_VALUE;
+    *plan = nullptr;
+    if (page_size < 1 || page_size > 1 << 20 || window < 0 || window > 1 << 30 || sinks < 0 || sinks > 1 << 30 ||
+        (sinks && !window))
+        return B2B_ERROR_INVALID_VALUE;
+    return create_attn(plan, dtype, heads, kv_heads, head_dim, scale, true, window, sinks, page_size);
+}
+
+b2b_status_t b2b_paged_attn_workspace(b2b_attn_t p, int32_t seqs, int64_t rows, int32_t width, size_t* bytes) {
+    if (!p || !bytes || !p->page || width < 0 || !key_sizes_ok(p, seqs, rows, (int64_t)width * p->page))
+        return B2B_ERROR_INVALID_VALUE;
+    *bytes = seqs && rows ? lay_out(p, seqs, rows, (int64_t)width * p->page).bytes : 0;
+    return B2B_SUCCESS;
+}
+
+b2b_status_t b2b_paged_attn_run(b2b_attn_t p, int32_t seqs, int64_t rows, b2b_rows_t Q, b2b_pages_t K, b2b_pages_t V,
+                                int32_t pages, const int32_t* table, int32_t width, int64_t table_stride, const int32_t* lens,
+                                const int32_t* cu_q, b2b_rows_t O, float* lse, void* workspace, size_t workspace_bytes,
+                                hipStream_t stream) {
+    if (!p || !p->page || width < 0 || pages < 0) return B2B_ERROR_INVALID_VALUE;
+    const int64_t keys = pages ? (int64_t)width * p->page : 0;
+    if (!key_sizes_ok(p, seqs, rows, (int64_t)width * p->page) || (!cu_q && rows != seqs)) return B2B_ERROR_INVALID_VALUE;
+    if (!seqs || !rows) return B2B_SUCCESS;
+    if (!rows_ok(Q, rows, p->dim) || !out_ok(O, rows, p->heads, p->dim) || O.data == Q.data || (uintptr_t)lse % 4)
+        return B2B_ERROR_INVALID_VALUE;
+    if (!lens) return B2B_ERROR_INVALID_VALUE;
+    if (keys && (!pages_ok(K, pages) || !pages_ok(V, pages) || !table || O.data == K.data || O.data == V.data ||
+                 table_stride < 0 || table_stride > kMaxFar || (seqs > 1 && table_stride < width)))
+        return B2B_ERROR_INVALID_VALUE;
+    // (by the table's width alone, as the _workspace call)
+    const Layout l = lay_out(p, seqs, rows, (int64_t)width * p->page);
+    if (!ready(l, p, workspace, workspace_bytes)) return B2B_ERROR_INVALID_VALUE;
+    b2bk::KeyArgs a = key_args(p, seqs, rows, keys, Q, O, cu_q, lse);
+    a.pk = dev(K);
+    a.pv = dev(V);
+    a.table = table;
+    a.table_ld = table_stride;
+    a.page.set(p->page);
+    a.pages = pages;
+    a.lens = lens;
+    return launch_keys(p, l, a, p->window ? KEYS_PAGED_WINDOW : KEYS_PAGED, workspace, stream);
+}
+
+}  // extern "C"

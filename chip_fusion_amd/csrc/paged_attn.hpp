@@ -1,0 +1,668 @@
+// Causal attention whose keys lie in the pages of a cache, and attention under
+// a window with the first keys still visible.
+//
+// The products, the softmax and their layouts are attn.hpp's: scores transposed
+// on v_mfma_f32_32x32x16, a query row a lane, the rounded probabilities the
+// second product's operand as they lie.  What differs is which keys a row meets
+// and where they are:
+//
+//   Pages.  Key j of sequence s is row j % size of page table[s][j / size].
+//   Every lane of a copy works out the address of the 16 bytes that it moves
+//   (64 bits: a cache may be larger than 4 GB, a page of any size may end inside
+//   a tile), and the loads write LDS directly.  The table's entries for a tile
+//   are asked for one tile ahead.  Places behind a sequence's last key are read
+//   from a block of zeros: what a page holds there may be anything, NaN too.
+//
+//   Window.  The row in place p sees keys p - window + 1 .. p and the first
+//   `sinks`: 128 rows' tiles are those of the sinks and those from the first
+//   row's window on, one range with a gap.  Only tiles at the range's borders
+//   are masked.
+//
+// Work is cut on the device, where the lengths are.  A (sequence, tile of 128
+// rows, key head) of T key tiles is cut into ceil(T / L) parts, with L the
+// whole call's key tiles over the workgroups that it should have, and at least
+// `least`: no chain of tiles is longer than L, whatever the lengths, and a
+// captured graph replays with new ones.  Since sum ceil(T / L) <= items +
+// sum T / L, the host knows the grid's size, and since a cut item has at most
+// 2 T / L parts, the partial results' as well.
+#pragma once
+#include "attn.hpp"
+
+namespace b2bk {
+
+struct Pages {
+    const void* p;
+    int64_t ps, ld, hs;     // from page to page, row to row, head to head
+};
+
+struct KeyArgs : AttnArgs {
+    Pages pk, pv;
+    const int32_t* table;   // [seqs, width], rows table_ld apart
+    int64_t table_ld;
+    FastDiv page;           // keys a page
+    int32_t pages, window, sinks;
+    int32_t split, least;   // whether items may be cut, and the fewest tiles a part has then
+    float per;              // key heads over the workgroups that a call should have
+    int32_t slots, slot_rows;   // partial results: slots a key head, rows a slot
+};
+
+constexpr int kKeyRows = 128;     // rows of a tile
+
+// 16 bytes a lane from an address of its own to LDS (lane i -> dst + 16 i),
+// issued and waited for as lds_dma16's.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void lds_dma16_from(const unsigned char* dst, const char* p) {
+    const unsigned a = (unsigned)(uintptr_t)(lds_ptr_t)dst;
+    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" : : "s"(a), "v"(p) : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+// what places behind a sequence's last key and columns past the head's read
+__device__ __attribute__((aligned(256))) const unsigned char kZeros[256] = {};
+
+// ---------------------------------------------------------------------------
+// Where a workgroup works
+// ---------------------------------------------------------------------------
+struct KeyItem {
+    int seq, tile, part, parts, slot;   // slot: the tile's first
+    int q0, nq, k0, nk;
+    int tiles;
+};
+
+__device__ __forceinline__ float lanes_total(float x) {
+    auto up = [&](int y) { x += __builtin_bit_cast(float, y); };
+    auto me = [&] { return __builtin_bit_cast(int, x); };
+    up(__builtin_amdgcn_update_dpp(0, me(), 0x111, 0xf, 0xf, false));
+    up(__builtin_amdgcn_update_dpp(0, me(), 0x112, 0xf, 0xf, false));
+    up(__builtin_amdgcn_update_dpp(0, me(), 0x114, 0xf, 0xf, false));
+    up(__builtin_amdgcn_update_dpp(0, me(), 0x118, 0xf, 0xf, false));
+    up(__builtin_amdgcn_update_dpp(0, me(), 0x142, 0xa, 0xf, false));
+    up(__builtin_amdgcn_update_dpp(0, me(), 0x143, 0xc, 0xf, false));
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(me(), 63));
+}
+
+// The item (JOIN: the tile, whatever its parts) number u, sequences 64 at a time.
+template <bool PAGED, bool WIN, bool JOIN>
+__device__ __forceinline__ bool find_item(const KeyArgs& a, int u, KeyItem* out) {
+    const int lane = threadIdx.x & 63, group = a.group.d;
+    int q0, n, k0, nk, tiles, span;
+    auto load = [&](int s0) __attribute__((always_inline)) {
+        const int s = s0 + lane;
+        q0 = n = k0 = nk = 0;
+        if (s < a.seqs) {
+            if (a.cu_q) seq_range(a.cu_q, s, (int)a.rows, &q0, &n);
+            else q0 = s, n = 1;
+            if constexpr (PAGED) {
+                nk = a.lens[s];
+                nk = nk < 0 ? 0 : (nk > (int)a.keys ? (int)a.keys : nk);
+            } else {
+                seq_range(a.cu_k, s, (int)a.keys, &k0, &nk);
+            }
+        }
+        tiles = (int)(((unsigned)n * (unsigned)group + kKeyRows - 1) / kKeyRows);
+        span = (nk + 31) >> 5;              // key tiles of the tile that has the most, or a few more
+        if constexpr (WIN) {
+            const int tokens = a.group(kKeyRows + group - 2) + 1;
+            const int w = ((a.window + (n < tokens ? n : tokens)) >> 5) + ((a.sinks + 31) >> 5) + 2;
+            span = span < w ? span : w;
+        }
+    };
+    load(0);
+    int most = 1 << 30;
+    if (a.split) {
+        double work = (double)tiles * span;
+        for (int s0 = 64; s0 < a.seqs; s0 += 64) {
+            load(s0);
+            work += (double)tiles * span;
+        }
+        if (a.seqs > 64) load(0);
+        // (a thousandth more than the sum, so that its rounding makes no part too many)
+        const float l = ceilf(lanes_total((float)work) * 1.001f * a.per);
+        most = l > (float)(1 << 30) ? 1 << 30 : (int)l;
+        most = most < a.least ? a.least : most;
+    }
+    int before = 0, slots = 0;
+    for (int s0 = 0;;) {
+        const int parts = a.split && span > most ? (int)(((unsigned)span + (unsigned)most - 1) / (unsigned)most) : 1;
+        const int mine = JOIN ? tiles : tiles * parts, cut = parts > 1 ? tiles * parts : 0;
+        const int sum = lanes_sum(mine), cuts = lanes_sum(cut);
+        const unsigned long long hit = __ballot(before + sum > u);
+        if (hit) {
+            const int at = __ffsll(hit) - 1;
+            const int local = u - before - (__builtin_amdgcn_readlane(sum, at) - __builtin_amdgcn_readlane(mine, at));
+            // (starts out of order may name more tiles than there can be rows: what the grid
+            // and the workspace were not made for is left out)
+            if ((unsigned)local >= (unsigned)__builtin_amdgcn_readlane(mine, at)) return false;
+            out->seq = s0 + at;
+            out->parts = __builtin_amdgcn_readlane(parts, at);
+            out->tiles = __builtin_amdgcn_readlane(tiles, at);
+            out->tile = JOIN || out->parts == 1 ? local : (int)((unsigned)local / (unsigned)out->parts);
+            out->part = JOIN ? 0 : local - out->tile * out->parts;
+            out->slot = slots + __builtin_amdgcn_readlane(cuts, at) - __builtin_amdgcn_readlane(cut, at) + out->tile * out->parts;
+            out->q0 = __builtin_amdgcn_readlane(q0, at);
+            out->nq = __builtin_amdgcn_readlane(n, at);
+            out->k0 = __builtin_amdgcn_readlane(k0, at);
+            out->nk = __builtin_amdgcn_readlane(nk, at);
+            return out->parts == 1 || out->slot + out->parts <= a.slots;
+        }
+        before += __builtin_amdgcn_readlane(sum, 63);
+        slots += __builtin_amdgcn_readlane(cuts, 63);
+        s0 += 64;
+        if (s0 >= a.seqs) return false;
+        load(s0);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// One item's geometry
+// ---------------------------------------------------------------------------
+// Which key tiles the rows of a tile meet: number i of [i0, i1) is tile
+// i < sink_tiles ? i : i + gap.
+template <int DT_, int DB_, bool PAGED_, bool WIN_>
+struct KeyCfg {
+    static constexpr int DT = DT_, DB = DB_, WAVES = 4, THREADS = 64 * WAVES, BM = kKeyRows, BN = 32;
+    static constexpr bool PAGED = PAGED_, WIN = WIN_;
+    static constexpr int KS = 2 * DB;                   // K-steps of the first product
+    static constexpr int TILE = BN * DB * 64;           // a tile of keys (or values) in LDS
+    static constexpr int JOIN = WAVES * TILE;           // behind it: the waves' maxima and sums
+    static constexpr int LDS_BYTES = JOIN + 2 * WAVES * 32 * 4;
+    static_assert(BM == 32 * WAVES, "many rows: 32 a wave");
+};
+
+template <class C>
+struct KeyTile {
+    const KeyArgs& a;
+    const KeyItem& w;
+    int kvh, row0, rows, shift;      // rows: the sequence's; row r is token r / group, in place r / group + shift
+    int i0, i1, sink_tiles, gap;
+
+    __device__ __forceinline__ KeyTile(const KeyArgs& args, const KeyItem& item, int head) : a(args), w(item), kvh(head) {
+        row0 = (w.tiles - 1 - w.tile) * C::BM;      // the last rows see the most keys: they start first
+        rows = w.nq * a.group.d;
+        shift = w.nk - w.nq;
+        const int last = (row0 + C::BM < rows ? row0 + C::BM : rows) - 1;
+        const int end = (sees(last) + C::BN - 1) / C::BN;
+        int n = end;
+        sink_tiles = end;
+        gap = 0;
+        if constexpr (C::WIN) {
+            const int lo = from(row0), first = lo > 0 ? lo / C::BN : 0, s = (a.sinks + C::BN - 1) / C::BN;
+            if (first > s && end > first) {
+                sink_tiles = s;
+                gap = first - s;
+                n = end - gap;
+            }
+        }
+        i0 = 0;
+        i1 = n;
+        if (w.parts > 1) {
+            const int whole = (int)((unsigned)n / (unsigned)w.parts), rest = n - whole * w.parts;
+            i0 = whole * w.part + (int)((unsigned)(rest * w.part) / (unsigned)w.parts);
+            i1 = whole * (w.part + 1) + (int)((unsigned)(rest * (w.part + 1)) / (unsigned)w.parts);
+        }
+    }
+    __device__ __forceinline__ int tile(int i) const { return C::WIN && i >= sink_tiles ? i + gap : i; }
+    // keys that row r sees end here (places 0 .. sees - 1) ...
+    __device__ __forceinline__ int sees(int r) const {
+        if (r >= rows) return 0;
+        const int n = a.group(r) + 1 + shift;
+        return n < 0 ? 0 : n;
+    }
+    // ... and begin here, the sinks apart
+    __device__ __forceinline__ int from(int r) const {
+        // (a window is 2^30 at most)
+        return a.group(r) + 1 + shift - a.window;
+    }
+    __device__ __forceinline__ int entry(int key) const {
+        key = key < w.nk ? key : w.nk - 1;
+        return a.table[w.seq * a.table_ld + a.page(key)];
+    }
+    // 16-byte piece `chunk` of key `key`'s row, whose page the table's entry names
+    __device__ __forceinline__ const char* row_at(const Pages& x, int key, int entry, int chunk) const {
+        const int in = key - a.page(key) * a.page.d;
+        const int pg = entry < 0 ? 0 : (entry < a.pages ? entry : a.pages - 1);
+        return (const char*)x.p + (pg * x.ps + in * x.ld + kvh * x.hs + 8 * chunk) * 2;
+    }
+    // one key's row, wherever it lies
+    __device__ __forceinline__ const char* key_row(bool values, int key) const {
+        if constexpr (C::PAGED) return row_at(values ? a.pv : a.pk, key, entry(key), 0);
+        const AttnRows& x = values ? a.V : a.K;
+        return (const char*)x.p + (((int64_t)w.k0 + key) * x.ld + kvh * x.hs) * 2;
+    }
+    // Copies row group rg (16 rows) of a tile, keys with their chunks swizzled,
+    // as attn_copy; e: the lane's table entry.
+    template <bool VALUES>
+    __device__ __forceinline__ void copy(const unsigned char* dst, int t, int rg, int e, int lane) const {
+        if constexpr (C::PAGED) {
+            const int row = 16 * rg + (lane >> 2), key = t * C::BN + row;
+            const int chunk = VALUES ? (lane & 3) : ((lane & 3) ^ ((row >> 2) & 3));
+            const bool in = key < w.nk;
+            const char* p = row_at(VALUES ? a.pv : a.pk, key, e, chunk);
+#pragma unroll
+            for (int b = 0; b < C::DB; ++b)
+                lds_dma16_from(dst + b * C::BN * 64 + rg * 1024, in && 32 * b + 8 * chunk < a.dim ? p + 64 * b : (const char*)kZeros);
+        } else {
+            const AttnRows& x = VALUES ? a.V : a.K;
+            const int n = w.nk - t * C::BN < C::BN ? w.nk - t * C::BN : C::BN;
+            const auto rs = attn_rsrc(x.p, (int64_t)w.k0 + (int64_t)t * C::BN, x.ld, (int64_t)kvh * x.hs, n, a.dim);
+            attn_copy<C::DB, C::BN, !VALUES>(dst, rs, (int)x.ld * 2, a.dim, rg, lane);
+        }
+    }
+    // lane's table entry for row group rg of tile t
+    __device__ __forceinline__ int entry_of(int t, int rg, int lane) const {
+        if constexpr (C::PAGED) return entry(t * C::BN + 16 * rg + (lane >> 2));
+        return 0;
+    }
+    __device__ __forceinline__ int64_t part_row(int rr) const {
+        return ((int64_t)(w.slot + w.part) * a.kv_heads.d + kvh) * a.slot_rows + (rr - row0);
+    }
+};
+
+// Whether a lane's row sees key c + 4 (lane / 32) of a tile; lim, lo and sinks
+// are counted from the tile's first key, less 4 for the upper half of the lanes.
+template <bool WIN>
+__device__ __forceinline__ bool key_seen(int c, int lim, int lo, int sinks) {
+    return c < lim && (!WIN || c >= lo || c < sinks);
+}
+
+template <bool WIN>
+__device__ __forceinline__ void key_mask(f16x_t& s, int lim, int lo, int sinks) {
+#pragma unroll
+    for (int r = 0; r < 16; ++r)
+        if (!key_seen<WIN>(8 * (r >> 2) + (r & 3), lim, lo, sinks)) s[r] = -__builtin_inff();
+}
+
+// Infinities and NaN among the values (see attn_finite): the wave's rows again,
+// straight from memory, tiles i0, i0 + step, ... below i1, values that are not
+// finite left out.  Then the rows that see such a value get it: a product of
+// ones (where a key is seen) with ones (where its value is +inf or NaN, then
+// -inf or NaN) counts them for every row and column, whatever the rows see.
+// Few registers before speed.
+template <class C>
+__device__ __forceinline__ void key_again(const KeyTile<C>& k, f16x_t (&o)[C::DB], const RowState& st, int rr, int i0, int step,
+                                          int lane) {
+    using M = Ty32<C::DT>;
+    constexpr unsigned kExp = C::DT == DT_BF16 ? 0x7F80 : 0x7C00, kOne = C::DT == DT_BF16 ? 0x3F80 : 0x3C00;
+    const KeyArgs& a = k.a;
+    const int m = lane & 31, h = lane >> 5, nk = k.w.nk;
+    const int pos = a.group(rr), head = k.kvh * a.group.d + (rr - pos * a.group.d);
+    const int lim = k.sees(rr) - 4 * h, lo = C::WIN ? k.from(rr) - 4 * h : 0;
+    // column 32b + m of 8 keys' values; kind 0: the finite ones, 1, 2: ones in place of the others
+    auto values = [&](int t, int ks, int b, int kind) __attribute__((always_inline)) {
+        u4_t x = {0, 0, 0, 0};
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int at = t * C::BN + 16 * ks + 8 * (u >> 2) + 4 * h + (u & 3), c = 32 * b + m;
+            unsigned v = 0;
+            if (at < nk && c < a.dim) v = *(const unsigned short*)(k.key_row(true, at) + 2 * c);
+            const bool odd = (v & kExp) == kExp, nan = odd && (v & 0x7FFF & ~kExp);
+            if (kind == 0) v = odd ? 0 : v;
+            else v = nan || (odd && (int)(v >> 15) == kind - 1) ? kOne : 0;
+            x[u >> 1] |= v << (16 * (u & 1));
+        }
+        return x;
+    };
+#pragma unroll
+    for (int b = 0; b < C::DB; ++b) o[b] = f16x_t{};
+    for (int i = i0; i < k.i1; i += step) {
+        const int t = k.tile(i), key = t * C::BN + m;
+        const char* kp = key < nk ? k.key_row(false, key) : (const char*)kZeros;
+        f16x_t s = f16x_t{};
+#pragma unroll 1
+        for (int j = 0; j < C::KS; ++j) {
+            const bool in = 16 * j + 8 * h < a.dim;
+            u4_t x = {0, 0, 0, 0}, y = {0, 0, 0, 0};
+            if (in && key < nk) x = *(const u4_t*)(kp + 32 * j + 16 * h);
+            if (in && rr < k.rows)
+                y = *(const u4_t*)((const char*)a.Q.p + ((k.w.q0 + pos) * a.Q.ld + (int64_t)head * a.Q.hs + 16 * j + 8 * h) * 2);
+            s = M::mma(x, y, s);
+        }
+        key_mask<C::WIN>(s, lim - t * C::BN, lo - t * C::BN, a.sinks - 4 * h - t * C::BN);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], a.sc, -st.m));
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            const u4_t p = attn_pack<C::DT>(s, ks);
+#pragma unroll
+            for (int b = 0; b < C::DB; ++b) {
+                o[b] = M::mma(values(t, ks, b, 0), p, o[b]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+    }
+#pragma unroll
+    for (int b = 0; b < C::DB; ++b)
+#pragma unroll 1
+        for (int kind = 1; kind <= 2; ++kind) {
+            f16x_t n = f16x_t{};
+            for (int i = i0; i < k.i1; i += step) {
+                const int t = k.tile(i), x = t * C::BN;
+#pragma unroll 1
+                for (int ks = 0; ks < 2; ++ks) {
+                    u4_t p = {0, 0, 0, 0};
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) {
+                        const int c = 16 * ks + 8 * (u >> 2) + (u & 3);
+                        if (key_seen<C::WIN>(c, lim - x, lo - x, a.sinks - 4 * h - x)) p[u >> 1] |= kOne << (16 * (u & 1));
+                    }
+                    n = M::mma(values(t, ks, b, kind), p, n);
+                }
+            }
+            const float give = kind == 1 ? __builtin_inff() : -__builtin_inff();
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                if (n[r] != 0.f) o[b][r] += give;
+        }
+}
+
+// ---------------------------------------------------------------------------
+// Many rows: 32 a wave, the key tiles shared (attn_tile_body's scheme)
+// ---------------------------------------------------------------------------
+template <class C>
+__device__ __forceinline__ void key_tile_body(const KeyTile<C>& k, unsigned char* lds) {
+    using M = Ty32<C::DT>;
+    const KeyArgs& a = k.a;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int wrow = k.row0 + 32 * wave, rr = wrow + (lane & 31), h = lane >> 5;
+    const int lim = k.sees(rr) - 4 * h, lo = C::WIN ? k.from(rr) - 4 * h : 0;
+    u4_t q[C::KS];
+    f16x_t o[C::DB];
+    RowState st;
+    st.init();
+#pragma unroll
+    for (int b = 0; b < C::DB; ++b) o[b] = f16x_t{};
+    // tiles below `clear` are full and end where every row of the wave sees; from `done` on none sees any;
+    // under a window rows see nothing of tiles that end at `dark` or before, everything from `open` on
+    const int clear = wrow + 32 <= k.rows ? k.sees(wrow) / C::BN : 0;
+    const int wlast = (wrow + 32 < k.rows ? wrow + 32 : k.rows) - 1;
+    const int done = wrow < k.rows ? (k.sees(wlast) + C::BN - 1) / C::BN : 0;
+    const int dark = C::WIN ? k.from(wrow) : 0, open = C::WIN ? k.from(wlast) : 0;
+    const bool keys = wave < 2;
+    auto copy = [&](int i, int e) __attribute__((always_inline)) {
+        const unsigned char* dst = lds + (2 * (i & 1) + (keys ? 0 : 1)) * C::TILE;
+        if (keys) k.template copy<false>(dst, k.tile(i), wave, e, lane);
+        else k.template copy<true>(dst, k.tile(i), wave - 2, e, lane);
+    };
+    auto entry = [&](int i) __attribute__((always_inline)) { return k.entry_of(k.tile(i), wave & 1, lane); };
+    const int kb0 = attn_kbase(lane, 0), kb1 = attn_kbase(lane, 1), vb = attn_vbase(lane);
+    int e = 0;
+    if (k.i0 < k.i1) {
+        copy(k.i0, entry(k.i0));
+        if (k.i0 + 1 < k.i1) e = entry(k.i0 + 1);
+    }
+    attn_load_q<C::KS>(q, a, k.w.q0, k.kvh, rr, k.rows, lane);
+    for (int i = k.i0; i < k.i1; ++i) {
+        barrier_vm<0>();          // tile i is in LDS, and everyone is done with tile i - 1
+        if (i == k.i0)
+#pragma unroll
+            for (int j = 0; j < C::KS; ++j) asm volatile("" : "+v"(q[j]));
+        if (i + 1 < k.i1) {
+            copy(i + 1, e);
+            if (i + 2 < k.i1) e = entry(i + 2);
+        }
+        const int t = k.tile(i), at = t * C::BN;
+        if (t >= done || (C::WIN && at + C::BN <= dark && at >= a.sinks)) continue;
+        const unsigned char* kt = lds + 2 * (i & 1) * C::TILE;
+        const unsigned char* vt = kt + C::TILE;
+        f16x_t s[1] = {f16x_t{}};
+#pragma unroll
+        for (int j = 0; j < C::KS; ++j)
+            s[0] = M::mma(*(const u4_t*)(kt + ((j & 1) ? kb1 : kb0) + (j >> 1) * C::BN * 64), q[j], s[0]);
+        if (t >= clear || (C::WIN && at < open && at + C::BN > a.sinks))
+            key_mask<C::WIN>(s[0], lim - at, lo - at, a.sinks - 4 * h - at);
+        attn_move_max<C::DB>(attn_max<1>(s), st, o, a.sc);
+        attn_probs<1>(s, st, a.sc);
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            const u4_t p = attn_pack<C::DT>(s[0], ks);
+#pragma unroll
+            for (int b = 0; b < C::DB; ++b) o[b] = M::mma(attn_vfrag<C::BN>(vt, vb, b, ks), p, o[b]);
+        }
+    }
+    if (!attn_finite<C>(o, st)) key_again<C>(k, o, st, rr, k.i0, 1, lane);
+    if (k.w.parts == 1) {
+        attn_store<C::DT, C::DB, false>(a, o, st, k.w.q0, k.kvh, rr, k.rows, 0, lane);
+        return;
+    }
+    const float l = st.l + other_half(st.l), inv = l == 0.f ? 0.f : 1.f / l;
+    if (rr >= k.rows) return;
+    const int64_t row = k.part_row(rr);
+    if (h == 0) a.part_lse[row] = l == 0.f ? -__builtin_inff() : st.m + __builtin_amdgcn_logf(l);
+#pragma unroll
+    for (int b = 0; b < C::DB; ++b)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const int c = 32 * b + 8 * x + 4 * h;
+            if (c < a.dim)
+                *(f4_t*)(a.part + row * a.dim + c) =
+                    f4_t{o[b][4 * x] * inv, o[b][4 * x + 1] * inv, o[b][4 * x + 2] * inv, o[b][4 * x + 3] * inv};
+        }
+}
+
+// ---------------------------------------------------------------------------
+// Up to 32 rows: the waves take different keys (attn_rows_body's scheme)
+// ---------------------------------------------------------------------------
+template <class C>
+__device__ __forceinline__ void key_rows_body(const KeyTile<C>& k, unsigned char* lds) {
+    using M = Ty32<C::DT>;
+    const KeyArgs& a = k.a;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int rr = k.row0 + (lane & 31), h = lane >> 5;
+    const int lim = k.sees(rr) - 4 * h, lo = C::WIN ? k.from(rr) - 4 * h : 0;
+    const int last = k.rows - 1;
+    // tiles below `clear` are seen whole by every row, but for what the window hides of those below `open`
+    const int clear = k.sees(k.row0) / C::BN, open = C::WIN ? k.from(last) : 0;
+    u4_t q[C::KS];
+    f16x_t o[C::DB];
+    RowState st;
+    attn_load_q<C::KS>(q, a, k.w.q0, k.kvh, rr, k.rows, lane);
+    st.init();
+#pragma unroll
+    for (int b = 0; b < C::DB; ++b) o[b] = f16x_t{};
+    unsigned char* mine = lds + wave * C::TILE;
+    auto copy = [&](auto VALUES, int t, int e0, int e1) __attribute__((always_inline)) {
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");    // what the rows held has been read
+        k.template copy<VALUES.value>(mine, t, 0, e0, lane);
+        k.template copy<VALUES.value>(mine, t, 1, e1, lane);
+    };
+    const int kb0 = attn_kbase(lane, 0), kb1 = attn_kbase(lane, 1), vb = attn_vbase(lane);
+    const int i0 = k.i0 + wave;
+    int e0 = 0, e1 = 0;
+    if (i0 < k.i1) {
+        e0 = k.entry_of(k.tile(i0), 0, lane);
+        e1 = k.entry_of(k.tile(i0), 1, lane);
+        copy(std::false_type{}, k.tile(i0), e0, e1);
+    }
+    for (int i = i0; i < k.i1; i += C::WAVES) {
+        const int t = k.tile(i), at = t * C::BN;
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        f16x_t s[1] = {f16x_t{}};
+#pragma unroll
+        for (int j = 0; j < C::KS; ++j)
+            s[0] = M::mma(*(const u4_t*)(mine + ((j & 1) ? kb1 : kb0) + (j >> 1) * C::BN * 64), q[j], s[0]);
+        copy(std::true_type{}, t, e0, e1);
+        int n0 = 0, n1 = 0;
+        if (i + C::WAVES < k.i1) {
+            n0 = k.entry_of(k.tile(i + C::WAVES), 0, lane);
+            n1 = k.entry_of(k.tile(i + C::WAVES), 1, lane);
+        }
+        if (t >= clear || (C::WIN && at < open && at + C::BN > a.sinks))
+            key_mask<C::WIN>(s[0], lim - at, lo - at, a.sinks - 4 * h - at);
+        attn_move_max<C::DB>(attn_max<1>(s), st, o, a.sc);
+        attn_probs<1>(s, st, a.sc);
+        u4_t p[2];
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) p[ks] = attn_pack<C::DT>(s[0], ks);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+#pragma unroll
+        for (int b = 0; b < C::DB; ++b)
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) o[b] = M::mma(attn_vfrag<C::BN>(mine, vb, b, ks), p[ks], o[b]);
+        e0 = n0;
+        e1 = n1;
+        if (i + C::WAVES < k.i1) copy(std::false_type{}, k.tile(i + C::WAVES), e0, e1);
+    }
+    if (!attn_finite<C>(o, st)) key_again<C>(k, o, st, rr, i0, C::WAVES, lane);
+    // join: every wave's maximum and sum, then its rows, scaled to the common maximum
+    float* ms = (float*)(lds + C::JOIN);           // [maximum, sum][wave][row]
+    const float l = st.l + other_half(st.l);
+    if (lane < 32) {
+        ms[wave * 32 + lane] = st.m;
+        ms[(C::WAVES + wave) * 32 + lane] = l;
+    }
+    __syncthreads();
+    float m = kLowest, sum = 0.f;
+#pragma unroll
+    for (int v = 0; v < C::WAVES; ++v) m = __builtin_fmaxf(m, ms[v * 32 + (lane & 31)]);
+#pragma unroll
+    for (int v = 0; v < C::WAVES; ++v)
+        sum += ms[(C::WAVES + v) * 32 + (lane & 31)] * __builtin_amdgcn_exp2f(ms[v * 32 + (lane & 31)] - m);
+    const float f = __builtin_amdgcn_exp2f(st.m - m) * (sum == 0.f ? 0.f : 1.f / sum);
+    const bool whole = k.w.parts == 1;
+    if (wave == 0 && lane < 32 && rr < k.rows) {
+        const float lse2 = sum == 0.f ? -__builtin_inff() : m + __builtin_amdgcn_logf(sum);
+        const int pos = a.group(rr);
+        if (!whole) a.part_lse[k.part_row(rr)] = lse2;
+        else if (a.lse) a.lse[(int64_t)(k.w.q0 + pos) * a.heads + k.kvh * a.group.d + (rr - pos * a.group.d)] = lse2 * kLn2;
+    }
+    const int live = k.rows - k.row0;              // 32 at most
+    // half of the columns at a time: a wave's tile of LDS holds 32 rows of
+    // 16 DB floats, [column quad][row]
+    float* mo = (float*)mine;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        __syncthreads();
+#pragma unroll
+        for (int x = 0; x < 2 * C::DB; ++x) {
+            const int y = half * 2 * C::DB + x, b = y / 4, g = y % 4;        // column quads 2y and 2y + 1
+            f4_t v;
+            // a wave that weighs nothing here gives its infinities and NaN all the same
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float z = o[b][4 * g + r];
+                v[r] = f == 0.f ? (__builtin_fabsf(z) <= -kLowest ? 0.f : z) : z * f;
+            }
+            *(f4_t*)(mo + ((2 * x + (lane >> 5)) * 32 + (lane & 31)) * 4) = v;
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < live * 4 * C::DB; i += C::THREADS) {
+            const int row = i / (4 * C::DB), c = i % (4 * C::DB), col = 4 * (half * 4 * C::DB + c);
+            if (col >= a.dim) continue;
+            f4_t v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int x = 0; x < C::WAVES; ++x) {
+                const f4_t y = *(const f4_t*)((const float*)(lds + x * C::TILE) + (c * 32 + row) * 4);
+#pragma unroll
+                for (int z = 0; z < 4; ++z) v[z] += y[z];
+            }
+            const int r = k.row0 + row;
+            if (!whole) {
+                *(f4_t*)(a.part + k.part_row(r) * a.dim + col) = v;
+            } else {
+                const int pos = a.group(r), head = k.kvh * a.group.d + (r - pos * a.group.d);
+                *(u2_t*)((char*)a.O + ((int64_t)(k.w.q0 + pos) * a.ldo + (int64_t)head * a.hso + col) * 2) =
+                    u2_t{Ty<C::DT>::pack(v[0], v[1]), Ty<C::DT>::pack(v[2], v[3])};
+            }
+        }
+    }
+}
+
+template <class C>
+__global__ __launch_bounds__(C::THREADS, 3) void key_attn_kernel(KeyArgs a) {
+    __shared__ __attribute__((aligned(1024))) unsigned char lds[C::LDS_BYTES];
+    const int u = a.kv_heads((int)blockIdx.x), kvh = (int)blockIdx.x - u * a.kv_heads.d;
+    KeyItem w;
+    if (!find_item<C::PAGED, C::WIN, false>(a, u, &w)) return;
+    const KeyTile<C> k(a, w, kvh);
+    if (k.rows - k.row0 <= 32) key_rows_body<C>(k, lds);
+    else key_tile_body<C>(k, lds);
+}
+
+// ---------------------------------------------------------------------------
+// Joining partial results: 32 rows of a tile a workgroup, 16 lanes a row, 8
+// columns a lane
+// ---------------------------------------------------------------------------
+// O = sum_s w_s O_s / sum_s w_s with w_s = 2^(lse_s - max); parts that saw no
+// key have lse = -inf and are left out, whatever they hold; those whose weight
+// is 0 give infinities and NaN all the same.  SUB = 4: a row's parts go over the
+// four quarters of a wave.
+template <int DT, int SUB>
+__device__ __forceinline__ void key_join_rows(const KeyArgs& a, const KeyItem& w, int kvh, int first, int live, int row0) {
+    const int lane = threadIdx.x & 15, sub = SUB == 1 ? 0 : (threadIdx.x >> 4) & (SUB - 1);
+    const bool in = 8 * lane < a.dim;
+    const int64_t step = (int64_t)a.kv_heads.d * a.slot_rows;      // from a part's row to the next part's
+    for (int r = threadIdx.x / (16 * SUB); r < live; r += 16 / SUB) {
+        const int rr = row0 + first + r;
+        const int64_t at = ((int64_t)w.slot * a.kv_heads.d + kvh) * a.slot_rows + first + r;
+        float m = -__builtin_inff();
+        for (int s = threadIdx.x & (16 * SUB - 1); s < w.parts; s += 16 * SUB) {
+            const float y = a.part_lse[at + s * step];
+            m = y > m || y != y ? y : m;
+        }
+#pragma unroll
+        for (int d = 1; d < 16 * SUB; d <<= 1) {
+            const float y = __shfl_xor(m, d);
+            m = y > m || y != y ? y : m;
+        }
+        const float m0 = m == -__builtin_inff() ? 0.f : m;
+        float sum = 0.f, x[8] = {};
+        constexpr int PER = 4;          // parts' loads in flight
+        for (int s0 = sub; s0 < w.parts; s0 += PER * SUB) {
+            float l[PER];
+            f4_t v[PER][2];
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const bool have = s0 + i * SUB < w.parts;
+                const int64_t p = at + (have ? s0 + i * SUB : s0) * step;
+                l[i] = have ? a.part_lse[p] : -__builtin_inff();
+                v[i][0] = v[i][1] = f4_t{0.f, 0.f, 0.f, 0.f};
+                if (in) {
+                    v[i][0] = *(const f4_t*)(a.part + p * a.dim + 8 * lane);
+                    v[i][1] = *(const f4_t*)(a.part + p * a.dim + 8 * lane + 4);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                if (l[i] == -__builtin_inff()) continue;
+                const float f = __builtin_amdgcn_exp2f(l[i] - m0);
+                sum += f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float y = v[i][e >> 2][e & 3];
+                    x[e] += f == 0.f ? (__builtin_fabsf(y) <= -kLowest ? 0.f : y) : f * y;
+                }
+            }
+        }
+#pragma unroll
+        for (int d = 16; d < 16 * SUB; d <<= 1) {
+            sum += __shfl_xor(sum, d);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] += __shfl_xor(x[e], d);
+        }
+        if (sub) continue;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const int pos = a.group(rr), head = kvh * a.group.d + (rr - pos * a.group.d);
+        const int64_t row = w.q0 + pos;
+        if (in)
+            *(u4_t*)((char*)a.O + (row * a.ldo + (int64_t)head * a.hso + 8 * lane) * 2) =
+                u4_t{Ty<DT>::pack(x[0] * inv, x[1] * inv), Ty<DT>::pack(x[2] * inv, x[3] * inv),
+                     Ty<DT>::pack(x[4] * inv, x[5] * inv), Ty<DT>::pack(x[6] * inv, x[7] * inv)};
+        if (lane == 0 && a.lse)
+            a.lse[row * a.heads + head] = sum == 0.f ? -__builtin_inff() : (m + __builtin_amdgcn_logf(sum)) * kLn2;
+    }
+}
+
+template <int DT, bool PAGED, bool WIN>
+__global__ __launch_bounds__(256) void key_join_kernel(KeyArgs a) {
+    const int v = a.kv_heads((int)blockIdx.x), kvh = (int)blockIdx.x - v * a.kv_heads.d;
+    KeyItem w;
+    if (!find_item<PAGED, WIN, true>(a, v >> 2, &w) || w.parts == 1) return;
+    const int first = 32 * (v & 3), row0 = (w.tiles - 1 - w.tile) * kKeyRows;
+    int live = w.nq * a.group.d - row0 - first;
+    live = live < 32 ? live : 32;
+    if (w.parts >= 4) key_join_rows<DT, 4>(a, w, kvh, first, live, row0);
+    else key_join_rows<DT, 1>(a, w, kvh, first, live, row0);
+}
+
+}  // namespace b2bk

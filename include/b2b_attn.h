@@ -107,6 +107,56 @@ b2b_status_t b2b_prefix_attn_run(b2b_attn_t plan, int32_t batch, int64_t prefix,
                                  int64_t v_stride, const int32_t* lens, b2b_rows_t O, void* workspace,
                                  size_t workspace_bytes, hipStream_t stream);
 
+/*
+ * Plans causal attention under a window, for b2b_attn_workspace and
+ * b2b_attn_run: the row in place p of its sequence (counted from the last key,
+ * as B2B_ATTN_CAUSAL) sees keys p - window + 1 .. p and the sequence's first
+ * `sinks` keys up to p.
+ *   window   1 to 2^30      sinks   0 to 2^30
+ * rows (of b2b_attn_run) up to 2^30.
+ */
+b2b_status_t b2b_attn_create_window(b2b_attn_t* plan, b2b_dtype_t dtype, int32_t heads, int32_t kv_heads, int32_t head_dim,
+                                    float scale, int32_t window, int32_t sinks);
+
+/* The pages of a cache, all of one size, in device memory: base 16-byte
+ * aligned, strides in elements, multiples of 8, in any order ([pages, size,
+ * heads, dim] and [pages, heads, size, dim] alike). */
+typedef struct {
+    void* data;            /* only b2b_rotary_append writes */
+    int64_t page_stride;
+    int64_t row_stride;    /* from one key of a page to the next */
+    int64_t head_stride;
+} b2b_pages_t;
+
+/*
+ * Plans causal attention of new tokens over a paged cache: key j of sequence s
+ * is row j % page_size of page table[s][j / page_size].
+ *   page_size      1 to 2^20, no power of two needed
+ *   window, sinks  as b2b_attn_create_window; window 0: every earlier key
+ */
+b2b_status_t b2b_paged_attn_create(b2b_attn_t* plan, b2b_dtype_t dtype, int32_t heads, int32_t kv_heads, int32_t head_dim,
+                                   int32_t page_size, float scale, int32_t window, int32_t sinks);
+
+/*
+ * Rows cu_q[s] .. cu_q[s+1]-1 of Q and O are the last tokens of sequence s, whose
+ * lens[s] keys (theirs among them) are in the cache: one token, a chunk of a
+ * prompt or none, each sequence as it comes.  A row sees the keys up to its own
+ * place, or those of its window; one that sees no key gets 0.  Rows that belong
+ * to no sequence are not written.  What pages hold behind a sequence's last key
+ * is never looked at; infinities and NaN as for b2b_attn_run.
+ *   pages   pages of K and V: entries of the table are clamped to them
+ *   table   device int32 [seqs, width], rows table_stride apart; entries of pages
+ *           behind a sequence's last key are not read
+ *   lens    device int32 [seqs], clamped to 0 .. width x page_size (2^30 at most)
+ *   cu_q    device int32 [seqs + 1], or NULL: row s is sequence s's one token
+ *   lse, workspace   as for b2b_attn_run (b2b_paged_attn_workspace)
+ */
+b2b_status_t b2b_paged_attn_workspace(b2b_attn_t plan, int32_t seqs, int64_t rows, int32_t width, size_t* bytes);
+b2b_status_t b2b_paged_attn_run(b2b_attn_t plan, int32_t seqs, int64_t rows, b2b_rows_t Q, b2b_pages_t K, b2b_pages_t V,
+                                int32_t pages, const int32_t* table, int32_t width, int64_t table_stride, const int32_t* lens,
+                                const int32_t* cu_q, b2b_rows_t O, float* lse, void* workspace, size_t workspace_bytes,
+                                hipStream_t stream);
+
 /* Releases a plan. NULL is a no-op. */
 b2b_status_t b2b_attn_destroy(b2b_attn_t plan);
 
@@ -161,6 +211,69 @@ b2b_status_t b2b_linear_attn_step(b2b_linear_attn_t plan, int32_t batch, b2b_row
 
 /* Releases a plan. NULL is a no-op. */
 b2b_status_t b2b_linear_attn_destroy(b2b_linear_attn_t plan);
+
+typedef struct b2b_rotary_plan* b2b_rotary_t;   /* opaque, owned by the library */
+
+/* Flags of b2b_rotary_create. */
+enum {
+    B2B_ROTARY_NORM = 1u << 0,         /* heads are normed first */
+    B2B_ROTARY_INTERLEAVED = 1u << 1   /* pair i is elements 2i, 2i + 1; else i, i + rotary_dim / 2 */
+};
+
+/*
+ * Plans what a decoder does to its queries and keys before the attention, in
+ * one pass: each head x is normed (B2B_ROTARY_NORM),
+ *     y = x / sqrt(mean(x^2) + eps) * weight,
+ * and pair i of its first rotary_dim elements is turned by the row's position,
+ *     (a, b) -> (a cos t - b sin t, b cos t + a sin t),  t = position[axes_of[i]] freqs[i].
+ * All of it in float32 (angles reduced in float64, so that far positions lose
+ * nothing; norms whose sums leave float32's range in float64), rounded once.
+ *   rotary_dim  a multiple of 8, 0 (no rotation) to head_dim
+ *   freqs       host, rotary_dim / 2 finite values: radians a position
+ *   axes_of     host, rotary_dim / 2 values below `axes`, or NULL (all axis 0)
+ *   axes        1 to 4 positions a row (time, height, width ...)
+ *   eps         0 or more, finite (without B2B_ROTARY_NORM not looked at)
+ * dtype, heads, kv_heads and head_dim as b2b_attn_create.
+ */
+b2b_status_t b2b_rotary_create(b2b_rotary_t* plan, b2b_dtype_t dtype, int32_t heads, int32_t kv_heads, int32_t head_dim,
+                               int32_t rotary_dim, const double* freqs, const int32_t* axes_of, int32_t axes, float eps,
+                               uint32_t flags);
+
+/*
+ * Q' and K' of `rows` rows: Qo and Ko may be Q and K (the same address and
+ * strides: in place), and must not overlap anything else.
+ *   positions        device int32 [axes, rows], axes position_stride apart (NULL where
+ *                    rotary_dim is 0)
+ *   q_weight, k_weight  device, head_dim values of dtype, 16-byte aligned, or NULL (1);
+ *                    NULL without B2B_ROTARY_NORM
+ */
+b2b_status_t b2b_rotary_run(b2b_rotary_t plan, int64_t rows, b2b_rows_t Q, b2b_rows_t K, b2b_rows_t Qo, b2b_rows_t Ko,
+                            const int32_t* positions, int64_t position_stride, const void* q_weight, const void* k_weight,
+                            hipStream_t stream);
+
+/*
+ * The same for new tokens whose keys and values go into a paged cache: rows
+ * cu[s] .. cu[s+1]-1 (or row s, without cu) are the last tokens of sequence s,
+ * which has lens[s] keys with theirs.  Q' goes to Qo, K' and V to the row's place
+ * in the pages, where b2b_paged_attn_run with the same table, lens and cu finds
+ * them.
+ *   positions   as above, or NULL: a row's place in its sequence, on every axis
+ *   pages, page_size, table, width, table_stride, lens, cu   as b2b_paged_attn_run.
+ *               A row whose place is below 0 or past the table, or whose entry
+ *               names no page, writes no key and no value; rows that belong to
+ *               no sequence write nothing
+ * No two rows of a call may have the same place of the same page (sequences that
+ * share pages have their new tokens in pages of their own); no two places of
+ * the pages may share an element.
+ */
+b2b_status_t b2b_rotary_append(b2b_rotary_t plan, int32_t seqs, int64_t rows, b2b_rows_t Q, b2b_rows_t K, b2b_rows_t V,
+                               b2b_rows_t Qo, b2b_pages_t k_cache, b2b_pages_t v_cache, int32_t pages, int32_t page_size,
+                               const int32_t* table, int32_t width, int64_t table_stride, const int32_t* lens,
+                               const int32_t* cu, const int32_t* positions, int64_t position_stride, const void* q_weight,
+                               const void* k_weight, hipStream_t stream);
+
+/* Releases a plan. NULL is a no-op. */
+b2b_status_t b2b_rotary_destroy(b2b_rotary_t plan);
 
 #ifdef __cplusplus
 }

@@ -60,6 +60,12 @@ __device__ __forceinline__ void unpack8(u4_t w, float (&x)[8]) {
     for (int u = 0; u < 8; ++u) x[u] = attn_unpack<DT>(w[u >> 1], u & 1);
 }
 
+// A head's 8 elements a lane: out = inv (x own + partner's x far), where `own` and
+// `far` are cosine and signed sine with the weights of either element folded in.
+struct Turn {
+    float own[8], far[8];
+};
+
 // APPEND: keys and values go to the pages.  NORM, INTER: the plan's flags.
 template <int DT, int L, bool APPEND, bool NORM, bool INTER>
 __global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a) {
@@ -72,25 +78,21 @@ __global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a) {
     const int group = threadIdx.x / L, c = threadIdx.x & (L - 1);
     const int r = group & (R - 1), row = row0 + r;
     // this lane's heads: Q's, then K's, then V's, `step` apart
-    const int items = a.heads + (APPEND ? 2 : 1) * a.kv_heads, step = (GROUPS >> a.row_log) * a.per_row.d;
-    const int first = (group >> a.row_log) + share * (GROUPS >> a.row_log);
+    const int step = (GROUPS >> a.row_log) * a.per_row.d, first = (group >> a.row_log) + share * (GROUPS >> a.row_log);
+    const int keys0 = a.heads, values0 = a.heads + a.kv_heads, items = values0 + (APPEND ? a.kv_heads : 0);
     const bool live = row < a.rows && 8 * c < a.dim;
-    auto source = [&](int i) __attribute__((always_inline)) {
-        const bool q = i < a.heads, k = !APPEND || i < a.heads + a.kv_heads;
-        const AttnRows& x = q ? a.Q : k ? a.K : a.V;
-        const int h = q ? i : k ? i - a.heads : i - a.heads - a.kv_heads;
-        return (const u4_t*)((const char*)x.p + (row * x.ld + h * x.hs + 8 * c) * 2);
-    };
     u4_t raw[BATCH];
-    auto fetch = [&](int i0) __attribute__((always_inline)) {
+    // the next BATCH heads from i0 on, below `end`, of an operand whose first head is item i1
+    auto fetch = [&](const AttnRows& x, int i1, int i0, int end) __attribute__((always_inline)) {
+        const char* p = (const char*)x.p + (row * x.ld + (int64_t)(i0 - i1) * x.hs + 8 * c) * 2;
 #pragma unroll
         for (int j = 0; j < BATCH; ++j) {
             raw[j] = u4_t{0, 0, 0, 0};
-            if (live && i0 + j * step < items) raw[j] = *source(i0 + j * step);
+            if (live && i0 + j * step < end) raw[j] = *(const u4_t*)(p + j * step * x.hs * 2);
         }
     };
-    fetch(first);
-    // the pieces of the weights that this lane and its partners hold
+    if (first < keys0) fetch(a.Q, 0, first, keys0);
+    // the partners of this lane's elements
     const int half = a.rotary >> 1;
     int from[2];                // lane (of L) with the partner of each half of the piece
     const int other = (half >> 2) & 1;      // whether it is in the other half of that lane's piece
@@ -102,6 +104,19 @@ __global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a) {
         lower[h] = 4 * v < half;
         from[h] = turned[h] ? (lower[h] ? v + (half >> 2) : v - (half >> 2)) >> 1 : c;
     }
+    auto partner = [&](u4_t w) __attribute__((always_inline)) {
+        u4_t out;
+        if constexpr (INTER) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) out[i] = w[i] >> 16 | w[i] << 16;
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) out[2 * h + j] = __shfl(other ? w[2 * (h ^ 1) + j] : w[2 * h + j], from[h], L);
+        }
+        return out;
+    };
     u4_t qw = {0, 0, 0, 0}, kw = qw;
     if constexpr (NORM) {
         if (a.qw && 8 * c < a.dim) qw = *((const u4_t*)a.qw + c);
@@ -149,15 +164,26 @@ __global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a) {
         turn[rr][p][1] = s;
     }
     __syncthreads();
-    float cosine[8], sine[8];       // the sine with the sign that the element's partner comes with
+    auto turn_of = [&](const void* weight, u4_t w) __attribute__((always_inline)) {
+        Turn t;
+        float x[8], y[8];
+        if (NORM && weight) {
+            unpack8<DT>(w, x);
+            unpack8<DT>(partner(w), y);
+        } else {
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-        const int e = 8 * c + u;
-        const int p = INTER ? e >> 1 : (lower[u >> 2] ? e : e - half);
-        cosine[u] = turned[u >> 2] ? turn[r][p & 63][0] : 1.f;
-        const float s = turned[u >> 2] ? turn[r][p & 63][1] : 0.f;
-        sine[u] = (INTER ? !(u & 1) : lower[u >> 2]) ? -s : s;
-    }
+            for (int u = 0; u < 8; ++u) x[u] = y[u] = 1.f;
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int e = 8 * c + u;
+            const int p = (INTER ? e >> 1 : (lower[u >> 2] ? e : e - half)) & 63;
+            const float co = turned[u >> 2] ? turn[r][p][0] : 1.f, s = turned[u >> 2] ? turn[r][p][1] : 0.f;
+            t.own[u] = x[u] * co;
+            t.far[u] = (INTER ? !(u & 1) : lower[u >> 2]) ? -s * y[u] : s * y[u];
+        }
+        return t;
+    };
     char *kp = nullptr, *vp = nullptr;      // append: where head 0's piece of the row goes
     bool writes = live;
     if constexpr (APPEND) {
@@ -172,101 +198,72 @@ __global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a) {
                 vp = (char*)a.cv.p + (entry * a.cv.ps + in * a.cv.ld + 8 * c) * 2;
             }
         }
+    } else {
+        kp = (char*)a.Ko + (row * a.ldko + 8 * c) * 2;
     }
-    auto partner = [&](u4_t w, u4_t& out) __attribute__((always_inline)) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const unsigned x = other ? w[2 * (h ^ 1) + j] : w[2 * h + j];
-                out[2 * h + j] = __shfl(x, from[h], L);
-            }
-    };
-    u4_t qwp = qw, kwp = kw;
-    if constexpr (NORM && !INTER) {
-        partner(qw, qwp);
-        partner(kw, kwp);
-    }
+    const bool all = a.rotary == a.dim;
     const float per = 1.f / a.dim;
-    for (int i0 = first; i0 < items; i0 += BATCH * step) {
-        u4_t now[BATCH];
+    auto head = [&](u4_t w, const Turn& t) __attribute__((always_inline)) {
+        float x[8], y[8];
+        unpack8<DT>(w, x);
+        unpack8<DT>(partner(w), y);
+        if (!all)       // an element that is not turned keeps its value whatever its neighbour holds
 #pragma unroll
-        for (int j = 0; j < BATCH; ++j) now[j] = raw[j];
-        fetch(i0 + BATCH * step);
+            for (int u = 0; u < 8; ++u) y[u] = turned[u >> 2] ? y[u] : 0.f;
+        float inv = 1.f;
+        if constexpr (NORM) {
+            float sum = 0.f;
 #pragma unroll
-        for (int j = 0; j < BATCH; ++j) {
-            const int i = i0 + j * step;
-            if (i >= items) break;
-            const bool q = i < a.heads, k = !q && (!APPEND || i < a.heads + a.kv_heads);
-            u4_t out = now[j];
-            if (q || k) {
-                float x[8], y[8];
-                unpack8<DT>(now[j], x);
-                if constexpr (INTER) {
+            for (int u = 0; u < 8; ++u) sum = __builtin_fmaf(x[u], x[u], sum);
+            sum = head_sum<L>(sum);
+            inv = __builtin_amdgcn_rsqf(__builtin_fmaf(sum, per, a.eps));
+            // squares that leave float32's range (the sum infinite, or so small that terms are lost)
+            const bool odd = !(sum < 0x1p126f && sum > 0x1p-100f) && sum == sum;
+            if (__any(odd)) {
+                double d = 0.0;
 #pragma unroll
-                    for (int u = 0; u < 8; ++u) y[u] = x[u ^ 1];
-                } else {
-                    u4_t p;
-                    partner(now[j], p);
-                    unpack8<DT>(p, y);
-                }
-                if constexpr (NORM) {
-                    float sum = 0.f;
+                for (int u = 0; u < 8; ++u) d += (double)x[u] * x[u];
+                d = 1.0 / sqrt(head_sum<L>(d) / a.dim + (double)a.eps);
+                if (odd) {
+                    inv = 1.f;
 #pragma unroll
-                    for (int u = 0; u < 8; ++u) sum = __builtin_fmaf(x[u], x[u], sum);
-                    sum = head_sum<L>(sum);
-                    const float inv = __builtin_amdgcn_rsqf(__builtin_fmaf(sum, per, a.eps));
-                    // squares that leave float32's range (the sum infinite, or so small that terms are lost)
-                    const bool far = !(sum < 0x1p126f && sum > 0x1p-100f) && sum == sum;
-                    if (__any(far)) {
-                        double d = 0.0;
-#pragma unroll
-                        for (int u = 0; u < 8; ++u) d += (double)x[u] * x[u];
-                        d = 1.0 / sqrt(head_sum<L>(d) / a.dim + (double)a.eps);
-#pragma unroll
-                        for (int u = 0; u < 8; ++u) {
-                            x[u] = far ? (float)(x[u] * d) : x[u] * inv;
-                            y[u] = far ? (float)(y[u] * d) : y[u] * inv;
-                        }
-                    } else {
-#pragma unroll
-                        for (int u = 0; u < 8; ++u) {
-                            x[u] *= inv;
-                            y[u] *= inv;
-                        }
-                    }
-                    if (q ? a.qw : a.kw) {
-                        float w[8];
-                        unpack8<DT>(q ? qw : kw, w);
-#pragma unroll
-                        for (int u = 0; u < 8; ++u) x[u] *= w[u];
-                        if constexpr (INTER) {
-#pragma unroll
-                            for (int u = 0; u < 8; ++u) y[u] *= w[u ^ 1];
-                        } else {
-                            unpack8<DT>(q ? qwp : kwp, w);
-#pragma unroll
-                            for (int u = 0; u < 8; ++u) y[u] *= w[u];
-                        }
+                    for (int u = 0; u < 8; ++u) {
+                        x[u] = (float)(x[u] * d);
+                        y[u] = (float)(y[u] * d);
                     }
                 }
-                // (an element that is not turned keeps its value whatever its neighbour holds)
-#pragma unroll
-                for (int u = 0; u < 8; ++u) x[u] = turned[u >> 2] ? __builtin_fmaf(y[u], sine[u], x[u] * cosine[u]) : x[u];
-                out = u4_t{Ty<DT>::pack(x[0], x[1]), Ty<DT>::pack(x[2], x[3]), Ty<DT>::pack(x[4], x[5]), Ty<DT>::pack(x[6], x[7])};
-            }
-            if (!writes) continue;
-            if (q) {
-                *(u4_t*)((char*)a.Qo + (row * a.ldqo + i * a.hqo + 8 * c) * 2) = out;
-            } else if constexpr (APPEND) {
-                char* p = k ? kp : vp;
-                const int h = i - a.heads - (k ? 0 : a.kv_heads);
-                if (p) *(u4_t*)(p + h * (k ? a.ck.hs : a.cv.hs) * 2) = out;
-            } else {
-                *(u4_t*)((char*)a.Ko + (row * a.ldko + (i - a.heads) * a.hko + 8 * c) * 2) = out;
             }
         }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            x[u] = __builtin_fmaf(y[u], t.far[u], x[u] * t.own[u]);
+            if constexpr (NORM) x[u] *= inv;
+        }
+        return u4_t{Ty<DT>::pack(x[0], x[1]), Ty<DT>::pack(x[2], x[3]), Ty<DT>::pack(x[4], x[5]), Ty<DT>::pack(x[6], x[7])};
+    };
+    int i0 = first;
+    // heads up to item `end`: `p` is where the operand's head 0 goes, `hs` from head to head
+    auto heads = [&](const AttnRows& x, int i1, int end, char* p, int64_t hs, const Turn* t) __attribute__((always_inline)) {
+        for (bool more = i1 == 0; i0 < end; more = false) {
+            if (!more) fetch(x, i1, i0, end);
+#pragma unroll
+            for (int j = 0; j < BATCH; ++j) {
+                if (i0 >= end) break;
+                const u4_t out = t ? head(raw[j], *t) : raw[j];
+                if (p && writes) *(u4_t*)(p + (i0 - i1) * hs * 2) = out;
+                i0 += step;
+            }
+        }
+    };
+    {
+        const Turn t = turn_of(a.qw, qw);
+        heads(a.Q, 0, keys0, (char*)a.Qo + (row * a.ldqo + 8 * c) * 2, a.hqo, &t);
     }
+    {
+        const Turn t = turn_of(a.kw, kw);
+        heads(a.K, keys0, values0, kp, APPEND ? a.ck.hs : a.hko, &t);
+    }
+    if constexpr (APPEND) heads(a.V, values0, items, vp, a.cv.hs, nullptr);
 }
 
 }  // namespace b2bk

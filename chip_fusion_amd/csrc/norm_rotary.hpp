@@ -19,6 +19,8 @@
 
 namespace b2bk {
 
+constexpr int kRotaryRows = 8;
+
 struct RotaryArgs {
     AttnRows Q, K, V;               // V: append only
     void *Qo, *Ko;
@@ -32,7 +34,7 @@ struct RotaryArgs {
     double turns[64];               // frequency / 2 pi of each pair
     uint8_t axis[64];
     FastDiv page, per_row;          // per_row: workgroups that share R rows' heads
-    int32_t rows, seqs, pages, width, heads, kv_heads, dim, rotary, row_log;    // R = 1 << row_log
+    int32_t rows, seqs, pages, width, heads, kv_heads, dim, rotary, axes, row_log;    // R = 1 << row_log, up to kRotaryRows
     float eps;
 };
 
@@ -70,8 +72,11 @@ struct Turn {
 template <int DT, int L, bool APPEND, bool NORM, bool INTER>
 __global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a) {
     constexpr int GROUPS = 256 / L, BATCH = 4;      // heads in flight a lane
-    __shared__ float turn[4][64][2];                // [row][pair][cos, sin]
-    __shared__ int place[4], row_seq[4];            // append: a row's place in its sequence, which one (-1: none)
+    constexpr int ROWS = kRotaryRows, TURNS = ROWS / 4;      // angles a thread works out, at most
+    __shared__ float turn[ROWS][64][2];             // [row][pair][cos, sin]
+    // append: a row's place in its sequence, or kNoRow of none, and the page that holds it (-1: none)
+    constexpr int kNoRow = -0x7FFFFFFF - 1;
+    __shared__ int place[ROWS], row_page[ROWS];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int R = 1 << a.row_log, block = a.per_row((int)blockIdx.x), share = (int)blockIdx.x - block * a.per_row.d;
     const int row0 = block << a.row_log;
@@ -81,17 +86,22 @@ __global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a) {
     const int step = (GROUPS >> a.row_log) * a.per_row.d, first = (group >> a.row_log) + share * (GROUPS >> a.row_log);
     const int keys0 = a.heads, values0 = a.heads + a.kv_heads, items = values0 + (APPEND ? a.kv_heads : 0);
     const bool live = row < a.rows && 8 * c < a.dim;
-    u4_t raw[BATCH];
-    // the next BATCH heads from i0 on, below `end`, of an operand whose first head is item i1
-    auto fetch = [&](const AttnRows& x, int i1, int i0, int end) __attribute__((always_inline)) {
+    // the next heads from item i0 on, below `end`, of an operand whose first head is item i1
+    auto fetch = [&](auto& raw, const AttnRows& x, int i1, int i0, int end) __attribute__((always_inline)) {
         const char* p = (const char*)x.p + (row * x.ld + (int64_t)(i0 - i1) * x.hs + 8 * c) * 2;
 #pragma unroll
-        for (int j = 0; j < BATCH; ++j) {
+        for (int j = 0; j < (int)(sizeof(raw) / 16); ++j) {
             raw[j] = u4_t{0, 0, 0, 0};
             if (live && i0 + j * step < end) raw[j] = *(const u4_t*)(p + j * step * x.hs * 2);
         }
     };
-    if (first < keys0) fetch(a.Q, 0, first, keys0);
+    // what a lane starts with is asked for at once: keys and values wait behind the same latency
+    const int first_k = keys0 > first ? first + (keys0 - first + step - 1) / step * step : first;
+    const int first_v = values0 > first ? first + (values0 - first + step - 1) / step * step : first;
+    u4_t rq[BATCH], rk[2], rv[2];
+    fetch(rq, a.Q, 0, first, keys0);
+    fetch(rk, a.K, keys0, first_k, values0);
+    if constexpr (APPEND) fetch(rv, a.V, values0, first_v, items);
     // the partners of this lane's elements
     const int half = a.rotary >> 1;
     int from[2];                // lane (of L) with the partner of each half of the piece
@@ -122,14 +132,31 @@ __global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a) {
         if (a.qw && 8 * c < a.dim) qw = *((const u4_t*)a.qw + c);
         if (a.kw && 8 * c < a.dim) kw = *((const u4_t*)a.kw + c);
     }
+    // pair threadIdx.x / R (and 256 / R on) of row threadIdx.x % R: its frequency and position
+    double turns[TURNS];
+    int at[TURNS];
+#pragma unroll
+    for (int t = 0; t < TURNS; ++t) {
+        const int i = threadIdx.x + 256 * t, p = i >> a.row_log, mine = row0 + (i & (R - 1));
+        turns[t] = 0.0;
+        at[t] = 0;
+        if (p < half && mine < a.rows) {
+            turns[t] = a.turns[p];
+            if (!APPEND || a.positions) at[t] = a.positions[(a.axes > 1 ? a.axis[p] * a.position_ld : 0) + mine];
+        }
+    }
+    [[maybe_unused]] int page_entry[ROWS / 4];
     if constexpr (APPEND) {
-        // one wave a row: which sequence holds it
-        const int mine = row0 + wave;
-        if (wave < R && mine < a.rows) {
-            int seq = -1, at = 0;
+        // a wave takes every fourth row: which sequence holds it, and its page, which is looked up under the sines
+#pragma unroll
+        for (int x = 0; x < ROWS / 4; ++x) {
+            page_entry[x] = -1;
+            const int rr = wave + 4 * x, mine = row0 + rr;
+            if (rr >= R || mine >= a.rows) continue;
+            int seq = -1, spot = 0;
             if (!a.cu) {
                 seq = mine;
-                at = (a.lens[mine] > 0 ? a.lens[mine] : 0) - 1;
+                spot = (a.lens[mine] > 0 ? a.lens[mine] : 0) - 1;
             } else {
                 for (int s0 = 0; s0 < a.seqs && seq < 0; s0 += 64) {
                     const int s = s0 + lane;
@@ -142,27 +169,32 @@ __global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a) {
                     if (hit) {
                         const int l = __ffsll(hit) - 1;
                         seq = s0 + l;
-                        at = __builtin_amdgcn_readlane(len, l) - (__builtin_amdgcn_readlane(q0, l) + __builtin_amdgcn_readlane(n, l) - mine);
+                        spot = __builtin_amdgcn_readlane(len, l) -
+                               (__builtin_amdgcn_readlane(q0, l) + __builtin_amdgcn_readlane(n, l) - mine);
                     }
                 }
             }
-            if (lane == 0) {
-                row_seq[wave] = seq;
-                place[wave] = at;
-            }
+            if (lane == 0) place[rr] = seq < 0 ? kNoRow : spot;
+            const int pg = spot >= 0 ? a.page(spot) : 0;
+            if (seq >= 0 && spot >= 0 && pg < a.width) page_entry[x] = a.table[seq * a.table_ld + pg];
         }
         __syncthreads();
     }
-    for (int i = threadIdx.x; i < half << a.row_log; i += 256) {
-        const int rr = i & (R - 1), p = i >> a.row_log;
-        if (row0 + rr >= a.rows) continue;
-        const int at = APPEND && !a.positions ? place[rr] : a.positions[a.axis[p] * a.position_ld + row0 + rr];
-        const double turns = at * a.turns[p];
+#pragma unroll
+    for (int t = 0; t < TURNS; ++t) {
+        const int i = threadIdx.x + 256 * t, p = i >> a.row_log, rr = i & (R - 1);
+        if (p >= half) break;
+        if (APPEND && !a.positions) at[t] = row0 + rr < a.rows ? place[rr] : 0;
+        const double x = at[t] * turns[t];
         float s, co;
-        sincospif(2.f * (float)(turns - __builtin_rint(turns)), &s, &co);
+        sincospif(2.f * (float)(x - __builtin_rint(x)), &s, &co);
         turn[rr][p][0] = co;
         turn[rr][p][1] = s;
     }
+    if constexpr (APPEND)
+#pragma unroll
+        for (int x = 0; x < ROWS / 4; ++x)
+            if (wave + 4 * x < R && lane == 0) row_page[wave + 4 * x] = page_entry[x];
     __syncthreads();
     auto turn_of = [&](const void* weight, u4_t w) __attribute__((always_inline)) {
         Turn t;
@@ -187,16 +219,12 @@ __global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a) {
     char *kp = nullptr, *vp = nullptr;      // append: where head 0's piece of the row goes
     bool writes = live;
     if constexpr (APPEND) {
-        const int seq = writes ? row_seq[r] : -1, at = writes ? place[r] : -1;
-        writes = seq >= 0;                  // (a row of no sequence writes nothing)
-        const int pg = at >= 0 ? a.page(at) : 0;
-        if (writes && at >= 0 && pg < a.width) {
-            const int entry = a.table[seq * a.table_ld + pg];
-            if (entry >= 0 && entry < a.pages) {
-                const int in = at - pg * a.page.d;
-                kp = (char*)a.ck.p + (entry * a.ck.ps + in * a.ck.ld + 8 * c) * 2;
-                vp = (char*)a.cv.p + (entry * a.cv.ps + in * a.cv.ld + 8 * c) * 2;
-            }
+        const int spot = writes ? place[r] : kNoRow, entry = writes ? row_page[r] : -1;
+        writes = spot != kNoRow;            // (a row of no sequence writes nothing)
+        if (entry >= 0 && entry < a.pages) {
+            const int in = spot - a.page(spot) * a.page.d;
+            kp = (char*)a.ck.p + (entry * a.ck.ps + in * a.ck.ld + 8 * c) * 2;
+            vp = (char*)a.cv.p + (entry * a.cv.ps + in * a.cv.ld + 8 * c) * 2;
         }
     } else {
         kp = (char*)a.Ko + (row * a.ldko + 8 * c) * 2;
@@ -241,29 +269,29 @@ __global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a) {
         }
         return u4_t{Ty<DT>::pack(x[0], x[1]), Ty<DT>::pack(x[2], x[3]), Ty<DT>::pack(x[4], x[5]), Ty<DT>::pack(x[6], x[7])};
     };
-    int i0 = first;
-    // heads up to item `end`: `p` is where the operand's head 0 goes, `hs` from head to head
-    auto heads = [&](const AttnRows& x, int i1, int end, char* p, int64_t hs, const Turn* t) __attribute__((always_inline)) {
-        for (bool more = i1 == 0; i0 < end; more = false) {
-            if (!more) fetch(x, i1, i0, end);
+    // heads from item i0 to `end`, the first of them in `raw`: `p` is where the operand's head 0 goes, `hs` from head to head
+    auto heads = [&](auto& raw, const AttnRows& x, int i1, int i0, int end, char* p, int64_t hs, const Turn* t)
+                     __attribute__((always_inline)) {
+        while (i0 < end) {
 #pragma unroll
-            for (int j = 0; j < BATCH; ++j) {
+            for (int j = 0; j < (int)(sizeof(raw) / 16); ++j) {
                 if (i0 >= end) break;
                 const u4_t out = t ? head(raw[j], *t) : raw[j];
                 if (p && writes) *(u4_t*)(p + (i0 - i1) * hs * 2) = out;
                 i0 += step;
             }
+            if (i0 < end) fetch(raw, x, i1, i0, end);
         }
     };
-    {
+    if (first < keys0) {
         const Turn t = turn_of(a.qw, qw);
-        heads(a.Q, 0, keys0, (char*)a.Qo + (row * a.ldqo + 8 * c) * 2, a.hqo, &t);
+        heads(rq, a.Q, 0, first, keys0, (char*)a.Qo + (row * a.ldqo + 8 * c) * 2, a.hqo, &t);
     }
-    {
+    if (first_k < values0) {
         const Turn t = turn_of(a.kw, kw);
-        heads(a.K, keys0, values0, kp, APPEND ? a.ck.hs : a.hko, &t);
+        heads(rk, a.K, keys0, first_k, values0, kp, APPEND ? a.ck.hs : a.hko, &t);
     }
-    if constexpr (APPEND) heads(a.V, values0, items, vp, a.cv.hs, nullptr);
+    if constexpr (APPEND) heads(rv, a.V, values0, first_v, items, vp, a.cv.hs, nullptr);
 }
 
 }  // namespace b2bk

@@ -64,6 +64,7 @@ void fill(const b2b_rotary_plan* p, b2bk::RotaryArgs& a, int64_t rows, const b2b
     a.kv_heads = p->kv_heads;
     a.dim = p->dim;
     a.rotary = p->rotary;
+    a.axes = p->axes;
     a.eps = p->eps;
 }
 
@@ -74,8 +75,18 @@ bool weights_ok(const b2b_rotary_plan* p, const void* qw, const void* kw) {
 
 b2b_status_t go(const b2b_rotary_plan* p, b2bk::RotaryArgs& a, bool append, hipStream_t stream) {
     const int items = p->heads + (append ? 2 : 1) * p->kv_heads, groups = p->dim > 64 ? 16 : 32;
-    a.row_log = a.rows >= 4096 ? 2 : a.rows >= 2048 ? 1 : 0;
-    const int share = a.rows < 512 ? (int)ceil_div(items, groups) : 1;
+    // Rows a workgroup: its angles and its lanes' factors cost as much as some heads
+    // do, so that a lane should take several, up to 10, as long as there are two
+    // workgroups a compute unit (32 + 8 heads of 128, 16384 rows: 86 us with 1 row, 68
+    // with 2, 64 with 4, 67 with 8; 16 + 4 of 64: 43, 32, 25 and 22; 2048 rows of the
+    // first: 14.1, 13.0, 12.5, 17.3; 1024 rows: 8.1 with 1, 8.6 with 2).
+    a.row_log = 0;
+    if (a.rows >= 2048)
+        while (2 << a.row_log <= b2bk::kRotaryRows && (2 << a.row_log) * items <= 10 * groups && a.rows >> (a.row_log + 1) >= 512)
+            ++a.row_log;
+    // Few rows: a head a lane, a row's heads over several workgroups (32 + 8 heads of
+    // 128: 32 rows 5.2 us in one, 3.8 in three, 256 rows 5.5 and 4.7, 512 rows 6.3 and 7.3).
+    const int share = a.rows <= 256 ? (int)ceil_div(items, groups) : 1;
     a.per_row.set(share);
     const int64_t grid = ceil_div(a.rows, (int64_t)1 << a.row_log) * share;
     if (grid > INT32_MAX) return B2B_ERROR_INVALID_VALUE;

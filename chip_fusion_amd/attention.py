@@ -156,17 +156,18 @@ class _NotCompiled:
     def attention(self, *args):
         return None
 
-    prefix = linear = linear_step = attention
+    prefix = linear = linear_step = paged = rotary = append = attention
 
 
-def _usual(handle, heads, kv_heads, dim, dtype, workspace, run, step=None):
+def _usual(handle, heads, kv_heads, dim, dtype, workspace, run, step=None, page=0, axes=1, weights=False):
     """The plan's usual calls (pyattn.cpp): on the current stream, tensors of the
     common layouts; they return None, with nothing launched, where the checks here
     are to be made."""
     if _attn is None:
         return _NotCompiled()
     at = lambda f: 0 if f is None else ctypes.cast(f, ctypes.c_void_p).value
-    return _attn.Call(handle.value, at(workspace), at(run), at(step), heads, kv_heads, dim, dtype, torch, _check)
+    return _attn.Call(handle.value, at(workspace), at(run), at(step), heads, kv_heads, dim, dtype, torch, _check, page,
+                      axes, weights)
 
 
 def _scale(scale):
@@ -183,6 +184,7 @@ class _Heads:
     """A plan of the attention of a model's heads (b2b_attn_create)."""
 
     _create_call = "b2b_attn_create"
+    page_size = 0       # keys a page
 
     def __init__(self, dtype, heads, kv_heads, head_dim, *rest):
         """rest: what the create call takes after head_dim."""
@@ -194,7 +196,7 @@ class _Heads:
         self.dtype = TORCH_DTYPES[code]
         self._call, workspace = getattr(lib(), self._run_call), getattr(lib(), self._workspace_call)
         self._workspaces = _Workspaces(workspace, h)
-        self._usual = _usual(h, heads, kv_heads, head_dim, self.dtype, workspace, self._call)
+        self._usual = _usual(h, heads, kv_heads, head_dim, self.dtype, workspace, self._call, page=self.page_size)
 
     def close(self):
         if getattr(self, "_h", None):
@@ -395,8 +397,8 @@ class PagedAttention(_Heads):
 
     def __init__(self, dtype, heads, kv_heads, head_dim, page_size, scale=None, window=None, sinks=0):
         window, sinks = _window(window, sinks)
-        super().__init__(dtype, heads, kv_heads, head_dim, page_size, _scale(scale), window, sinks)
         self.page_size = page_size
+        super().__init__(dtype, heads, kv_heads, head_dim, page_size, _scale(scale), window, sinks)
 
     def run(self, Q, K, V, table, lens, cu=None, O=None, lse=False, stream=None):
         """Q [rows, heads, dim]: rows cu[s] .. cu[s+1]-1 (device int32; None: row
@@ -406,6 +408,10 @@ class PagedAttention(_Heads):
         [seqs, width]).  Returns O, or (O, LSE) with `lse` (True, or a float32
         tensor [rows, heads] to write).  Rows that belong to no sequence are
         not written."""
+        if stream is None:
+            out = self._usual.paged(Q, K, V, table, lens, cu, O, lse)
+            if out is not None:
+                return out
         dtype, heads, kv_heads, dim = self.dtype, self.heads, self.kv_heads, self.dim
         q = _heads3(Q, "Q", dtype, None, heads, dim)
         rows = Q.shape[0]
@@ -479,6 +485,8 @@ class NormRotary:
         self.dtype = TORCH_DTYPES[code]
         self.heads, self.kv_heads, self.dim, self.rotary_dim, self.axes, self.norm = \
             heads, kv_heads, head_dim, rotary_dim, axes, eps is not None
+        self._usual = _usual(h, heads, kv_heads, head_dim, self.dtype, None, lib().b2b_rotary_run, lib().b2b_rotary_append,
+                             axes=axes, weights=self.norm)
 
     def _common(self, Q, K, positions, q_weight, k_weight, Q_out):
         dtype, dim = self.dtype, self.dim
@@ -509,6 +517,10 @@ class NormRotary:
         [rows], or [axes, rows] with several axes (None only where rotary_dim is
         0); weights: [dim], 1 by default.  Returns Q_out and K_out, which may be
         Q and K."""
+        if stream is None:
+            out = self._usual.rotary(Q, K, positions, q_weight, k_weight, Q_out, K_out)
+            if out is not None:
+                return out
         rows, q, k, qo, far = self._common(Q, K, positions, q_weight, k_weight, Q_out)
         if positions is None and self.rotary_dim:
             raise ValueError("positions: a tensor is expected")
@@ -537,6 +549,10 @@ class NormRotary:
         PagedAttention.run finds them with the same table, lens and cu.
         positions: the rows' places in their sequences by default.  Returns Q_out,
         which may be Q."""
+        if stream is None:
+            out = self._usual.append(Q, K, V, k_cache, v_cache, table, lens, cu, positions, q_weight, k_weight, Q_out)
+            if out is not None:
+                return out
         rows, q, k, qo, far = self._common(Q, K, positions, q_weight, k_weight, Q_out)
         v = _heads3(V, "V", self.dtype, rows, self.kv_heads, self.dim)
         kc = _pages(k_cache, "k_cache", self.dtype, None, None, self.kv_heads, self.dim)
@@ -563,6 +579,7 @@ class NormRotary:
 
     def close(self):
         if getattr(self, "_h", None):
+            self._usual.close()
             lib().b2b_rotary_destroy(self._h)
             self._h = None
 

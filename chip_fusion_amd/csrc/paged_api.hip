@@ -11,20 +11,23 @@ namespace {
 
 using namespace b2b;
 
-// Workgroups that a call's key tiles are cut for: two a compute unit.
+// Workgroups that a call's key tiles are cut for: two a compute unit (2048 rows of 4
+// sequences behind up to 16384 keys, 32 heads of 128, with the join: 368 us, 383 at
+// 768, 394 at 1024), and four times as many of sequences of few rows (64 requests of
+// up to 8192 keys: 246 us at 512, 230 at 1024, 220 at 2048).
 constexpr int kTarget = 512;
-// Key tiles of a part, at least.
-constexpr int kLeast = 8;
+// Key tiles of a part, at least: below 512 keys a second launch takes longer than
+// the four waves of one workgroup do (3 requests of up to 300 keys: 12 us cut, 7.6 whole).
+constexpr int kLeast = 16;
 
 struct Layout {
     int64_t tiles;          // row tiles a key head, at most
     int64_t items;          // workgroups a key head, at most
-    int64_t slots;          // partial results a key head, at most (0: nothing is cut)
-    int32_t slot_rows;
+    int64_t granules;       // of partial results, a key head, at most (0: nothing is cut)
+    int64_t subs;           // granules of a row tile
     size_t bytes;
 };
 
-// cu: whether sequences have starts (else one row each)
 Layout lay_out(const b2b_attn_plan* p, int64_t seqs, int64_t rows, int64_t keys) {
     const int64_t group = p->heads / p->kv_heads;
     Layout l = {};
@@ -36,12 +39,12 @@ Layout lay_out(const b2b_attn_plan* p, int64_t seqs, int64_t rows, int64_t keys)
     // are as many as workgroups are wanted nothing is gained by cutting them.
     const bool enough = p->window && rows * group / b2bk::kKeyRows * p->kv_heads >= kTarget;
     l.items = l.tiles;
+    l.subs = rows * group <= 32 ? 1 : b2bk::kKeyRows / 32;
     if (most > kLeast && !enough) {
-        l.items += kTarget / p->kv_heads;
-        l.slots = std::min<int64_t>(l.items, 2 * kTarget / p->kv_heads);
+        l.items += 4 * kTarget / p->kv_heads;
+        l.granules = std::min<int64_t>(l.subs * l.items, 8 * kTarget / p->kv_heads);
     }
-    l.slot_rows = (int32_t)std::min<int64_t>(b2bk::kKeyRows, rows * group);
-    l.bytes = (size_t)l.slots * p->kv_heads * l.slot_rows * (p->dim + 1) * 4;
+    l.bytes = (size_t)l.granules * p->kv_heads * 32 * (p->dim + 1) * 4;
     return l;
 }
 
@@ -52,23 +55,26 @@ bool key_sizes_ok(const b2b_attn_plan* p, int64_t seqs, int64_t rows, int64_t ke
 
 bool ready(const Layout& l, const b2b_attn_plan* p, const void* workspace, size_t bytes) {
     if (l.bytes && (!workspace || (uintptr_t)workspace % 16 || bytes < l.bytes)) return false;
-    return std::max(l.items, 4 * l.tiles) * p->kv_heads <= INT32_MAX;
+    return std::max(l.items + 8, l.subs * l.tiles) * p->kv_heads <= INT32_MAX;
 }
 
-b2b_status_t launch_keys(b2b_attn_t p, const Layout& l, b2bk::KeyArgs& a, int kind, void* workspace, hipStream_t stream) {
+b2b_status_t launch_keys(b2b_attn_t p, const Layout& l, b2bk::KeyArgs& a, int where, void* workspace, hipStream_t stream) {
     a.causal = 1;
-    a.window = (int32_t)std::min<int64_t>(p->window, std::max<int64_t>(a.keys, 1));
+    a.window = (int32_t)std::min<int64_t>(p->window, std::max<int64_t>(a.keys, 1));     // (0 stays 0)
     a.sinks = (int32_t)std::min<int64_t>(p->sinks, a.keys);
-    a.split = l.slots > 0;
+    a.split = l.granules > 0;
     a.least = kLeast;
     a.per = (float)p->kv_heads / kTarget;
-    a.slots = (int32_t)l.slots;
-    a.slot_rows = l.slot_rows;
+    a.granules = (int32_t)l.granules;
+    a.subs = !a.cu_q && a.group.d <= 32 ? 1 : (int32_t)l.subs;
     a.part = (float*)workspace;
-    a.part_lse = a.part + (size_t)l.slots * p->kv_heads * l.slot_rows * p->dim;
+    a.part_lse = a.part + (size_t)l.granules * p->kv_heads * 32 * p->dim;
+    // few rows a sequence: see key_attn_kernel
+    a.spread = a.rows * a.group.d <= (int64_t)32 * a.seqs;
+    const int64_t items = a.spread ? ceil_div(l.items, 8) * 8 : l.items;
     const KeyLaunch& L = p->dtype == B2B_DTYPE_F16 ? key_attn_f16() : key_attn_bf16();
-    if (L.run(a, kind, (unsigned)(l.items * p->kv_heads), stream) != hipSuccess) return B2B_ERROR_HIP;
-    if (a.split && L.join(a, kind, (unsigned)(4 * l.tiles * p->kv_heads), stream) != hipSuccess) return B2B_ERROR_HIP;
+    if (L.run(a, where, (unsigned)(items * p->kv_heads), stream) != hipSuccess) return B2B_ERROR_HIP;
+    if (a.split && L.join(a, where, (unsigned)(a.subs * l.tiles * p->kv_heads), stream) != hipSuccess) return B2B_ERROR_HIP;
     return B2B_SUCCESS;
 }
 
@@ -106,7 +112,7 @@ b2b_status_t b2b::window_run(b2b_attn_t p, int32_t seqs, int64_t rows, int64_t k
     a.K = b2b::dev(K, p->dim);
     a.V = b2b::dev(V, p->dim);
     a.cu_k = cu_k;
-    return launch_keys(p, l, a, KEYS_WINDOW, workspace, stream);
+    return launch_keys(p, l, a, b2bk::KEYS_PACKED, workspace, stream);
 }
 
 extern "C" {
@@ -161,7 +167,8 @@ b2b_status_t b2b_paged_attn_run(b2b_attn_t p, int32_t seqs, int64_t rows, b2b_ro
     a.page.set(p->page);
     a.pages = pages;
     a.lens = lens;
-    return launch_keys(p, l, a, p->window ? KEYS_PAGED_WINDOW : KEYS_PAGED, workspace, stream);
+    const bool whole = p->page % 16 == 0 && K.row_stride <= kMaxStride && V.row_stride <= kMaxStride;
+    return launch_keys(p, l, a, whole ? b2bk::KEYS_PAGES16 : b2bk::KEYS_PAGES, workspace, stream);
 }
 
 }  // extern "C"

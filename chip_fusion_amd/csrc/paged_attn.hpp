@@ -6,12 +6,16 @@
 // second product's operand as they lie.  What differs is which keys a row meets
 // and where they are:
 //
-//   Pages.  Key j of sequence s is row j % size of page table[s][j / size].
-//   Every lane of a copy works out the address of the 16 bytes that it moves
-//   (64 bits: a cache may be larger than 4 GB, a page of any size may end inside
-//   a tile), and the loads write LDS directly.  The table's entries for a tile
-//   are asked for one tile ahead.  Places behind a sequence's last key are read
-//   from a block of zeros: what a page holds there may be anything, NaN too.
+//   Pages.  Key j of sequence s is row j % size of page table[s][j / size].  Loads
+//   write LDS directly, 16 rows of 64 bytes each.  Pages of a multiple of 16 keys:
+//   the 16 rows lie in one page, whose address is one scalar calculation and a
+//   buffer resource that ends at the sequence's last key (many rows, whose time is
+//   instructions: 2048 rows behind 16384 keys 437 us -> 401; the few rows' kernel waits for
+//   memory and is faster without the scalar chain, 215 us against 223).  Else, as
+//   pages of other sizes may end anywhere, every lane works out the address (64 bits) of the 16 bytes that it
+//   moves, and those behind the last key come from a block of zeros.  Either way
+//   what a page holds behind a sequence's keys may be anything, NaN too.  The
+//   table's entries for a tile are asked for one tile ahead.
 //
 //   Window.  The row in place p sees keys p - window + 1 .. p and the first
 //   `sinks`: 128 rows' tiles are those of the sinks and those from the first
@@ -22,9 +26,11 @@
 // rows, key head) of T key tiles is cut into ceil(T / L) parts, with L the
 // whole call's key tiles over the workgroups that it should have, and at least
 // `least`: no chain of tiles is longer than L, whatever the lengths, and a
-// captured graph replays with new ones.  Since sum ceil(T / L) <= items +
-// sum T / L, the host knows the grid's size, and since a cut item has at most
-// 2 T / L parts, the partial results' as well.
+// captured graph replays with new ones.  Sequences of up to 32 rows, whose partial
+// results are small and whose time is the bytes of their keys, are cut four times
+// as fine.  Since sum ceil(T / L) <= items + sum T / L, the host knows the grid's
+// size, and since a cut item has at most 2 T / L parts, the partial results' as
+// well: 32 rows a granule, one of a part of few rows, four of a tile's.
 #pragma once
 #include "attn.hpp"
 
@@ -43,7 +49,9 @@ struct KeyArgs : AttnArgs {
     int32_t pages, window, sinks;
     int32_t split, least;   // whether items may be cut, and the fewest tiles a part has then
     float per;              // key heads over the workgroups that a call should have
-    int32_t slots, slot_rows;   // partial results: slots a key head, rows a slot
+    int32_t granules;       // of partial results, a key head
+    int32_t subs;           // granules of a tile that the join looks for (1: no sequence has more than 32 rows)
+    int32_t spread;         // whether a key head's workgroups go over all XCDs
 };
 
 constexpr int kKeyRows = 128;     // rows of a tile
@@ -65,7 +73,8 @@ __device__ __attribute__((aligned(256))) const unsigned char kZeros[256] = {};
 // Where a workgroup works
 // ---------------------------------------------------------------------------
 struct KeyItem {
-    int seq, tile, part, parts, slot;   // slot: the tile's first
+    int seq, tile, part, parts;
+    int granule, per_part;              // the tile's first, and those of a part
     int q0, nq, k0, nk;
     int tiles;
 };
@@ -122,10 +131,14 @@ __device__ __forceinline__ bool find_item(const KeyArgs& a, int u, KeyItem* out)
         most = l > (float)(1 << 30) ? 1 << 30 : (int)l;
         most = most < a.least ? a.least : most;
     }
-    int before = 0, slots = 0;
+    int before = 0, used = 0;
     for (int s0 = 0;;) {
-        const int parts = a.split && span > most ? (int)(((unsigned)span + (unsigned)most - 1) / (unsigned)most) : 1;
-        const int mine = JOIN ? tiles : tiles * parts, cut = parts > 1 ? tiles * parts : 0;
+        const bool few = (unsigned)n * (unsigned)group <= 32;
+        int l = few ? (most + 3) >> 2 : most;
+        l = l < a.least ? a.least : l;
+        const int parts = a.split && span > l ? (int)(((unsigned)span + (unsigned)l - 1) / (unsigned)l) : 1;
+        const int per_part = few ? 1 : kKeyRows / 32;
+        const int mine = JOIN ? tiles : tiles * parts, cut = parts > 1 ? tiles * parts * per_part : 0;
         const int sum = lanes_sum(mine), cuts = lanes_sum(cut);
         const unsigned long long hit = __ballot(before + sum > u);
         if (hit) {
@@ -136,18 +149,20 @@ __device__ __forceinline__ bool find_item(const KeyArgs& a, int u, KeyItem* out)
             if ((unsigned)local >= (unsigned)__builtin_amdgcn_readlane(mine, at)) return false;
             out->seq = s0 + at;
             out->parts = __builtin_amdgcn_readlane(parts, at);
+            out->per_part = __builtin_amdgcn_readlane(per_part, at);
             out->tiles = __builtin_amdgcn_readlane(tiles, at);
             out->tile = JOIN || out->parts == 1 ? local : (int)((unsigned)local / (unsigned)out->parts);
             out->part = JOIN ? 0 : local - out->tile * out->parts;
-            out->slot = slots + __builtin_amdgcn_readlane(cuts, at) - __builtin_amdgcn_readlane(cut, at) + out->tile * out->parts;
+            out->granule = used + __builtin_amdgcn_readlane(cuts, at) - __builtin_amdgcn_readlane(cut, at) +
+                           out->tile * out->parts * out->per_part;
             out->q0 = __builtin_amdgcn_readlane(q0, at);
             out->nq = __builtin_amdgcn_readlane(n, at);
             out->k0 = __builtin_amdgcn_readlane(k0, at);
             out->nk = __builtin_amdgcn_readlane(nk, at);
-            return out->parts == 1 || out->slot + out->parts <= a.slots;
+            return out->parts == 1 || out->granule + out->parts * out->per_part <= a.granules;
         }
         before += __builtin_amdgcn_readlane(sum, 63);
-        slots += __builtin_amdgcn_readlane(cuts, 63);
+        used += __builtin_amdgcn_readlane(cuts, 63);
         s0 += 64;
         if (s0 >= a.seqs) return false;
         load(s0);
@@ -159,10 +174,13 @@ __device__ __forceinline__ bool find_item(const KeyArgs& a, int u, KeyItem* out)
 // ---------------------------------------------------------------------------
 // Which key tiles the rows of a tile meet: number i of [i0, i1) is tile
 // i < sink_tiles ? i : i + gap.
-template <int DT_, int DB_, bool PAGED_, bool WIN_>
+// Where keys lie: side by side, in pages of a multiple of 16 keys, in pages of any size.
+enum { KEYS_PACKED, KEYS_PAGES16, KEYS_PAGES };
+
+template <int DT_, int DB_, int WHERE_, bool WIN_>
 struct KeyCfg {
-    static constexpr int DT = DT_, DB = DB_, WAVES = 4, THREADS = 64 * WAVES, BM = kKeyRows, BN = 32;
-    static constexpr bool PAGED = PAGED_, WIN = WIN_;
+    static constexpr int DT = DT_, DB = DB_, WAVES = 4, THREADS = 64 * WAVES, BM = kKeyRows, BN = 32, WHERE = WHERE_;
+    static constexpr bool PAGED = WHERE != KEYS_PACKED, WIN = WIN_;
     static constexpr int KS = 2 * DB;                   // K-steps of the first product
     static constexpr int TILE = BN * DB * 64;           // a tile of keys (or values) in LDS
     static constexpr int JOIN = WAVES * TILE;           // behind it: the waves' maxima and sums
@@ -230,24 +248,26 @@ struct KeyTile {
         const AttnRows& x = values ? a.V : a.K;
         return (const char*)x.p + (((int64_t)w.k0 + key) * x.ld + kvh * x.hs) * 2;
     }
-    // Copies row group rg (16 rows) of a tile, keys with their chunks swizzled,
-    // as attn_copy; e: the lane's table entry.
+    // Copies row group rg (16 rows) of a tile of a cache, keys with their chunks
+    // swizzled as attn_copy's, every lane from an address of its own; e: the
+    // lane's table entry.
     template <bool VALUES>
-    __device__ __forceinline__ void copy(const unsigned char* dst, int t, int rg, int e, int lane) const {
-        if constexpr (C::PAGED) {
-            const int row = 16 * rg + (lane >> 2), key = t * C::BN + row;
-            const int chunk = VALUES ? (lane & 3) : ((lane & 3) ^ ((row >> 2) & 3));
-            const bool in = key < w.nk;
-            const char* p = row_at(VALUES ? a.pv : a.pk, key, e, chunk);
+    __device__ __forceinline__ void copy_lanes(const unsigned char* dst, int t, int rg, int e, int lane) const {
+        const int row = 16 * rg + (lane >> 2), key = t * C::BN + row;
+        const int chunk = VALUES ? (lane & 3) : ((lane & 3) ^ ((row >> 2) & 3));
+        const bool in = key < w.nk;
+        const char* p = row_at(VALUES ? a.pv : a.pk, key, e, chunk);
 #pragma unroll
-            for (int b = 0; b < C::DB; ++b)
-                lds_dma16_from(dst + b * C::BN * 64 + rg * 1024, in && 32 * b + 8 * chunk < a.dim ? p + 64 * b : (const char*)kZeros);
-        } else {
-            const AttnRows& x = VALUES ? a.V : a.K;
-            const int n = w.nk - t * C::BN < C::BN ? w.nk - t * C::BN : C::BN;
-            const auto rs = attn_rsrc(x.p, (int64_t)w.k0 + (int64_t)t * C::BN, x.ld, (int64_t)kvh * x.hs, n, a.dim);
-            attn_copy<C::DB, C::BN, !VALUES>(dst, rs, (int)x.ld * 2, a.dim, rg, lane);
-        }
+        for (int b = 0; b < C::DB; ++b)
+            lds_dma16_from(dst + b * C::BN * 64 + rg * 1024, in && 32 * b + 8 * chunk < a.dim ? p + 64 * b : (const char*)kZeros);
+    }
+    // The same of keys side by side.
+    template <bool VALUES>
+    __device__ __forceinline__ void copy_packed(const unsigned char* dst, int t, int rg, int lane) const {
+        const AttnRows& x = VALUES ? a.V : a.K;
+        const int n = w.nk - t * C::BN < C::BN ? w.nk - t * C::BN : C::BN;
+        const auto rs = attn_rsrc(x.p, (int64_t)w.k0 + (int64_t)t * C::BN, x.ld, (int64_t)kvh * x.hs, n, a.dim);
+        attn_copy<C::DB, C::BN, !VALUES>(dst, rs, (int)x.ld * 2, a.dim, rg, lane);
     }
     // lane's table entry for row group rg of tile t
     __device__ __forceinline__ int entry_of(int t, int rg, int lane) const {
@@ -255,7 +275,8 @@ struct KeyTile {
         return 0;
     }
     __device__ __forceinline__ int64_t part_row(int rr) const {
-        return ((int64_t)(w.slot + w.part) * a.kv_heads.d + kvh) * a.slot_rows + (rr - row0);
+        const int r = rr - row0;
+        return ((int64_t)(w.granule + w.part * w.per_part + (r >> 5)) * a.kv_heads.d + kvh) * 32 + (r & 31);
     }
 };
 
@@ -378,18 +399,59 @@ __device__ __forceinline__ void key_tile_body(const KeyTile<C>& k, unsigned char
     const int wlast = (wrow + 32 < k.rows ? wrow + 32 : k.rows) - 1;
     const int done = wrow < k.rows ? (k.sees(wlast) + C::BN - 1) / C::BN : 0;
     const int dark = C::WIN ? k.from(wrow) : 0, open = C::WIN ? k.from(wlast) : 0;
+    // Two waves copy the keys, two the values, a group of 16 rows each.  Where a
+    // group's rows are evenly spaced (keys side by side, pages of whole groups) its
+    // address is scalar, and all but the table's entry is worked out early.
+    constexpr bool EVEN = C::WHERE != KEYS_PAGES;
     const bool keys = wave < 2;
-    auto copy = [&](int i, int e) __attribute__((always_inline)) {
-        const unsigned char* dst = lds + (2 * (i & 1) + (keys ? 0 : 1)) * C::TILE;
-        if (keys) k.template copy<false>(dst, k.tile(i), wave, e, lane);
-        else k.template copy<true>(dst, k.tile(i), wave - 2, e, lane);
+    const int rg = wave & 1;
+    const Pages src = C::PAGED ? (keys ? a.pk : a.pv)
+                               : Pages{keys ? a.K.p : a.V.p, 0, keys ? a.K.ld : a.V.ld, keys ? a.K.hs : a.V.hs};
+    const char* src0 = (const char*)src.p + (C::PAGED ? 0 : k.w.k0 * src.ld * 2) + k.kvh * src.hs * 2;
+    const uint32_t ld2 = (uint32_t)src.ld * 2;
+    int off[C::DB];         // a lane's 16 bytes of each block of 32 columns (past the head: past the resource)
+    if constexpr (EVEN) {
+        const int chunk = keys ? (lane & 3) ^ ((lane >> 4) & 3) : lane & 3;      // swizzled as attn_copy's
+#pragma unroll
+        for (int b = 0; b < C::DB; ++b) off[b] = 32 * b + 8 * chunk < a.dim ? (lane >> 2) * (int)ld2 + 16 * chunk + 64 * b : -16;
+    }
+    struct {
+        int e, in;          // the next tile's entry and its first row's place in the page
+    } next = {0, 0};
+    auto look = [&](int i) __attribute__((always_inline)) {
+        if constexpr (C::WHERE == KEYS_PAGES16) {
+            const int key = k.tile(i) * C::BN + 16 * rg, pg = a.page(key < k.w.nk ? key : k.w.nk - 1);
+            next.e = a.table[k.w.seq * a.table_ld + pg];
+            next.in = key - pg * a.page.d;
+        } else {
+            next.e = k.entry_of(k.tile(i), rg, lane);
+        }
     };
-    auto entry = [&](int i) __attribute__((always_inline)) { return k.entry_of(k.tile(i), wave & 1, lane); };
+    auto copy = [&](int i) __attribute__((always_inline)) {
+        const unsigned char* dst = lds + (2 * (i & 1) + (keys ? 0 : 1)) * C::TILE;
+        const int t = k.tile(i);
+        if constexpr (EVEN) {
+            const int key = t * C::BN + 16 * rg, n = k.w.nk - key;
+            const char* p = src0;
+            if constexpr (C::PAGED) {
+                const int e = __builtin_amdgcn_readfirstlane(next.e), pg = e < 0 ? 0 : (e < a.pages ? e : a.pages - 1);
+                p += pg * src.ps * 2 + (uint64_t)(uint32_t)next.in * ld2;
+            } else {
+                p += (uint64_t)(uint32_t)key * ld2;
+            }
+            const auto rs = make_rsrc(p, n > 0 ? (uint32_t)((n < 16 ? n : 16) - 1) * ld2 + 2 * a.dim : 0u);
+#pragma unroll
+            for (int b = 0; b < C::DB; ++b) lds_dma16<false>(rs, dst + b * C::BN * 64 + rg * 1024, off[b]);
+        } else {
+            if (keys) k.template copy_lanes<false>(dst, t, rg, next.e, lane);
+            else k.template copy_lanes<true>(dst, t, rg, next.e, lane);
+        }
+    };
     const int kb0 = attn_kbase(lane, 0), kb1 = attn_kbase(lane, 1), vb = attn_vbase(lane);
-    int e = 0;
     if (k.i0 < k.i1) {
-        copy(k.i0, entry(k.i0));
-        if (k.i0 + 1 < k.i1) e = entry(k.i0 + 1);
+        look(k.i0);
+        copy(k.i0);
+        if (k.i0 + 1 < k.i1) look(k.i0 + 1);
     }
     attn_load_q<C::KS>(q, a, k.w.q0, k.kvh, rr, k.rows, lane);
     for (int i = k.i0; i < k.i1; ++i) {
@@ -397,28 +459,46 @@ __device__ __forceinline__ void key_tile_body(const KeyTile<C>& k, unsigned char
         if (i == k.i0)
 #pragma unroll
             for (int j = 0; j < C::KS; ++j) asm volatile("" : "+v"(q[j]));
-        if (i + 1 < k.i1) {
-            copy(i + 1, e);
-            if (i + 2 < k.i1) e = entry(i + 2);
-        }
         const int t = k.tile(i), at = t * C::BN;
-        if (t >= done || (C::WIN && at + C::BN <= dark && at >= a.sinks)) continue;
         const unsigned char* kt = lds + 2 * (i & 1) * C::TILE;
         const unsigned char* vt = kt + C::TILE;
+        // Fragments are read ahead of their use, four keys' under the next tile's
+        // addresses, the first half of the values' under the softmax: a wave then
+        // waits for LDS once a product, not once an instruction.
+        auto key = [&](int j) __attribute__((always_inline)) {
+            return *(const u4_t*)(kt + ((j & 1) ? kb1 : kb0) + (j >> 1) * C::BN * 64);
+        };
+        u4_t f[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[j] = key(j);
+        __builtin_amdgcn_sched_barrier(0);
+        if (i + 1 < k.i1) {
+            copy(i + 1);
+            if (i + 2 < k.i1) look(i + 2);
+        }
+        if (t >= done || (C::WIN && at + C::BN <= dark && at >= a.sinks)) continue;
         f16x_t s[1] = {f16x_t{}};
 #pragma unroll
-        for (int j = 0; j < C::KS; ++j)
-            s[0] = M::mma(*(const u4_t*)(kt + ((j & 1) ? kb1 : kb0) + (j >> 1) * C::BN * 64), q[j], s[0]);
+        for (int j = 0; j < C::KS; ++j) {
+            s[0] = M::mma(f[j & 3], q[j], s[0]);
+            if (j + 4 < C::KS) f[j & 3] = key(j + 4);
+        }
+#pragma unroll
+        for (int b = 0; b < C::DB; ++b) f[b] = attn_vfrag<C::BN>(vt, vb, b, 0);
+        __builtin_amdgcn_sched_barrier(0);
         if (t >= clear || (C::WIN && at < open && at + C::BN > a.sinks))
             key_mask<C::WIN>(s[0], lim - at, lo - at, a.sinks - 4 * h - at);
         attn_move_max<C::DB>(attn_max<1>(s), st, o, a.sc);
         attn_probs<1>(s, st, a.sc);
+        u4_t p = attn_pack<C::DT>(s[0], 0);
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            const u4_t p = attn_pack<C::DT>(s[0], ks);
-#pragma unroll
-            for (int b = 0; b < C::DB; ++b) o[b] = M::mma(attn_vfrag<C::BN>(vt, vb, b, ks), p, o[b]);
+        for (int b = 0; b < C::DB; ++b) {
+            o[b] = M::mma(f[b], p, o[b]);
+            f[b] = attn_vfrag<C::BN>(vt, vb, b, 1);
         }
+        p = attn_pack<C::DT>(s[0], 1);
+#pragma unroll
+        for (int b = 0; b < C::DB; ++b) o[b] = M::mma(f[b], p, o[b]);
     }
     if (!attn_finite<C>(o, st)) key_again<C>(k, o, st, rr, k.i0, 1, lane);
     if (k.w.parts == 1) {
@@ -463,8 +543,13 @@ __device__ __forceinline__ void key_rows_body(const KeyTile<C>& k, unsigned char
     unsigned char* mine = lds + wave * C::TILE;
     auto copy = [&](auto VALUES, int t, int e0, int e1) __attribute__((always_inline)) {
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");    // what the rows held has been read
-        k.template copy<VALUES.value>(mine, t, 0, e0, lane);
-        k.template copy<VALUES.value>(mine, t, 1, e1, lane);
+        if constexpr (C::PAGED) {
+            k.template copy_lanes<VALUES.value>(mine, t, 0, e0, lane);
+            k.template copy_lanes<VALUES.value>(mine, t, 1, e1, lane);
+        } else {
+            k.template copy_packed<VALUES.value>(mine, t, 0, lane);
+            k.template copy_packed<VALUES.value>(mine, t, 1, lane);
+        }
     };
     const int kb0 = attn_kbase(lane, 0), kb1 = attn_kbase(lane, 1), vb = attn_vbase(lane);
     const int i0 = k.i0 + wave;
@@ -571,9 +656,33 @@ __device__ __forceinline__ void key_rows_body(const KeyTile<C>& k, unsigned char
 template <class C>
 __global__ __launch_bounds__(C::THREADS, 3) void key_attn_kernel(KeyArgs a) {
     __shared__ __attribute__((aligned(1024))) unsigned char lds[C::LDS_BYTES];
-    const int u = a.kv_heads((int)blockIdx.x), kvh = (int)blockIdx.x - u * a.kv_heads.d;
+    // Workgroups go to the XCDs in turn.  A key head's own row tiles read the same
+    // keys: neighbours in `u` with 8 key heads share an XCD's L2.  Few rows a sequence
+    // share nothing but the lines on a row's borders, and an XCD should see all heads
+    // of a row, which lie on all of its L2's channels (36 requests, 4 key heads of 96:
+    // 37.4 us -> 32.6; rows of prompts would lose their L2: 32768 tokens 1858 us -> 2187).
+    int u, kvh;
+    if (a.spread) {
+        const int j = (int)blockIdx.x >> 3;
+        u = a.kv_heads(j);
+        kvh = j - u * a.kv_heads.d;
+        u = u * 8 + ((int)blockIdx.x & 7);
+    } else {
+        u = a.kv_heads((int)blockIdx.x);
+        kvh = (int)blockIdx.x - u * a.kv_heads.d;
+    }
     KeyItem w;
-    if (!find_item<C::PAGED, C::WIN, false>(a, u, &w)) return;
+    if (!C::PAGED && !a.split && a.seqs <= 64) {
+        // whole row tiles, those that see the most first (see find_tile_by_size)
+        SeqTile x;
+        const bool found = a.seqs == 1 ? only_tile(a.cu_q, a.cu_k, (int)a.rows, (int)a.keys, a.group.d, C::BM, u, &x)
+                                       : find_tile_by_size(a.cu_q, a.cu_k, a.seqs, (int)a.rows, (int)a.keys, a.group.d, C::BM,
+                                                           true, u, &x);
+        if (!found) return;
+        w = KeyItem{x.seq, x.local, 0, 1, 0, 0, x.q0, x.nq, x.k0, x.nk, x.tiles};
+    } else if (!find_item<C::PAGED, C::WIN, false>(a, u, &w)) {
+        return;
+    }
     const KeyTile<C> k(a, w, kvh);
     if (k.rows - k.row0 <= 32) key_rows_body<C>(k, lds);
     else key_tile_body<C>(k, lds);
@@ -591,10 +700,10 @@ template <int DT, int SUB>
 __device__ __forceinline__ void key_join_rows(const KeyArgs& a, const KeyItem& w, int kvh, int first, int live, int row0) {
     const int lane = threadIdx.x & 15, sub = SUB == 1 ? 0 : (threadIdx.x >> 4) & (SUB - 1);
     const bool in = 8 * lane < a.dim;
-    const int64_t step = (int64_t)a.kv_heads.d * a.slot_rows;      // from a part's row to the next part's
+    const int64_t step = (int64_t)w.per_part * a.kv_heads.d * 32;      // from a part's row to the next part's
     for (int r = threadIdx.x / (16 * SUB); r < live; r += 16 / SUB) {
         const int rr = row0 + first + r;
-        const int64_t at = ((int64_t)w.slot * a.kv_heads.d + kvh) * a.slot_rows + first + r;
+        const int64_t at = ((int64_t)(w.granule + (first >> 5)) * a.kv_heads.d + kvh) * 32 + r;
         float m = -__builtin_inff();
         for (int s = threadIdx.x & (16 * SUB - 1); s < w.parts; s += 16 * SUB) {
             const float y = a.part_lse[at + s * step];
@@ -657,8 +766,9 @@ template <int DT, bool PAGED, bool WIN>
 __global__ __launch_bounds__(256) void key_join_kernel(KeyArgs a) {
     const int v = a.kv_heads((int)blockIdx.x), kvh = (int)blockIdx.x - v * a.kv_heads.d;
     KeyItem w;
-    if (!find_item<PAGED, WIN, true>(a, v >> 2, &w) || w.parts == 1) return;
-    const int first = 32 * (v & 3), row0 = (w.tiles - 1 - w.tile) * kKeyRows;
+    const int tile = a.subs == 1 ? v : v >> 2;
+    if (!find_item<PAGED, WIN, true>(a, tile, &w) || w.parts == 1) return;
+    const int first = a.subs == 1 ? 0 : 32 * (v & 3), row0 = (w.tiles - 1 - w.tile) * kKeyRows;
     int live = w.nq * a.group.d - row0 - first;
     live = live < 32 ? live : 32;
     if (w.parts >= 4) key_join_rows<DT, 4>(a, w, kvh, first, live, row0);

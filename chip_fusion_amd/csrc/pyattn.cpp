@@ -25,6 +25,7 @@ struct Call {
     // the plan, and the library's functions for it
     void *handle, *workspace, *run, *step;
     long heads, kv_heads, dim;
+    long page, axes, weights;       // keys a page (0: any); of rotations: axes of the positions, whether norms have weights
     // borrowed from the torch module for as long as it lives, held all the same
     PyObject *dtype, *f32, *i32, *u8, *tensor, *empty_like, *get_device, *raw_stream, *check;
 };
@@ -102,6 +103,21 @@ bool rows4(Call* c, PyObject* t, int64_t batch, int64_t rows, b2b_rows_t* r, int
     return true;
 }
 
+// Pages [pages, size, kv_heads, dim] of a cache (pages < 0: any number; size 0: any)
+bool pages4(Call* c, PyObject* t, int64_t* pages, int64_t* size, b2b_pages_t* x, int64_t* dev) {
+    int64_t n[4], st[4];
+    void* p;
+    if (!look(c, t, c->dtype, 4, n, st, &p, dev)) return false;
+    if ((*pages >= 0 && n[0] != *pages) || n[0] < 1 || n[0] > INT32_MAX || (*size && n[1] != *size) || n[1] < 1 ||
+        n[1] > INT32_MAX || n[2] != c->kv_heads || n[3] != c->dim)
+        return false;
+    if (st[3] != 1 || ((st[0] | st[1] | st[2] | ((intptr_t)p >> 1)) & 7)) return false;
+    *pages = n[0];
+    *size = n[1];
+    *x = b2b_pages_t{p, st[0], st[1], st[2]};
+    return true;
+}
+
 // n contiguous values (n < 0: any number, which it returns there)
 bool vec(Call* c, PyObject* t, PyObject* dtype, int64_t* n, void** p, int64_t* dev) {
     int64_t size, st;
@@ -147,18 +163,19 @@ PyObject* fresh(PyObject* like, PyObject* size, PyObject* dtype, void** p) {
 }
 
 // The output: the one that was given, or a dense one like Q.
-PyObject* output(Call* c, PyObject* given, PyObject* Q, const b2b_rows_t& q, int64_t rows, b2b_rows_t* o, int64_t* dev) {
+PyObject* output(Call* c, PyObject* given, PyObject* Q, const b2b_rows_t& q, int64_t rows, long heads, b2b_rows_t* o,
+                 int64_t* dev) {
     int64_t n;
     if (given != Py_None) {
-        if (!rows3(c, given, rows, c->heads, o, &n, dev)) return nullptr;
+        if (!rows3(c, given, rows, heads, o, &n, dev)) return nullptr;
         Py_INCREF(given);
         return given;
     }
-    if (q.row_stride != c->heads * c->dim || (c->heads > 1 && q.head_stride != c->dim)) return nullptr;
+    if (q.row_stride != heads * c->dim || (heads > 1 && q.head_stride != c->dim)) return nullptr;
     Ref t(PyObject_CallOneArg(c->empty_like, Q));
     int64_t at;
     if (!t.o || !method_int(t.o, n_data_ptr, &at)) return nullptr;
-    *o = b2b_rows_t{(const void*)at, (int64_t)c->heads * c->dim, c->dim};
+    *o = b2b_rows_t{(const void*)at, (int64_t)heads * c->dim, c->dim};
     return t.take();
 }
 
@@ -192,7 +209,7 @@ PyObject* call_attention(PyObject* self, PyObject* const* a, Py_ssize_t na) {
     if (nq < 1 || nq > INT32_MAX || !stream_of(c, dev, &s) ||
         ((decltype(&b2b_attn_workspace))c->workspace)((b2b_attn_t)c->handle, (int32_t)(nq - 1), rows, keys, &bytes))
         return other();
-    Ref out(output(c, a[5], Q, q, rows, &o, &dev));
+    Ref out(output(c, a[5], Q, q, rows, c->heads, &o, &dev));
     if (!out.o) return other();
     Ref ws(bytes ? fresh(Q, PyLong_FromSize_t(bytes), c->u8, &w) : nullptr);
     if (bytes && !ws.o) return other();
@@ -222,7 +239,7 @@ PyObject* call_prefix(PyObject* self, PyObject* const* a, Py_ssize_t na) {
     if (!vec(c, a[5], c->i32, &n, &lens, &dev) || batch > INT32_MAX || !stream_of(c, dev, &s) ||
         ((decltype(&b2b_prefix_attn_workspace))c->workspace)((b2b_attn_t)c->handle, (int32_t)batch, prefix, own, &bytes))
         return other();
-    Ref out(output(c, a[6], a[0], q, batch, &o, &dev));
+    Ref out(output(c, a[6], a[0], q, batch, c->heads, &o, &dev));
     if (!out.o) return other();
     Ref ws(bytes ? fresh(a[0], PyLong_FromSize_t(bytes), c->u8, &w) : nullptr);
     if (bytes && !ws.o) return other();
@@ -254,7 +271,7 @@ PyObject* call_linear(PyObject* self, PyObject* const* a, Py_ssize_t na) {
         return other();
     size_t bytes;
     if (!stream_of(c, dev, &s) || ((decltype(&b2b_linear_attn_workspace))c->workspace)((b2b_linear_attn_t)c->handle, (int32_t)(ncu - 1), rows, &bytes)) return other();
-    Ref out(output(c, a[6], a[0], q, rows, &o, &dev));
+    Ref out(output(c, a[6], a[0], q, rows, c->heads, &o, &dev));
     if (!out.o) return other();
     Ref after(a[7]);
     if (a[7] != Py_None) Py_INCREF(a[7]);
@@ -281,7 +298,7 @@ PyObject* call_linear_step(PyObject* self, PyObject* const* a, Py_ssize_t na) {
     if (!linear_operands(c, a, &q, &k, &v, &rows, &g, &dev) || rows > INT32_MAX || !states(c, a[4], rows, &s0, &dev) ||
         (a[6] != Py_None && !states(c, a[6], rows, &s1, &dev)) || !stream_of(c, dev, &s))
         return other();
-    Ref out(output(c, a[5], a[0], q, rows, &o, &dev));
+    Ref out(output(c, a[5], a[0], q, rows, c->heads, &o, &dev));
     if (!out.o) return other();
     Ref after(a[6]);
     if (a[6] != Py_None) Py_INCREF(a[6]);
@@ -298,6 +315,132 @@ PyObject* call_linear_step(PyObject* self, PyObject* const* a, Py_ssize_t na) {
     return st ? failed(c, st, "b2b_linear_attn_step") : PyTuple_Pack(2, out.o, after.o);
 }
 
+// A table of pages [seqs, width], lengths and starts (None: a row each) of new tokens
+struct Sequences {
+    int64_t seqs, width, ld;
+    void *table, *lens, *cu;
+};
+bool sequences(Call* c, PyObject* table, PyObject* lens, PyObject* cu, int64_t rows, Sequences* s, int64_t* dev) {
+    int64_t n[2], st[2], starts;
+    if (!look(c, table, c->i32, 2, n, st, &s->table, dev) || n[0] < 1 || n[0] >= INT32_MAX || n[1] < 1 || n[1] > INT32_MAX ||
+        st[1] != 1 || (n[0] > 1 && st[0] < n[1]))
+        return false;
+    s->seqs = n[0];
+    s->width = n[1];
+    s->ld = n[0] > 1 ? st[0] : n[1];
+    s->cu = nullptr;
+    starts = n[0] + 1;
+    return vec(c, lens, c->i32, &s->seqs, &s->lens, dev) &&
+           (cu == Py_None ? rows == n[0] : vec(c, cu, c->i32, &starts, &s->cu, dev));
+}
+
+PyObject* call_paged(PyObject* self, PyObject* const* a, Py_ssize_t na) {
+    Call* c = (Call*)self;
+    if (na != 8 || !c->handle || (a[7] != Py_False && a[7] != Py_True)) return other();
+    b2b_rows_t q, o;
+    b2b_pages_t k, v;
+    Sequences x;
+    int64_t rows, pages = -1, size = c->page, dev = -1;
+    void *s, *w = nullptr, *l = nullptr;
+    if (!rows3(c, a[0], -1, c->heads, &q, &rows, &dev) || !pages4(c, a[1], &pages, &size, &k, &dev) ||
+        !pages4(c, a[2], &pages, &size, &v, &dev) || !sequences(c, a[3], a[4], a[5], rows, &x, &dev))
+        return other();
+    size_t bytes;
+    if (!stream_of(c, dev, &s) || ((decltype(&b2b_paged_attn_workspace))c->workspace)((b2b_attn_t)c->handle, (int32_t)x.seqs, rows,
+                                                                                      (int32_t)x.width, &bytes))
+        return other();
+    Ref out(output(c, a[6], a[0], q, rows, c->heads, &o, &dev));
+    if (!out.o) return other();
+    Ref ws(bytes ? fresh(a[0], PyLong_FromSize_t(bytes), c->u8, &w) : nullptr);
+    if (bytes && !ws.o) return other();
+    Ref lse(a[7] == Py_True ? fresh(a[0], Py_BuildValue("(Ll)", (long long)rows, c->heads), c->f32, &l) : nullptr);
+    if (a[7] == Py_True && !lse.o) return other();
+    int st;
+    Py_BEGIN_ALLOW_THREADS
+    st = ((decltype(&b2b_paged_attn_run))c->run)((b2b_attn_t)c->handle, (int32_t)x.seqs, rows, q, k, v, (int32_t)pages,
+                                                 (int32_t*)x.table, (int32_t)x.width, x.ld, (int32_t*)x.lens, (int32_t*)x.cu, o,
+                                                 (float*)l, w, bytes, (hipStream_t)s);
+    Py_END_ALLOW_THREADS
+    if (st) return failed(c, st, "b2b_paged_attn_run");
+    return lse.o ? PyTuple_Pack(2, out.o, lse.o) : out.take();
+}
+
+// Q, K, positions and weights: what rotations have alike (positions None: null)
+struct Turns {
+    b2b_rows_t q, k;
+    int64_t rows, ld;
+    void *positions, *qw, *kw;
+};
+bool turns(Call* c, PyObject* Q, PyObject* K, PyObject* positions, PyObject* qw, PyObject* kw, Turns* t, int64_t* dev) {
+    int64_t n;
+    t->positions = t->qw = t->kw = nullptr;
+    if (!rows3(c, Q, -1, c->heads, &t->q, &t->rows, dev) || !rows3(c, K, t->rows, c->kv_heads, &t->k, &n, dev)) return false;
+    t->ld = t->rows;
+    if (positions != Py_None) {
+        if (c->axes == 1) {
+            n = t->rows;
+            if (!vec(c, positions, c->i32, &n, &t->positions, dev)) return false;
+        } else {
+            int64_t size[2], st[2];
+            if (!look(c, positions, c->i32, 2, size, st, &t->positions, dev) || size[0] != c->axes || size[1] != t->rows ||
+                (st[1] != 1 && size[1] > 1))
+                return false;
+            t->ld = st[0];
+        }
+    }
+    PyObject* w[2] = {qw, kw};
+    void** to[2] = {&t->qw, &t->kw};
+    for (int i = 0; i < 2; ++i) {
+        n = c->dim;
+        if (w[i] != Py_None && (!c->weights || !vec(c, w[i], c->dtype, &n, to[i], dev) || ((intptr_t)*to[i] & 15))) return false;
+    }
+    return true;
+}
+
+PyObject* call_rotary(PyObject* self, PyObject* const* a, Py_ssize_t na) {
+    Call* c = (Call*)self;
+    if (na != 7 || !c->handle || a[2] == Py_None) return other();
+    Turns t;
+    b2b_rows_t qo, ko;
+    int64_t dev = -1;
+    void* s;
+    if (!turns(c, a[0], a[1], a[2], a[3], a[4], &t, &dev) || !stream_of(c, dev, &s)) return other();
+    Ref q(output(c, a[5], a[0], t.q, t.rows, c->heads, &qo, &dev));
+    Ref k(q.o ? output(c, a[6], a[1], t.k, t.rows, c->kv_heads, &ko, &dev) : nullptr);
+    if (!k.o) return other();
+    int st;
+    Py_BEGIN_ALLOW_THREADS
+    st = ((decltype(&b2b_rotary_run))c->run)((b2b_rotary_t)c->handle, t.rows, t.q, t.k, qo, ko, (int32_t*)t.positions, t.ld, t.qw,
+                                             t.kw, (hipStream_t)s);
+    Py_END_ALLOW_THREADS
+    return st ? failed(c, st, "b2b_rotary_run") : PyTuple_Pack(2, q.o, k.o);
+}
+
+PyObject* call_append(PyObject* self, PyObject* const* a, Py_ssize_t na) {
+    Call* c = (Call*)self;
+    if (na != 12 || !c->handle) return other();
+    Turns t;
+    Sequences x;
+    b2b_rows_t v, qo;
+    b2b_pages_t kc, vc;
+    int64_t n, pages = -1, size = 0, dev = -1;
+    void* s;
+    if (!turns(c, a[0], a[1], a[8], a[9], a[10], &t, &dev) || !rows3(c, a[2], t.rows, c->kv_heads, &v, &n, &dev) ||
+        !pages4(c, a[3], &pages, &size, &kc, &dev) || !pages4(c, a[4], &pages, &size, &vc, &dev) ||
+        !sequences(c, a[5], a[6], a[7], t.rows, &x, &dev) || !stream_of(c, dev, &s))
+        return other();
+    Ref q(output(c, a[11], a[0], t.q, t.rows, c->heads, &qo, &dev));
+    if (!q.o) return other();
+    int st;
+    Py_BEGIN_ALLOW_THREADS
+    st = ((decltype(&b2b_rotary_append))c->step)((b2b_rotary_t)c->handle, (int32_t)x.seqs, t.rows, t.q, t.k, v, qo, kc, vc,
+                                                 (int32_t)pages, (int32_t)size, (int32_t*)x.table, (int32_t)x.width, x.ld,
+                                                 (int32_t*)x.lens, (int32_t*)x.cu, (int32_t*)t.positions, t.ld, t.qw, t.kw,
+                                                 (hipStream_t)s);
+    Py_END_ALLOW_THREADS
+    return st ? failed(c, st, "b2b_rotary_append") : q.take();
+}
+
 PyObject* call_close(PyObject* self, PyObject*) {
     ((Call*)self)->handle = nullptr;
     Py_RETURN_NONE;
@@ -309,14 +452,15 @@ PyObject** const held(Call* c, int i) {
     return i < 9 ? all[i] : nullptr;
 }
 
-// Call(handle, workspace, run, step, heads, kv_heads, dim, dtype, torch, check): addresses
-// of the plan and of the library's functions, as integers; check(status, name)
-// raises for a status that is not 0.
+// Call(handle, workspace, run, step, heads, kv_heads, dim, dtype, torch, check, page, axes,
+// weights): addresses of the plan and of the library's functions, as integers;
+// check(status, name) raises for a status that is not 0.
 PyObject* call_new(PyTypeObject* type, PyObject* args, PyObject*) {
     unsigned long long handle, workspace, run, step;
-    long heads, kv, dim;
+    long heads, kv, dim, page = 0, axes = 1, weights = 0;
     PyObject *dtype, *torch, *check;
-    if (!PyArg_ParseTuple(args, "KKKKlllOOO", &handle, &workspace, &run, &step, &heads, &kv, &dim, &dtype, &torch, &check))
+    if (!PyArg_ParseTuple(args, "KKKKlllOOO|lll", &handle, &workspace, &run, &step, &heads, &kv, &dim, &dtype, &torch, &check,
+                          &page, &axes, &weights))
         return nullptr;
     Call* c = (Call*)type->tp_alloc(type, 0);
     if (!c) return nullptr;
@@ -327,6 +471,9 @@ PyObject* call_new(PyTypeObject* type, PyObject* args, PyObject*) {
     c->heads = heads;
     c->kv_heads = kv;
     c->dim = dim;
+    c->page = page;
+    c->axes = axes;
+    c->weights = weights;
     Py_INCREF(dtype);
     c->dtype = dtype;
     Py_INCREF(check);
@@ -359,6 +506,11 @@ PyMethodDef call_methods[] = {
     {"linear", (PyCFunction)(void (*)(void))call_linear, METH_FASTCALL, "linear(Q, K, V, log_decay, cu, state, O, state_out)"},
     {"linear_step", (PyCFunction)(void (*)(void))call_linear_step, METH_FASTCALL,
      "linear_step(Q, K, V, log_decay, state, O, state_out)"},
+    {"paged", (PyCFunction)(void (*)(void))call_paged, METH_FASTCALL, "paged(Q, K, V, table, lens, cu, O, lse)"},
+    {"rotary", (PyCFunction)(void (*)(void))call_rotary, METH_FASTCALL,
+     "rotary(Q, K, positions, q_weight, k_weight, Q_out, K_out)"},
+    {"append", (PyCFunction)(void (*)(void))call_append, METH_FASTCALL,
+     "append(Q, K, V, k_cache, v_cache, table, lens, cu, positions, q_weight, k_weight, Q_out)"},
     {"close", call_close, METH_NOARGS, "the plan is gone: every call returns None"},
     {nullptr, nullptr, 0, nullptr}};
 

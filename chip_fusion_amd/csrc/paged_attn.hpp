@@ -47,7 +47,7 @@ struct KeyArgs : AttnArgs {
     int64_t table_ld;
     FastDiv page;           // keys a page
     int32_t pages, window, sinks;
-    int32_t split, least;   // whether items may be cut, and the fewest tiles a part has then
+    int32_t split, least;   // whether items may be cut: those of more than `least` key tiles
     float per;              // key heads over the workgroups that a call should have
     int32_t granules;       // of partial results, a key head
     int32_t subs;           // granules of a tile that the join looks for (1: no sequence has more than 32 rows)
@@ -63,6 +63,11 @@ constexpr int kKeyRows = 128;     // rows of a tile
 __device__ __forceinline__ void lds_dma16_from(const unsigned char* dst, const char* p) {
     const unsigned a = (unsigned)(uintptr_t)(lds_ptr_t)dst;
     asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" : : "s"(a), "v"(p) : "memory", "m0");
+}
+// The same of 4 bytes a lane.
+__device__ __forceinline__ void lds_dma4_from(const unsigned char* dst, const void* p) {
+    const unsigned a = (unsigned)(uintptr_t)(lds_ptr_t)dst;
+    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, off" : : "s"(a), "v"(p) : "memory", "m0");
 }
 #pragma clang diagnostic pop
 
@@ -118,7 +123,7 @@ __device__ __forceinline__ bool find_item(const KeyArgs& a, int u, KeyItem* out)
         }
     };
     load(0);
-    int most = 1 << 30;
+    int most = 1 << 30, fine = 1 << 30;      // key tiles of a part; of sequences of few rows
     if (a.split) {
         double work = (double)tiles * span;
         for (int s0 = 64; s0 < a.seqs; s0 += 64) {
@@ -129,14 +134,20 @@ __device__ __forceinline__ bool find_item(const KeyArgs& a, int u, KeyItem* out)
         // (a thousandth more than the sum, so that its rounding makes no part too many)
         const float l = ceilf(lanes_total((float)work) * 1.001f * a.per);
         most = l > (float)(1 << 30) ? 1 << 30 : (int)l;
+        // Of few rows: the less work there is, the finer, for a wave's chain of tiles is
+        // then all the time (one request of 2048 keys, 8 key heads: 19.8 us in parts of 32
+        // tiles, 14.9 of 16, 12.9 of 8; 16 requests: 30.2, 32.5, 34.8).
+        const int some = most < 8 ? 4 * most : 32;
+        fine = (most + 3) >> 2;
+        fine = fine < some ? some : fine;
+        fine = fine < 8 ? 8 : fine;
         most = most < a.least ? a.least : most;
     }
     int before = 0, used = 0;
     for (int s0 = 0;;) {
         const bool few = (unsigned)n * (unsigned)group <= 32;
-        int l = few ? (most + 3) >> 2 : most;
-        l = l < a.least ? a.least : l;
-        const int parts = a.split && span > l ? (int)(((unsigned)span + (unsigned)l - 1) / (unsigned)l) : 1;
+        const int l = few ? fine : most;
+        const int parts = a.split && span > a.least && span > l ? (int)(((unsigned)span + (unsigned)l - 1) / (unsigned)l) : 1;
         const int per_part = few ? 1 : kKeyRows / 32;
         const int mine = JOIN ? tiles : tiles * parts, cut = parts > 1 ? tiles * parts * per_part : 0;
         const int sum = lanes_sum(mine), cuts = lanes_sum(cut);
@@ -177,15 +188,18 @@ __device__ __forceinline__ bool find_item(const KeyArgs& a, int u, KeyItem* out)
 // Where keys lie: side by side, in pages of a multiple of 16 keys, in pages of any size.
 enum { KEYS_PACKED, KEYS_PAGES16, KEYS_PAGES };
 
-template <int DT_, int DB_, int WHERE_, bool WIN_>
+// FEW: for calls whose sequences have few rows, with LDS for twice the keys in flight.
+template <int DT_, int DB_, int WHERE_, bool WIN_, bool FEW_ = false>
 struct KeyCfg {
     static constexpr int DT = DT_, DB = DB_, WAVES = 4, THREADS = 64 * WAVES, BM = kKeyRows, BN = 32, WHERE = WHERE_;
-    static constexpr bool PAGED = WHERE != KEYS_PACKED, WIN = WIN_;
+    static constexpr bool PAGED = WHERE != KEYS_PACKED, WIN = WIN_, FEW = FEW_;
     static constexpr int KS = 2 * DB;                   // K-steps of the first product
     static constexpr int TILE = BN * DB * 64;           // a tile of keys (or values) in LDS
-    static constexpr int JOIN = WAVES * TILE;           // behind it: the waves' maxima and sums
+    static constexpr int MINE = FEW ? 2 * TILE + 256 : TILE;     // a wave's LDS where waves take different keys
+    static constexpr int JOIN = WAVES * MINE;           // behind it: the waves' maxima and sums
     static constexpr int LDS_BYTES = JOIN + 2 * WAVES * 32 * 4;
     static_assert(BM == 32 * WAVES, "many rows: 32 a wave");
+    static_assert(!FEW || PAGED, "few rows: pages");
 };
 
 template <class C>
@@ -540,53 +554,102 @@ __device__ __forceinline__ void key_rows_body(const KeyTile<C>& k, unsigned char
     st.init();
 #pragma unroll
     for (int b = 0; b < C::DB; ++b) o[b] = f16x_t{};
-    unsigned char* mine = lds + wave * C::TILE;
-    auto copy = [&](auto VALUES, int t, int e0, int e1) __attribute__((always_inline)) {
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");    // what the rows held has been read
-        if constexpr (C::PAGED) {
-            k.template copy_lanes<VALUES.value>(mine, t, 0, e0, lane);
-            k.template copy_lanes<VALUES.value>(mine, t, 1, e1, lane);
-        } else {
-            k.template copy_packed<VALUES.value>(mine, t, 0, lane);
-            k.template copy_packed<VALUES.value>(mine, t, 1, lane);
-        }
-    };
+    unsigned char* mine = lds + wave * C::MINE;
     const int kb0 = attn_kbase(lane, 0), kb1 = attn_kbase(lane, 1), vb = attn_vbase(lane);
     const int i0 = k.i0 + wave;
-    int e0 = 0, e1 = 0;
-    if (i0 < k.i1) {
-        e0 = k.entry_of(k.tile(i0), 0, lane);
-        e1 = k.entry_of(k.tile(i0), 1, lane);
-        copy(std::false_type{}, k.tile(i0), e0, e1);
-    }
-    for (int i = i0; i < k.i1; i += C::WAVES) {
-        const int t = k.tile(i), at = t * C::BN;
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        f16x_t s[1] = {f16x_t{}};
+    auto copy = [&](auto VALUES, unsigned char* dst, int t, int e0, int e1) __attribute__((always_inline)) {
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");    // what the rows held has been read
+        if constexpr (C::PAGED) {
+            k.template copy_lanes<VALUES.value>(dst, t, 0, e0, lane);
+            k.template copy_lanes<VALUES.value>(dst, t, 1, e1, lane);
+        } else {
+            k.template copy_packed<VALUES.value>(dst, t, 0, lane);
+            k.template copy_packed<VALUES.value>(dst, t, 1, lane);
+        }
+    };
+    f16x_t s[1];
+    auto scores = [&]() __attribute__((always_inline)) {
+        s[0] = f16x_t{};
 #pragma unroll
         for (int j = 0; j < C::KS; ++j)
             s[0] = M::mma(*(const u4_t*)(mine + ((j & 1) ? kb1 : kb0) + (j >> 1) * C::BN * 64), q[j], s[0]);
-        copy(std::true_type{}, t, e0, e1);
-        int n0 = 0, n1 = 0;
-        if (i + C::WAVES < k.i1) {
-            n0 = k.entry_of(k.tile(i + C::WAVES), 0, lane);
-            n1 = k.entry_of(k.tile(i + C::WAVES), 1, lane);
-        }
+    };
+    u4_t p[2];
+    auto softmax = [&](int t) __attribute__((always_inline)) {
+        const int at = t * C::BN;
         if (t >= clear || (C::WIN && at < open && at + C::BN > a.sinks))
             key_mask<C::WIN>(s[0], lim - at, lo - at, a.sinks - 4 * h - at);
         attn_move_max<C::DB>(attn_max<1>(s), st, o, a.sc);
         attn_probs<1>(s, st, a.sc);
-        u4_t p[2];
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) p[ks] = attn_pack<C::DT>(s[0], ks);
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    };
+    auto output = [&](const unsigned char* v) __attribute__((always_inline)) {
 #pragma unroll
         for (int b = 0; b < C::DB; ++b)
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks) o[b] = M::mma(attn_vfrag<C::BN>(mine, vb, b, ks), p[ks], o[b]);
-        e0 = n0;
-        e1 = n1;
-        if (i + C::WAVES < k.i1) copy(std::false_type{}, k.tile(i + C::WAVES), e0, e1);
+            for (int ks = 0; ks < 2; ++ks) o[b] = M::mma(attn_vfrag<C::BN>(v, vb, b, ks), p[ks], o[b]);
+    };
+    int e0 = 0, e1 = 0;
+    if (i0 < k.i1) {
+        e0 = k.entry_of(k.tile(i0), 0, lane);
+        e1 = k.entry_of(k.tile(i0), 1, lane);
+    }
+    if constexpr (C::FEW) {
+        // Keys and values have rows of their own: the next tile's keys are under way
+        // under the softmax, its values under the next scores, so that a wave waits
+        // for one latency a tile and has 8 to 16 KB in flight all the time.  Waits
+        // count instructions (2 DB a copy), so nothing else may load in the loop: the
+        // table's entries come through LDS too, two tiles ahead.
+        unsigned char* values = mine + C::TILE;
+        unsigned char* entries = values + C::TILE;
+        auto ask = [&](int i) __attribute__((always_inline)) {
+            const int key = k.tile(i) * C::BN + (lane & 31);
+            lds_dma4_from(entries, a.table + k.w.seq * a.table_ld + a.page(key < k.w.nk ? key : k.w.nk - 1));
+        };
+        if (i0 < k.i1) {
+            if (i0 + C::WAVES < k.i1) ask(i0 + C::WAVES);
+            copy(std::false_type{}, mine, k.tile(i0), e0, e1);
+            copy(std::true_type{}, values, k.tile(i0), e0, e1);
+        }
+        for (int i = i0; i < k.i1; i += C::WAVES) {
+            const int t = k.tile(i);
+            const bool more = i + C::WAVES < k.i1;
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * C::DB) : "memory");         // all but the values
+            scores();
+            if (more) {
+                e0 = ((const int*)entries)[lane >> 2];
+                e1 = ((const int*)entries)[16 + (lane >> 2)];
+                asm volatile("s_waitcnt lgkmcnt(0)" : "+v"(e0), "+v"(e1)::"memory");
+                const int after = i + 2 * C::WAVES < k.i1 ? i + 2 * C::WAVES : i + C::WAVES;
+                ask(after);
+                copy(std::false_type{}, mine, k.tile(i + C::WAVES), e0, e1);
+            }
+            softmax(t);
+            if (more) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * C::DB + 1) : "memory");     // all but entries and keys
+            else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            output(values);
+            if (more) copy(std::true_type{}, values, k.tile(i + C::WAVES), e0, e1);
+        }
+    } else {
+        if (i0 < k.i1) copy(std::false_type{}, mine, k.tile(i0), e0, e1);
+        for (int i = i0; i < k.i1; i += C::WAVES) {
+            const int t = k.tile(i);
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            scores();
+            copy(std::true_type{}, mine, t, e0, e1);
+            int n0 = 0, n1 = 0;
+            if (i + C::WAVES < k.i1) {
+                n0 = k.entry_of(k.tile(i + C::WAVES), 0, lane);
+                n1 = k.entry_of(k.tile(i + C::WAVES), 1, lane);
+            }
+            softmax(t);
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            output(mine);
+            e0 = n0;
+            e1 = n1;
+            if (i + C::WAVES < k.i1) copy(std::false_type{}, mine, k.tile(i + C::WAVES), e0, e1);
+        }
     }
     if (!attn_finite<C>(o, st)) key_again<C>(k, o, st, rr, i0, C::WAVES, lane);
     // join: every wave's maximum and sum, then its rows, scaled to the common maximum
@@ -614,7 +677,7 @@ __device__ __forceinline__ void key_rows_body(const KeyTile<C>& k, unsigned char
     const int live = k.rows - k.row0;              // 32 at most
     // half of the columns at a time: a wave's tile of LDS holds 32 rows of
     // 16 DB floats, [column quad][row]
-    float* mo = (float*)mine;
+    float* mo = (float*)(lds + wave * C::TILE);
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
         __syncthreads();
@@ -654,7 +717,7 @@ __device__ __forceinline__ void key_rows_body(const KeyTile<C>& k, unsigned char
 }
 
 template <class C>
-__global__ __launch_bounds__(C::THREADS, 3) void key_attn_kernel(KeyArgs a) {
+__global__ __launch_bounds__(C::THREADS, C::FEW ? 2 : 3) void key_attn_kernel(KeyArgs a) {
     __shared__ __attribute__((aligned(1024))) unsigned char lds[C::LDS_BYTES];
     // Workgroups go to the XCDs in turn.  A key head's own row tiles read the same
     // keys: neighbours in `u` with 8 key heads share an XCD's L2.  Few rows a sequence
@@ -692,71 +755,85 @@ __global__ __launch_bounds__(C::THREADS, 3) void key_attn_kernel(KeyArgs a) {
 // Joining partial results: 32 rows of a tile a workgroup, 16 lanes a row, 8
 // columns a lane
 // ---------------------------------------------------------------------------
-// O = sum_s w_s O_s / sum_s w_s with w_s = 2^(lse_s - max); parts that saw no
-// key have lse = -inf and are left out, whatever they hold; those whose weight
-// is 0 give infinities and NaN all the same.  SUB = 4: a row's parts go over the
-// four quarters of a wave.
+// O = sum_s w_s O_s / sum_s w_s with w_s = 2^(lse_s - max), in one pass with a
+// running maximum, 4 parts' loads in flight (8: 135 registers, and tiles' joins 5 us longer).  Parts that saw no key have lse = -inf and are left
+// out, whatever they hold; infinities and NaN of the others stay, also where the
+// weight is 0.  SUB: groups of 16 lanes that a row's parts go over, for few rows.
 template <int DT, int SUB>
 __device__ __forceinline__ void key_join_rows(const KeyArgs& a, const KeyItem& w, int kvh, int first, int live, int row0) {
+    constexpr int PER = 4;
     const int lane = threadIdx.x & 15, sub = SUB == 1 ? 0 : (threadIdx.x >> 4) & (SUB - 1);
     const bool in = 8 * lane < a.dim;
     const int64_t step = (int64_t)w.per_part * a.kv_heads.d * 32;      // from a part's row to the next part's
     for (int r = threadIdx.x / (16 * SUB); r < live; r += 16 / SUB) {
         const int rr = row0 + first + r;
         const int64_t at = ((int64_t)(w.granule + (first >> 5)) * a.kv_heads.d + kvh) * 32 + r;
-        float m = -__builtin_inff();
-        for (int s = threadIdx.x & (16 * SUB - 1); s < w.parts; s += 16 * SUB) {
-            const float y = a.part_lse[at + s * step];
-            m = y > m || y != y ? y : m;
-        }
+        float m = -__builtin_inff(), sum = 0.f, x[8] = {}, odd[8] = {};
+        auto scale_to = [&](float m1) __attribute__((always_inline)) {
+            const float f = __builtin_amdgcn_exp2f(m - (m1 == -__builtin_inff() ? 0.f : m1));
+            m = m1;
+            sum *= f;
 #pragma unroll
-        for (int d = 1; d < 16 * SUB; d <<= 1) {
-            const float y = __shfl_xor(m, d);
-            m = y > m || y != y ? y : m;
-        }
-        const float m0 = m == -__builtin_inff() ? 0.f : m;
-        float sum = 0.f, x[8] = {};
-        constexpr int PER = 4;          // parts' loads in flight
+            for (int e = 0; e < 8; ++e) x[e] *= f;
+        };
         for (int s0 = sub; s0 < w.parts; s0 += PER * SUB) {
-            float l[PER];
+            float l[PER], m1 = m;
             f4_t v[PER][2];
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
-                const bool have = s0 + i * SUB < w.parts;
-                const int64_t p = at + (have ? s0 + i * SUB : s0) * step;
-                l[i] = have ? a.part_lse[p] : -__builtin_inff();
+                l[i] = -__builtin_inff();
                 v[i][0] = v[i][1] = f4_t{0.f, 0.f, 0.f, 0.f};
-                if (in) {
-                    v[i][0] = *(const f4_t*)(a.part + p * a.dim + 8 * lane);
-                    v[i][1] = *(const f4_t*)(a.part + p * a.dim + 8 * lane + 4);
+                if (s0 + i * SUB < w.parts) {
+                    const int64_t p = at + (s0 + i * SUB) * step;
+                    l[i] = a.part_lse[p];
+                    if (in) {
+                        v[i][0] = *(const f4_t*)(a.part + p * a.dim + 8 * lane);
+                        v[i][1] = *(const f4_t*)(a.part + p * a.dim + 8 * lane + 4);
+                    }
                 }
             }
 #pragma unroll
+            for (int i = 0; i < PER; ++i) m1 = __builtin_fmaxf(m1, l[i]);
+            scale_to(m1);
+            const float m0 = m1 == -__builtin_inff() ? 0.f : m1;
+#pragma unroll
             for (int i = 0; i < PER; ++i) {
-                if (l[i] == -__builtin_inff()) continue;
+                const bool saw = l[i] != -__builtin_inff();
                 const float f = __builtin_amdgcn_exp2f(l[i] - m0);
                 sum += f;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const float y = v[i][e >> 2][e & 3];
-                    x[e] += f == 0.f ? (__builtin_fabsf(y) <= -kLowest ? 0.f : y) : f * y;
+                    const bool fine = __builtin_fabsf(y) <= -kLowest;
+                    x[e] = __builtin_fmaf(f, saw && fine ? y : 0.f, x[e]);
+                    odd[e] += saw && !fine ? y : 0.f;
                 }
             }
         }
+        if constexpr (SUB > 1) {
+            float m1 = m;
 #pragma unroll
-        for (int d = 16; d < 16 * SUB; d <<= 1) {
-            sum += __shfl_xor(sum, d);
+            for (int d = 16; d < 16 * SUB; d <<= 1) m1 = __builtin_fmaxf(m1, __shfl_xor(m1, d));
+            scale_to(m1);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] += __shfl_xor(x[e], d);
+            for (int d = 16; d < 16 * SUB; d <<= 1) {
+                sum += __shfl_xor(sum, d);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    x[e] += __shfl_xor(x[e], d);
+                    odd[e] += __shfl_xor(odd[e], d);
+                }
+            }
         }
         if (sub) continue;
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
         const int pos = a.group(rr), head = kvh * a.group.d + (rr - pos * a.group.d);
         const int64_t row = w.q0 + pos;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = __builtin_fmaf(x[e], inv, odd[e]);
         if (in)
             *(u4_t*)((char*)a.O + (row * a.ldo + (int64_t)head * a.hso + 8 * lane) * 2) =
-                u4_t{Ty<DT>::pack(x[0] * inv, x[1] * inv), Ty<DT>::pack(x[2] * inv, x[3] * inv),
-                     Ty<DT>::pack(x[4] * inv, x[5] * inv), Ty<DT>::pack(x[6] * inv, x[7] * inv)};
+                u4_t{Ty<DT>::pack(x[0], x[1]), Ty<DT>::pack(x[2], x[3]), Ty<DT>::pack(x[4], x[5]), Ty<DT>::pack(x[6], x[7])};
         if (lane == 0 && a.lse)
             a.lse[row * a.heads + head] = sum == 0.f ? -__builtin_inff() : (m + __builtin_amdgcn_logf(sum)) * kLn2;
     }
@@ -771,7 +848,8 @@ __global__ __launch_bounds__(256) void key_join_kernel(KeyArgs a) {
     const int first = a.subs == 1 ? 0 : 32 * (v & 3), row0 = (w.tiles - 1 - w.tile) * kKeyRows;
     int live = w.nq * a.group.d - row0 - first;
     live = live < 32 ? live : 32;
-    if (w.parts >= 4) key_join_rows<DT, 4>(a, w, kvh, first, live, row0);
+    if (live <= 4) key_join_rows<DT, 4>(a, w, kvh, first, live, row0);
+    else if (live <= 8) key_join_rows<DT, 2>(a, w, kvh, first, live, row0);
     else key_join_rows<DT, 1>(a, w, kvh, first, live, row0);
 }
 

@@ -23,9 +23,15 @@ struct KeyLaunchers {
         };
         using namespace b2bk;
         if (where == KEYS_PACKED) return go(KeyCfg<DT, DB, KEYS_PACKED, true>{});       // (without a window: attn.hpp)
-        if (where == KEYS_PAGES16)
-            return a.window ? go(KeyCfg<DT, DB, KEYS_PAGES16, true>{}) : go(KeyCfg<DT, DB, KEYS_PAGES16, false>{});
-        return a.window ? go(KeyCfg<DT, DB, KEYS_PAGES, true>{}) : go(KeyCfg<DT, DB, KEYS_PAGES, false>{});
+        auto flag = [](bool on, auto f) { return on ? f(std::true_type{}) : f(std::false_type{}); };
+        return flag(a.window != 0, [&](auto WIN) {
+            return flag(a.spread != 0, [&](auto FEW) {
+                // (few rows: their kernel takes pages of any size alike)
+                if (where == KEYS_PAGES16 && !FEW.value)
+                    return go(KeyCfg<DT, DB, KEYS_PAGES16, decltype(WIN)::value, false>{});
+                return go(KeyCfg<DT, DB, KEYS_PAGES, decltype(WIN)::value, decltype(FEW)::value>{});
+            });
+        });
     }
     static hipError_t run(const b2bk::KeyArgs& a, int where, unsigned grid, hipStream_t s) {
         if (a.dim <= 64) return run_db<2>(a, where, grid, s);

@@ -87,20 +87,41 @@ def _compile(src, remarks):
     return obj, r.stderr if remarks else ""
 
 
+def _torch_flags():
+    """What compiles and links against torch's own headers and libraries (which the
+    process has loaded by the time the binding is)."""
+    try:
+        import torch
+        from torch.utils.cpp_extension import include_paths
+        flags = ["-DB2B_TORCH", "-DUSE_ROCM=1", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+        for p in include_paths():
+            flags += ["-isystem", p]
+        return flags, ["-L", os.path.join(os.path.dirname(torch.__file__), "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    except Exception:
+        return None
+
+
 def binding():
     """The attention plans' compiled calls.  They are a shortcut past Python, which
     makes every call without them: where they cannot be compiled (no g++, no
-    Python.h), a line says so and the build goes on.  Their path, or None."""
+    Python.h), a line says so and the build goes on; without torch's headers they
+    look at tensors through Python's methods.  Their path, or None."""
     tmp = PYATTN + ".tmp%d" % os.getpid()
-    try:
-        subprocess.check_call(["g++", "-std=c++17", "-O2", "-fPIC", "-Wall", "-shared", "-D__HIP_PLATFORM_AMD__=1",
-                               "-I", os.path.join(ROOT, "include"), "-isystem", "/opt/rocm/include",
-                               "-isystem", sysconfig.get_paths()["include"], os.path.join(CSRC, "pyattn.cpp"), "-o", tmp])
-    except (subprocess.CalledProcessError, OSError) as e:
+    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-Wall", "-shared", "-D__HIP_PLATFORM_AMD__=1",
+           "-I", os.path.join(ROOT, "include"), "-isystem", "/opt/rocm/include",
+           "-isystem", sysconfig.get_paths()["include"], os.path.join(CSRC, "pyattn.cpp"), "-o", tmp]
+    extra = _torch_flags()
+    for flags, libs in ([extra] if extra else []) + [([], [])]:
+        try:
+            subprocess.check_call(cmd[:1] + flags + cmd[1:] + libs, **({"stderr": subprocess.DEVNULL} if flags else {}))
+            break
+        except (subprocess.CalledProcessError, OSError) as e:
+            error = e
+    else:
         for f in (tmp, PYATTN):         # (one of an earlier build may not fit the library)
             if os.path.exists(f):
                 os.remove(f)
-        sys.stderr.write(f"{os.path.basename(PYATTN)} is not built ({e}): attention calls are made in Python\n")
+        sys.stderr.write(f"{os.path.basename(PYATTN)} is not built ({error}): attention calls are made in Python\n")
         return None
     os.replace(tmp, PYATTN)
     return PYATTN

@@ -7,12 +7,23 @@
 // 77 tokens take 6.0 us a call so, about what the device takes for them, and 10.0
 // with all of it in Python.
 //
-// CPython's API only: tensors are asked for their shape, strides and address
-// through their methods, so nothing depends on torch's headers.
+// CPython's API is enough: tensors are asked for their shape, strides and address
+// through their methods (0.5 us a tensor, 1.2 an allocation).  Where it is built
+// with torch's own headers (B2B_TORCH), torch's plain tensors are looked at and
+// made directly instead; subclasses and stand-ins still go through their methods.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
 #include <cstdint>
+#include <initializer_list>
+
+#ifdef B2B_TORCH
+#include <ATen/ops/empty.h>
+#include <ATen/ops/empty_like.h>
+#include <torch/csrc/Dtype.h>
+#include <torch/csrc/DynamicTypes.h>
+#include <torch/csrc/autograd/python_variable.h>
+#endif
 
 #include "b2b_attn.h"
 
@@ -59,9 +70,53 @@ bool ints(PyObject* tuple, int n, int64_t* v) {
     return true;
 }
 
+#ifdef B2B_TORCH
+// torch's own tensor, and no subclass with methods of its own.
+bool plain(Call* c, PyObject* t) { return c->tensor == THPVariableClass && THPVariable_CheckExact(t); }
+
+// What may throw, without the interpreter's lock: a tensor that allocates, as a new reference.
+template <class F>
+PyObject* allocate(F make) {
+    struct Unlocked {
+        PyThreadState* s = PyEval_SaveThread();
+        ~Unlocked() { PyEval_RestoreThread(s); }
+    };
+    try {
+        at::Tensor t;
+        {
+            Unlocked u;
+            t = make();
+        }
+        return THPVariable_Wrap(std::move(t));
+    } catch (...) {         // Python makes the call again and says what it is
+        return nullptr;
+    }
+}
+#endif
+
 // A tensor of that type with n dimensions on device `dev` (-1: any, which it
 // returns there): its sizes, strides and address.
 bool look(Call* c, PyObject* t, PyObject* dtype, int n, int64_t* size, int64_t* stride, void** p, int64_t* dev) {
+#ifdef B2B_TORCH
+    if (plain(c, t)) {
+        try {
+            const at::Tensor& x = THPVariable_Unpack(t);
+            if ((PyObject*)torch::getTHPDtype(x.scalar_type()) != dtype || x.layout() != at::kStrided || x.dim() != n || !x.is_cuda())
+                return false;
+            for (int i = 0; i < n; ++i) {
+                size[i] = x.size(i);
+                stride[i] = x.stride(i);
+            }
+            const int64_t index = x.get_device();
+            if (index < 0 || (*dev >= 0 && index != *dev)) return false;
+            *dev = index;
+            *p = x.data_ptr();
+            return *p != nullptr;
+        } catch (...) {
+            return false;
+        }
+    }
+#endif
     if (!PyObject_TypeCheck(t, (PyTypeObject*)c->tensor)) return false;
     Ref d(PyObject_GetAttr(t, n_dtype));
     if (d.o != dtype) return false;
@@ -150,12 +205,45 @@ bool stream_of(Call* c, int64_t dev, void** s) {
 }
 
 // like.new_empty(size, dtype=dtype), its address
-PyObject* fresh(PyObject* like, PyObject* size, PyObject* dtype, void** p) {
-    Ref s(size), kw(Py_BuildValue("{s:O}", "dtype", dtype));
+PyObject* fresh(Call* c, PyObject* like, std::initializer_list<int64_t> size, PyObject* dtype, void** p) {
+#ifdef B2B_TORCH
+    if (plain(c, like)) {
+        const at::Tensor& x = THPVariable_Unpack(like);
+        PyObject* t = allocate([&] {
+            return at::empty(at::IntArrayRef(size), x.options().dtype(((THPDtype*)dtype)->scalar_type));
+        });
+        if (t) *p = THPVariable_Unpack(t).data_ptr();
+        return t;
+    }
+#endif
+    Ref s(PyTuple_New((Py_ssize_t)size.size())), kw(Py_BuildValue("{s:O}", "dtype", dtype));
     if (!s.o || !kw.o) return nullptr;
+    Py_ssize_t i = 0;
+    for (int64_t n : size) {
+        PyObject* v = PyLong_FromLongLong(n);
+        if (!v) return nullptr;
+        PyTuple_SET_ITEM(s.o, i++, v);
+    }
     Ref f(PyObject_GetAttr(like, n_new_empty)), args(PyTuple_Pack(1, s.o));
     if (!f.o || !args.o) return nullptr;
     Ref t(PyObject_Call(f.o, args.o, kw.o));
+    int64_t at;
+    if (!t.o || !method_int(t.o, n_data_ptr, &at)) return nullptr;
+    *p = (void*)at;
+    return t.take();
+}
+
+// torch.empty_like(like), its address
+PyObject* fresh_like(Call* c, PyObject* like, void** p) {
+#ifdef B2B_TORCH
+    if (plain(c, like)) {
+        const at::Tensor& x = THPVariable_Unpack(like);
+        PyObject* t = allocate([&] { return at::empty_like(x); });
+        if (t) *p = THPVariable_Unpack(t).data_ptr();
+        return t;
+    }
+#endif
+    Ref t(PyObject_CallOneArg(c->empty_like, like));
     int64_t at;
     if (!t.o || !method_int(t.o, n_data_ptr, &at)) return nullptr;
     *p = (void*)at;
@@ -172,10 +260,10 @@ PyObject* output(Call* c, PyObject* given, PyObject* Q, const b2b_rows_t& q, int
         return given;
     }
     if (q.row_stride != heads * c->dim || (heads > 1 && q.head_stride != c->dim)) return nullptr;
-    Ref t(PyObject_CallOneArg(c->empty_like, Q));
-    int64_t at;
-    if (!t.o || !method_int(t.o, n_data_ptr, &at)) return nullptr;
-    *o = b2b_rows_t{(const void*)at, (int64_t)heads * c->dim, c->dim};
+    void* p;
+    Ref t(fresh_like(c, Q, &p));
+    if (!t.o) return nullptr;
+    *o = b2b_rows_t{p, (int64_t)heads * c->dim, c->dim};
     return t.take();
 }
 
@@ -211,9 +299,9 @@ PyObject* call_attention(PyObject* self, PyObject* const* a, Py_ssize_t na) {
         return other();
     Ref out(output(c, a[5], Q, q, rows, c->heads, &o, &dev));
     if (!out.o) return other();
-    Ref ws(bytes ? fresh(Q, PyLong_FromSize_t(bytes), c->u8, &w) : nullptr);
+    Ref ws(bytes ? fresh(c, Q, {(int64_t)bytes}, c->u8, &w) : nullptr);
     if (bytes && !ws.o) return other();
-    Ref lse(a[6] == Py_True ? fresh(Q, Py_BuildValue("(Ll)", (long long)rows, c->heads), c->f32, &l) : nullptr);
+    Ref lse(a[6] == Py_True ? fresh(c, Q, {rows, c->heads}, c->f32, &l) : nullptr);
     if (a[6] == Py_True && !lse.o) return other();
     int st;
     Py_BEGIN_ALLOW_THREADS
@@ -241,7 +329,7 @@ PyObject* call_prefix(PyObject* self, PyObject* const* a, Py_ssize_t na) {
         return other();
     Ref out(output(c, a[6], a[0], q, batch, c->heads, &o, &dev));
     if (!out.o) return other();
-    Ref ws(bytes ? fresh(a[0], PyLong_FromSize_t(bytes), c->u8, &w) : nullptr);
+    Ref ws(bytes ? fresh(c, a[0], {(int64_t)bytes}, c->u8, &w) : nullptr);
     if (bytes && !ws.o) return other();
     int st;
     Py_BEGIN_ALLOW_THREADS
@@ -276,10 +364,10 @@ PyObject* call_linear(PyObject* self, PyObject* const* a, Py_ssize_t na) {
     Ref after(a[7]);
     if (a[7] != Py_None) Py_INCREF(a[7]);
     else {
-        after.o = fresh(a[0], Py_BuildValue("(Llll)", (long long)(ncu - 1), c->heads, c->dim, c->dim), c->f32, &s1);
+        after.o = fresh(c, a[0], {ncu - 1, c->heads, c->dim, c->dim}, c->f32, &s1);
         if (!after.o) return other();
     }
-    Ref ws(bytes ? fresh(a[0], PyLong_FromSize_t(bytes), c->u8, &w) : nullptr);
+    Ref ws(bytes ? fresh(c, a[0], {(int64_t)bytes}, c->u8, &w) : nullptr);
     if (bytes && !ws.o) return other();
     int st;
     Py_BEGIN_ALLOW_THREADS
@@ -293,7 +381,7 @@ PyObject* call_linear_step(PyObject* self, PyObject* const* a, Py_ssize_t na) {
     Call* c = (Call*)self;
     if (na != 7 || !c->handle) return other();
     b2b_rows_t q, k, v, o;
-    int64_t rows, at, dev = -1;
+    int64_t rows, dev = -1;
     void *g, *s, *s0, *s1;
     if (!linear_operands(c, a, &q, &k, &v, &rows, &g, &dev) || rows > INT32_MAX || !states(c, a[4], rows, &s0, &dev) ||
         (a[6] != Py_None && !states(c, a[6], rows, &s1, &dev)) || !stream_of(c, dev, &s))
@@ -303,9 +391,8 @@ PyObject* call_linear_step(PyObject* self, PyObject* const* a, Py_ssize_t na) {
     Ref after(a[6]);
     if (a[6] != Py_None) Py_INCREF(a[6]);
     else {
-        after.o = PyObject_CallOneArg(c->empty_like, a[4]);
-        if (!after.o || !method_int(after.o, n_data_ptr, &at)) return other();
-        s1 = (void*)at;
+        after.o = fresh_like(c, a[4], &s1);
+        if (!after.o) return other();
     }
     int st;
     Py_BEGIN_ALLOW_THREADS
@@ -351,9 +438,9 @@ PyObject* call_paged(PyObject* self, PyObject* const* a, Py_ssize_t na) {
         return other();
     Ref out(output(c, a[6], a[0], q, rows, c->heads, &o, &dev));
     if (!out.o) return other();
-    Ref ws(bytes ? fresh(a[0], PyLong_FromSize_t(bytes), c->u8, &w) : nullptr);
+    Ref ws(bytes ? fresh(c, a[0], {(int64_t)bytes}, c->u8, &w) : nullptr);
     if (bytes && !ws.o) return other();
-    Ref lse(a[7] == Py_True ? fresh(a[0], Py_BuildValue("(Ll)", (long long)rows, c->heads), c->f32, &l) : nullptr);
+    Ref lse(a[7] == Py_True ? fresh(c, a[0], {rows, c->heads}, c->f32, &l) : nullptr);
     if (a[7] == Py_True && !lse.o) return other();
     int st;
     Py_BEGIN_ALLOW_THREADS

@@ -153,3 +153,13 @@ print("made in Python")
 def test_calls_without_the_compiled_binding():
     r = subprocess.run([sys.executable, "-c", CALLS], cwd=ROOT, capture_output=True, text=True)
     assert r.returncode == 0 and "made in Python" in r.stdout, r.stderr[-2000:]
+
+
+def test_the_binding_builds_without_torchs_headers(monkeypatch, tmp_path):
+    """Then it looks at all tensors through their methods."""
+    from chip_fusion_amd import build
+    out = tmp_path / "_attn.so"
+    monkeypatch.setattr(build, "PYATTN", str(out))
+    monkeypatch.setattr(build, "_torch_flags", lambda: None)
+    assert build.binding() == str(out) and out.exists()
+    assert b"libtorch_python" not in out.read_bytes()

@@ -71,7 +71,11 @@ struct Turn {
 // APPEND: keys and values go to the pages.  NORM, INTER: the plan's flags.
 template <int DT, int L, bool APPEND, bool NORM, bool INTER>
 __global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a) {
-    constexpr int GROUPS = 256 / L, BATCH = 4;      // heads in flight a lane
+    // Heads in flight a lane.  Two, for more workgroups a compute unit, but where the
+    // norm's steps a head leave the loads more to cover and nothing is appended (8001
+    // rows of 40 heads of 128: 38.0 us with 2, 36.1 with 4, 38.6 with 8; without a norm,
+    // 5003 rows of 28 heads of 96: 14.4, 15.3, 16.1; 4097 rows into pages: 12.0, 12.6, 12.7).
+    constexpr int GROUPS = 256 / L, BATCH = L == 16 && NORM && !APPEND ? 4 : 2;
     constexpr int ROWS = kRotaryRows, TURNS = ROWS / 4;      // angles a thread works out, at most
     __shared__ float turn[ROWS][64][2];             // [row][pair][cos, sin]
     // append: a row's place in its sequence, or kNoRow of none, and the page that holds it (-1: none)

@@ -152,35 +152,50 @@ __global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a) {
     [[maybe_unused]] int page_entry[ROWS / 4];
     if constexpr (APPEND) {
         // a wave takes every fourth row: which sequence holds it, and its page, which is looked up under the sines
+        int seq[ROWS / 4], spot[ROWS / 4];
 #pragma unroll
         for (int x = 0; x < ROWS / 4; ++x) {
-            page_entry[x] = -1;
             const int rr = wave + 4 * x, mine = row0 + rr;
-            if (rr >= R || mine >= a.rows) continue;
-            int seq = -1, spot = 0;
-            if (!a.cu) {
-                seq = mine;
-                spot = (a.lens[mine] > 0 ? a.lens[mine] : 0) - 1;
-            } else {
-                for (int s0 = 0; s0 < a.seqs && seq < 0; s0 += 64) {
-                    const int s = s0 + lane;
-                    int q0 = 0, n = 0, len = 0;
-                    if (s < a.seqs) {
-                        seq_range(a.cu, s, a.rows, &q0, &n);
-                        len = a.lens[s] > 0 ? a.lens[s] : 0;
-                    }
+            seq[x] = -1;
+            spot[x] = 0;
+            if (!a.cu && rr < R && mine < a.rows) {
+                seq[x] = mine;
+                spot[x] = (a.lens[mine] > 0 ? a.lens[mine] : 0) - 1;
+            }
+        }
+        if (a.cu)
+            for (int s0 = 0; s0 < a.seqs; s0 += 64) {
+                const int s = s0 + lane;
+                int q0 = 0, n = 0, len = 0;
+                if (s < a.seqs) {
+                    seq_range(a.cu, s, a.rows, &q0, &n);
+                    len = a.lens[s] > 0 ? a.lens[s] : 0;
+                }
+                bool all = true;
+#pragma unroll
+                for (int x = 0; x < ROWS / 4; ++x) {
+                    const int rr = wave + 4 * x, mine = row0 + rr;
+                    if (rr >= R || seq[x] >= 0) continue;
                     const unsigned long long hit = __ballot(mine >= q0 && mine < q0 + n);
                     if (hit) {
                         const int l = __ffsll(hit) - 1;
-                        seq = s0 + l;
-                        spot = __builtin_amdgcn_readlane(len, l) -
-                               (__builtin_amdgcn_readlane(q0, l) + __builtin_amdgcn_readlane(n, l) - mine);
+                        seq[x] = s0 + l;
+                        spot[x] = __builtin_amdgcn_readlane(len, l) -
+                                  (__builtin_amdgcn_readlane(q0, l) + __builtin_amdgcn_readlane(n, l) - mine);
+                    } else {
+                        all = false;
                     }
                 }
+                if (all) break;
             }
-            if (lane == 0) place[rr] = seq < 0 ? kNoRow : spot;
-            const int pg = spot >= 0 ? a.page(spot) : 0;
-            if (seq >= 0 && spot >= 0 && pg < a.width) page_entry[x] = a.table[seq * a.table_ld + pg];
+#pragma unroll
+        for (int x = 0; x < ROWS / 4; ++x) {
+            const int rr = wave + 4 * x;
+            page_entry[x] = -1;
+            if (rr >= R) continue;
+            if (lane == 0) place[rr] = seq[x] < 0 ? kNoRow : spot[x];
+            const int pg = spot[x] >= 0 ? a.page(spot[x]) : 0;
+            if (seq[x] >= 0 && spot[x] >= 0 && pg < a.width) page_entry[x] = a.table[seq[x] * a.table_ld + pg];
         }
         __syncthreads();
     }

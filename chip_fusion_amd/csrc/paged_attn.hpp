@@ -407,9 +407,11 @@ __device__ __forceinline__ void key_tile_body(const KeyTile<C>& k, unsigned char
     st.init();
 #pragma unroll
     for (int b = 0; b < C::DB; ++b) o[b] = f16x_t{};
-    // tiles below `clear` are full and end where every row of the wave sees; from `done` on none sees any;
-    // under a window rows see nothing of tiles that end at `dark` or before, everything from `open` on
-    const int clear = wrow + 32 <= k.rows ? k.sees(wrow) / C::BN : 0;
+    // tiles below `clear` are full and end where every row of the wave sees (lanes past the
+    // last row are not looked at: a wave that masked all its tiles for them took a third
+    // longer, and the launch with it); from `done` on none sees any; under a window rows
+    // see nothing of tiles that end at `dark` or before, everything from `open` on
+    const int clear = wrow < k.rows ? k.sees(wrow) / C::BN : 0;
     const int wlast = (wrow + 32 < k.rows ? wrow + 32 : k.rows) - 1;
     const int done = wrow < k.rows ? (k.sees(wlast) + C::BN - 1) / C::BN : 0;
     const int dark = C::WIN ? k.from(wrow) : 0, open = C::WIN ? k.from(wlast) : 0;

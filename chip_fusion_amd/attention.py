@@ -458,8 +458,12 @@ class NormRotary:
                  interleaved=False, eps=1e-6):
         code = DTYPES[dtype] if isinstance(dtype, str) else int(dtype)
         rotary_dim = head_dim if rotary_dim is None else rotary_dim
+        if not isinstance(rotary_dim, int) or rotary_dim < 0:
+            raise ValueError(f"rotary_dim: a whole number from 0 is expected, got {rotary_dim!r}")
         pairs = rotary_dim // 2
         if freqs is None:
+            if not base > 0:
+                raise ValueError("base: a positive number is expected")
             freqs = [base ** (-2.0 * i / rotary_dim) for i in range(pairs)]
         freqs = [float(f) for f in freqs]
         if len(freqs) != pairs:

@@ -141,7 +141,7 @@ b2b_status_t b2b_rotary_run(b2b_rotary_t p, int64_t rows, b2b_rows_t Q, b2b_rows
     if (!rows_ok(Q, rows, p->dim) || !rows_ok(K, rows, p->dim) || !written_ok(Qo, Q, rows, p->heads, p->dim) ||
         !written_ok(Ko, K, rows, p->kv_heads, p->dim) || Qo.data == Ko.data || Qo.data == K.data || Ko.data == Q.data)
         return B2B_ERROR_INVALID_VALUE;
-    if (p->rotary && (!positions || (p->axes > 1 && (position_stride < rows || position_stride > kMaxFar))))
+    if (p->rotary && (!positions || (p->axes > 1 && (position_stride < 0 || position_stride > kMaxFar))))
         return B2B_ERROR_INVALID_VALUE;
     b2bk::RotaryArgs a = {};
     fill(p, a, rows, Q, K, Qo, positions, position_stride, q_weight, k_weight);
@@ -163,7 +163,7 @@ b2b_status_t b2b_rotary_append(b2b_rotary_t p, int32_t seqs, int64_t rows, b2b_r
     if (!rows_ok(Q, rows, p->dim) || !rows_ok(K, rows, p->dim) || !rows_ok(V, rows, p->dim) ||
         !written_ok(Qo, Q, rows, p->heads, p->dim) || Qo.data == K.data || Qo.data == V.data || !lens)
         return B2B_ERROR_INVALID_VALUE;
-    if (positions && p->axes > 1 && (position_stride < rows || position_stride > kMaxFar)) return B2B_ERROR_INVALID_VALUE;
+    if (positions && p->axes > 1 && (position_stride < 0 || position_stride > kMaxFar)) return B2B_ERROR_INVALID_VALUE;
     if (pages && width) {
         if (!table || table_stride < 0 || table_stride > kMaxFar || (seqs > 1 && table_stride < width)) return B2B_ERROR_INVALID_VALUE;
         for (const b2b_pages_t* x : {&k_cache, &v_cache})

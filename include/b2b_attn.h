@@ -242,8 +242,8 @@ b2b_status_t b2b_rotary_create(b2b_rotary_t* plan, b2b_dtype_t dtype, int32_t he
 /*
  * Q' and K' of `rows` rows: Qo and Ko may be Q and K (the same address and
  * strides: in place), and must not overlap anything else.
- *   positions        device int32 [axes, rows], axes position_stride apart (NULL where
- *                    rotary_dim is 0)
+ *   positions        device int32 [axes, rows], axes position_stride apart (0: all axes
+ *                    alike; NULL where rotary_dim is 0)
  *   q_weight, k_weight  device, head_dim values of dtype, 16-byte aligned, or NULL (1);
  *                    NULL without B2B_ROTARY_NORM
  */

@@ -78,7 +78,11 @@ def test_several_axes(order, inter):
     wide = torch.zeros((3, T + 5), dtype=torch.int32, device="cuda")       # axes further apart than rows
     wide[:, :T] = pos
     again = cf.NormRotary("f16", H, Hkv, D, freqs=freqs, interleaved=inter, eps=None, **kw).run(q, k, wide[:, :T])
+    one = pos[:1].expand(3, T)                     # text: the same place on every axis
+    alike = cf.NormRotary("f16", H, Hkv, D, freqs=freqs, interleaved=inter, eps=None, **kw).run(q, k, one)
+    plain = cf.NormRotary("f16", H, Hkv, D, freqs=freqs, interleaved=inter, eps=None).run(q, k, pos[0])
     torch.cuda.synchronize()
+    assert torch.equal(alike[0], plain[0]) and torch.equal(alike[1], plain[1])
     for x, y, z in ((q, got[0], again[0]), (k, got[1], again[1])):
         want, bound = R.norm_rotary(x, None, pos, D, freqs, axes, inter, None)
         R.check(y, want, bound)

@@ -151,8 +151,34 @@ def test_chunks_of_all_sizes(group, before):
     R.check(lse, want_lse, bl, "LSE")
 
 
+@pytest.mark.parametrize("dtype,H,Hkv,D,size", [("bf16", 8, 2, 128, 16), ("f16", 12, 2, 96, 24), ("f16", 8, 8, 64, 1)])
+@pytest.mark.parametrize("window,sinks", [(None, 0), (700, 40)])
+def test_single_tokens_and_chunks_together(dtype, H, Hkv, D, size, window, sinks):
+    """Mostly single tokens, few and many keys, whole and cut; a chunk among them
+    whose rows fill tiles; requests that pad the batch; pages that sequences share."""
+    lq = [1] * 30 + [40] + [0, 1, 1]
+    lk = [(37 * i * i) % 300 + 1 for i in range(28)] + [6000, 2500, 1900, 0, 0, 5]
+    _flush(f"single tokens and a chunk {dtype} {D} window {window}")
+    case = (dtype, H, Hkv, D, size, lq, lk, window, sinks, "rows")
+    plan, q, kc, vc, table, cu, k, v = _paged(case)
+    got, lse = plan.run(q, kc, vc, table, _int(lk), cu, lse=True)
+    torch.cuda.synchronize()
+    want, want_lse, b, bl = R.attend(q, k, v, lq, lk, window, sinks)
+    R.check(got, want, b, "O")
+    R.check(lse, want_lse, bl, "LSE")
+    # a second request behind the longest one's pages
+    share, n = table[28:29].expand(3, -1).contiguous(), _int([6000, 6000, 5999])
+    q3 = torch.cat([q[28:29], q[28:29], q[:1]])
+    both = plan.run(q3, kc, vc, share, n)
+    torch.cuda.synchronize()
+    at = sum(lk[:28])
+    want, _, b, _ = R.attend(q3, *(torch.cat([x[at:at + 6000], x[at:at + 6000], x[at:at + 5999]]) for x in (k, v)), [1] * 3,
+                             n.tolist(), window, sinks)
+    R.check(both, want, b, "shared pages")
+
+
 @pytest.mark.parametrize("window,sinks", [(None, 0), (45, 0), (45, 10)])
-@pytest.mark.parametrize("rows", [4, 150])
+@pytest.mark.parametrize("rows", [1, 4, 150])
 def test_infinities_and_nan_reach_the_rows_that_see_them(window, sinks, rows):
     H, Hkv, D, size, n = 2, 1, 64, 16, 260
     _flush(f"infinities, window {window} {sinks}, {rows} rows")

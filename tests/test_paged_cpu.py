@@ -173,7 +173,7 @@ def test_create_rotary(kw, status):
     (dict(Ko=_rows(P)), INVALID), (dict(Qo=_rows(P * 4)), INVALID),          # over the keys, the queries, each other
     (dict(Qo=_rows(P, ld=512)), INVALID), (dict(Qo=_rows(P, hs=128, ld=512)), INVALID),      # in place at other strides
     (dict(Ko=_rows(P * 2, ld=64, hs=256)), INVALID), (dict(Qo=_rows(P * 3, hs=0)), INVALID),
-    (dict(pos=None), INVALID), (dict(far=3), INVALID), (dict(far=1 << 41), INVALID), (dict(qw=P + 8), INVALID),
+    (dict(pos=None), INVALID), (dict(far=-4), INVALID), (dict(far=1 << 41), INVALID), (dict(qw=P + 8), INVALID),
     (dict(kw_=P + 2), INVALID),
 ])
 def test_rotary_run_refuses(kw, status):
@@ -192,7 +192,7 @@ def test_rotary_run_refuses(kw, status):
     (dict(kc=_pages(P)), INVALID), (dict(vc=_pages(P * 4)), INVALID), (dict(vc=_pages(P * 6, ps=0)), INVALID),
     (dict(kc=_pages(P * 5, ps=1024)), INVALID), (dict(kc=_pages(P * 5, ld=64)), INVALID),                   # rows overlap
     (dict(kc=_pages(P * 5, hs=56)), INVALID), (dict(kc=_pages(P * 5, ps=1024, ld=64, hs=512)), INVALID),
-    (dict(far=3), INVALID), (dict(qw=P + 8), INVALID), (dict(plan=None), INVALID),
+    (dict(far=-4), INVALID), (dict(qw=P + 8), INVALID), (dict(plan=None), INVALID),
 ])
 def test_rotary_append_refuses(kw, status):
     plan = cf.NormRotary("f16", 4, 2, 64, sections=(16, 16))
@@ -206,7 +206,8 @@ def test_rotary_append_refuses(kw, status):
 
 @pytest.mark.parametrize("kw,match", [
     (dict(freqs=[1.0]), "freqs"), (dict(sections=(16, 15)), "sections"), (dict(sections=(40, -8)), "sections"),
-    (dict(sections=(16, 16), axes_of=[0] * 32), "axes_of"), (dict(axes_of=[0] * 31), "axes_of"),
+    (dict(sections=(16, 16), axes_of=[0] * 32), "axes_of"), (dict(axes_of=[0] * 31), "axes_of"), (dict(base=0.0), "base"),
+    (dict(base=-2.0), "base"), (dict(rotary_dim=-8), "rotary_dim"), (dict(rotary_dim=1.5), "rotary_dim"),
 ])
 def test_rotary_arguments(kw, match):
     with pytest.raises(ValueError, match=match):

@@ -1,5 +1,7 @@
 """Attention plans (b2b_attn.h): argument checks and marshalling for the
-library's attention kernels.
+library's attention kernels: packed prompts (under a window or not), single
+tokens behind a shared prefix, new tokens over a paged cache, linear attention,
+and the norms and rotations of queries and keys before them.
 
 Tensors are taken as they lie: [rows, heads, dim] with any row and head
 strides that are multiples of 8 elements, dim contiguous -- slices of a fused

@@ -14,6 +14,12 @@
 // its 8 elements in registers over the heads it takes.  An angle is position x
 // frequency / 2 pi in float64, of which only the fraction of a turn counts: off by
 // 2^-25 of a turn at positions of 2^31.
+//
+// Measured (bf16, 32 + 8 heads of 128, normed): 8001 rows, 164 MB, in 34 us on the
+// device (a copy of as many bytes 32.6), 32768 rows in 125 us, 5.4 TB/s.  Few rows
+// take the latencies one after another: positions, angles, heads, 3.7 us for 3 rows;
+// appended, starts and lengths before them, 5.4 us for 128 rows and 11.4 for 4097 of
+// 16 + 4 + 4 heads of 64 (5 by their bytes).
 #pragma once
 #include "paged_attn.hpp"
 

@@ -394,6 +394,16 @@ __device__ __forceinline__ void key_again(const KeyTile<C>& k, f16x_t (&o)[C::DB
 // ---------------------------------------------------------------------------
 // Many rows: 32 a wave, the key tiles shared (attn_tile_body's scheme)
 // ---------------------------------------------------------------------------
+// Measured (bf16, 32 heads of 128 on 8 key heads): 32768 tokens under a window of
+// 4096 in 1.81 to 1.98 ms by the card, 1040 to 1142 TFLOP/s of the 1280 that a product
+// of 8192^3 reaches (matrix cores busy 0.64 of the cycles at a clock that power holds
+// near 1.74 GHz); 8001 tokens in 17 sequences under a window of 512 in 63 to 68 us, of
+// whose 37 thousand cycles a workgroup spends 4.3 on finding its place, 7.2 on its first
+// keys and queries, 22.6 on 10 tiles and 2.9 on its output; 2048 rows of 4 sequences
+// behind up to 16384 keys in pages of 64 in 367 us and 8 for the join (matrix cores
+// busy 0.56).  Tile i's probabilities worked out under tile i + 1's scores, which
+// costs no LDS but 16 registers, was slower (1858 us -> 1925 and 380 -> 393): what
+// waves do side by side covers that already.
 template <class C>
 __device__ __forceinline__ void key_tile_body(const KeyTile<C>& k, unsigned char* lds) {
     using M = Ty32<C::DT>;
@@ -539,6 +549,10 @@ __device__ __forceinline__ void key_tile_body(const KeyTile<C>& k, unsigned char
 // ---------------------------------------------------------------------------
 // Up to 32 rows: the waves take different keys (attn_rows_body's scheme)
 // ---------------------------------------------------------------------------
+// What bounds it is the bytes of K and V.  Measured (bf16, 32 heads of 128 on 8 key
+// heads): 64 requests of up to 8192 keys in pages of 16, 1.02 GB, in 197 us and 5.6
+// for the join, 5.05 TB/s in all (a copy of 1 GiB: 5.0 to 5.1); 64 of 8192 each
+// 412 us, 5.2 TB/s; one request of 2048 keys 13 us, of 32768 42.
 template <class C>
 __device__ __forceinline__ void key_rows_body(const KeyTile<C>& k, unsigned char* lds) {
     using M = Ty32<C::DT>;
@@ -770,7 +784,7 @@ __device__ __forceinline__ void key_join_rows(const KeyArgs& a, const KeyItem& w
     for (int r = threadIdx.x / (16 * SUB); r < live; r += 16 / SUB) {
         const int rr = row0 + first + r;
         const int64_t at = ((int64_t)(w.granule + (first >> 5)) * a.kv_heads.d + kvh) * 32 + r;
-        float m = -__builtin_inff(), sum = 0.f, x[8] = {}, odd[8] = {};
+        float m = -__builtin_inff(), sum = 0.f, x[8] = {};
         auto scale_to = [&](float m1) __attribute__((always_inline)) {
             const float f = __builtin_amdgcn_exp2f(m - (m1 == -__builtin_inff() ? 0.f : m1));
             m = m1;
@@ -800,16 +814,10 @@ __device__ __forceinline__ void key_join_rows(const KeyArgs& a, const KeyItem& w
             const float m0 = m1 == -__builtin_inff() ? 0.f : m1;
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
-                const bool saw = l[i] != -__builtin_inff();
                 const float f = __builtin_amdgcn_exp2f(l[i] - m0);
                 sum += f;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float y = v[i][e >> 2][e & 3];
-                    const bool fine = __builtin_fabsf(y) <= -kLowest;
-                    x[e] = __builtin_fmaf(f, saw && fine ? y : 0.f, x[e]);
-                    odd[e] += saw && !fine ? y : 0.f;
-                }
+                for (int e = 0; e < 8; ++e) x[e] = __builtin_fmaf(f, v[i][e >> 2][e & 3], x[e]);
             }
         }
         if constexpr (SUB > 1) {
@@ -821,9 +829,25 @@ __device__ __forceinline__ void key_join_rows(const KeyArgs& a, const KeyItem& w
             for (int d = 16; d < 16 * SUB; d <<= 1) {
                 sum += __shfl_xor(sum, d);
 #pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] += __shfl_xor(x[e], d);
+            }
+        }
+        float z = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) z = __builtin_fmaf(x[e], 0.f, z);
+        if (__any(z != 0.f)) {
+            // infinities or NaN among the parts: a weight of 0, or a rescaling by 0, has made NaN of some
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = 0.f;
+            const float m0 = m == -__builtin_inff() ? 0.f : m;
+#pragma unroll 1
+            for (int s = 0; s < w.parts; ++s) {
+                const int64_t p = at + s * step;
+                const float l = a.part_lse[p], f = __builtin_amdgcn_exp2f(l - m0);
+#pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    x[e] += __shfl_xor(x[e], d);
-                    odd[e] += __shfl_xor(odd[e], d);
+                    const float y = in && l != -__builtin_inff() ? a.part[p * a.dim + 8 * lane + e] : 0.f;
+                    x[e] += __builtin_fabsf(y) <= -kLowest ? f * y : y;
                 }
             }
         }
@@ -832,7 +856,7 @@ __device__ __forceinline__ void key_join_rows(const KeyArgs& a, const KeyItem& w
         const int pos = a.group(rr), head = kvh * a.group.d + (rr - pos * a.group.d);
         const int64_t row = w.q0 + pos;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = __builtin_fmaf(x[e], inv, odd[e]);
+        for (int e = 0; e < 8; ++e) x[e] *= inv;
         if (in)
             *(u4_t*)((char*)a.O + (row * a.ldo + (int64_t)head * a.hso + 8 * lane) * 2) =
                 u4_t{Ty<DT>::pack(x[0], x[1]), Ty<DT>::pack(x[2], x[3]), Ty<DT>::pack(x[4], x[5]), Ty<DT>::pack(x[6], x[7])};

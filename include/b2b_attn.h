@@ -4,6 +4,8 @@
  * with a mask, a softmax or a decay between the products.  As in the GEMM
  * cascades of b2b.h the intermediate never leaves the chip: the first
  * product's accumulator fragment becomes the second one's operand in place.
+ * And what comes before them: norms and rotations of queries and keys, alone
+ * or into the pages of a cache.
  *
  * Layouts: every operand is a set of rows (tokens) of heads, head_dim
  * elements contiguous, with a stride from row to row and one from head to
@@ -13,9 +15,10 @@
  * to 2^23 (a single row's is not looked at).  Query head h reads key/value head
  * h / (heads / kv_heads).
  *
- * Sequence starts (cu_*) and lengths (lens) are read on the device, so a
- * captured graph replays with new ones; the kernels clamp them to the rows
- * that the call names, so no value of theirs reaches outside the tensors.
+ * Sequence starts (cu_*), lengths (lens), tables of pages and positions are
+ * read on the device, so a captured graph replays with new ones; the kernels
+ * clamp them to the rows and pages that the call names, so no value of theirs
+ * reaches outside the tensors.
  *
  * Plans hold host data only; any number of runs of one plan may overlap.  A
  * run that splits its keys or its sequences over workgroups needs a

@@ -199,6 +199,34 @@ def test_infinities_and_nan_reach_the_rows_that_see_them(window, sinks, rows):
         R.check(got, want, b, "side by side")
 
 
+@pytest.mark.parametrize("rows", [1, 2, 40])
+@pytest.mark.parametrize("window,sinks", [(None, 0), (4000, 50)])
+def test_infinities_in_parts(rows, window, sinks):
+    """Cut keys: infinities and NaN in parts of any weight, and in keys that nobody sees."""
+    H, Hkv, D, size, n = 8, 2, 64, 16, 6500
+    _flush(f"infinities in parts, {rows} rows, window {window}")
+    case = ("bf16", H, Hkv, D, size, [rows], [n], window, sinks, "rows")
+    plan, q, kc, vc, table, cu, k, v = _paged(case)
+    tab = table.cpu()
+    for key, col, x in ((3, 1, math.inf), (60, 2, -math.inf), (1200, 3, math.nan), (3000, 4, math.inf), (5000, 5, -math.inf),
+                        (6000, 5, math.inf), (6470, 6, math.nan), (6499, 7, math.inf)):
+        v[key, 0, col] = x
+        vc[int(tab[0, key // size]), key % size, 0, col] = x
+    got, lse = plan.run(q, kc, vc, table, _int([n]), cu, lse=True)
+    torch.cuda.synchronize()
+    want, want_lse, b, bl = R.attend(q, k, v, [rows], [n], window, sinks)
+    R.check(got, want, b)
+    R.check(lse, want_lse, bl)
+    # one part holds all the weight: the others' infinities stay
+    q2 = q.clone()
+    q2[:] = k[6400].repeat_interleave(H // Hkv, 0) * 40
+    got = plan.run(q2, kc, vc, table, _int([n]), cu)
+    torch.cuda.synchronize()
+    want, _, _, _ = R.attend(q2, k, v, [rows], [n], window, sinks)
+    odd = ~torch.isfinite(want)
+    assert not bool(torch.isfinite(got.cpu()[odd]).any()) and bool(torch.isfinite(got.cpu()[~odd]).all())
+
+
 def test_keys_of_nan_that_a_row_does_not_see():
     """NaN among keys: rows that see them are NaN, others as they would be."""
     H, Hkv, D, n = 2, 2, 64, 200

@@ -453,11 +453,12 @@ __device__ __forceinline__ void key_tile_body(const KeyTile<C>& k, unsigned char
             next.e = k.entry_of(k.tile(i), rg, lane);
         }
     };
-    auto copy = [&](int i) __attribute__((always_inline)) {
+    // WHOLE: all of the tile's rows are keys.
+    auto copy = [&](int i, auto WHOLE) __attribute__((always_inline)) {
         const unsigned char* dst = lds + (2 * (i & 1) + (keys ? 0 : 1)) * C::TILE;
         const int t = k.tile(i);
         if constexpr (EVEN) {
-            const int key = t * C::BN + 16 * rg, n = k.w.nk - key;
+            const int key = t * C::BN + 16 * rg, n = WHOLE.value ? 16 : k.w.nk - key;
             const char* p = src0;
             if constexpr (C::PAGED) {
                 const int e = __builtin_amdgcn_readfirstlane(next.e), pg = e < 0 ? 0 : (e < a.pages ? e : a.pages - 1);
@@ -476,15 +477,18 @@ __device__ __forceinline__ void key_tile_body(const KeyTile<C>& k, unsigned char
     const int kb0 = attn_kbase(lane, 0), kb1 = attn_kbase(lane, 1), vb = attn_vbase(lane);
     if (k.i0 < k.i1) {
         look(k.i0);
-        copy(k.i0);
+        copy(k.i0, std::false_type{});
         if (k.i0 + 1 < k.i1) look(k.i0 + 1);
     }
     attn_load_q<C::KS>(q, a, k.w.q0, k.kvh, rr, k.rows, lane);
-    for (int i = k.i0; i < k.i1; ++i) {
-        barrier_vm<0>();          // tile i is in LDS, and everyone is done with tile i - 1
-        if (i == k.i0)
+    if (k.i0 < k.i1) {
+        barrier_vm<0>();
 #pragma unroll
-            for (int j = 0; j < C::KS; ++j) asm volatile("" : "+v"(q[j]));
+        for (int j = 0; j < C::KS; ++j) asm volatile("" : "+v"(q[j]));
+    }
+    // INNER: the wave's rows see all of the tile, and the next one is whole.
+    auto step = [&](int i, auto INNER) __attribute__((always_inline)) {
+        barrier_vm<0>();          // tile i is in LDS, and everyone is done with tile i - 1
         const int t = k.tile(i), at = t * C::BN;
         const unsigned char* kt = lds + 2 * (i & 1) * C::TILE;
         const unsigned char* vt = kt + C::TILE;
@@ -498,11 +502,11 @@ __device__ __forceinline__ void key_tile_body(const KeyTile<C>& k, unsigned char
 #pragma unroll
         for (int j = 0; j < 4; ++j) f[j] = key(j);
         __builtin_amdgcn_sched_barrier(0);
-        if (i + 1 < k.i1) {
-            copy(i + 1);
+        if (INNER.value || i + 1 < k.i1) {
+            copy(i + 1, INNER);
             if (i + 2 < k.i1) look(i + 2);
         }
-        if (t >= done || (C::WIN && at + C::BN <= dark && at >= a.sinks)) continue;
+        if (!INNER.value && (t >= done || (C::WIN && at + C::BN <= dark && at >= a.sinks))) return;
         f16x_t s[1] = {f16x_t{}};
 #pragma unroll
         for (int j = 0; j < C::KS; ++j) {
@@ -512,7 +516,7 @@ __device__ __forceinline__ void key_tile_body(const KeyTile<C>& k, unsigned char
 #pragma unroll
         for (int b = 0; b < C::DB; ++b) f[b] = attn_vfrag<C::BN>(vt, vb, b, 0);
         __builtin_amdgcn_sched_barrier(0);
-        if (t >= clear || (C::WIN && at < open && at + C::BN > a.sinks))
+        if (!INNER.value && (t >= clear || (C::WIN && at < open && at + C::BN > a.sinks)))
             key_mask<C::WIN>(s[0], lim - at, lo - at, a.sinks - 4 * h - at);
         attn_move_max<C::DB>(attn_max<1>(s), st, o, a.sc);
         attn_probs<1>(s, st, a.sc);
@@ -525,7 +529,19 @@ __device__ __forceinline__ void key_tile_body(const KeyTile<C>& k, unsigned char
         p = attn_pack<C::DT>(s[0], 1);
 #pragma unroll
         for (int b = 0; b < C::DB; ++b) o[b] = M::mma(f[b], p, o[b]);
+    };
+    // The inner tiles need none of the questions that those at the borders ask.
+    int in0 = k.i0, in1 = (clear < k.w.nk / C::BN - 1 ? clear : k.w.nk / C::BN - 1) - k.gap;
+    if constexpr (C::WIN) {
+        const int first = open > 0 ? (open + C::BN - 1) / C::BN - k.gap : 0;
+        in0 = first > in0 ? first : in0;
+        if (k.gap) in0 = k.sink_tiles > in0 ? k.sink_tiles : in0;
     }
+    in1 = in1 < k.i1 - 1 ? in1 : k.i1 - 1;
+    int i = k.i0;
+    for (const int end = in0 < k.i1 ? in0 : k.i1; i < end; ++i) step(i, std::false_type{});
+    for (; i < in1; ++i) step(i, std::true_type{});
+    for (; i < k.i1; ++i) step(i, std::false_type{});
     if (!attn_finite<C>(o, st)) key_again<C>(k, o, st, rr, k.i0, 1, lane);
     if (k.w.parts == 1) {
         attn_store<C::DT, C::DB, false>(a, o, st, k.w.q0, k.kvh, rr, k.rows, 0, lane);

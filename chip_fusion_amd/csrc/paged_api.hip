@@ -167,7 +167,11 @@ b2b_status_t b2b_paged_attn_run(b2b_attn_t p, int32_t seqs, int64_t rows, b2b_ro
     a.page.set(p->page);
     a.pages = pages;
     a.lens = lens;
-    const bool whole = p->page % 16 == 0 && K.row_stride <= kMaxStride && V.row_stride <= kMaxStride;
+    // pages of whole groups of 16 rows, whose addresses the kernel works out in 32 bits
+    auto near = [&](const b2b_pages_t& x) {
+        return x.row_stride <= kMaxStride && x.row_stride * p->page <= INT32_MAX && x.page_stride <= INT32_MAX;
+    };
+    const bool whole = p->page % 16 == 0 && near(K) && near(V);
     return launch_keys(p, l, a, whole ? b2bk::KEYS_PAGES16 : b2bk::KEYS_PAGES, workspace, stream);
 }
 

@@ -10,12 +10,12 @@
 //   write LDS directly, 16 rows of 64 bytes each.  Pages of a multiple of 16 keys:
 //   the 16 rows lie in one page, whose address is one scalar calculation and a
 //   buffer resource that ends at the sequence's last key (many rows, whose time is
-//   instructions: 2048 rows behind 16384 keys 437 us -> 401; the few rows' kernel waits for
-//   memory and is faster without the scalar chain, 215 us against 223).  Else, as
-//   pages of other sizes may end anywhere, every lane works out the address (64 bits) of the 16 bytes that it
-//   moves, and those behind the last key come from a block of zeros.  Either way
-//   what a page holds behind a sequence's keys may be anything, NaN too.  The
-//   table's entries for a tile are asked for one tile ahead.
+//   instructions: 2048 rows behind 16384 keys 437 us -> 401; the few rows' kernel
+//   waits for memory and is faster without the scalar chain, 215 us against 223).
+//   Else, as pages of other sizes may end anywhere, every lane works out the address
+//   (64 bits) of the 16 bytes that it moves, and those behind the last key come from
+//   a block of zeros.  Either way what a page holds behind a sequence's keys may be
+//   anything, NaN too.  The table's entries for a tile are asked for a tile ahead.
 //
 //   Window.  The row in place p sees keys p - window + 1 .. p and the first
 //   `sinks`: 128 rows' tiles are those of the sinks and those from the first
@@ -183,8 +183,6 @@ __device__ __forceinline__ bool find_item(const KeyArgs& a, int u, KeyItem* out)
 // ---------------------------------------------------------------------------
 // One item's geometry
 // ---------------------------------------------------------------------------
-// Which key tiles the rows of a tile meet: number i of [i0, i1) is tile
-// i < sink_tiles ? i : i + gap.
 // Where keys lie: side by side, in pages of a multiple of 16 keys, in pages of any size.
 enum { KEYS_PACKED, KEYS_PAGES16, KEYS_PAGES };
 
@@ -202,6 +200,8 @@ struct KeyCfg {
     static_assert(!FEW || PAGED, "few rows: pages");
 };
 
+// Which key tiles the rows of a tile meet: number i of [i0, i1) is tile
+// i < sink_tiles ? i : i + gap.
 template <class C>
 struct KeyTile {
     const KeyArgs& a;
@@ -306,6 +306,24 @@ __device__ __forceinline__ void key_mask(f16x_t& s, int lim, int lo, int sinks) 
 #pragma unroll
     for (int r = 0; r < 16; ++r)
         if (!key_seen<WIN>(8 * (r >> 2) + (r & 3), lim, lo, sinks)) s[r] = -__builtin_inff();
+}
+
+// attn_move_max, the two halves' maxima joined by a swap alone.
+template <int NO>
+__device__ __forceinline__ void key_move_max(float mx, RowState& st, f16x_t (&o)[NO], float sc) {
+    unsigned x = __builtin_bit_cast(unsigned, mx), y = x;
+    swap32(x, y);       // x: the low half's in all lanes, y: the high half's
+    mx = __builtin_fmaxf(__builtin_bit_cast(float, x), __builtin_bit_cast(float, y)) * sc;
+    if (__any(mx - st.m > kMaxLag)) {
+        const float m1 = __builtin_fmaxf(st.m, mx);
+        const float alpha = __builtin_amdgcn_exp2f(st.m - m1);
+        st.m = m1;
+        st.l *= alpha;
+#pragma unroll
+        for (int t = 0; t < NO; ++t)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) o[t][r] *= alpha;
+    }
 }
 
 // Infinities and NaN among the values (see attn_finite): the wave's rows again,
@@ -434,7 +452,7 @@ __device__ __forceinline__ void key_tile_body(const KeyTile<C>& k, unsigned char
     const Pages src = C::PAGED ? (keys ? a.pk : a.pv)
                                : Pages{keys ? a.K.p : a.V.p, 0, keys ? a.K.ld : a.V.ld, keys ? a.K.hs : a.V.hs};
     const char* src0 = (const char*)src.p + (C::PAGED ? 0 : k.w.k0 * src.ld * 2) + k.kvh * src.hs * 2;
-    const uint32_t ld2 = (uint32_t)src.ld * 2;
+    const uint32_t ld2 = (uint32_t)src.ld * 2, ps2 = (uint32_t)src.ps * 2;     // (pages of whole groups: 4 GB apart at most)
     int off[C::DB];         // a lane's 16 bytes of each block of 32 columns (past the head: past the resource)
     if constexpr (EVEN) {
         const int chunk = keys ? (lane & 3) ^ ((lane >> 4) & 3) : lane & 3;      // swizzled as attn_copy's
@@ -442,27 +460,28 @@ __device__ __forceinline__ void key_tile_body(const KeyTile<C>& k, unsigned char
         for (int b = 0; b < C::DB; ++b) off[b] = 32 * b + 8 * chunk < a.dim ? (lane >> 2) * (int)ld2 + 16 * chunk + 64 * b : -16;
     }
     struct {
-        int e, in;          // the next tile's entry and its first row's place in the page
+        int e;              // the next tile's entry ...
+        uint32_t in;        // ... and how far into the page its first row lies
     } next = {0, 0};
     auto look = [&](int i) __attribute__((always_inline)) {
         if constexpr (C::WHERE == KEYS_PAGES16) {
             const int key = k.tile(i) * C::BN + 16 * rg, pg = a.page(key < k.w.nk ? key : k.w.nk - 1);
             next.e = a.table[k.w.seq * a.table_ld + pg];
-            next.in = key - pg * a.page.d;
+            next.in = (uint32_t)(key - pg * a.page.d) * ld2;
         } else {
             next.e = k.entry_of(k.tile(i), rg, lane);
         }
     };
     // WHOLE: all of the tile's rows are keys.
-    auto copy = [&](int i, auto WHOLE) __attribute__((always_inline)) {
-        const unsigned char* dst = lds + (2 * (i & 1) + (keys ? 0 : 1)) * C::TILE;
+    auto copy = [&](int i, int slot, auto WHOLE) __attribute__((always_inline)) {
+        const unsigned char* dst = lds + (keys ? 0 : C::TILE) + slot;
         const int t = k.tile(i);
         if constexpr (EVEN) {
             const int key = t * C::BN + 16 * rg, n = WHOLE.value ? 16 : k.w.nk - key;
             const char* p = src0;
             if constexpr (C::PAGED) {
                 const int e = __builtin_amdgcn_readfirstlane(next.e), pg = e < 0 ? 0 : (e < a.pages ? e : a.pages - 1);
-                p += pg * src.ps * 2 + (uint64_t)(uint32_t)next.in * ld2;
+                p += (uint64_t)(uint32_t)pg * ps2 + next.in;
             } else {
                 p += (uint64_t)(uint32_t)key * ld2;
             }
@@ -477,7 +496,7 @@ __device__ __forceinline__ void key_tile_body(const KeyTile<C>& k, unsigned char
     const int kb0 = attn_kbase(lane, 0), kb1 = attn_kbase(lane, 1), vb = attn_vbase(lane);
     if (k.i0 < k.i1) {
         look(k.i0);
-        copy(k.i0, std::false_type{});
+        copy(k.i0, 0, std::false_type{});
         if (k.i0 + 1 < k.i1) look(k.i0 + 1);
     }
     attn_load_q<C::KS>(q, a, k.w.q0, k.kvh, rr, k.rows, lane);
@@ -487,10 +506,12 @@ __device__ __forceinline__ void key_tile_body(const KeyTile<C>& k, unsigned char
         for (int j = 0; j < C::KS; ++j) asm volatile("" : "+v"(q[j]));
     }
     // INNER: the wave's rows see all of the tile, and the next one is whole.
+    int slot = 2 * C::TILE;       // of tile i - 1
     auto step = [&](int i, auto INNER) __attribute__((always_inline)) {
         barrier_vm<0>();          // tile i is in LDS, and everyone is done with tile i - 1
-        const int t = k.tile(i), at = t * C::BN;
-        const unsigned char* kt = lds + 2 * (i & 1) * C::TILE;
+        const int t = k.tile(i), at = t * C::BN, other = slot;
+        slot = 2 * C::TILE - slot;
+        const unsigned char* kt = lds + slot;
         const unsigned char* vt = kt + C::TILE;
         // Fragments are read ahead of their use, four keys' under the next tile's
         // addresses, the first half of the values' under the softmax: a wave then
@@ -503,7 +524,7 @@ __device__ __forceinline__ void key_tile_body(const KeyTile<C>& k, unsigned char
         for (int j = 0; j < 4; ++j) f[j] = key(j);
         __builtin_amdgcn_sched_barrier(0);
         if (INNER.value || i + 1 < k.i1) {
-            copy(i + 1, INNER);
+            copy(i + 1, other, INNER);
             if (i + 2 < k.i1) look(i + 2);
         }
         if (!INNER.value && (t >= done || (C::WIN && at + C::BN <= dark && at >= a.sinks))) return;
@@ -518,7 +539,7 @@ __device__ __forceinline__ void key_tile_body(const KeyTile<C>& k, unsigned char
         __builtin_amdgcn_sched_barrier(0);
         if (!INNER.value && (t >= clear || (C::WIN && at < open && at + C::BN > a.sinks)))
             key_mask<C::WIN>(s[0], lim - at, lo - at, a.sinks - 4 * h - at);
-        attn_move_max<C::DB>(attn_max<1>(s), st, o, a.sc);
+        key_move_max<C::DB>(attn_max<1>(s), st, o, a.sc);
         attn_probs<1>(s, st, a.sc);
         u4_t p = attn_pack<C::DT>(s[0], 0);
 #pragma unroll
@@ -611,7 +632,7 @@ __device__ __forceinline__ void key_rows_body(const KeyTile<C>& k, unsigned char
         const int at = t * C::BN;
         if (t >= clear || (C::WIN && at < open && at + C::BN > a.sinks))
             key_mask<C::WIN>(s[0], lim - at, lo - at, a.sinks - 4 * h - at);
-        attn_move_max<C::DB>(attn_max<1>(s), st, o, a.sc);
+        key_move_max<C::DB>(attn_max<1>(s), st, o, a.sc);
         attn_probs<1>(s, st, a.sc);
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) p[ks] = attn_pack<C::DT>(s[0], ks);

@@ -500,11 +500,10 @@ __device__ __forceinline__ void key_tile_body(const KeyTile<C>& k, unsigned char
         if (k.i0 + 1 < k.i1) look(k.i0 + 1);
     }
     attn_load_q<C::KS>(q, a, k.w.q0, k.kvh, rr, k.rows, lane);
-    if (k.i0 < k.i1) {
-        barrier_vm<0>();
+    // (the queries are taken here, where waiting for them costs nothing: the first tile is waited for too)
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 #pragma unroll
-        for (int j = 0; j < C::KS; ++j) asm volatile("" : "+v"(q[j]));
-    }
+    for (int j = 0; j < C::KS; ++j) asm volatile("" : "+v"(q[j]));
     // INNER: the wave's rows see all of the tile, and the next one is whole.
     int slot = 2 * C::TILE;       // of tile i - 1
     auto step = [&](int i, auto INNER) __attribute__((always_inline)) {

@@ -196,6 +196,10 @@ struct KeyCfg {
     static constexpr int MINE = FEW ? 2 * TILE + 256 : TILE;     // a wave's LDS where waves take different keys
     static constexpr int JOIN = WAVES * MINE;           // behind it: the waves' maxima and sums
     static constexpr int LDS_BYTES = JOIN + 2 * WAVES * 32 * 4;
+    // Workgroups a compute unit, by registers.  Heads of up to 96 under a window and over pages: single tokens among
+    // prompts' chunks go beside three of the chunks' (4 chunks of 1464 rows and 36 tokens behind 2048 keys each: 88 us
+    // -> 80); alone neither gains, nor do rows without a window.
+    static constexpr int PER_CU = FEW ? 2 : DB == 3 && WHERE == KEYS_PAGES16 && WIN ? 4 : 3;
     static_assert(BM == 32 * WAVES, "many rows: 32 a wave");
     static_assert(!FEW || PAGED, "few rows: pages");
 };
@@ -306,6 +310,14 @@ __device__ __forceinline__ void key_mask(f16x_t& s, int lim, int lo, int sinks) 
 #pragma unroll
     for (int r = 0; r < 16; ++r)
         if (!key_seen<WIN>(8 * (r >> 2) + (r & 3), lim, lo, sinks)) s[r] = -__builtin_inff();
+}
+
+// The lane's number, from which nothing that was worked out before is kept: behind a
+// loop it costs instructions, not registers inside it.
+__device__ __forceinline__ int lane_again() {
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));
+    return lane;
 }
 
 // attn_move_max, the two halves' maxima joined by a swap alone.
@@ -562,20 +574,21 @@ __device__ __forceinline__ void key_tile_body(const KeyTile<C>& k, unsigned char
     for (const int end = in0 < k.i1 ? in0 : k.i1; i < end; ++i) step(i, std::false_type{});
     for (; i < in1; ++i) step(i, std::true_type{});
     for (; i < k.i1; ++i) step(i, std::false_type{});
-    if (!attn_finite<C>(o, st)) key_again<C>(k, o, st, rr, k.i0, 1, lane);
+    const int lane1 = lane_again(), rr1 = wrow + (lane1 & 31), h1 = lane1 >> 5;
+    if (!attn_finite<C>(o, st)) key_again<C>(k, o, st, rr1, k.i0, 1, lane1);
     if (k.w.parts == 1) {
-        attn_store<C::DT, C::DB, false>(a, o, st, k.w.q0, k.kvh, rr, k.rows, 0, lane);
+        attn_store<C::DT, C::DB, false>(a, o, st, k.w.q0, k.kvh, rr1, k.rows, 0, lane1);
         return;
     }
     const float l = st.l + other_half(st.l), inv = l == 0.f ? 0.f : 1.f / l;
-    if (rr >= k.rows) return;
-    const int64_t row = k.part_row(rr);
-    if (h == 0) a.part_lse[row] = l == 0.f ? -__builtin_inff() : st.m + __builtin_amdgcn_logf(l);
+    if (rr1 >= k.rows) return;
+    const int64_t row = k.part_row(rr1);
+    if (h1 == 0) a.part_lse[row] = l == 0.f ? -__builtin_inff() : st.m + __builtin_amdgcn_logf(l);
 #pragma unroll
     for (int b = 0; b < C::DB; ++b)
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-            const int c = 32 * b + 8 * x + 4 * h;
+            const int c = 32 * b + 8 * x + 4 * h1;
             if (c < a.dim)
                 *(f4_t*)(a.part + row * a.dim + c) =
                     f4_t{o[b][4 * x] * inv, o[b][4 * x + 1] * inv, o[b][4 * x + 2] * inv, o[b][4 * x + 3] * inv};
@@ -593,7 +606,7 @@ template <class C>
 __device__ __forceinline__ void key_rows_body(const KeyTile<C>& k, unsigned char* lds) {
     using M = Ty32<C::DT>;
     const KeyArgs& a = k.a;
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int lane = lane_again(), wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int rr = k.row0 + (lane & 31), h = lane >> 5;
     const int lim = k.sees(rr) - 4 * h, lo = C::WIN ? k.from(rr) - 4 * h : 0;
     const int last = k.rows - 1;
@@ -703,28 +716,29 @@ __device__ __forceinline__ void key_rows_body(const KeyTile<C>& k, unsigned char
             if (i + C::WAVES < k.i1) copy(std::false_type{}, mine, k.tile(i + C::WAVES), e0, e1);
         }
     }
-    if (!attn_finite<C>(o, st)) key_again<C>(k, o, st, rr, i0, C::WAVES, lane);
+    const int lane1 = lane_again(), rr1 = k.row0 + (lane1 & 31);
+    if (!attn_finite<C>(o, st)) key_again<C>(k, o, st, rr1, i0, C::WAVES, lane1);
     // join: every wave's maximum and sum, then its rows, scaled to the common maximum
     float* ms = (float*)(lds + C::JOIN);           // [maximum, sum][wave][row]
     const float l = st.l + other_half(st.l);
-    if (lane < 32) {
-        ms[wave * 32 + lane] = st.m;
-        ms[(C::WAVES + wave) * 32 + lane] = l;
+    if (lane1 < 32) {
+        ms[wave * 32 + lane1] = st.m;
+        ms[(C::WAVES + wave) * 32 + lane1] = l;
     }
     __syncthreads();
     float m = kLowest, sum = 0.f;
 #pragma unroll
-    for (int v = 0; v < C::WAVES; ++v) m = __builtin_fmaxf(m, ms[v * 32 + (lane & 31)]);
+    for (int v = 0; v < C::WAVES; ++v) m = __builtin_fmaxf(m, ms[v * 32 + (lane1 & 31)]);
 #pragma unroll
     for (int v = 0; v < C::WAVES; ++v)
-        sum += ms[(C::WAVES + v) * 32 + (lane & 31)] * __builtin_amdgcn_exp2f(ms[v * 32 + (lane & 31)] - m);
+        sum += ms[(C::WAVES + v) * 32 + (lane1 & 31)] * __builtin_amdgcn_exp2f(ms[v * 32 + (lane1 & 31)] - m);
     const float f = __builtin_amdgcn_exp2f(st.m - m) * (sum == 0.f ? 0.f : 1.f / sum);
     const bool whole = k.w.parts == 1;
-    if (wave == 0 && lane < 32 && rr < k.rows) {
+    if (wave == 0 && lane1 < 32 && rr1 < k.rows) {
         const float lse2 = sum == 0.f ? -__builtin_inff() : m + __builtin_amdgcn_logf(sum);
-        const int pos = a.group(rr);
-        if (!whole) a.part_lse[k.part_row(rr)] = lse2;
-        else if (a.lse) a.lse[(int64_t)(k.w.q0 + pos) * a.heads + k.kvh * a.group.d + (rr - pos * a.group.d)] = lse2 * kLn2;
+        const int pos = a.group(rr1);
+        if (!whole) a.part_lse[k.part_row(rr1)] = lse2;
+        else if (a.lse) a.lse[(int64_t)(k.w.q0 + pos) * a.heads + k.kvh * a.group.d + (rr1 - pos * a.group.d)] = lse2 * kLn2;
     }
     const int live = k.rows - k.row0;              // 32 at most
     // half of the columns at a time: a wave's tile of LDS holds 32 rows of
@@ -743,7 +757,7 @@ __device__ __forceinline__ void key_rows_body(const KeyTile<C>& k, unsigned char
                 const float z = o[b][4 * g + r];
                 v[r] = f == 0.f ? (__builtin_fabsf(z) <= -kLowest ? 0.f : z) : z * f;
             }
-            *(f4_t*)(mo + ((2 * x + (lane >> 5)) * 32 + (lane & 31)) * 4) = v;
+            *(f4_t*)(mo + ((2 * x + (lane1 >> 5)) * 32 + (lane1 & 31)) * 4) = v;
         }
         __syncthreads();
         for (int i = threadIdx.x; i < live * 4 * C::DB; i += C::THREADS) {
@@ -769,7 +783,7 @@ __device__ __forceinline__ void key_rows_body(const KeyTile<C>& k, unsigned char
 }
 
 template <class C>
-__global__ __launch_bounds__(C::THREADS, C::FEW ? 2 : 3) void key_attn_kernel(KeyArgs a) {
+__global__ __launch_bounds__(C::THREADS, C::PER_CU) void key_attn_kernel(KeyArgs a) {
     __shared__ __attribute__((aligned(1024))) unsigned char lds[C::LDS_BYTES];
     // Workgroups go to the XCDs in turn.  A key head's own row tiles read the same
     // keys: neighbours in `u` with 8 key heads share an XCD's L2.  Few rows a sequence

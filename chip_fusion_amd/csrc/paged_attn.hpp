@@ -822,12 +822,14 @@ __global__ __launch_bounds__(C::THREADS, C::PER_CU) void key_attn_kernel(KeyArgs
 // columns a lane
 // ---------------------------------------------------------------------------
 // O = sum_s w_s O_s / sum_s w_s with w_s = 2^(lse_s - max), in one pass with a
-// running maximum, 4 parts' loads in flight (8: 135 registers, and tiles' joins 5 us longer).  Parts that saw no key have lse = -inf and are left
-// out, whatever they hold; infinities and NaN of the others stay, also where the
-// weight is 0.  SUB: groups of 16 lanes that a row's parts go over, for few rows.
-template <int DT, int SUB>
+// running maximum.  Parts that saw no key have lse = -inf and are left out,
+// whatever they hold; infinities and NaN of the others stay, also where the weight
+// is 0.  SUB: groups of 16 lanes that a row's parts go over, for few rows.  PER:
+// parts whose loads are in flight, 4 for few rows, whose parts are many, 2 for
+// tiles, of which more workgroups then fit (276 tiles of 96 columns in two parts
+// each: 8.6 us with 2, 10.4 with 4, 15 with 8; 50, 84 and 135 registers).
+template <int DT, int PER, int SUB>
 __device__ __forceinline__ void key_join_rows(const KeyArgs& a, const KeyItem& w, int kvh, int first, int live, int row0) {
-    constexpr int PER = 4;
     const int lane = threadIdx.x & 15, sub = SUB == 1 ? 0 : (threadIdx.x >> 4) & (SUB - 1);
     const bool in = 8 * lane < a.dim;
     const int64_t step = (int64_t)w.per_part * a.kv_heads.d * 32;      // from a part's row to the next part's
@@ -915,7 +917,7 @@ __device__ __forceinline__ void key_join_rows(const KeyArgs& a, const KeyItem& w
     }
 }
 
-template <int DT, bool PAGED, bool WIN>
+template <int DT, int PER, bool PAGED, bool WIN>
 __global__ __launch_bounds__(256) void key_join_kernel(KeyArgs a) {
     const int v = a.kv_heads((int)blockIdx.x), kvh = (int)blockIdx.x - v * a.kv_heads.d;
     KeyItem w;
@@ -924,9 +926,9 @@ __global__ __launch_bounds__(256) void key_join_kernel(KeyArgs a) {
     const int first = a.subs == 1 ? 0 : 32 * (v & 3), row0 = (w.tiles - 1 - w.tile) * kKeyRows;
     int live = w.nq * a.group.d - row0 - first;
     live = live < 32 ? live : 32;
-    if (live <= 4) key_join_rows<DT, 4>(a, w, kvh, first, live, row0);
-    else if (live <= 8) key_join_rows<DT, 2>(a, w, kvh, first, live, row0);
-    else key_join_rows<DT, 1>(a, w, kvh, first, live, row0);
+    if (live <= 4) key_join_rows<DT, PER, 4>(a, w, kvh, first, live, row0);
+    else if (live <= 8) key_join_rows<DT, PER, 2>(a, w, kvh, first, live, row0);
+    else key_join_rows<DT, PER, 1>(a, w, kvh, first, live, row0);
 }
 
 }  // namespace b2bk

@@ -40,9 +40,10 @@ struct KeyLaunchers {
     }
     static hipError_t join(const b2bk::KeyArgs& a, int where, unsigned grid, hipStream_t s) {
         using namespace b2bk;
-        if (where == KEYS_PACKED) return launch(key_join_kernel<DT, false, true>, grid, 256, s, a);
-        return a.window ? launch(key_join_kernel<DT, true, true>, grid, 256, s, a)
-                        : launch(key_join_kernel<DT, true, false>, grid, 256, s, a);
+        auto go = [&](auto kernel) { return launch(kernel, grid, 256, s, a); };
+        if (where == KEYS_PACKED) return go(key_join_kernel<DT, 2, false, true>);
+        if (a.subs == 1) return a.window ? go(key_join_kernel<DT, 4, true, true>) : go(key_join_kernel<DT, 4, true, false>);
+        return a.window ? go(key_join_kernel<DT, 2, true, true>) : go(key_join_kernel<DT, 2, true, false>);
     }
     static const KeyLaunch& table() {
         static const KeyLaunch t = {&run, &join};

@@ -195,7 +195,9 @@ struct KeyCfg {
     static constexpr int TILE = BN * DB * 64;           // a tile of keys (or values) in LDS
     static constexpr int MINE = FEW ? 2 * TILE + 256 : TILE;     // a wave's LDS where waves take different keys
     static constexpr int JOIN = WAVES * MINE;           // behind it: the waves' maxima and sums
-    static constexpr int LDS_BYTES = JOIN + 2 * WAVES * 32 * 4;
+    static constexpr int QUERIES = 2 * TILE;            // the waves' queries on their way: the second slot of keys and behind it
+    static constexpr int LDS_BYTES = QUERIES + WAVES * TILE > JOIN + 2 * WAVES * 32 * 4 ? QUERIES + WAVES * TILE
+                                                                                        : JOIN + 2 * WAVES * 32 * 4;
     // Workgroups a compute unit, by registers.  Heads of up to 96 under a window and over pages: single tokens among
     // prompts' chunks go beside three of the chunks' (4 chunks of 1464 rows and 36 tokens behind 2048 keys each: 88 us
     // -> 80); alone neither gains, nor do rows without a window.
@@ -286,6 +288,15 @@ struct KeyTile {
         const int n = w.nk - t * C::BN < C::BN ? w.nk - t * C::BN : C::BN;
         const auto rs = attn_rsrc(x.p, (int64_t)w.k0 + (int64_t)t * C::BN, x.ld, (int64_t)kvh * x.hs, n, a.dim);
         attn_copy<C::DB, C::BN, !VALUES>(dst, rs, (int)x.ld * 2, a.dim, rg, lane);
+    }
+    // Copies a lane's 16-byte pieces of query row rr, one of group rg (16 rows) of a
+    // wave's, laid out as keys.
+    __device__ __forceinline__ void copy_queries(const unsigned char* dst, int rr, int rg, int lane) const {
+        const int chunk = (lane & 3) ^ ((lane >> 4) & 3), pos = a.group(rr), head = kvh * a.group.d + (rr - pos * a.group.d);
+        const char* p = (const char*)a.Q.p + ((w.q0 + pos) * a.Q.ld + head * a.Q.hs + 8 * chunk) * 2;
+#pragma unroll
+        for (int b = 0; b < C::DB; ++b)
+            lds_dma16_from(dst + b * C::BN * 64 + rg * 1024, rr < rows && 32 * b + 8 * chunk < a.dim ? p + 64 * b : (const char*)kZeros);
     }
     // lane's table entry for row group rg of tile t
     __device__ __forceinline__ int entry_of(int t, int rg, int lane) const {
@@ -511,9 +522,14 @@ __device__ __forceinline__ void key_tile_body(const KeyTile<C>& k, unsigned char
         copy(k.i0, 0, std::false_type{});
         if (k.i0 + 1 < k.i1) look(k.i0 + 1);
     }
-    attn_load_q<C::KS>(q, a, k.w.q0, k.kvh, rr, k.rows, lane);
-    // (the queries are taken here, where waiting for them costs nothing: the first tile is waited for too)
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    // Queries come through LDS as the keys do: 4 lanes bring 64 bytes of a row, where
+    // the fragments' own loads would ask for 32 at a time.
+    unsigned char* qs = lds + C::QUERIES + wave * C::TILE;
+    for (int g = 0; g < 2; ++g) k.copy_queries(qs, wrow + 16 * g + (lane >> 2), g, lane);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");        // (the first tile is waited for too)
+#pragma unroll
+    for (int j = 0; j < C::KS; ++j) q[j] = *(const u4_t*)(qs + ((j & 1) ? kb1 : kb0) + (j >> 1) * C::BN * 64);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");      // before the second tile comes here
 #pragma unroll
     for (int j = 0; j < C::KS; ++j) asm volatile("" : "+v"(q[j]));
     // INNER: the wave's rows see all of the tile, and the next one is whole.

@@ -199,8 +199,7 @@ struct KeyCfg {
     static constexpr int LDS_BYTES = QUERIES + WAVES * TILE > JOIN + 2 * WAVES * 32 * 4 ? QUERIES + WAVES * TILE
                                                                                         : JOIN + 2 * WAVES * 32 * 4;
     // Workgroups a compute unit, by registers.  Heads of up to 96 under a window and over pages: single tokens among
-    // prompts' chunks go beside three of the chunks' (4 chunks of 1464 rows and 36 tokens behind 2048 keys each: 88 us
-    // -> 80); alone neither gains, nor do rows without a window.
+    // prompts' chunks go beside three of the chunks' (1464 rows in 4 chunks and 36 tokens, 2048 keys each: 79 us -> 70); alone neither gains, nor do rows without a window.
     static constexpr int PER_CU = FEW ? 2 : DB == 3 && WHERE == KEYS_PAGES16 && WIN ? 4 : 3;
     static_assert(BM == 32 * WAVES, "many rows: 32 a wave");
     static_assert(!FEW || PAGED, "few rows: pages");
@@ -436,13 +435,14 @@ __device__ __forceinline__ void key_again(const KeyTile<C>& k, f16x_t (&o)[C::DB
 // Many rows: 32 a wave, the key tiles shared (attn_tile_body's scheme)
 // ---------------------------------------------------------------------------
 // Measured (bf16, 32 heads of 128 on 8 key heads): 32768 tokens under a window of
-// 4096 in 1.81 to 1.98 ms by the card, 1040 to 1142 TFLOP/s of the 1280 that a product
-// of 8192^3 reaches (matrix cores busy 0.64 of the cycles at a clock that power holds
-// near 1.74 GHz); 8001 tokens in 17 sequences under a window of 512 in 63 to 68 us, of
-// whose 37 thousand cycles a workgroup spends 4.3 on finding its place, 7.2 on its first
-// keys and queries, 22.6 on 10 tiles and 2.9 on its output; 2048 rows of 4 sequences
-// behind up to 16384 keys in pages of 64 in 367 us and 8 for the join (matrix cores
-// busy 0.56).  Tile i's probabilities worked out under tile i + 1's scores, which
+// 4096 in 1.77 to 1.98 ms by the card, 1040 to 1165 TFLOP/s of the 1230 to 1290 that a
+// product of 8192^3 reaches (matrix cores busy 0.74 of the cycles at a clock that power
+// holds at 1.5 to 1.6 GHz); 8001 tokens in 17 sequences under a window of 512 in 65 to 68
+// us, 59 where the caches hold all of it: of a workgroup's 37 thousand cycles some 4.3
+// went to finding its place, 7.2 to its first keys and queries (before these came
+// through LDS), 22.6 to 10 tiles and 2.9 to its output; 2048 rows of 4 sequences behind
+// up to 16384 keys in pages of 64 in 360 to 380 us and 7 for the join (matrix cores
+// busy 0.59).  Tile i's probabilities worked out under tile i + 1's scores, which
 // costs no LDS but 16 registers, was slower (1858 us -> 1925 and 380 -> 393): what
 // waves do side by side covers that already.
 template <class C>
@@ -615,7 +615,7 @@ __device__ __forceinline__ void key_tile_body(const KeyTile<C>& k, unsigned char
 // Up to 32 rows: the waves take different keys (attn_rows_body's scheme)
 // ---------------------------------------------------------------------------
 // What bounds it is the bytes of K and V.  Measured (bf16, 32 heads of 128 on 8 key
-// heads): 64 requests of up to 8192 keys in pages of 16, 1.02 GB, in 197 us and 5.6
+// heads): 64 requests of up to 8192 keys in pages of 16, 1.02 GB, in 196 us and 5.1
 // for the join, 5.05 TB/s in all (a copy of 1 GiB: 5.0 to 5.1); 64 of 8192 each
 // 412 us, 5.2 TB/s; one request of 2048 keys 13 us, of 32768 42.
 template <class C>

@@ -437,7 +437,7 @@ __device__ __forceinline__ void key_again(const KeyTile<C>& k, f16x_t (&o)[C::DB
 // Measured (bf16, 32 heads of 128 on 8 key heads): 32768 tokens under a window of
 // 4096 in 1.77 to 1.98 ms by the card, 1040 to 1165 TFLOP/s of the 1230 to 1290 that a
 // product of 8192^3 reaches (matrix cores busy 0.74 of the cycles at a clock that power
-// holds at 1.5 to 1.6 GHz); 8001 tokens in 17 sequences under a window of 512 in 65 to 68
+// holds at 1.5 to 1.6 GHz); 8001 tokens in 17 sequences under a window of 512 in 64 to 68
 // us, 59 where the caches hold all of it: of a workgroup's 37 thousand cycles some 4.3
 // went to finding its place, 7.2 to its first keys and queries (before these came
 // through LDS), 22.6 to 10 tiles and 2.9 to its output; 2048 rows of 4 sequences behind

@@ -70,9 +70,25 @@ __device__ __forceinline__ void unpack8(u4_t w, float (&x)[8]) {
 
 // A head's 8 elements a lane: out = inv (x own + partner's x far), where `own` and
 // `far` are cosine and signed sine with the weights of either element folded in.
+// Elements meet them before the norm's factor: in float32 while the head's sum of
+// squares is below `most`, 2^126 (elements below 2^63), or for no sum where a weight
+// lies outside 2^-60 to 2^60 (bf16 alone has such weights).
 struct Turn {
-    float own[8], far[8];
+    float own[8], far[8], most;
 };
+
+// Whether any lane of the wave holds a bf16 weight outside 2^-60 to 2^60, 0 apart (two at a time, as integers).
+__device__ __forceinline__ bool far_weights(u4_t w) {
+    typedef unsigned short us2_t __attribute__((ext_vector_type(2)));
+    us2_t big = {0, 0}, small = {0xFFFF, 0xFFFF};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const us2_t m = __builtin_bit_cast(us2_t, w[i] & 0x7FFF7FFFu);
+        big = __builtin_elementwise_max(big, m);
+        small = __builtin_elementwise_min(small, (us2_t)(m - (unsigned short)1));      // (0 becomes the largest)
+    }
+    return __any(big[0] > 0x5D80 || big[1] > 0x5D80 || small[0] < 0x217F || small[1] < 0x217F);
+}
 
 // APPEND: keys and values go to the pages.  NORM, INTER: the plan's flags.
 template <int DT, int L, bool APPEND, bool NORM, bool INTER>
@@ -231,6 +247,9 @@ __global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a) {
 #pragma unroll
             for (int u = 0; u < 8; ++u) x[u] = y[u] = 1.f;
         }
+        t.most = 0x1p126f;
+        if constexpr (NORM && DT == DT_BF16)
+            if (far_weights(w)) t.most = 0.f;
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
             const int e = 8 * c + u;
@@ -270,8 +289,9 @@ __global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a) {
             for (int u = 0; u < 8; ++u) sum = __builtin_fmaf(x[u], x[u], sum);
             sum = head_sum<L>(sum);
             inv = __builtin_amdgcn_rsqf(__builtin_fmaf(sum, per, a.eps));
-            // squares that leave float32's range (the sum infinite, or so small that terms are lost)
-            const bool odd = !(sum < 0x1p126f && sum > 0x1p-100f) && sum == sum;
+            // squares that leave float32's range (the sum infinite, or so small that terms
+            // are lost), or that would with the weights
+            const bool odd = !(sum < t.most && sum > 0x1p-100f) && sum == sum;
             if (__any(odd)) {
                 double d = 0.0;
 #pragma unroll

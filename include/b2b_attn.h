@@ -230,7 +230,8 @@ enum {
  * and pair i of its first rotary_dim elements is turned by the row's position,
  *     (a, b) -> (a cos t - b sin t, b cos t + a sin t),  t = position[axes_of[i]] freqs[i].
  * All of it in float32 (angles reduced in float64, so that far positions lose
- * nothing; norms whose sums leave float32's range in float64), rounded once.
+ * nothing; norms whose sums, alone or with the weights, leave float32's range in
+ * float64), rounded once.
  *   rotary_dim  a multiple of 8, 0 (no rotation) to head_dim
  *   freqs       host, rotary_dim / 2 finite values: radians a position
  *   axes_of     host, rotary_dim / 2 values below `axes`, or NULL (all axis 0)

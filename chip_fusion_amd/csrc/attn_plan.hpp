@@ -7,6 +7,7 @@
 
 #include "attn_launch.hpp"
 #include "b2b_attn.h"
+#include "extent.hpp"
 #include "paged_attn.hpp"
 
 struct b2b_attn_plan {
@@ -45,6 +46,18 @@ inline bool pages_ok(const b2b_pages_t& x, int64_t pages) {
     for (int64_t s : {x.page_stride, x.row_stride, x.head_stride})
         if (s % 8 || s < 0 || s > kMaxFar) return false;
     return x.page_stride <= ((int64_t)1 << 46) / std::max<int64_t>(pages, 1);
+}
+inline Extent extent(const b2b_rows_t& r, int64_t n, int heads, int dim) {
+    return Extent(r.data, dim, {{n, r.row_stride}, {heads, r.head_stride}});
+}
+inline Extent extent(const b2b_pages_t& x, int64_t pages, int64_t size, int heads, int dim) {
+    return Extent(x.data, dim, {{pages, x.page_stride}, {size, x.row_stride}, {heads, x.head_stride}});
+}
+// Whether what is written shares no element with any of the others.
+inline bool apart(const Extent& o, std::initializer_list<Extent> others) {
+    for (const Extent& x : others)
+        if (overlap(o, x)) return false;
+    return true;
 }
 inline b2bk::Pages dev(const b2b_pages_t& x) { return {x.data, x.page_stride, x.row_stride, x.head_stride}; }
 

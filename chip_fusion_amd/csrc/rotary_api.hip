@@ -28,7 +28,8 @@ bool sizes_ok(const b2b_rotary_plan* p, int64_t rows) {
 // Written rows: in place over their input, or apart from it, no two sharing an element.
 bool written_ok(const b2b_rows_t& o, const b2b_rows_t& in, int64_t rows, int heads, int dim) {
     if (!out_ok(o, rows, heads, dim)) return false;
-    return o.data != in.data || ((rows <= 1 || o.row_stride == in.row_stride) && (heads <= 1 || o.head_stride == in.head_stride));
+    if (o.data != in.data) return apart(extent(o, rows, heads, dim), {extent(in, rows, heads, dim)});
+    return (rows <= 1 || o.row_stride == in.row_stride) && (heads <= 1 || o.head_stride == in.head_stride);
 }
 
 // Pages that are written: no two of their (page, row, head) share an element.
@@ -139,7 +140,10 @@ b2b_status_t b2b_rotary_run(b2b_rotary_t p, int64_t rows, b2b_rows_t Q, b2b_rows
     if (!p || !sizes_ok(p, rows) || !weights_ok(p, q_weight, k_weight)) return B2B_ERROR_INVALID_VALUE;
     if (!rows) return B2B_SUCCESS;
     if (!rows_ok(Q, rows, p->dim) || !rows_ok(K, rows, p->dim) || !written_ok(Qo, Q, rows, p->heads, p->dim) ||
-        !written_ok(Ko, K, rows, p->kv_heads, p->dim) || Qo.data == Ko.data || Qo.data == K.data || Ko.data == Q.data)
+        !written_ok(Ko, K, rows, p->kv_heads, p->dim))
+        return B2B_ERROR_INVALID_VALUE;
+    const Extent qo = extent(Qo, rows, p->heads, p->dim), ko = extent(Ko, rows, p->kv_heads, p->dim);
+    if (!apart(qo, {ko, extent(K, rows, p->kv_heads, p->dim)}) || !apart(ko, {extent(Q, rows, p->heads, p->dim)}))
         return B2B_ERROR_INVALID_VALUE;
     if (p->rotary && (!positions || (p->axes > 1 && (position_stride < 0 || position_stride > kMaxFar))))
         return B2B_ERROR_INVALID_VALUE;
@@ -161,16 +165,19 @@ b2b_status_t b2b_rotary_append(b2b_rotary_t p, int32_t seqs, int64_t rows, b2b_r
         return B2B_ERROR_INVALID_VALUE;
     if (!rows || !seqs) return B2B_SUCCESS;
     if (!rows_ok(Q, rows, p->dim) || !rows_ok(K, rows, p->dim) || !rows_ok(V, rows, p->dim) ||
-        !written_ok(Qo, Q, rows, p->heads, p->dim) || Qo.data == K.data || Qo.data == V.data || !lens)
+        !written_ok(Qo, Q, rows, p->heads, p->dim) || !lens)
         return B2B_ERROR_INVALID_VALUE;
+    const Extent q = extent(Q, rows, p->heads, p->dim), k = extent(K, rows, p->kv_heads, p->dim),
+                 v = extent(V, rows, p->kv_heads, p->dim), qo = extent(Qo, rows, p->heads, p->dim);
+    if (!apart(qo, {k, v})) return B2B_ERROR_INVALID_VALUE;
     if (positions && p->axes > 1 && (position_stride < 0 || position_stride > kMaxFar)) return B2B_ERROR_INVALID_VALUE;
     if (pages && width) {
         if (!table || table_stride < 0 || table_stride > kMaxFar || (seqs > 1 && table_stride < width)) return B2B_ERROR_INVALID_VALUE;
         for (const b2b_pages_t* x : {&k_cache, &v_cache})
-            if (!pages_ok(*x, pages) || !pages_apart(*x, pages, page_size, p->kv_heads, p->dim) || x->data == Q.data ||
-                x->data == K.data || x->data == V.data || x->data == Qo.data)
-                return B2B_ERROR_INVALID_VALUE;
-        if (k_cache.data == v_cache.data) return B2B_ERROR_INVALID_VALUE;
+            if (!pages_ok(*x, pages) || !pages_apart(*x, pages, page_size, p->kv_heads, p->dim)) return B2B_ERROR_INVALID_VALUE;
+        const Extent kc = extent(k_cache, pages, page_size, p->kv_heads, p->dim),
+                     vc = extent(v_cache, pages, page_size, p->kv_heads, p->dim);
+        if (!apart(kc, {q, k, v, qo, vc}) || !apart(vc, {q, k, v, qo})) return B2B_ERROR_INVALID_VALUE;
     }
     b2bk::RotaryArgs a = {};
     fill(p, a, rows, Q, K, Qo, positions, position_stride, q_weight, k_weight);

@@ -245,7 +245,8 @@ b2b_status_t b2b_rotary_create(b2b_rotary_t* plan, b2b_dtype_t dtype, int32_t he
 
 /*
  * Q' and K' of `rows` rows: Qo and Ko may be Q and K (the same address and
- * strides: in place), and must not overlap anything else.
+ * strides: in place), and must share no element with anything else (INVALID_VALUE;
+ * they may lie between others' rows, as slices of one projection do).
  *   positions        device int32 [axes, rows], axes position_stride apart (0: all axes
  *                    alike; NULL where rotary_dim is 0)
  *   q_weight, k_weight  device, head_dim values of dtype, 16-byte aligned, or NULL (1);
@@ -267,8 +268,8 @@ b2b_status_t b2b_rotary_run(b2b_rotary_t plan, int64_t rows, b2b_rows_t Q, b2b_r
  *               names no page, writes no key and no value; rows that belong to
  *               no sequence write nothing
  * No two rows of a call may have the same place of the same page (sequences that
- * share pages have their new tokens in pages of their own); no two places of
- * the pages may share an element.
+ * share pages have their new tokens in pages of their own).  No two places of the
+ * pages, and no place and another operand, may share an element (INVALID_VALUE).
  */
 b2b_status_t b2b_rotary_append(b2b_rotary_t plan, int32_t seqs, int64_t rows, b2b_rows_t Q, b2b_rows_t K, b2b_rows_t V,
                                b2b_rows_t Qo, b2b_pages_t k_cache, b2b_pages_t v_cache, int32_t pages, int32_t page_size,

@@ -41,9 +41,9 @@ NON_CASCADE_SOURCES = ("api.hip", "plan.cpp", "plan.hpp", "microbench.hip",
                        "attn.hpp", "attn_launch.hpp", "attn_api.hip", "inst_attn_f16.hip", "inst_attn_bf16.hip",
                        "linear_attn.hpp", "linear_attn_launch.hpp", "inst_linear_attn_f16.hip",
                        "inst_linear_attn_bf16.hip",
-                       "attn_plan.hpp", "extent.hpp", "paged_attn.hpp", "paged_attn_launch.hpp", "paged_api.hip", "inst_paged_attn_f16.hip",
-                       "inst_paged_attn_bf16.hip", "norm_rotary.hpp", "rotary_launch.hpp", "rotary_api.hip",
-                       "inst_rotary_f16.hip", "inst_rotary_bf16.hip")
+                       "attn_plan.hpp", "extent.hpp", "paged_attn.hpp", "paged_attn_launch.hpp", "paged_api.hip",
+                       "inst_paged_attn_f16.hip", "inst_paged_attn_bf16.hip", "norm_rotary.hpp", "rotary_launch.hpp",
+                       "rotary_api.hip", "inst_rotary_f16.hip", "inst_rotary_bf16.hip")
 
 
 def source_digest():

@@ -106,6 +106,10 @@ b2b_status_t b2b::window_run(b2b_attn_t p, int32_t seqs, int64_t rows, int64_t k
                              const b2b_rows_t& V, const b2b_rows_t& O, const int32_t* cu_q, const int32_t* cu_k, float* lse,
                              void* workspace, size_t workspace_bytes, hipStream_t stream) {
     if (!key_sizes_ok(p, seqs, rows, keys)) return B2B_ERROR_INVALID_VALUE;
+    const Extent o = extent(O, rows, p->heads, p->dim);
+    if (!apart(o, {extent(Q, rows, p->heads, p->dim)}) ||
+        (keys && !apart(o, {extent(K, keys, p->kv_heads, p->dim), extent(V, keys, p->kv_heads, p->dim)})))
+        return B2B_ERROR_INVALID_VALUE;
     const Layout l = lay_out(p, seqs, rows, keys);
     if (!ready(l, p, workspace, workspace_bytes)) return B2B_ERROR_INVALID_VALUE;
     b2bk::KeyArgs a = key_args(p, seqs, rows, keys, Q, O, cu_q, lse);
@@ -150,11 +154,14 @@ b2b_status_t b2b_paged_attn_run(b2b_attn_t p, int32_t seqs, int64_t rows, b2b_ro
     const int64_t keys = pages ? (int64_t)width * p->page : 0;
     if (!key_sizes_ok(p, seqs, rows, (int64_t)width * p->page) || (!cu_q && rows != seqs)) return B2B_ERROR_INVALID_VALUE;
     if (!seqs || !rows) return B2B_SUCCESS;
-    if (!rows_ok(Q, rows, p->dim) || !out_ok(O, rows, p->heads, p->dim) || O.data == Q.data || (uintptr_t)lse % 4)
-        return B2B_ERROR_INVALID_VALUE;
+    if (!rows_ok(Q, rows, p->dim) || !out_ok(O, rows, p->heads, p->dim) || (uintptr_t)lse % 4) return B2B_ERROR_INVALID_VALUE;
     if (!lens) return B2B_ERROR_INVALID_VALUE;
-    if (keys && (!pages_ok(K, pages) || !pages_ok(V, pages) || !table || O.data == K.data || O.data == V.data ||
-                 table_stride < 0 || table_stride > kMaxFar || (seqs > 1 && table_stride < width)))
+    if (keys && (!pages_ok(K, pages) || !pages_ok(V, pages) || !table || table_stride < 0 || table_stride > kMaxFar ||
+                 (seqs > 1 && table_stride < width)))
+        return B2B_ERROR_INVALID_VALUE;
+    const Extent o = extent(O, rows, p->heads, p->dim);
+    if (!apart(o, {extent(Q, rows, p->heads, p->dim)}) ||
+        (keys && !apart(o, {extent(K, pages, p->page, p->kv_heads, p->dim), extent(V, pages, p->page, p->kv_heads, p->dim)})))
         return B2B_ERROR_INVALID_VALUE;
     // (by the table's width alone, as the _workspace call)
     const Layout l = lay_out(p, seqs, rows, (int64_t)width * p->page);

@@ -116,7 +116,8 @@ b2b_status_t b2b_prefix_attn_run(b2b_attn_t plan, int32_t batch, int64_t prefix,
  * as B2B_ATTN_CAUSAL) sees keys p - window + 1 .. p and the sequence's first
  * `sinks` keys up to p.
  *   window   1 to 2^30      sinks   0 to 2^30
- * rows (of b2b_attn_run) up to 2^30.
+ * rows (of b2b_attn_run) below 2^30.  O that shares an element with an input is
+ * INVALID_VALUE.
  */
 b2b_status_t b2b_attn_create_window(b2b_attn_t* plan, b2b_dtype_t dtype, int32_t heads, int32_t kv_heads, int32_t head_dim,
                                     float scale, int32_t window, int32_t sinks);
@@ -150,9 +151,11 @@ b2b_status_t b2b_paged_attn_create(b2b_attn_t* plan, b2b_dtype_t dtype, int32_t 
  *   pages   pages of K and V: entries of the table are clamped to them
  *   table   device int32 [seqs, width], rows table_stride apart; entries of pages
  *           behind a sequence's last key are not read
- *   lens    device int32 [seqs], clamped to 0 .. width x page_size (2^30 at most)
+ *   lens    device int32 [seqs], clamped to 0 .. width x page_size (below 2^30)
  *   cu_q    device int32 [seqs + 1], or NULL: row s is sequence s's one token
  *   lse, workspace   as for b2b_attn_run (b2b_paged_attn_workspace)
+ * INVALID_VALUE as for b2b_attn_run, and for O that shares an element with an
+ * input (it may lie between others' rows).
  */
 b2b_status_t b2b_paged_attn_workspace(b2b_attn_t plan, int32_t seqs, int64_t rows, int32_t width, size_t* bytes);
 b2b_status_t b2b_paged_attn_run(b2b_attn_t plan, int32_t seqs, int64_t rows, b2b_rows_t Q, b2b_pages_t K, b2b_pages_t V,

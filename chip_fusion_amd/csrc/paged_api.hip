@@ -20,6 +20,17 @@ constexpr int kTarget = 512;
 // the four waves of one workgroup do (3 requests of up to 300 keys: 12 us cut, 7.6 whole).
 constexpr int kLeast = 16;
 
+// Under a window, with as many row tiles as workgroups are wanted, nothing is cut
+// while the keys before a sequence's rows make no row tile longer than this, or than
+// the others take together (a row tile's start and end cost some 7 key tiles, 256 run
+// at full rate: n of them take n / 36 key tiles' time at least).  Cutting costs the
+// join's launch where row tiles are alike and a multiple where they are not (520 row
+// tiles, 32 heads of 128 on 8 key heads: all behind a window of 512, 22 key tiles,
+// 38 us whole and 42 cut; 1000: 58 and 62; 4096: 196 and 201; one chunk of 64 rows
+// behind as much, 60 prompts of 40 behind nothing: 22 and 27, 32 and 30, 88 and 34,
+// behind 100000 keys 2240 and 166).
+constexpr int kFar = 32;
+
 struct Layout {
     int64_t tiles;          // row tiles a key head, at most
     int64_t items;          // workgroups a key head, at most
@@ -28,16 +39,20 @@ struct Layout {
     size_t bytes;
 };
 
-Layout lay_out(const b2b_attn_plan* p, int64_t seqs, int64_t rows, int64_t keys) {
+// keys: the most that a sequence may have; before: the most that come before its rows
+Layout lay_out(const b2b_attn_plan* p, int64_t seqs, int64_t rows, int64_t keys, int64_t before) {
     const int64_t group = p->heads / p->kv_heads;
     Layout l = {};
     l.tiles = rows * group / b2bk::kKeyRows + seqs;
     // key tiles of a row tile, at most
-    int64_t most = ceil_div(keys, 32);
-    if (p->window) most = std::min<int64_t>(most, ((int64_t)p->window + b2bk::kKeyRows) / 32 + ceil_div(p->sinks, 32) + 2);
-    // Under a window no row tile has many more key tiles than another: once there
-    // are as many as workgroups are wanted nothing is gained by cutting them.
-    const bool enough = p->window && rows * group / b2bk::kKeyRows * p->kv_heads >= kTarget;
+    int64_t most = ceil_div(keys, 32), far = ceil_div(before, 32);
+    if (p->window) {
+        const int64_t w = ((int64_t)p->window + b2bk::kKeyRows) / 32 + ceil_div(p->sinks, 32) + 2;
+        most = std::min(most, w);
+        far = std::min(far, w);
+    }
+    const int64_t wgs = rows * group / b2bk::kKeyRows * p->kv_heads;
+    const bool enough = p->window && wgs >= kTarget && far <= std::max<int64_t>(kFar, wgs / 32);
     l.items = l.tiles;
     l.subs = rows * group <= 32 ? 1 : b2bk::kKeyRows / 32;
     if (most > kLeast && !enough) {
@@ -98,7 +113,7 @@ b2bk::KeyArgs key_args(const b2b_attn_plan* p, int32_t seqs, int64_t rows, int64
 
 b2b_status_t b2b::window_workspace(b2b_attn_t p, int32_t seqs, int64_t rows, int64_t keys, size_t* bytes) {
     if (!key_sizes_ok(p, seqs, rows, keys)) return B2B_ERROR_INVALID_VALUE;
-    *bytes = seqs && rows ? lay_out(p, seqs, rows, keys).bytes : 0;
+    *bytes = seqs && rows ? lay_out(p, seqs, rows, keys, std::max<int64_t>(keys - rows, 0)).bytes : 0;
     return B2B_SUCCESS;
 }
 
@@ -110,7 +125,7 @@ b2b_status_t b2b::window_run(b2b_attn_t p, int32_t seqs, int64_t rows, int64_t k
     if (!apart(o, {extent(Q, rows, p->heads, p->dim)}) ||
         (keys && !apart(o, {extent(K, keys, p->kv_heads, p->dim), extent(V, keys, p->kv_heads, p->dim)})))
         return B2B_ERROR_INVALID_VALUE;
-    const Layout l = lay_out(p, seqs, rows, keys);
+    const Layout l = lay_out(p, seqs, rows, keys, std::max<int64_t>(keys - rows, 0));
     if (!ready(l, p, workspace, workspace_bytes)) return B2B_ERROR_INVALID_VALUE;
     b2bk::KeyArgs a = key_args(p, seqs, rows, keys, Q, O, cu_q, lse);
     a.K = b2b::dev(K, p->dim);
@@ -142,7 +157,7 @@ b2b_status_t b2b_paged_attn_create(b2b_attn_t* plan, b2b_dtype_t dtype, int32_t 
 b2b_status_t b2b_paged_attn_workspace(b2b_attn_t p, int32_t seqs, int64_t rows, int32_t width, size_t* bytes) {
     if (!p || !bytes || !p->page || width < 0 || !key_sizes_ok(p, seqs, rows, (int64_t)width * p->page))
         return B2B_ERROR_INVALID_VALUE;
-    *bytes = seqs && rows ? lay_out(p, seqs, rows, (int64_t)width * p->page).bytes : 0;
+    *bytes = seqs && rows ? lay_out(p, seqs, rows, (int64_t)width * p->page, (int64_t)width * p->page).bytes : 0;
     return B2B_SUCCESS;
 }
 
@@ -164,7 +179,7 @@ b2b_status_t b2b_paged_attn_run(b2b_attn_t p, int32_t seqs, int64_t rows, b2b_ro
         (keys && !apart(o, {extent(K, pages, p->page, p->kv_heads, p->dim), extent(V, pages, p->page, p->kv_heads, p->dim)})))
         return B2B_ERROR_INVALID_VALUE;
     // (by the table's width alone, as the _workspace call)
-    const Layout l = lay_out(p, seqs, rows, (int64_t)width * p->page);
+    const Layout l = lay_out(p, seqs, rows, (int64_t)width * p->page, (int64_t)width * p->page);
     if (!ready(l, p, workspace, workspace_bytes)) return B2B_ERROR_INVALID_VALUE;
     b2bk::KeyArgs a = key_args(p, seqs, rows, keys, Q, O, cu_q, lse);
     a.pk = dev(K);

@@ -89,11 +89,12 @@ def _compile(src, remarks):
 
 def _torch_flags():
     """What compiles and links against torch's own headers and libraries (which the
-    process has loaded by the time the binding is)."""
+    process has loaded by the time the binding is), for this torch alone."""
     try:
         import torch
         from torch.utils.cpp_extension import include_paths
-        flags = ["-DB2B_TORCH", "-DUSE_ROCM=1", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+        flags = [f'-DB2B_TORCH="{torch.__version__} {torch.version.git_version}"', "-DUSE_ROCM=1",
+                 f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
         for p in include_paths():
             flags += ["-isystem", p]
         return flags, ["-L", os.path.join(os.path.dirname(torch.__file__), "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]

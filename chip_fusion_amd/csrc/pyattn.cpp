@@ -9,8 +9,10 @@
 //
 // CPython's API is enough: tensors are asked for their shape, strides and address
 // through their methods (0.5 us a tensor, 1.2 an allocation).  Where it is built
-// with torch's own headers (B2B_TORCH), torch's plain tensors are looked at and
-// made directly instead; subclasses and stand-ins still go through their methods.
+// with torch's own headers (B2B_TORCH, the version's text), torch's plain tensors are
+// looked at and made directly instead; subclasses and stand-ins still go through
+// their methods.  Those headers hold the layout of one torch's tensors: beside any
+// other the module is not imported, and every call is made in Python.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -606,6 +608,21 @@ PyTypeObject call_type = {PyVarObject_HEAD_INIT(nullptr, 0) "chip_fusion_amd._at
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_attn", "The attention plans' usual calls.", -1, nullptr, nullptr, nullptr,
                       nullptr, nullptr};
 
+#ifdef B2B_TORCH
+// ImportError unless the process's torch is the one whose headers these are.
+bool same_torch() {
+    Ref torch(PyImport_ImportModule("torch")), about(PyImport_ImportModule("torch.version"));
+    if (!torch.o || !about.o) return false;
+    Ref v(PyObject_GetAttrString(torch.o, "__version__")), git(PyObject_GetAttrString(about.o, "git_version"));
+    if (!v.o || !git.o) return false;
+    Ref here(PyUnicode_FromFormat("%S %S", v.o, git.o));
+    if (!here.o) return false;
+    if (!PyUnicode_CompareWithASCIIString(here.o, B2B_TORCH)) return true;
+    PyErr_Format(PyExc_ImportError, "_attn.so is built for torch %s, this is %U", B2B_TORCH, here.o);
+    return false;
+}
+#endif
+
 }  // namespace
 
 PyMODINIT_FUNC PyInit__attn(void) {
@@ -616,6 +633,12 @@ PyMODINIT_FUNC PyInit__attn(void) {
                  {&n_dtype, "dtype"},           {&n_get_device, "get_device"}, {&n_new_empty, "new_empty"}};
     for (auto& n : names)
         if (!(*n.at = PyUnicode_InternFromString(n.name))) return nullptr;
+#ifdef B2B_TORCH
+    if (!same_torch()) return nullptr;
+    const char* built = B2B_TORCH;
+#else
+    const char* built = nullptr;
+#endif
     call_type.tp_basicsize = sizeof(Call);
     call_type.tp_flags = Py_TPFLAGS_DEFAULT;
     call_type.tp_new = call_new;
@@ -630,5 +653,9 @@ PyMODINIT_FUNC PyInit__attn(void) {
         Py_DECREF(&call_type);
         return nullptr;
     }
+    // the torch whose tensors are looked at directly, or None
+    Ref torch(Py_BuildValue("z", built));
+    if (!torch.o || PyModule_AddObject(m.o, "torch", torch.o) < 0) return nullptr;
+    torch.take();
     return m.take();
 }

@@ -8,6 +8,7 @@ import re
 import subprocess
 import sys
 import sysconfig
+import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -105,19 +106,24 @@ def _torch_flags():
 def binding():
     """The attention plans' compiled calls.  They are a shortcut past Python, which
     makes every call without them: where they cannot be compiled (no g++, no
-    Python.h), a line says so and the build goes on; without torch's headers they
-    look at tensors through Python's methods.  Their path, or None."""
+    Python.h), a line says so and the build goes on; without torch's headers, which
+    another line says, they look at tensors through Python's methods.  Their path, or
+    None."""
     tmp = PYATTN + ".tmp%d" % os.getpid()
     cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-Wall", "-shared", "-D__HIP_PLATFORM_AMD__=1",
            "-I", os.path.join(ROOT, "include"), "-isystem", "/opt/rocm/include",
            "-isystem", sysconfig.get_paths()["include"], os.path.join(CSRC, "pyattn.cpp"), "-o", tmp]
     extra = _torch_flags()
     for flags, libs in ([extra] if extra else []) + [([], [])]:
-        try:
-            subprocess.check_call(cmd[:1] + flags + cmd[1:] + libs, **({"stderr": subprocess.DEVNULL} if flags else {}))
-            break
-        except (subprocess.CalledProcessError, OSError) as e:
-            error = e
+        with tempfile.TemporaryFile("w+") as said:
+            try:
+                subprocess.check_call(cmd[:1] + flags + cmd[1:] + libs, stderr=said)
+                break
+            except (subprocess.CalledProcessError, OSError) as e:
+                said.seek(0)
+                error = next((line.strip() for line in said if "error" in line), str(e))
+        if flags:
+            sys.stderr.write(f"{os.path.basename(PYATTN)} is built without torch's headers ({error})\n")
     else:
         for f in (tmp, PYATTN):         # (one of an earlier build may not fit the library)
             if os.path.exists(f):

@@ -358,6 +358,8 @@ def _pages(t, name, dtype, pages, size, heads, dim):
     if t.dim() != 4 or any(n is not None and n != m for n, m in zip(want, t.shape)):
         raise ValueError(f"{name}: shape [{', '.join('any' if n is None else str(n) for n in want)}] expected, "
                          f"got {list(t.shape)}")
+    if max(t.shape[:2]) >= 1 << 31:         # (the library's own checks see 32 bits)
+        raise ValueError(f"{name}: fewer than 2^31 pages and keys a page are expected, got {list(t.shape)}")
     if t.numel() == 0:
         return Pages(None, 0, 0, 0)
     strides = [st if n > 1 else 0 for st, n in zip(t.stride(), t.shape)]      # 0: never stepped by
@@ -380,6 +382,8 @@ def _table(table, lens, cu, rows):
             or (table.shape[1] > 1 and table.stride(1) != 1) or (table.shape[0] > 1 and table.stride(0) < table.shape[1]):
         raise ValueError("table: an int32 tensor [seqs, width] with contiguous rows is expected")
     seqs, width = table.shape
+    if max(seqs, width) >= 1 << 31:         # (the library's own checks see 32 bits)
+        raise ValueError(f"table: fewer than 2^31 sequences and places are expected, got {list(table.shape)}")
     _ints(lens, "lens", (seqs,))
     if cu is not None:
         _starts(cu, "cu", seqs)

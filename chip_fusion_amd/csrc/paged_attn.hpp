@@ -198,9 +198,10 @@ struct KeyCfg {
     static constexpr int QUERIES = 2 * TILE;            // the waves' queries on their way: the second slot of keys and behind it
     static constexpr int LDS_BYTES = QUERIES + WAVES * TILE > JOIN + 2 * WAVES * 32 * 4 ? QUERIES + WAVES * TILE
                                                                                         : JOIN + 2 * WAVES * 32 * 4;
-    // Workgroups a compute unit, by registers.  Heads of up to 96 under a window and over pages: single tokens among
-    // prompts' chunks go beside three of the chunks' (1464 rows in 4 chunks and 36 tokens, 2048 keys each: 79 us -> 70); alone neither gains, nor do rows without a window.
-    static constexpr int PER_CU = FEW ? 2 : DB == 3 && WHERE == KEYS_PAGES16 && WIN ? 4 : 3;
+    // Workgroups a compute unit, by registers: 110 to 164 of them.  (Heads of 65 to 96 held to the 128 of four spill 3
+    // to 21 but for pages of whole groups under a window, which gain nothing by it: 24 heads of 96 on 4, 1464 rows in
+    // 4 chunks and 36 single tokens 66.5 us with either bound, 2048 rows behind 30000 keys 65.1; heads of up to 64 take 114.)
+    static constexpr int PER_CU = FEW ? 2 : 3;
     static_assert(BM == 32 * WAVES, "many rows: 32 a wave");
     static_assert(!FEW || PAGED, "few rows: pages");
 };

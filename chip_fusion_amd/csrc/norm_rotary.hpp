@@ -13,7 +13,7 @@
 // out R x rotary_dim / 2 sines and cosines once, in LDS, and a lane keeps those of
 // its 8 elements in registers over the heads it takes.  An angle is position x
 // frequency / 2 pi in float64, of which only the fraction of a turn counts: off by
-// 2^-24 of a turn at positions of 2^31.
+// 2^-24 of a turn at positions of 2^31 and frequencies up to 1.
 //
 // Measured (bf16, 32 + 8 heads of 128, normed): 8001 rows, 164 MB, in 34 us on the
 // device (a copy of as many bytes 32.6), 32768 rows in 125 us, 5.4 TB/s.  Few rows

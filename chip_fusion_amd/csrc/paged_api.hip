@@ -12,12 +12,12 @@ namespace {
 using namespace b2b;
 
 // Workgroups that a call's key tiles are cut for: two a compute unit (2048 rows of 4
-// sequences behind up to 16384 keys, 32 heads of 128, with the join: 368 us, 383 at
-// 768, 394 at 1024), and four times as many of sequences of few rows (64 requests of
-// up to 8192 keys: 246 us at 512, 230 at 1024, 220 at 2048).
+// sequences behind up to 16384 keys, 32 heads of 128, with the join: 362 us, 378 at
+// 768, 376 at 1024), and four times as many of sequences of few rows (64 requests of
+// up to 8192 keys: 221 us at 512, 204 at 1024, 201 at 2048).
 constexpr int kTarget = 512;
 // Key tiles of a part, at least: below 512 keys a second launch takes longer than
-// the four waves of one workgroup do (3 requests of up to 300 keys: 12 us cut, 7.6 whole).
+// the four waves of one workgroup do (3 requests of up to 300 keys: 10.5 us cut, 7.1 whole).
 constexpr int kLeast = 16;
 
 // Under a window, with as many row tiles as workgroups are wanted, nothing is cut
@@ -84,7 +84,12 @@ b2b_status_t launch_keys(b2b_attn_t p, const Layout& l, b2bk::KeyArgs& a, int wh
     a.subs = !a.cu_q && a.group.d <= 32 ? 1 : (int32_t)l.subs;
     a.part = (float*)workspace;
     a.part_lse = a.part + (size_t)l.granules * p->kv_heads * 32 * p->dim;
-    // few rows a sequence: see key_attn_kernel
+    // Few rows a sequence, on average: the few rows' kernel, heads over all XCDs (see
+    // key_attn_kernel).  32 heads of 128 on 8, against the other kernel: 128 single tokens
+    // behind up to 8000 keys under a window of 1024 120 us and 125, 64 behind up to 4000
+    // 113 and 115, 512 behind up to 512 127 and 122.  A chunk among them goes along, 1000
+    // rows with 200 single tokens behind up to 4000: that begins its prompt 374 and 385,
+    // behind 8192 keys 457 and 418, of which a window leaves 1024 220 and 211.
     a.spread = a.rows * a.group.d <= (int64_t)32 * a.seqs;
     const int64_t items = a.spread ? ceil_div(l.items, 8) * 8 : l.items;
     const KeyLaunch& L = p->dtype == B2B_DTYPE_F16 ? key_attn_f16() : key_attn_bf16();

@@ -10,8 +10,9 @@
 //   write LDS directly, 16 rows of 64 bytes each.  Pages of a multiple of 16 keys:
 //   the 16 rows lie in one page, whose address is one scalar calculation and a
 //   buffer resource that ends at the sequence's last key (many rows, whose time is
-//   instructions: 2048 rows behind 16384 keys 437 us -> 401; the few rows' kernel
-//   waits for memory and is faster without the scalar chain, 215 us against 223).
+//   instructions: 2048 rows behind 16384 keys 404 us -> 362; the few rows' kernel
+//   waits for memory and was faster without the scalar chain, 215 us against 223
+//   when its 64 requests took that, 201 now).
 //   Else, as pages of other sizes may end anywhere, every lane works out the address
 //   (64 bits) of the 16 bytes that it moves, and those behind the last key come from
 //   a block of zeros.  Either way what a page holds behind a sequence's keys may be
@@ -23,14 +24,17 @@
 //   are masked.
 //
 // Work is cut on the device, where the lengths are.  A (sequence, tile of 128
-// rows, key head) of T key tiles is cut into ceil(T / L) parts, with L the
-// whole call's key tiles over the workgroups that it should have, and at least
-// `least`: no chain of tiles is longer than L, whatever the lengths, and a
+// rows, key head) of T key tiles is cut into ceil(T / L) parts, with L the larger
+// of `least` and the whole call's key tiles over the workgroups that it should
+// have: no chain of tiles is longer than that, whatever the lengths, and a
 // captured graph replays with new ones.  Sequences of up to 32 rows, whose partial
-// results are small and whose time is the bytes of their keys, are cut four times
-// as fine.  Since sum ceil(T / L) <= items + sum T / L, the host knows the grid's
-// size, and since a cut item has at most 2 T / L parts, the partial results' as
-// well: 32 rows a granule, one of a part of few rows, four of a tile's.
+// results are small and whose time is the bytes of their keys, are cut finer, into
+// parts of max(L / 4, min(4 L, 32), 8), of this L without `least`: four times as fine
+// where there is much work, 32 tiles from L = 8 on, less where there is little.
+// Since sum ceil(T / L) <= items + sum T / L, four times the sum for few rows, the
+// host knows the grid's size, and since a cut item has at most twice its T / L
+// parts, the partial results' as well: 32 rows a granule, one of a part of few
+// rows, four of a tile's.
 #pragma once
 #include "attn.hpp"
 
@@ -135,8 +139,8 @@ __device__ __forceinline__ bool find_item(const KeyArgs& a, int u, KeyItem* out)
         const float l = ceilf(lanes_total((float)work) * 1.001f * a.per);
         most = l > (float)(1 << 30) ? 1 << 30 : (int)l;
         // Of few rows: the less work there is, the finer, for a wave's chain of tiles is
-        // then all the time (one request of 2048 keys, 8 key heads: 19.8 us in parts of 32
-        // tiles, 14.9 of 16, 12.9 of 8; 16 requests: 30.2, 32.5, 34.8).
+        // then all the time (one request of 2048 keys, 8 key heads: 19.5 us in parts of 32
+        // tiles, 15.1 of 16, 12.9 of 8; 16 requests: 35.5, 37.2, 40.0).
         const int some = most < 8 ? 4 * most : 32;
         fine = (most + 3) >> 2;
         fine = fine < some ? some : fine;
@@ -618,7 +622,9 @@ __device__ __forceinline__ void key_tile_body(const KeyTile<C>& k, unsigned char
 // What bounds it is the bytes of K and V.  Measured (bf16, 32 heads of 128 on 8 key
 // heads): 64 requests of up to 8192 keys in pages of 16, 1.02 GB, in 196 us and 5.1
 // for the join, 5.05 TB/s in all (a copy of 1 GiB: 5.0 to 5.1); 64 of 8192 each
-// 412 us, 5.2 TB/s; one request of 2048 keys 13 us, of 32768 42.
+// 400 to 412 us, 5.2 to 5.4 TB/s; one request of 2048 keys 13 us, of 32768 37 to 42.
+// A compute unit holds two workgroups, of which each takes some 7.5 us for a request
+// of up to 32 keys: 64 such requests 8.4 us, 128 15.4, 256 31, 512 63.
 template <class C>
 __device__ __forceinline__ void key_rows_body(const KeyTile<C>& k, unsigned char* lds) {
     using M = Ty32<C::DT>;
@@ -805,8 +811,9 @@ __global__ __launch_bounds__(C::THREADS, C::PER_CU) void key_attn_kernel(KeyArgs
     // Workgroups go to the XCDs in turn.  A key head's own row tiles read the same
     // keys: neighbours in `u` with 8 key heads share an XCD's L2.  Few rows a sequence
     // share nothing but the lines on a row's borders, and an XCD should see all heads
-    // of a row, which lie on all of its L2's channels (36 requests, 4 key heads of 96:
-    // 37.4 us -> 32.6; rows of prompts would lose their L2: 32768 tokens 1858 us -> 2187).
+    // of a row, which lie on all of its L2's channels (36 requests under a window of
+    // 2048, 4 key heads of 96: 34.2 us -> 31.6; rows of prompts would lose their L2:
+    // 32768 tokens 1823 us -> 2170, 8001 in 17 sequences 65 -> 74).
     int u, kvh;
     if (a.spread) {
         const int j = (int)blockIdx.x >> 3;

@@ -236,7 +236,8 @@ enum {
  * nothing; norms whose sums, alone or with the weights, leave float32's range in
  * float64), rounded once.
  *   rotary_dim  a multiple of 8, 0 (no rotation) to head_dim
- *   freqs       host, rotary_dim / 2 finite values: radians a position
+ *   freqs       host, rotary_dim / 2 finite values: radians a position (an angle is
+ *               off by 2^-52 of itself, that of a frequency up to 1 by 2^-24 of a turn)
  *   axes_of     host, rotary_dim / 2 values below `axes`, or NULL (all axis 0)
  *   axes        1 to 4 positions a row (time, height, width ...)
  *   eps         0 or more, finite (without B2B_ROTARY_NORM not looked at)
